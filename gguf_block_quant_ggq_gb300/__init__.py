@@ -17,7 +17,9 @@ LIB_PATH = os.path.join(_PKG, "libggq.so")
 
 TYPE = {"Q4_0": 2, "Q8_0": 8, "Q8_1": 9, "Q2_K": 10, "Q3_K": 11, "Q4_K": 12, "Q5_K": 13, "Q6_K": 14, "Q8_K": 15,
         "MXFP4": 39}
-OP = {"quantize_act": 0, "dequant": 1, "mul_mat_vec": 2, "moe": 3}
+OP = {"quantize_act": 0, "dequant": 1, "mul_mat_vec": 2, "moe": 3, "kv_cache": 4}
+DTYPE = {"float32": 0, "float16": 1, "bfloat16": 30}  # ggq_dtype of activations
+SCORING = {"softmax": 0, "sigmoid": 1}
 STATUS = {0: "GGQ_OK", 1: "GGQ_ERR_INVALID_ARG", 2: "GGQ_ERR_SHAPE", 3: "GGQ_ERR_UNSUPPORTED", 4: "GGQ_ERR_ARCH",
           5: "GGQ_ERR_CUDA", 6: "GGQ_ERR_CAPACITY", 7: "GGQ_ERR_CAPTURE_ALLOC", 8: "GGQ_ERR_DEVICE"}
 BLOCK_ELEMS = {"Q4_0": 32, "Q8_0": 32, "MXFP4": 32, "Q8_1": 32, "Q4_K": 256, "Q5_K": 256, "Q6_K": 256, "Q8_K": 256,
@@ -48,6 +50,12 @@ SIGNATURES = {
     "ggq_set_moe_counters": (_I32, [_P, _P, _I64, _P]),
     "ggq_moe_experts_q": (_I32, [_P, _P, _I64, _I64, _I64, _I32, _P, _P, _I64, _P, _P, _P]),
     "ggq_mul_mat_vec_qa": (_I32, [_P, _I32, _I32, _P, _I64, _I64, _P, _I64, _P, _P]),
+    "ggq_kv_page_bytes": (ctypes.c_size_t, [_I32, _I32, _I32, _I32]),
+    "ggq_kv_store": (_I32, [_P, _P, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P]),
+    "ggq_kv_load": (_I32, [_P, _P, _I32, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P]),
+    "ggq_attention": (_I32, [_P, _P, _P, _P]),
+    "ggq_reserve_attention": (_I32, [_P, _P]),
+    "ggq_moe_route": (_I32, [_P, _P, _I32, _P, _I64, _I64, _P, _P, _P]),
     "ggq_block_dots_qa": (_I32, [_P, _I32, _I32, _P, _I64, _I64, _P, _I64, _P, _P]),
 }
 
@@ -65,6 +73,26 @@ class ggq_moe_weights(ctypes.Structure):
 class ggq_moe_dump(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("ids", "weights", "xq", "g", "u", "h", "hq", "o", "coefs_gate",
                                                "coefs_up", "coefs_down")]
+
+
+class ggq_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("k_type", "v_type", "n_kv_heads", "head_dim", "page_size")] + [
+        ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class ggq_attn(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("n_tokens", ctypes.c_int64),
+                ("n_seqs", ctypes.c_int64), ("q", ctypes.c_void_p), ("q_token", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_token", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p), ("max_q", ctypes.c_int64),
+                ("max_len", ctypes.c_int64), ("scale", ctypes.c_float), ("cap", ctypes.c_float),
+                ("window", ctypes.c_int64), ("slopes", ctypes.c_void_p)]
+
+
+class ggq_router(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("scoring", "n_groups", "top_groups", "group_best", "top_k",
+                                              "normalize")] + [("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
 
 
 class GGQError(RuntimeError):
@@ -124,6 +152,51 @@ def _ptr(t, dtype: str | None = None):
     if dtype is not None and str(t.dtype) != "torch." + dtype:
         raise ValueError(f"expected a {dtype} tensor, got {t.dtype}")
     return t.data_ptr()
+
+
+def _rows(t, heads: int, dim: int):
+    """(address, ggq_dtype, token stride, head stride) of a [tokens][heads][dim]
+    CUDA tensor whose last axis is dense; the other strides are free."""
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"libggq takes CUDA tensors (device memory), got one on {getattr(t, 'device', type(t))}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"expected a [tokens, {heads}, {dim}] tensor, got {tuple(t.shape)}")
+    token, head, one = t.stride()
+    if one != 1:
+        raise ValueError("the channels of a head have to be dense")
+    code = _DTYPE_CODES.get(str(t.dtype))
+    if code is None:
+        raise ValueError(f"expected a float32, float16 or bfloat16 tensor, got {t.dtype}")
+    return t.data_ptr(), code, token, head
+
+
+_DTYPE_CODES = {"torch." + k: v for k, v in DTYPE.items()}
+
+
+class KVCache:
+    """A paged key/value cache in Q8_0 or Q4_0 blocks: two uint8 pools on the
+    context's device (given, or made here), and the C structure that names them."""
+
+    def __init__(self, ctx, k_type, v_type, n_pages, page_size, n_kv_heads, head_dim, k=None, v=None):
+        torch = ctx._torch
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
+        pools = []
+        for fmt, pool in ((k_type, k), (v_type, v)):
+            size = load().ggq_kv_page_bytes(TYPE[fmt], n_kv_heads, head_dim, page_size)
+            if not size:
+                raise ValueError(f"a cache of {fmt} blocks with {n_kv_heads} heads of {head_dim} channels and pages of "
+                                 f"{page_size} tokens is not supported: Q8_0 or Q4_0, head_dim 64, 128 or 256, pages of "
+                                 "a multiple of 16 tokens")
+            if pool is None:
+                pool = torch.zeros(n_pages * size, dtype=torch.uint8, device=f"cuda:{ctx.device}")
+            _ptr(pool, "uint8")
+            if pool.numel() != n_pages * size:
+                raise ValueError(f"{n_pages} pages of {size} bytes need a pool of {n_pages * size}, got {pool.numel()}")
+            pools.append(pool)
+        self.k, self.v = pools
+        self.struct = ggq_kv_cache(TYPE[k_type], TYPE[v_type], n_kv_heads, head_dim, page_size, n_pages,
+                                   pools[0].data_ptr(), pools[1].data_ptr())
+        self.ref = ctypes.byref(self.struct)
 
 
 class Context:
@@ -234,6 +307,87 @@ class Context:
         self._check(load().ggq_block_dots(self.handle, TYPE[fmt], _ptr(W), N, K, _ptr(Xq), T, _ptr(out),
                                           self._stream(stream)))
         return out
+
+    def kv_cache(self, k_type: str, v_type: str, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+                 k=None, v=None) -> KVCache:
+        """A paged cache of Q8_0 or Q4_0 blocks (zeroed pools are made where none are given)."""
+        return KVCache(self, k_type, v_type, n_pages, page_size, n_kv_heads, head_dim, k, v)
+
+    def kv_store(self, cache: KVCache, k, v, slots, stream=None):
+        """Quantize k and v [tokens][kv heads][D] into the cache's slots (int64 [tokens], negative: skipped)."""
+        kp, code, kt, kh = _rows(k, cache.n_kv_heads, cache.head_dim)
+        vp, vcode, vt, vh = _rows(v, cache.n_kv_heads, cache.head_dim)
+        if code != vcode or k.shape[0] != v.shape[0] or slots.numel() != k.shape[0]:
+            raise ValueError("k, v and slots have to agree in type and tokens")
+        self._check(load().ggq_kv_store(self.handle, cache.ref, code, kp, kt, kh, vp, vt, vh, _ptr(slots, "int64"),
+                                        k.shape[0], self._stream(stream)))
+
+    def kv_load(self, cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
+        """Values of the cache's slots, [tokens][kv heads][D] each of K and V (float32 unless dtype says otherwise)."""
+        n, shape = slots.numel(), (slots.numel(), cache.n_kv_heads, cache.head_dim)
+        if k is None:
+            k = self._torch.empty(shape, dtype=dtype or self._torch.float32, device=slots.device)
+        if v is None:
+            v = self._torch.empty(shape, dtype=dtype or self._torch.float32, device=slots.device)
+        kp, code, kt, kh = _rows(k, cache.n_kv_heads, cache.head_dim)
+        vp, vcode, vt, vh = _rows(v, cache.n_kv_heads, cache.head_dim)
+        if code != vcode or k.shape[0] != n or v.shape[0] != n:
+            raise ValueError("k, v and slots have to agree in type and tokens")
+        self._check(load().ggq_kv_load(self.handle, cache.ref, code, _ptr(slots, "int64"), n, kp, kt, kh, vp, vt, vh,
+                                       self._stream(stream)))
+        return k, v
+
+    def attention(self, cache: KVCache, q, lens, table, q_start=None, max_q=None, max_len=0, scale=None, cap=0.0,
+                  window=0, slopes=None, out=None, stream=None, reserve=True):
+        """Attention of q [tokens][heads][D] over the cache: lens int32 [sequences] (new tokens included), table
+        int32 [sequences][pages], q_start int32 [sequences + 1] unless every sequence has one token; max_q and
+        max_len bound a sequence's rows and length (default: all rows, the table's capacity)."""
+        if q.dim() != 3:
+            raise ValueError(f"expected a [tokens, heads, {cache.head_dim}] tensor, got {tuple(q.shape)}")
+        n, heads, dim = q.shape
+        if out is None:
+            out = self._torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
+        qp, code, qt, qh = _rows(q, heads, cache.head_dim)
+        op, ocode, ot, oh = _rows(out, heads, cache.head_dim)
+        seqs = lens.numel()
+        if ocode != code or out.shape[0] != n:
+            raise ValueError("out has to have q's type and tokens")
+        if table.dim() != 2 or table.shape[0] != seqs or (q_start is not None and q_start.numel() != seqs + 1):
+            raise ValueError(f"{seqs} sequences need a table row each and {seqs + 1} row starts")
+        if q_start is None and n != seqs:
+            raise ValueError(f"{n} rows for {seqs} sequences: q_start is needed")
+        if slopes is not None and slopes.numel() != heads:
+            raise ValueError(f"expected {heads} slopes, got {slopes.numel()}")
+        if reserve:
+            self._check(load().ggq_reserve_attention(self.handle, self._stream(stream)))
+        a = ggq_attn(code, heads, n, seqs, qp, qt, qh, op, ot, oh, _ptr(table, "int32"), table.shape[1],
+                     _ptr(lens, "int32"), _ptr(q_start, "int32"), n if max_q is None else max_q, max_len,
+                     dim ** -0.5 if scale is None else scale, cap, window, _ptr(slopes, "float32"))
+        self._check(load().ggq_attention(self.handle, cache.ref, ctypes.byref(a), self._stream(stream)))
+        return out
+
+    def moe_route(self, logits, top_k: int, scoring: str = "softmax", bias=None, n_groups: int = 1,
+                  top_groups: int = 1, group_best: int = 1, normalize: bool = True, scale: float = 1.0, ids=None,
+                  weights=None, stream=None):
+        """Expert ids [tokens][top_k] int32 and weights fp32 for moe_experts, of logits [tokens][experts]."""
+        T, E = logits.shape
+        code = _DTYPE_CODES.get(str(logits.dtype))
+        if code is None:
+            raise ValueError(f"expected float32, float16 or bfloat16 logits, got {logits.dtype}")
+        if bias is not None and bias.numel() != E:
+            raise ValueError(f"expected a bias of {E} experts, got {bias.numel()}")
+        for t in (ids, weights):
+            if t is not None and tuple(t.shape) != (T, top_k):
+                raise ValueError(f"expected a [{T}, {top_k}] output, got {tuple(t.shape)}")
+        if ids is None:
+            ids = self._torch.empty((T, top_k), dtype=self._torch.int32, device=logits.device)
+        if weights is None:
+            weights = self._torch.empty((T, top_k), dtype=self._torch.float32, device=logits.device)
+        r = ggq_router(SCORING[scoring], n_groups, top_groups, group_best, top_k, 1 if normalize else 0, scale,
+                       _ptr(bias, "float32"))
+        self._check(load().ggq_moe_route(self.handle, ctypes.byref(r), code, _ptr(logits), T, E, _ptr(ids, "int32"),
+                                         _ptr(weights, "float32"), self._stream(stream)))
+        return ids, weights
 
     def moe_weights(self, gate_fmt, gate, up_fmt, up, down_fmt, down):
         return ggq_moe_weights(TYPE[gate_fmt], TYPE[up_fmt], TYPE[down_fmt], _ptr(gate), _ptr(up), _ptr(down))

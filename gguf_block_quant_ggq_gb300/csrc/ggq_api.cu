@@ -8,14 +8,11 @@
 // instead of a boolean, and refusals that name the unsupported formats.
 #include <cuda_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <algorithm>
 #include <cstring>
-#include <string>
-#include <vector>
 
 #include "../../include/ggq.h"
+#include "ggq_ctx.h"
 #include "ggq_device.cuh"
 #include "ggq_direct.cuh"
 #include "ggq_internal.h"
@@ -42,16 +39,6 @@ cudaError_t launch_stream(int kind, int fmt, int nt, const StreamParams& p, int 
 using namespace ggq;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v, size_t a = kAlign) { return (v + a - 1) / a * a; }
-
-// Layout of the control block (allocated once at create).
-struct Ctrl {
-    int err;
-    int pad[63];
-};
 
 int fmt_of(int t) {
     switch (t) {
@@ -113,8 +100,6 @@ MoeScratch moe_scratch(int64_t T, int64_t H, int64_t I, int64_t k) {
     return m;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 // Expert-sorted route (5 tokens and up): pitched activation rows for the
 // grouped kernel's 16-byte row copies.
 struct SortedScratch {
@@ -164,42 +149,7 @@ SortedScratch sorted_scratch(int64_t T, int64_t E, int64_t H, int64_t I, int64_t
 
 }  // namespace
 
-struct ggq_ctx {
-    int device = 0;
-    int nsm = 0;
-    uint8_t* pool = nullptr;
-    size_t pool_bytes = 0;
-    std::vector<void*> retired;
-    Ctrl* ctrl = nullptr;
-    int static_weights = 0;  // weights never written while calls are in flight
-    int direct_max = 32;     // largest token count of the direct MoE route (calls of <= 4 tokens above 4)
-    unsigned long long* tel_pairs = nullptr;  // expert-load telemetry (caller's device buffers)
-    unsigned long long* tel_calls = nullptr;
-    int64_t tel_experts = 0;
-    std::string err;
-};
-
 namespace {
-
-ggq_status fail(ggq_ctx* c, ggq_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    if (c) c->err = buf;
-    return s;
-}
-
-ggq_status cuda_fail(ggq_ctx* c, cudaError_t e, const char* what) {
-    return fail(c, GGQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-ggq_status need_scratch(ggq_ctx* c, size_t bytes) {
-    if (bytes <= c->pool_bytes) return GGQ_OK;
-    return fail(c, GGQ_ERR_CAPACITY, "call needs %zu scratch bytes but the pool holds %zu: call ggq_reserve first",
-                bytes, c->pool_bytes);
-}
 
 int pow2_tokens(int64_t T) { return T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8; }
 
@@ -236,28 +186,6 @@ bool plan_group(GroupParams& p, int nmat, bool resident_x, int* smem) {
     p.xstages = xs;
     *smem = ws * p.wslot + xs * p.xslot + fixed;
     return true;
-}
-
-// Makes the context's device current for one call and puts the caller's
-// device back when the call returns.
-struct DeviceScope {
-    int prev = -1;
-    ~DeviceScope() {
-        if (prev >= 0) cudaSetDevice(prev);
-    }
-};
-
-ggq_status check_ctx(ggq_ctx* c, DeviceScope& scope) {
-    if (!c) return GGQ_ERR_INVALID_ARG;
-    int cur = -1;
-    cudaError_t e = cudaGetDevice(&cur);
-    if (e != cudaSuccess) return cuda_fail(c, e, "cudaGetDevice");
-    if (cur != c->device) {
-        e = cudaSetDevice(c->device);
-        if (e != cudaSuccess) return cuda_fail(c, e, "cudaSetDevice");
-        scope.prev = cur;
-    }
-    return GGQ_OK;
 }
 
 ggq_status gemv_checks(ggq_ctx* c, int w, const void* W, int64_t N, int64_t K, const void* X, int64_t T,
@@ -1051,6 +979,7 @@ int ggq_supported(int w, int act, int op) {
         if (f < 0) return 0;
         if (act == GGQ_TYPE_Q8_0) return f == F_Q4_0 || f == F_Q8_0;
         return f == F_Q4_0 ? act == GGQ_TYPE_Q8_1 : act == GGQ_TYPE_Q8_K;
+    case GGQ_OP_KV_CACHE: return (f == F_Q8_0 || f == F_Q4_0) && (act == GGQ_TYPE_Q8_0 || act == GGQ_TYPE_Q4_0);
     case GGQ_OP_MOE: return f >= 0 && f != F_Q4_0 && !low_bit_kquant(f) && act == GGQ_TYPE_Q8_K;
     default: return 0;
     }
@@ -1211,6 +1140,8 @@ ggq_status ggq_sync_status(ggq_ctx* c, void* stream) {
         return fail(c, GGQ_ERR_DEVICE, "device error word %d (%s)", word,
                     word == DEV_ERR_TIMEOUT   ? "a bounded wait ran out"
                     : word == DEV_ERR_BAD_IDS ? "a routed expert id out of range"
+                    : word == DEV_ERR_BAD_PLACE
+                        ? "a slot, page id, length or row range outside the key/value cache or its bounds"
                                               : "unknown device error");
     }
     return GGQ_OK;

@@ -1,0 +1,33 @@
+// ggq_attn.cuh -- parameters of the attention kernels over the packed cache.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ggq_kv.cuh"
+
+namespace ggq {
+
+struct AttnParams {
+    const void* q;
+    void* out;
+    int64_t q_token, q_head, out_token, out_head;  // strides in elements
+    const uint8_t* k;
+    const uint8_t* v;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* q_start;  // null: row b belongs to sequence b
+    const float* slopes;
+    int64_t table_stride;
+    int64_t n_pages;
+    int64_t n_tokens, n_seqs;
+    int dtype;               // 0 f32, 1 f16, 2 bf16
+    int H, Hkv, G, D, page;
+    int k_q4, v_q4;
+    int max_q, max_len, window;
+    float scale, cap;
+    int* err;
+};
+
+cudaError_t launch_attention(const AttnParams& p, cudaStream_t s);
+
+}  // namespace ggq

@@ -85,8 +85,13 @@ typedef enum ggq_op {
     GGQ_OP_QUANTIZE_ACT = 0, /* ggq_quantize_act                                  */
     GGQ_OP_DEQUANT = 1,      /* ggq_dequant                                        */
     GGQ_OP_MUL_MAT_VEC = 2,  /* ggq_mul_mat_vec / _q / _qa / ggq_block_dots (op 74) */
-    GGQ_OP_MOE = 3           /* ggq_moe_experts / _routed, as gate/up or down (op 75) */
+    GGQ_OP_MOE = 3,          /* ggq_moe_experts / _routed, as gate/up or down (op 75) */
+    GGQ_OP_KV_CACHE = 4      /* ggq_kv_store / ggq_kv_load / ggq_attention: w = K format, act = V format */
 } ggq_op;
+
+/* Element types of activations in ggq_kv_store, ggq_kv_load, ggq_attention and
+ * ggq_moe_route (the GGUF type ids of the unquantized types). */
+typedef enum ggq_dtype { GGQ_F32 = 0, GGQ_F16 = 1, GGQ_BF16 = 30 } ggq_dtype;
 
 typedef struct ggq_ctx ggq_ctx;
 
@@ -134,6 +139,66 @@ typedef struct ggq_moe_dump {
     int32_t* coefs_up;   /* [T*k][I][H/blk * c] up integer core            */
     int32_t* coefs_down; /* [T*k][H][I/blk * c] down integer core (h^)     */
 } ggq_moe_dump;
+
+/* A paged key/value cache in GGUF blocks.  A page holds page_size tokens of every
+ * kv head; token i of a sequence lives in the page that the sequence's table row
+ * names at i / page_size.  Values are those of Q8_0 (q * d) or Q4_0 ((q - 8) * d)
+ * blocks of 32 channels, one token's blocks independent of every other's; K and V
+ * may differ in format.  The bytes are laid out for the attention kernels:
+ *   pool: [n_pages][n_kv_heads][page_size / 16][blob], blob = 16 tokens of a head:
+ *   the quants (16 * D bytes Q8_0, stored + 128; 8 * D bytes Q4_0), then the fp16
+ *   scales [16][D / 32].  Quants are 32-bit words; word f of lane l is at byte
+ *   ((f / 4) * 32 + l) * 16 + (f % 4) * 4, and with token r = 8 o + g (K) or
+ *   r = 8 o + 2 t + e (V) of the blob and channel d it holds:
+ *     K Q8_0: l = 4 g + t, f = o D/16 + j, byte i:  d = 16 j + 4 t + i;
+ *     K Q4_0: l = 4 g + t, f = o D/32 + b, nibble 4 (i & 1) + 2 jj + (i >> 1):
+ *             d = 32 b + 16 jj + 4 t + i;
+ *     V Q8_0: l = 4 g + t, f = n, byte 2 o + e:  d = 8 n + g;
+ *     V Q4_0: l = 4 g + t, f = n / 2, nibble 4 e + 2 o + (n & 1):  d = 8 n + g.
+ * head_dim is 64, 128 or 256, page_size a multiple of 16, the pools are 16-byte
+ * aligned caller-owned device memory of n_pages * ggq_kv_page_bytes bytes. */
+typedef struct ggq_kv_cache {
+    int32_t k_type, v_type; /* GGQ_TYPE_Q8_0 or GGQ_TYPE_Q4_0 */
+    int32_t n_kv_heads, head_dim, page_size;
+    int64_t n_pages;
+    void* k;
+    void* v;
+} ggq_kv_cache;
+
+/* Arguments of ggq_attention (device pointers; strides in elements). */
+typedef struct ggq_attn {
+    int32_t dtype;          /* ggq_dtype of q and out                                   */
+    int32_t n_heads;        /* query heads, a multiple of the cache's n_kv_heads        */
+    int64_t n_tokens;       /* rows of q and out                                        */
+    int64_t n_seqs;
+    const void* q;          /* token t, head h: q + t * q_token + h * q_head, D dense   */
+    int64_t q_token, q_head;
+    void* out;
+    int64_t out_token, out_head;
+    const int32_t* table;   /* [n_seqs][table_stride] page ids                          */
+    int64_t table_stride;
+    const int32_t* lens;    /* [n_seqs] cached tokens, the new ones included            */
+    const int32_t* q_start; /* [n_seqs + 1] first row of each sequence; NULL: row b is sequence b's one new token */
+    int64_t max_q;          /* upper bound of a sequence's rows (ignored without q_start) */
+    int64_t max_len;        /* upper bound of lens (0: table_stride * page_size)        */
+    float scale;            /* of q . k                                                 */
+    float cap;              /* > 0: cap * tanh(score / cap)                             */
+    int64_t window;         /* > 0: a token sees the last `window` tokens, itself included */
+    const float* slopes;    /* [n_heads] or NULL: slope * (key position - own position) is added after the cap */
+} ggq_attn;
+
+/* How ggq_moe_route scores and chooses (see there). */
+typedef enum ggq_scoring { GGQ_SCORE_SOFTMAX = 0, GGQ_SCORE_SIGMOID = 1 } ggq_scoring;
+typedef struct ggq_router {
+    int32_t scoring;    /* ggq_scoring                                           */
+    int32_t n_groups;   /* groups of E / n_groups neighbouring experts; 1: none  */
+    int32_t top_groups; /* groups that stay open                                 */
+    int32_t group_best; /* a group's score: the sum of its best 1 or 2 choices   */
+    int32_t top_k;
+    int32_t normalize;  /* weights divided by their sum                          */
+    float scale;        /* then multiplied by this                               */
+    const float* bias;  /* [E] added to the score for the choice only, or NULL   */
+} ggq_router;
 
 /* Create a context on `device` (a CUDA ordinal).  Refuses any device that is
  * not compute capability 10.3 with GGQ_ERR_ARCH: the kernels are built for
@@ -342,6 +407,61 @@ ggq_status ggq_mul_mat_vec_noalloc(int w, const void* W, int64_t N, int64_t K, c
  * return GGQ_ERR_SHAPE while the telemetry is on.  pairs = calls = NULL turns
  * it off.  No allocation, no synchronisation: capture-safe like the calls. */
 ggq_status ggq_set_moe_counters(ggq_ctx* ctx, int64_t* pairs, int64_t n_experts, int64_t* calls);
+
+/* Bytes of one page in a pool of blocks `type` (0 for a type, head_dim or
+ * page_size that the cache does not take). */
+size_t ggq_kv_page_bytes(int type, int n_kv_heads, int head_dim, int page_size);
+
+/* Quantize T tokens' keys and values into the cache: k and v [T][n_kv_heads][D]
+ * of dtype, token and head strides in elements (multiples of 4, pointers aligned
+ * to 4 elements), go to the slots [T] (int64: page * page_size + place; a
+ * negative slot is skipped; two tokens with one slot leave it undefined).
+ *   Q8_0: d = amax/127 (fp32), q = round-half-away(x * (1/d)) clamped to +-127
+ *     (the arithmetic of ggq_quantize_act);
+ *   Q4_0: m = the first value of the largest magnitude, d = m / -8,
+ *     q = floor(x * (1/d) + 8.5) clamped to 0..15;
+ * d is stored as fp16.  A NaN counts as the smallest quant; a block whose scale
+ * leaves fp16's range reads back as infinities and NaNs.  A slot outside the
+ * cache is skipped and reported by ggq_sync_status.  Needs no scratch. */
+ggq_status ggq_kv_store(ggq_ctx* ctx, const ggq_kv_cache* cache, int dtype, const void* k, int64_t k_token,
+                        int64_t k_head, const void* v, int64_t v_token, int64_t v_head, const int64_t* slots, int64_t T,
+                        void* stream);
+
+/* Read the values of `T` slots back: the reverse of ggq_kv_store (fp32 product of
+ * quant and scale, rounded once to dtype).  A negative slot reads as zeros, one
+ * outside the cache too (and is reported). */
+ggq_status ggq_kv_load(ggq_ctx* ctx, const ggq_kv_cache* cache, int dtype, const int64_t* slots, int64_t T, void* k,
+                       int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head, void* stream);
+
+/* Attention of new tokens over a paged cache that already holds them
+ * (ggq_kv_store first).  Row i of sequence b (n_b rows, l_b = lens[b]) stands at
+ * position p = l_b - n_b + i and sees the keys j <= p (with a window: j > p -
+ * window).  For query head h (kv head h / (n_heads / n_kv_heads)):
+ *   s_j = scale * q . k_j;  cap > 0: s_j = cap * tanh(s_j / cap);
+ *   s_j += slope_h * (j - p);  out = sum_j softmax(s)_j v_j.
+ * Scores, statistics and sums are fp32.  A row that sees nothing (p < 0) is
+ * zeros; whatever unseen places hold never reaches an output.  Rows outside
+ * q_start's ranges are not written.  A page id outside the cache counts as page 0,
+ * lengths above max_len and ranges above max_q are cut; each is reported by
+ * ggq_sync_status.  Scratch: ggq_reserve_attention. */
+ggq_status ggq_attention(ggq_ctx* ctx, const ggq_kv_cache* cache, const ggq_attn* args, void* stream);
+
+/* Grow the scratch pool to fit every ggq_attention call (as ggq_reserve does). */
+ggq_status ggq_reserve_attention(ggq_ctx* ctx, void* stream);
+
+/* Route T tokens to experts: logits [T][E] of dtype, dense rows.
+ *   score = softmax(logits) over E, or sigmoid(logits); choice = score + bias;
+ *   n_groups > 1: only the top_groups groups with the largest sum of their
+ *     group_best largest choices stay open (ties to the lower group);
+ *   ids = the top_k open experts by choice, best first (ties to the lower id);
+ *   weights = their scores (without the bias), with `normalize` divided by their
+ *     sum (a sum of 0 leaves zeros), times scale.
+ * Softmax without bias compares the logits themselves.  A NaN logit is chosen
+ * last and weighs 0.  1 <= top_k <= 32, E <= 4096, n_groups <= 32 dividing E, top_k <=
+ * top_groups * E / n_groups.  ids and weights [T][top_k] are what
+ * ggq_moe_experts_routed takes.  Needs no scratch. */
+ggq_status ggq_moe_route(ggq_ctx* ctx, const ggq_router* router, int dtype, const void* logits, int64_t T, int64_t E,
+                         int32_t* ids, float* weights, void* stream);
 
 /* Synchronise `stream` and read the device error word: GGQ_OK, or
  * GGQ_ERR_DEVICE (a bounded wait inside a kernel ran out; the word is cleared),
