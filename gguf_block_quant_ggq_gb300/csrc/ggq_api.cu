@@ -954,20 +954,7 @@ ggq_status ggq_reserve(ggq_ctx* c, const ggq_plan* plan, void* stream) {
         }
         if (m > need) need = m;
     }
-    if (need <= c->pool_bytes) return GGQ_OK;
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs);
-    if (e != cudaSuccess) return cuda_fail(c, e, "reserve: cudaStreamIsCapturing");
-    if (cs != cudaStreamCaptureStatusNone)
-        return fail(c, GGQ_ERR_CAPTURE_ALLOC, "reserve: pool must grow to %zu bytes while the stream is capturing",
-                    need);
-    void* p = nullptr;
-    e = cudaMalloc(&p, need);
-    if (e != cudaSuccess) return cuda_fail(c, e, "reserve: cudaMalloc");
-    if (c->pool) c->retired.push_back(c->pool);  // work in flight may still use it
-    c->pool = static_cast<uint8_t*>(p);
-    c->pool_bytes = need;
-    return GGQ_OK;
+    return grow_pool(c, need, stream);
 }
 
 int ggq_supported(int w, int act, int op) {
@@ -1136,7 +1123,7 @@ ggq_status ggq_sync_status(ggq_ctx* c, void* stream) {
     e = cudaMemcpy(&word, &c->ctrl->err, sizeof(int), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(c, e, "sync_status: read");
     if (word != 0) {
-        cudaMemset(&c->ctrl->err, 0, sizeof(int));
+        cudaMemset(c->ctrl, 0, sizeof(Ctrl));  // the word, and what a kernel that gave up may have left
         return fail(c, GGQ_ERR_DEVICE, "device error word %d (%s)", word,
                     word == DEV_ERR_TIMEOUT   ? "a bounded wait ran out"
                     : word == DEV_ERR_BAD_IDS ? "a routed expert id out of range"

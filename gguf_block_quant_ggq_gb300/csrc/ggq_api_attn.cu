@@ -36,6 +36,9 @@ ggq_status cache_checks(ggq_ctx* c, const ggq_kv_cache* kv, const char* op) {
     return GGQ_OK;
 }
 
+// Partial results of items that two or more CTAs share, for the widest heads.
+size_t attn_scratch() { return align_up(2ull * kAttnMaxCtas * attn_part_floats(256) * sizeof(float)); }
+
 // Rows of four elements at a time: pointer and strides are multiples of 4.
 bool rows4(const void* p, int64_t token, int64_t head, int dtype) {
     return (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(4 * dtype_bytes(dtype))) == 0 && token % 4 == 0 &&
@@ -160,14 +163,19 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     p.scale = a->scale;
     p.cap = a->cap > 0.0f ? a->cap : 0.0f;
     p.err = &c->ctrl->err;
-    const cudaError_t e = launch_attention(p, static_cast<cudaStream_t>(stream));
+    s = need_scratch(c, attn_scratch());
+    if (s != GGQ_OK) return s;
+    p.min_share = 4;
+    p.parts = reinterpret_cast<float*>(c->pool);
+    p.pieces = c->ctrl->attn_pieces;
+    const cudaError_t e = launch_attention(p, c->nsm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GGQ_OK : cuda_fail(c, e, "attention launch");
 }
 
 ggq_status ggq_reserve_attention(ggq_ctx* c, void* stream) {
     DeviceScope scope;
-    (void)stream;
-    return check_ctx(c, scope);
+    ggq_status s = check_ctx(c, scope);
+    return s == GGQ_OK ? grow_pool(c, attn_scratch(), stream) : s;
 }
 
 ggq_status ggq_moe_route(ggq_ctx* c, const ggq_router* r, int dtype, const void* logits, int64_t T, int64_t E,

@@ -25,9 +25,20 @@ struct AttnParams {
     int k_q4, v_q4;
     int max_q, max_len, window;
     float scale, cap;
+    int min_share;           // 16-token groups below which a CTA's share is not cut
+    float* parts;            // partial results [2 * kAttnMaxCtas][attn_part_floats(D)]
+    int* pieces;             // pieces of an item that have arrived [kAttnMaxCtas], zero between calls
     int* err;
 };
 
-cudaError_t launch_attention(const AttnParams& p, cudaStream_t s);
+constexpr int kAttnMaxCtas = 1024;
+
+// A partial result: reference maxima [16], sums [16], values [16][D].
+__host__ __device__ constexpr int attn_part_floats(int D) { return 32 + 16 * D; }
+
+cudaError_t launch_attention(const AttnParams& p, int nsm, cudaStream_t s);
+cudaError_t launch_attn_stream_64(const AttnParams& p, int nsm, cudaStream_t s);
+cudaError_t launch_attn_stream_128(const AttnParams& p, int nsm, cudaStream_t s);
+cudaError_t launch_attn_stream_256(const AttnParams& p, int nsm, cudaStream_t s);
 
 }  // namespace ggq

@@ -20,6 +20,7 @@ inline size_t align_up(size_t v, size_t a = kAlign) { return (v + a - 1) / a * a
 struct Ctrl {
     int err;
     int pad[63];
+    int attn_pieces[1024];  // attention: arrived pieces of shared items, zero between calls
 };
 
 }  // namespace ggq
@@ -61,6 +62,24 @@ inline ggq_status need_scratch(ggq_ctx* c, size_t bytes) {
     if (bytes <= c->pool_bytes) return GGQ_OK;
     return fail(c, GGQ_ERR_CAPACITY, "call needs %zu scratch bytes but the pool holds %zu: call ggq_reserve first",
                 bytes, c->pool_bytes);
+}
+
+// The grow-only pool: a larger one replaces it, the old one lives until ggq_destroy.
+inline ggq_status grow_pool(ggq_ctx* c, size_t need, void* stream) {
+    if (need <= c->pool_bytes) return GGQ_OK;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs);
+    if (e != cudaSuccess) return cuda_fail(c, e, "reserve: cudaStreamIsCapturing");
+    if (cs != cudaStreamCaptureStatusNone)
+        return fail(c, GGQ_ERR_CAPTURE_ALLOC, "reserve: pool must grow to %zu bytes while the stream is capturing",
+                    need);
+    void* p = nullptr;
+    e = cudaMalloc(&p, need);
+    if (e != cudaSuccess) return cuda_fail(c, e, "reserve: cudaMalloc");
+    if (c->pool) c->retired.push_back(c->pool);  // work in flight may still use it
+    c->pool = static_cast<uint8_t*>(p);
+    c->pool_bytes = need;
+    return GGQ_OK;
 }
 
 // Makes the context's device current for one call and puts the caller's

@@ -1,6 +1,6 @@
 // ggq_kv.cu -- quantizing keys and values into the paged cache and reading them back.
 //
-// Mathematics: per token and 32 channels, Q8_0 d = amax / 127, q = round(x / d);
+// Mathematics: per token and 32 channels, Q8_0 d = amax * (1/127), q = round(x / d);
 // Q4_0 d = m / -8 with m the first value of the largest magnitude, q = floor(x /
 // d + 8.5) in 0..15.  Bound by memory: each value is read once and stands in the
 // cache for 17/16 (Q8_0) or 9/16 (Q4_0) bytes.
@@ -52,10 +52,16 @@ __device__ __forceinline__ uint32_t q4_one(float x, float id) {
 }
 __device__ __forceinline__ uint32_t q8_one(float x, float id) { return static_cast<uint32_t>(quant_one(x, id) + 128); }
 
+__device__ __forceinline__ float q8_scale(float amax, float* id) {
+    const float d = __fmul_rn(amax, 1.0f / 127.0f);
+    *id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+    return d;
+}
+
 // A block's scale from its reduced extreme (Q8_0: the magnitude) and its inverse.
 template <bool Q4>
 __device__ __forceinline__ float block_scale(const Extreme& m, float* id) {
-    return Q4 ? q4_scale(m.v, id) : quant_scale(m.v, id);
+    return Q4 ? q4_scale(m.v, id) : q8_scale(m.v, id);
 }
 template <bool Q4>
 __device__ __forceinline__ void extreme_of(Extreme& m, float x, int at) {
@@ -123,7 +129,7 @@ __device__ __forceinline__ void store_group_k(const T* src, int64_t st, uint8_t*
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 float id;
-                const float d = quant_scale(m, &id);
+                const float d = q8_scale(m, &id);
 #pragma unroll
                 for (int i = 2 * b; i < 2 * b + 2; ++i)
                     w[i] = q8_one(x[i].x, id) | q8_one(x[i].y, id) << 8 | q8_one(x[i].z, id) << 16 | q8_one(x[i].w, id) << 24;

@@ -416,8 +416,8 @@ size_t ggq_kv_page_bytes(int type, int n_kv_heads, int head_dim, int page_size);
  * of dtype, token and head strides in elements (multiples of 4, pointers aligned
  * to 4 elements), go to the slots [T] (int64: page * page_size + place; a
  * negative slot is skipped; two tokens with one slot leave it undefined).
- *   Q8_0: d = amax/127 (fp32), q = round-half-away(x * (1/d)) clamped to +-127
- *     (the arithmetic of ggq_quantize_act);
+ *   Q8_0: d = amax * (1/127) (an fp32 product with the rounded reciprocal), q =
+ *     round-half-away(x * (1/d)) clamped to +-127;
  *   Q4_0: m = the first value of the largest magnitude, d = m / -8,
  *     q = floor(x * (1/d) + 8.5) clamped to 0..15;
  * d is stored as fp16.  A NaN counts as the smallest quant; a block whose scale

@@ -54,7 +54,7 @@ def quantize(x, fmt):
     b = x.astype(np.float32).reshape(*x.shape[:-1], -1, 32)
     with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
         if fmt == "Q8_0":
-            d = (np.abs(b).max(-1, keepdims=True) / np.float32(127)).astype(np.float32)
+            d = (np.abs(b).max(-1, keepdims=True) * (np.float32(1) / np.float32(127))).astype(np.float32)
             inv = np.where(d != 0, np.float32(1) / d, np.float32(0)).astype(np.float32)
             r = (b * inv).astype(np.float32)
             q = np.clip(np.sign(r) * np.floor(np.abs(r.astype(np.float64)) + 0.5), -127, 127) + 128
