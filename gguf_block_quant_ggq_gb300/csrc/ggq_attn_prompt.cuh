@@ -16,7 +16,7 @@
 //   * warps 8-11: the packed blobs, read straight from the cache, to fp16 (V with
 //     bf16 activations: bf16) tiles in the K-major 128-byte-swizzled layout, two
 //     buffers each for K and V;
-//   * warps 12, 13: one thread each issues a tile's MMAs: S of step j when its K
+//   * warps 12, 13 (14, 15 idle): one thread each issues a tile's MMAs: S of step j when its K
 //     tile is there, then O += P V when the softmax has written P.  The two tiles'
 //     products and softmaxes take turns.
 // The running maximum is raised (and O rescaled in tensor memory) only when a row
@@ -33,7 +33,10 @@
 
 namespace ggq {
 
-constexpr int kPromptThreads = 14 * 32;
+constexpr int kPromptThreads = 16 * 32;
+// registers a thread of the softmax, decoding and MMA warps (512 threads launch with 128 each)
+constexpr int kSoftmaxRegs = 168, kDecodeRegs = 128, kMmaRegs = 48;
+static_assert(256 * kSoftmaxRegs + 128 * kDecodeRegs + 128 * kMmaRegs <= kPromptThreads * 128, "register split");
 
 template <int D>
 struct PromptShape {
@@ -59,12 +62,66 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+// 32 columns, to be used after prompt_wait_ld on the same registers
+__device__ __forceinline__ void prompt_ld32(uint32_t taddr, float* v) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void prompt_ld16(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void prompt_st16(uint32_t taddr, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void prompt_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// keeps uses of v behind the wait
+__device__ __forceinline__ void prompt_tie32(float* v) {
+    asm volatile(""
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                   "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                   "+f"(v[30]), "+f"(v[31]));
+}
+__device__ __forceinline__ void prompt_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+// packed fp32: (a0, a1) * b + (c0, c1), (a0, a1) + (b0, b1), (a0, a1) * (b0, b1)
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -93,17 +150,6 @@ __device__ __forceinline__ uint32_t prompt_fma2(uint32_t a, uint32_t b, uint32_t
                               *reinterpret_cast<const __half2*>(&c));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-// A pair of exact fp16 integers times a pair of fp16 scales, in the operand's type
-// (bf16: one rounding of the fp32 product).
-template <bool BF>
-__device__ __forceinline__ uint32_t prompt_scaled(uint32_t q, uint32_t d) {
-    if constexpr (BF) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&q));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&d));
-        return prompt_pack<true>(a.x * b.x, a.y * b.y);
-    }
-    return prompt_mul2(q, d);
-}
 // Quants of a word as pairs of exact fp16 integers: bytes (0, 1) and (2, 3); nibbles
 // (0, 4), (1, 5), (2, 6), (3, 7).
 __device__ __forceinline__ void prompt_ints8(uint32_t w, uint32_t (&h)[2]) {
@@ -116,6 +162,44 @@ __device__ __forceinline__ void prompt_ints4(uint32_t w, uint32_t (&h)[4]) {
     h[1] = prompt_fma2((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);             // (1024 + 16 q) / 16 - 72
     h[2] = prompt_sub2((y & 0x000F000Fu) | 0x64006400u, 0x64086408u);
     h[3] = prompt_fma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+}
+
+// The two key pairs of a V word (bytes 0, 1 and 2, 3) times the keys' scales, in
+// the operand's type (bf16: one rounding of the fp32 product, whose integer comes
+// out of 2^23 + u).
+template <bool BF>
+__device__ __forceinline__ void prompt_v8(uint32_t w, const float (&df)[4], uint32_t d01, uint32_t d23, uint32_t (&o)[2]) {
+    if constexpr (BF) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(prmt(w, 0x4B000000u, 0x7440u + i));
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            add2(x[i], x[i + 1], x[i], x[i + 1], -8388736.0f, -8388736.0f);
+            mul2(x[i], x[i + 1], x[i], x[i + 1], df[i], df[i + 1]);
+            o[i >> 1] = prompt_pack<true>(x[i], x[i + 1]);
+        }
+    } else {
+        uint32_t h[2];
+        prompt_ints8(w, h);
+        o[0] = prompt_mul2(h[0], d01), o[1] = prompt_mul2(h[1], d23);
+    }
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t prompt_v4(uint32_t h, float d0, float d1, uint32_t d2) {
+    if constexpr (BF) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        float x, y;
+        mul2(x, y, a.x, a.y, d0, d1);
+        return prompt_pack<true>(x, y);
+    }
+    return prompt_mul2(h, d2);
+}
+
+template <bool REGS_UP, int N>
+__device__ __forceinline__ void prompt_regs() {
+    if (REGS_UP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <bool K4, bool V4, int D, bool BF>
@@ -192,15 +276,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         }
         const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
         const int sh = ex == 128 ? 0 : min(13 - ex, 100);
-        const float up = __uint_as_float(static_cast<uint32_t>(sh + 127) << 23);
-        rscale = p.scale * scalbnf(1.0f, -sh);
+        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(sh + 127) << 23), p.scale);
+        rscale = fabsf(p.scale) * scalbnf(1.0f, -sh);  // not negative: the largest product is the largest logit
         uint8_t* const row = smem + (tid >> 7) * SH::kQ + (tid & 127) * 128;
 #pragma unroll 4
-        for (int d = 0; d < D; d += 8) {
-            const float4 x = q4(d), y = q4(d + 4);
+        for (int c = 0; c < D / 8; ++c) {  // the K tile's channel order: 16 t + 4 j + i holds 16 j + 4 t + i of 64
+            const int d = 64 * (c >> 3) + 32 * (c & 1) + 4 * ((c & 7) >> 1);
+            const float4 x = q4(d), y = q4(d + 16);
             const uint4 u = make_uint4(prompt_pack<false>(x.x * up, x.y * up), prompt_pack<false>(x.z * up, x.w * up),
                                        prompt_pack<false>(y.x * up, y.y * up), prompt_pack<false>(y.z * up, y.w * up));
-            *reinterpret_cast<uint4*>(row + (d >> 6) * (128 * 128) + ((((d & 63) >> 3) ^ (tid & 7)) << 4)) = u;
+            *reinterpret_cast<uint4*>(row + (c >> 3) * (128 * 128) + (((c & 7) ^ (tid & 7)) << 4)) = u;
         }
         fence_proxy_async_smem();
     }
@@ -229,6 +314,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
 
     if (warp >= 12) {
         // ================================================================ MMA: one thread a tile
+        prompt_regs<false, kMmaRegs>();
         const int t = warp - 12;
         if (t < ntiles && lane == 0 && steps > 0) {
             const uint32_t id_s = prompt_idesc(KT, false), id_o = prompt_idesc(D, BF);
@@ -261,166 +347,190 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         }
     } else if (warp >= 8) {
         // ================================================================ packed blobs -> operand tiles
+        prompt_regs<false, kDecodeRegs>();
         const int cw = warp - 8, g8 = lane >> 2, t4 = lane & 3, gpp = p.page >> 4;
         constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
-        constexpr int kPer = KG / 4;  // groups of a step and warp: cw, cw + 4
-        constexpr int KL = K4 ? D / 64 : D / 32, VL = V4 ? D / 64 : D / 32;  // 16-byte words of a lane and blob
-        const auto page_at = [&](int s) {  // page of this warp's s-th group; 32 at a time, one a lane
-            const int g = glo + (s / kPer) * KG + cw + 4 * (s % kPer);
-            int pg = -1;
-            if (g < ghi) {
-                pg = p.table[b * p.table_stride + g / gpp];
+        constexpr int kPer = KG / 4;                              // groups of a step and warp (keys): 2 or 1
+        constexpr int KL = K4 ? D / 64 : D / 32;                  // 16-byte words of a lane and blob
+        constexpr int VP = KG / 2, VH = 4 / VP;                   // values: pairs of groups, parts of a pair's lines
+        constexpr int VL = (V4 ? D / 64 : D / 32) / VH;
+        const int pair = cw % VP, v_line = (cw / VP) * VL;
+        // blobs of the step's groups, one a lane
+        const auto locate = [&](int j) {
+            const int g = glo + j * KG + (lane & (KG - 1));
+            int64_t at = -1;
+            if (j < steps && g < ghi) {
+                int pg = p.table[b * p.table_stride + g / gpp];
                 if (pg < 0 || pg >= p.n_pages) {
                     set_error(p.err, DEV_ERR_BAD_PLACE);
                     pg = 0;
                 }
+                at = (static_cast<int64_t>(pg) * p.Hkv + hk) * gpp + g % gpp;
             }
-            return pg;
+            return at;
         };
-        const int total = steps * kPer;
-        int pages = page_at(lane);
-        uint4 kq[KL], vq[VL];
-        uint32_t ks[2][NB / 2], vsc[4][NB / 2];
-        int64_t blob = -1;
-        const auto locate = [&](int s) {
-            if ((s & 31) == 0 && s > 0) pages = page_at(s + lane);
-            const int pg = __shfl_sync(0xffffffffu, pages, s & 31);
-            const int g = glo + (s / kPer) * KG + cw + 4 * (s % kPer);
-            return pg < 0 ? int64_t(-1) : (static_cast<int64_t>(pg) * p.Hkv + hk) * gpp + g % gpp;
+        uint4 kq[kPer][KL], vq[2][VL];
+        uint32_t ks[kPer][2][NB / 2], vsc[2][4][NB / 2];
+        const auto load_k = [&](int64_t blobs) {
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+                const int64_t at = __shfl_sync(0xffffffffu, blobs, cw * kPer + c);
+                if (at < 0) continue;  // past the last key: the tile keeps what it held, every row masks it
+                const uint8_t* const src = p.k + at * kKB;
+#pragma unroll
+                for (int i = 0; i < KL; ++i) kq[c][i] = __ldg(reinterpret_cast<const uint4*>(src + (i * 32 + lane) * 16));
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i)
+                        ks[c][o][i] = __ldg(reinterpret_cast<const uint32_t*>(src + kv_quant_bytes(K4, D) + (8 * o + g8) * NB * 2) + i);
+            }
         };
-        const auto load_k = [&](int64_t at) {
-            if (at < 0) return;
-            const uint8_t* const src = p.k + at * kKB;
+        const auto load_v = [&](int64_t blobs) {
 #pragma unroll
-            for (int i = 0; i < KL; ++i) kq[i] = __ldg(reinterpret_cast<const uint4*>(src + (i * 32 + lane) * 16));
+            for (int c = 0; c < 2; ++c) {
+                const int64_t at = __shfl_sync(0xffffffffu, blobs, 2 * pair + c);
+                if (at < 0) {
 #pragma unroll
-            for (int o = 0; o < 2; ++o)
+                    for (int i = 0; i < VL; ++i) vq[c][i] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int i = 0; i < NB / 2; ++i)
-                    ks[o][i] = __ldg(reinterpret_cast<const uint32_t*>(src + kv_quant_bytes(K4, D) + (8 * o + g8) * NB * 2) + i);
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int i = 0; i < NB / 2; ++i) vsc[c][r][i] = 0u;
+                    continue;
+                }
+                const uint8_t* const src = p.v + at * kVB;
+#pragma unroll
+                for (int i = 0; i < VL; ++i) vq[c][i] = __ldg(reinterpret_cast<const uint4*>(src + ((v_line + i) * 32 + lane) * 16));
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i)
+                        vsc[c][r][i] = __ldg(reinterpret_cast<const uint32_t*>(src + kv_quant_bytes(V4, D) +
+                                                                               (8 * (r >> 1) + 2 * t4 + (r & 1)) * NB * 2) + i);
+            }
         };
-        const auto load_v = [&](int64_t at) {
-            if (at < 0) return;
-            const uint8_t* const src = p.v + at * kVB;
-#pragma unroll
-            for (int i = 0; i < VL; ++i) vq[i] = __ldg(reinterpret_cast<const uint4*>(src + (i * 32 + lane) * 16));
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int i = 0; i < NB / 2; ++i)
-                    vsc[r][i] = __ldg(reinterpret_cast<const uint32_t*>(src + kv_quant_bytes(V4, D) +
-                                                                        (8 * (r >> 1) + 2 * t4 + (r & 1)) * NB * 2) + i);
-        };
-        if (total > 0) {
-            blob = locate(0);
-            load_k(blob);
-            load_v(blob);
+        int64_t blobs = locate(0), next = locate(1);
+        if (steps > 0) {
+            load_k(blobs);
+            load_v(blobs);
         }
-        bool ok = true;
-        for (int s = 0; s < total && ok; ++s) {
-            const int j = s / kPer, buf = j & 1, gi = cw + 4 * (s % kPer), g = glo + j * KG + gi;
-            const int64_t now = blob;
-            blob = s + 1 < total ? locate(s + 1) : -1;
-            // keys
-            if (s % kPer == 0 && j >= 2) ok = wait(kempty + buf, ((j >> 1) - 1) & 1);
-            if (!ok) break;
-            if (now >= 0) {
-                uint8_t* const kt = smem + SH::oK + buf * SH::kK + (gi * 16 + g8) * 128 + 8 * (t4 & 1);
+        for (int j = 0; j < steps; ++j) {
+            const int buf = j & 1;
+            blobs = next;
+            next = locate(j + 2);
+            // ---- keys: lane (g, t) writes 16 channels of a 64-channel atom as two chunks of its token's row
+            if (j >= 2 && !wait(kempty + buf, ((j >> 1) - 1) & 1)) break;
+            uint8_t* const kt = smem + SH::oK + buf * SH::kK + (cw * kPer * 16 + g8) * 128;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c)
 #pragma unroll
                 for (int i = 0; i < KL; ++i) {
-                    const uint32_t w[4] = {kq[i].x, kq[i].y, kq[i].z, kq[i].w};
+                    const uint32_t w[4] = {kq[c][i].x, kq[c][i].y, kq[c][i].z, kq[c][i].w};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int f = 4 * i + c, per = K4 ? NB : D / 16, o = f / per, jj = f % per;
-                        const int blk = K4 ? jj : jj >> 1;
-                        const uint32_t d2 = prmt(ks[o][blk >> 1], 0u, (blk & 1) ? 0x3232u : 0x1010u);
-                        uint8_t* const row = kt + o * (8 * 128);
+                    for (int q = 0; q < 4; q += K4 ? 1 : 2) {  // a chunk: one word of 8 nibbles or two of 4 bytes
+                        const int f = 4 * i + q, per = K4 ? NB : D / 16, o = f / per, jj = f % per;
+                        const int blk = K4 ? jj : jj >> 1, chunk = 2 * t4 + (blk & 1);
+                        const uint32_t d2 = prmt(ks[c][o][blk >> 1], 0u, (blk & 1) ? 0x3232u : 0x1010u);
+                        uint32_t h[4];
                         if constexpr (K4) {
-                            uint32_t h[4];
-                            prompt_ints4(w[c], h);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int ks16 = 2 * jj + k;  // 16-channel step
-                                *reinterpret_cast<uint2*>(row + (ks16 >> 2) * (KT * 128) + (((2 * (ks16 & 3) + (t4 >> 1)) ^ g8) << 4)) =
-                                    make_uint2(prompt_mul2(h[2 * k], d2), prompt_mul2(h[2 * k + 1], d2));
-                            }
+                            prompt_ints4(w[q], h);
                         } else {
-                            uint32_t h[2];
-                            prompt_ints8(w[c], h);
-                            *reinterpret_cast<uint2*>(row + (jj >> 2) * (KT * 128) + (((2 * (jj & 3) + (t4 >> 1)) ^ g8) << 4)) =
-                                make_uint2(prompt_mul2(h[0], d2), prompt_mul2(h[1], d2));
+                            uint32_t a[2], e[2];
+                            prompt_ints8(w[q], a);
+                            prompt_ints8(w[q + 1 < 4 ? q + 1 : 3], e);
+                            h[0] = a[0], h[1] = a[1], h[2] = e[0], h[3] = e[1];
+                        }
+                        *reinterpret_cast<uint4*>(kt + (16 * c + 8 * o) * 128 + (blk >> 1) * (KT * 128) + ((chunk ^ g8) << 4)) =
+                            make_uint4(prompt_mul2(h[0], d2), prompt_mul2(h[1], d2), prompt_mul2(h[2], d2), prompt_mul2(h[3], d2));
+                    }
+                }
+            load_k(blobs);
+            fence_proxy_async_smem();
+            mbar_arrive(kfull + buf);
+            // ---- values: whatever lies past the sequence's end counts as 0
+            if (j >= 2 && !wait(vempty + buf, ((j >> 1) - 1) & 1)) break;
+            const int key0 = 16 * (glo + j * KG + 2 * pair);
+            uint32_t odd = 0u;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i) {
+                        if (key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1) >= len) vsc[c][r][i] = 0u;
+                        odd = __vmaxu2(odd, vsc[c][r][i] & 0x7C007C00u);
+                    }
+            if ((odd & 0xFFFFu) == 0x7C00u || (odd >> 16) == 0x7C00u) {
+                // scales that are not finite: 0 here, and the rows that see them are told
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int i = 0; i < NB / 2; ++i) {
+                            const uint32_t u = vsc[c][r][i];
+                            const int key = key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1);
+                            const bool lo = (u & 0x7C00u) == 0x7C00u, hi = (u & 0x7C000000u) == 0x7C000000u;
+                            if (lo) atomicMin(s_bad + 4 * i, key), atomicMax(s_bad + 4 * i + 1, key);
+                            if (hi) atomicMin(s_bad + 4 * i + 2, key), atomicMax(s_bad + 4 * i + 3, key);
+                            vsc[c][r][i] = (lo ? 0u : u & 0xFFFFu) | (hi ? 0u : u & 0xFFFF0000u);
+                        }
+            }
+            // lane (g, t) writes 8 keys of both groups as one chunk of channel 8 n + g
+            uint8_t* const vt = smem + SH::oV + buf * SH::kV + (pair >> 1) * (D * 128) + g8 * 128 +
+                                (((2 * t4 + (pair & 1)) ^ g8) << 4);
+#pragma unroll
+            for (int i = 0; i < VL; ++i) {
+#pragma unroll
+                for (int half = 0; half < (V4 ? 2 : 1); ++half) {  // a line: one block of 32 channels, or two
+                    float df[2][4];
+                    uint32_t d2[2][2];
+                    const auto scales = [&](int lo_blk) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                d2[c][k] = prmt(vsc[c][2 * k][lo_blk >> 1], vsc[c][2 * k + 1][lo_blk >> 1], (lo_blk & 1) ? 0x7632u : 0x5410u);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) df[c][k] = (k & 1) ? half_hi(d2[c][k >> 1]) : half_lo(d2[c][k >> 1]);
+                        }
+                    };
+                    if (VH == 1 || v_line == 0) scales(V4 ? 2 * i + half : i);
+                    else scales(V4 ? 2 * (VL + i) + half : VL + i);
+                    if constexpr (V4) {
+#pragma unroll
+                        for (int q = 2 * half; q < 2 * half + 2; ++q) {
+                            uint32_t h[2][4];
+                            prompt_ints4(q == 0 ? vq[0][i].x : q == 1 ? vq[0][i].y : q == 2 ? vq[0][i].z : vq[0][i].w, h[0]);
+                            prompt_ints4(q == 0 ? vq[1][i].x : q == 1 ? vq[1][i].y : q == 2 ? vq[1][i].z : vq[1][i].w, h[1]);
+                            uint8_t* const row = vt + 2 * (4 * (v_line + i) + q) * (8 * 128);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)  // even and odd eights of channels
+                                *reinterpret_cast<uint4*>(row + k * (8 * 128)) =
+                                    make_uint4(prompt_v4<BF>(h[0][k], df[0][0], df[0][1], d2[0][0]),
+                                               prompt_v4<BF>(h[0][2 + k], df[0][2], df[0][3], d2[0][1]),
+                                               prompt_v4<BF>(h[1][k], df[1][0], df[1][1], d2[1][0]),
+                                               prompt_v4<BF>(h[1][2 + k], df[1][2], df[1][3], d2[1][1]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t x[2], y[2];
+                            prompt_v8<BF>(q == 0 ? vq[0][i].x : q == 1 ? vq[0][i].y : q == 2 ? vq[0][i].z : vq[0][i].w, df[0], d2[0][0], d2[0][1], x);
+                            prompt_v8<BF>(q == 0 ? vq[1][i].x : q == 1 ? vq[1][i].y : q == 2 ? vq[1][i].z : vq[1][i].w, df[1], d2[1][0], d2[1][1], y);
+                            *reinterpret_cast<uint4*>(vt + (4 * (v_line + i) + q) * (8 * 128)) = make_uint4(x[0], x[1], y[0], y[1]);
                         }
                     }
                 }
             }
-            load_k(blob);
-            if (s % kPer == kPer - 1) {
-                fence_proxy_async_smem();
-                mbar_arrive(kfull + buf);
-            }
-            // values: whatever lies past the sequence's end counts as 0
-            if (s % kPer == 0 && j >= 2) ok = wait(vempty + buf, ((j >> 1) - 1) & 1);
-            if (!ok) break;
-            if (now < 0) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i) vsc[r][i] = 0u;
-#pragma unroll
-                for (int i = 0; i < VL; ++i) vq[i] = make_uint4(0u, 0u, 0u, 0u);
-            } else if (16 * g + 16 > len) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (16 * g + 8 * (r >> 1) + 2 * t4 + (r & 1) >= len)
-#pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) vsc[r][i] = 0u;
-            }
-            // scales that are not finite: 0 here, and the rows that see them are told
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int i = 0; i < NB / 2; ++i) {
-                    const uint32_t u = vsc[r][i];
-                    if ((u & 0x7C00u) == 0x7C00u || (u & 0x7C000000u) == 0x7C000000u) {
-                        const int key = 16 * g + 8 * (r >> 1) + 2 * t4 + (r & 1);
-                        if ((u & 0x7C00u) == 0x7C00u) atomicMin(s_bad + 4 * i, key), atomicMax(s_bad + 4 * i + 1, key);
-                        if ((u & 0x7C000000u) == 0x7C000000u) atomicMin(s_bad + 4 * i + 2, key), atomicMax(s_bad + 4 * i + 3, key);
-                        vsc[r][i] = ((u & 0x7C00u) == 0x7C00u ? 0u : u & 0xFFFFu) |
-                                    ((u & 0x7C000000u) == 0x7C000000u ? 0u : u & 0xFFFF0000u);
-                    }
-                }
-            uint8_t* const vt = smem + SH::oV + buf * SH::kV + (gi >> 2) * (D * 128) + g8 * 128 +
-                                (((2 * (gi & 3) + (t4 >> 1)) ^ g8) << 4) + 8 * (t4 & 1);
-#pragma unroll
-            for (int i = 0; i < VL; ++i) {
-                const uint32_t w[4] = {vq[i].x, vq[i].y, vq[i].z, vq[i].w};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int blk = V4 ? (4 * i + c) >> 1 : i;
-                    // scales of the key pairs (2t, 2t+1) and (8+2t, 9+2t) in this block
-                    const uint32_t sel = (blk & 1) ? 0x7632u : 0x5410u;
-                    const uint32_t d0 = prmt(vsc[0][blk >> 1], vsc[1][blk >> 1], sel);
-                    const uint32_t d1 = prmt(vsc[2][blk >> 1], vsc[3][blk >> 1], sel);
-                    if constexpr (V4) {
-                        uint32_t h[4];
-                        prompt_ints4(w[c], h);
-                        const int n0 = 2 * (4 * i + c);
-                        *reinterpret_cast<uint2*>(vt + n0 * (8 * 128)) = make_uint2(prompt_scaled<BF>(h[0], d0), prompt_scaled<BF>(h[2], d1));
-                        *reinterpret_cast<uint2*>(vt + (n0 + 1) * (8 * 128)) = make_uint2(prompt_scaled<BF>(h[1], d0), prompt_scaled<BF>(h[3], d1));
-                    } else {
-                        uint32_t h[2];
-                        prompt_ints8(w[c], h);
-                        *reinterpret_cast<uint2*>(vt + (4 * i + c) * (8 * 128)) = make_uint2(prompt_scaled<BF>(h[0], d0), prompt_scaled<BF>(h[1], d1));
-                    }
-                }
-            }
-            load_v(blob);
-            if (s % kPer == kPer - 1) {
-                fence_proxy_async_smem();
-                mbar_arrive(vfull + buf);
-            }
+            load_v(blobs);
+            fence_proxy_async_smem();
+            mbar_arrive(vfull + buf);
         }
-    } else if ((warp >> 2) < ntiles) {
+    } else {
+        prompt_regs<true, kSoftmaxRegs>();
+        if ((warp >> 2) < ntiles) {
         // ================================================================ softmax: one thread a row
         const int t = warp >> 2, r = min(r_begin + tid, r_end - 1);
         const bool there = r_begin + tid < r_end;
@@ -429,7 +539,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         const int i_row = r / p.G, h = hk * p.G + r - i_row * p.G, pos = from + i_row;
         const int first_key = p.window > 0 ? pos - p.window + 1 : 0;
         const float slope = p.slopes ? p.slopes[h] : 0.0f;
-        const bool plain = p.cap <= 0.0f && !p.slopes;
+        const bool plain = p.cap <= 0.0f && !p.slopes && rscale > 0.0f;
         constexpr float kLog2e = 1.44269504088896340736f;
         const float sx = plain ? rscale * kLog2e : rscale;
         const float inv_cap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
@@ -442,40 +552,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             tc_fence_after();
             const int key0 = 16 * glo + j * KT;
             const bool whole = key0 + KT - 1 <= t_first && key0 >= seen_from;
-            // logits of 32 keys in units of log2
-            const auto logits = [&](int c, float (&x)[32]) {
-                tmem_ld32(cs + 32 * c, x);
-                if (plain) {
+            float x[KT];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) x[k] *= sx;
-                } else {
+            for (int c = 0; c < KT / 32; ++c) prompt_ld32(cs + 32 * c, x + 32 * c);
+            prompt_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        float y = x[k] * sx;
-                        // tanh(z) = 1 - 2 / (1 + exp(2 z))
-                        if (p.cap > 0.0f) {
-                            const float z = y * inv_cap;
-                            y = p.cap - __fdividef(2.0f * p.cap, 1.0f + prompt_ex2(z > 120.0f ? 120.0f : z));
-                        }
-                        x[k] = fmaf(slope, static_cast<float>(key0 + 32 * c + k - pos), y) * kLog2e;
+            for (int c = 0; c < KT / 32; ++c) prompt_tie32(x + 32 * c);
+            // logits in units of log2 (plain: still to be multiplied by sx)
+            if (!plain) {
+#pragma unroll
+                for (int k = 0; k < KT; ++k) {
+                    float y = x[k] * sx;
+                    // tanh(z) = 1 - 2 / (1 + exp(2 z))
+                    if (p.cap > 0.0f) {
+                        const float z = y * inv_cap;
+                        y = p.cap - __fdividef(2.0f * p.cap, 1.0f + prompt_ex2(z > 120.0f ? 120.0f : z));
                     }
+                    x[k] = fmaf(slope, static_cast<float>(key0 + k - pos), y) * kLog2e;
                 }
-                if (!whole) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int key = key0 + 32 * c + k;
-                        if (key > pos || key < first_key) x[k] = -INFINITY;
-                    }
-                }
-            };
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < KT / 32; ++c) {
-                float x[32];
-                logits(c, x);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) top = fmaxf(top, x[k]);
             }
+            if (!whole) {
+#pragma unroll
+                for (int k = 0; k < KT; ++k)
+                    if (key0 + k > pos || key0 + k < first_key) x[k] = -INFINITY;
+            }
+            float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < KT; ++k) tops[k & 3] = fmaxf(tops[k & 3], x[k]);
+            const float mul = plain ? sx : 1.0f;
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;
             const bool raise = top > m + 8.0f;
             if (__any_sync(0xffffffffu, raise)) {
                 const float mn = raise ? top : m, a = prompt_ex2(m - mn);
@@ -485,37 +590,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                     if (!wait(ofull + t, (j - 1) & 1)) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tmem_ld32(co + 32 * c, o);
+                    for (int c = 0; c < D / 16; ++c) {
+                        float o[16];
+                        prompt_ld16(co + 16 * c, o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= a;
-                        tmem_st32(co + 32 * c, o);
+                        for (int k = 0; k < 16; ++k) o[k] *= a;
+                        prompt_st16(co + 16 * c, o);
                     }
                 }
             }
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < KT / 32; ++c) {
-                float x[32];
-                logits(c, x);
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int at = 0; at < KT / 64; ++at) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    x[k] = prompt_ex2(x[k] - m);
-                    sum[k & 3] += x[k];
+                for (int k = 64 * at; k < 64 * at + 64; k += 2) {
+                    ffma2(x[k], x[k + 1], x[k], x[k + 1], mul, -m, -m);
+                    x[k] = prompt_ex2(x[k]);
+                    x[k + 1] = prompt_ex2(x[k + 1]);
+                    add2(sum[k & 2], sum[(k & 2) + 1], sum[k & 2], sum[(k & 2) + 1], x[k], x[k + 1]);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                // the V tile's key order: 2t, 2t + 1, 8 + 2t, 9 + 2t inside a group of 16
-                uint32_t w[16];
+                // the V tile's key order in an atom of 64: word 8 t + 2 g holds keys 2 t, 2 t + 1 of group g,
+                // the next one keys 8 + 2 t, 9 + 2 t
+                uint32_t w[32];
 #pragma unroll
-                for (int gq = 0; gq < 2; ++gq)
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        w[8 * gq + 2 * q] = prompt_pack<BF>(x[16 * gq + 2 * q], x[16 * gq + 2 * q + 1]);
-                        w[8 * gq + 2 * q + 1] = prompt_pack<BF>(x[16 * gq + 8 + 2 * q], x[16 * gq + 9 + 2 * q]);
+                    for (int gq = 0; gq < 4; ++gq) {
+                        const int k = 64 * at + 16 * gq + 2 * q;
+                        w[8 * q + 2 * gq] = prompt_pack<BF>(x[k], x[k + 1]);
+                        w[8 * q + 2 * gq + 1] = prompt_pack<BF>(x[k + 8], x[k + 9]);
                     }
-                tmem_st16(cs + 16 * c, w);
+                prompt_st32(cs + 32 * at, w);
             }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(pfull + t);
@@ -526,25 +633,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         const int64_t at = (first + i_row) * p.out_token + h * p.out_head;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            if (steps > 0) tmem_ld32(co + 32 * c, o);
+        for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            if (steps > 0) prompt_ld16(co + 16 * c, o);
             // an infinite or NaN value among those that the row sees
-            const bool spoilt = s_bad[2 * c] <= pos && s_bad[2 * c + 1] >= first_key && s_bad[2 * c + 1] >= 0;
+            const int* const sb = s_bad + 2 * (c >> 1);
+            const bool spoilt = sb[0] <= pos && sb[1] >= first_key && sb[1] >= 0;
             if (there) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
+                for (int k = 0; k < 16; k += 8) {
                     uint32_t w[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const float a = steps > 0 && l != 0.0f ? o[k + 2 * q] * inv : 0.0f, b2 = steps > 0 && l != 0.0f ? o[k + 2 * q + 1] * inv : 0.0f;
                         w[q] = prompt_pack<BF>(spoilt ? NAN : a, spoilt ? NAN : b2);
                     }
-                    uint2* const dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at + 32 * c + k);
+                    uint2* const dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at + 16 * c + k);
                     dst[0] = make_uint2(w[0], w[1]);
                     dst[1] = make_uint2(w[2], w[3]);
                 }
             }
+        }
         }
     }
     tc_fence_before();
