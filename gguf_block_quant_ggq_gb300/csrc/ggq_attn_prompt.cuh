@@ -16,9 +16,9 @@
 //   * warps 8-11: the packed blobs, read straight from the cache, to fp16 (V with
 //     bf16 activations: bf16) tiles in the K-major 128-byte-swizzled layout, two
 //     buffers each for K and V;
-//   * warps 12, 13 (14, 15 idle): one thread each issues a tile's MMAs: S of step j when its K
-//     tile is there, then O += P V when the softmax has written P.  The two tiles'
-//     products and softmaxes take turns.
+//   * warps 12, 13 and 14, 15: one thread each issues a tile's S = Q K^T and O +=
+//     P V, 64 keys a turn; two score buffers a tile let the next turn's scores be
+//     computed while the softmax works on this one's.
 // The running maximum is raised (and O rescaled in tensor memory) only when a row
 // passes it by 2^8.  fp16 queries are exact; bf16 ones too (rows are scaled by a
 // power of two).  K is rounded to fp16; V and P to the activations' type, so that
@@ -34,9 +34,13 @@
 namespace ggq {
 
 constexpr int kPromptThreads = 16 * 32;
-// registers a thread of the softmax, decoding and MMA warps (512 threads launch with 128 each)
-constexpr int kSoftmaxRegs = 168, kDecodeRegs = 128, kMmaRegs = 48;
-static_assert(256 * kSoftmaxRegs + 128 * kDecodeRegs + 128 * kMmaRegs <= kPromptThreads * 128, "register split");
+// Registers a thread: 512 threads launch with 128 each; the decoding and MMA warps
+// give some back (setmaxnreg.dec, never above 128), the softmax warps take them.
+constexpr int kSoftmaxRegs = 152, kDecodeRegs = 128, kMmaRegs = 80;
+static_assert(kSoftmaxRegs >= 128 && kDecodeRegs <= 128 && kMmaRegs <= 128 && kSoftmaxRegs % 8 == 0 &&
+                  kDecodeRegs % 8 == 0 && kMmaRegs % 8 == 0 &&
+                  256 * kSoftmaxRegs + 128 * kDecodeRegs + 128 * kMmaRegs <= kPromptThreads * 128,
+              "register split");
 
 template <int D>
 struct PromptShape {
@@ -46,9 +50,11 @@ struct PromptShape {
     static constexpr int kQ = 128 * D * 2;             // bytes of a tile's queries
     static constexpr int kK = kKeys * D * 2, kV = kK;  // bytes of a step's keys, values
     static constexpr int oK = kTiles * kQ, oV = oK + 2 * kK, oBar = oV + 2 * kV;
-    static constexpr int kTotal = oBar + 256 + 1024;   // + alignment of the tiles
-    // tensor-memory columns: scores of each tile (probabilities over them), then the outputs
-    static constexpr uint32_t cS = kKeys, cO = kTiles * cS;
+    static constexpr int kTotal = oBar + 384 + 1024;   // + alignment of the tiles
+    // tensor-memory columns: two 64-key score buffers of each tile (probabilities over
+    // them), then the outputs
+    static constexpr uint32_t cS = 128, cO = kTiles * cS;
+    static_assert(cO + kTiles * D <= 512, "tensor memory");
 };
 
 __host__ __device__ constexpr uint32_t prompt_idesc(uint32_t n, bool bf16) {
@@ -211,8 +217,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + SH::oBar);
     uint64_t *const kfull = bars, *const kempty = bars + 2, *const vfull = bars + 4, *const vempty = bars + 6;
-    uint64_t *const sfull = bars + 8, *const pfull = bars + 10, *const ofull = bars + 12, *const done = bars + 14;
-    uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 16);
+    // per tile and score buffer: scores there, probabilities there, P V done; per MMA thread: all done
+    uint64_t *const sfull = bars + 8, *const pfull = bars + 12, *const pdone = bars + 16, *const done = bars + 20;
+    uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 24);
     volatile int* const abort = reinterpret_cast<volatile int*>(tslot + 1);
     int* const s_bad = reinterpret_cast<int*>(tslot + 2);  // [NB][2] first and last key whose value scale is not finite
 
@@ -238,7 +245,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
     const int pos_last = from + (r_end - 1) / p.G, pos_first = from + r_begin / p.G;
     const int glo = p.window > 0 && pos_first - p.window + 1 > 0 ? (pos_first - p.window + 1) >> 4 : 0;
     const int ghi = pos_last < 0 ? glo : (pos_last >> 4) + 1;
-    const int steps = ghi > glo ? (ghi - glo + KG - 1) / KG : 0;
+    const int steps = ghi > glo ? (ghi - glo + KG - 1) / KG : 0;   // K and V tiles
+    const int turns = ghi > glo ? (ghi - glo + 3) / 4 : 0;         // of 64 keys
+    constexpr int kTurns = KT / 64;                                // of a step
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -246,9 +255,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             mbar_init(vfull + i, 128);
             mbar_init(kempty + i, static_cast<uint32_t>(ntiles));
             mbar_init(vempty + i, static_cast<uint32_t>(ntiles));
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(sfull + i, 1);
             mbar_init(pfull + i, 128);
-            mbar_init(ofull + i, 1);
+            mbar_init(pdone + i, 1);
             mbar_init(done + i, 1);
         }
         *abort = 0;
@@ -315,35 +326,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
     if (warp >= 12) {
         // ================================================================ MMA: one thread a tile
         prompt_regs<false, kMmaRegs>();
-        const int t = warp - 12;
-        if (t < ntiles && lane == 0 && steps > 0) {
-            const uint32_t id_s = prompt_idesc(KT, false), id_o = prompt_idesc(D, BF);
+        const int t = (warp - 12) & 1;
+        const bool scores = warp < 14;
+        if (t < ntiles && lane == 0 && turns > 0) {
             const uint32_t cs = tmem + t * SH::cS, co = tmem + SH::cO + t * D;
-            const uint64_t qd = umma_desc_sw128(smem_addr(smem + t * SH::kQ));
-            for (int j = 0; j < steps; ++j) {
-                const int buf = j & 1;
-                const uint32_t ph = (j >> 1) & 1;
-                if (!wait1(kfull + buf, ph)) break;
-                tc_fence_after();
-                const uint64_t kd = umma_desc_sw128(smem_addr(smem + SH::oK + buf * SH::kK));
+            if (scores) {
+                const uint64_t qd = umma_desc_sw128(smem_addr(smem + t * SH::kQ));
+                constexpr uint32_t id = prompt_idesc(64, false);
+                for (int i = 0; i < turns; ++i) {
+                    const int j = i / kTurns, h = i % kTurns, buf = j & 1, sb = i & 1;
+                    if (h == 0 && !wait1(kfull + buf, (j >> 1) & 1)) break;
+                    if (i >= 2 && !wait1(pdone + 2 * t + sb, ((i >> 1) - 1) & 1)) break;
+                    tc_fence_after();
+                    const uint64_t kd = umma_desc_sw128(smem_addr(smem + SH::oK + buf * SH::kK + h * (64 * 128)));
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)  // 32 bytes a step inside a 64-channel atom
-                    tc_mma(cs, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3), kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3),
-                           id_s, k > 0);
-                tc_commit(sfull + t);
-                tc_commit(kempty + buf);
-                if (!wait1(pfull + t, j & 1)) break;
-                if (!wait1(vfull + buf, ph)) break;
-                tc_fence_after();
-                const uint64_t vd = umma_desc_sw128(smem_addr(smem + SH::oV + buf * SH::kV));
+                    for (int k = 0; k < D / 16; ++k)  // 32 bytes a step inside a 64-channel atom
+                        tc_mma(cs + 64 * sb, qd + (k >> 2) * (128 * 128 / 16) + 2 * (k & 3),
+                               kd + (k >> 2) * (KT * 128 / 16) + 2 * (k & 3), id, k > 0);
+                    tc_commit(sfull + 2 * t + sb);
+                    if (h == kTurns - 1) tc_commit(kempty + buf);
+                }
+            } else {
+                constexpr uint32_t id = prompt_idesc(D, BF);
+                for (int i = 0; i < turns; ++i) {
+                    const int j = i / kTurns, h = i % kTurns, buf = j & 1, sb = i & 1;
+                    if (h == 0 && !wait1(vfull + buf, (j >> 1) & 1)) break;
+                    if (!wait1(pfull + 2 * t + sb, (i >> 1) & 1)) break;
+                    tc_fence_after();
+                    const uint64_t vd = umma_desc_sw128(smem_addr(smem + SH::oV + buf * SH::kV + h * (D * 128)));
 #pragma unroll
-                for (int k = 0; k < KT / 16; ++k)
-                    tc_mma_ts(co, cs + 8 * k, vd + (k >> 2) * (D * 128 / 16) + 2 * (k & 3), id_o, (j > 0 || k > 0) ? 1u : 0u);
-                tc_commit(ofull + t);
-                tc_commit(vempty + buf);
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_ts(co, cs + 64 * sb + 8 * k, vd + 2 * k, id, (i > 0 || k > 0) ? 1u : 0u);
+                    tc_commit(pdone + 2 * t + sb);
+                    if (h == kTurns - 1) tc_commit(vempty + buf);
+                }
             }
-            tc_commit(done + t);
-            mbar_wait(done + t, 0);  // every MMA has ended before tensor memory goes
+            tc_commit(done + warp - 12);
+            mbar_wait(done + warp - 12, 0);  // every MMA has ended before tensor memory goes
         }
     } else if (warp >= 8) {
         // ================================================================ packed blobs -> operand tiles
@@ -547,21 +566,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         const int t_first = from + (r_begin + 128 * t) / p.G, t_last = from + (min(r_end, r_begin + 128 * t + 128) - 1) / p.G;
         const int seen_from = p.window > 0 ? t_last - p.window + 1 : 0;
         float m = -1e30f, l = 0.0f;
-        for (int j = 0; j < steps; ++j) {
-            if (!wait(sfull + t, j & 1)) break;
+        for (int i = 0; i < turns; ++i) {
+            const int sb = i & 1;
+            if (!wait(sfull + 2 * t + sb, (i >> 1) & 1)) break;
             tc_fence_after();
-            const int key0 = 16 * glo + j * KT;
-            const bool whole = key0 + KT - 1 <= t_first && key0 >= seen_from;
-            float x[KT];
-#pragma unroll
-            for (int c = 0; c < KT / 32; ++c) prompt_ld32(cs + 32 * c, x + 32 * c);
+            const int key0 = 16 * glo + i * 64;
+            const bool whole = key0 + 63 <= t_first && key0 >= seen_from;
+            float x[64];
+            prompt_ld32(cs + 64 * sb, x);
+            prompt_ld32(cs + 64 * sb + 32, x + 32);
             prompt_wait_ld();
-#pragma unroll
-            for (int c = 0; c < KT / 32; ++c) prompt_tie32(x + 32 * c);
+            prompt_tie32(x);
+            prompt_tie32(x + 32);
             // logits in units of log2 (plain: still to be multiplied by sx)
             if (!plain) {
 #pragma unroll
-                for (int k = 0; k < KT; ++k) {
+                for (int k = 0; k < 64; ++k) {
                     float y = x[k] * sx;
                     // tanh(z) = 1 - 2 / (1 + exp(2 z))
                     if (p.cap > 0.0f) {
@@ -573,12 +593,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             }
             if (!whole) {
 #pragma unroll
-                for (int k = 0; k < KT; ++k)
+                for (int k = 0; k < 64; ++k)
                     if (key0 + k > pos || key0 + k < first_key) x[k] = -INFINITY;
             }
             float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int k = 0; k < KT; ++k) tops[k & 3] = fmaxf(tops[k & 3], x[k]);
+            for (int k = 0; k < 64; ++k) tops[k & 3] = fmaxf(tops[k & 3], x[k]);
             const float mul = plain ? sx : 1.0f;
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;
             const bool raise = top > m + 8.0f;
@@ -586,8 +606,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                 const float mn = raise ? top : m, a = prompt_ex2(m - mn);
                 m = mn;
                 l *= a;
-                if (j > 0) {
-                    if (!wait(ofull + t, (j - 1) & 1)) break;
+                if (i > 0) {
+                    if (!wait(pdone + 2 * t + (sb ^ 1), ((i - 1) >> 1) & 1)) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
@@ -601,34 +621,31 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             }
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int at = 0; at < KT / 64; ++at) {
-#pragma unroll
-                for (int k = 64 * at; k < 64 * at + 64; k += 2) {
-                    ffma2(x[k], x[k + 1], x[k], x[k + 1], mul, -m, -m);
-                    x[k] = prompt_ex2(x[k]);
-                    x[k + 1] = prompt_ex2(x[k + 1]);
-                    add2(sum[k & 2], sum[(k & 2) + 1], sum[k & 2], sum[(k & 2) + 1], x[k], x[k + 1]);
-                }
-                // the V tile's key order in an atom of 64: word 8 t + 2 g holds keys 2 t, 2 t + 1 of group g,
-                // the next one keys 8 + 2 t, 9 + 2 t
-                uint32_t w[32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int gq = 0; gq < 4; ++gq) {
-                        const int k = 64 * at + 16 * gq + 2 * q;
-                        w[8 * q + 2 * gq] = prompt_pack<BF>(x[k], x[k + 1]);
-                        w[8 * q + 2 * gq + 1] = prompt_pack<BF>(x[k + 8], x[k + 9]);
-                    }
-                prompt_st32(cs + 32 * at, w);
+            for (int k = 0; k < 64; k += 2) {
+                ffma2(x[k], x[k + 1], x[k], x[k + 1], mul, -m, -m);
+                x[k] = prompt_ex2(x[k]);
+                x[k + 1] = prompt_ex2(x[k + 1]);
+                add2(sum[k & 2], sum[(k & 2) + 1], sum[k & 2], sum[(k & 2) + 1], x[k], x[k + 1]);
             }
+            // the V tile's key order in an atom of 64: word 8 t + 2 g holds keys 2 t, 2 t + 1 of group g,
+            // the next one keys 8 + 2 t, 9 + 2 t
+            uint32_t w[32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int gq = 0; gq < 4; ++gq) {
+                    const int k = 16 * gq + 2 * q;
+                    w[8 * q + 2 * gq] = prompt_pack<BF>(x[k], x[k + 1]);
+                    w[8 * q + 2 * gq + 1] = prompt_pack<BF>(x[k + 8], x[k + 9]);
+                }
+            prompt_st32(cs + 64 * sb, w);
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(pfull + t);
+            mbar_arrive(pfull + 2 * t + sb);
         }
         // ---- output rows
-        if (steps > 0) wait(ofull + t, (steps - 1) & 1);
+        if (turns > 0) wait(pdone + 2 * t + ((turns - 1) & 1), ((turns - 1) >> 1) & 1);
         tc_fence_after();
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         const int64_t at = (first + i_row) * p.out_token + h * p.out_head;
