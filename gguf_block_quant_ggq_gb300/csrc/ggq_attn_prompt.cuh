@@ -13,10 +13,10 @@
 //     from tensor memory; probabilities go back over them as the first operand of
 //     P V (tensor memory holds it, so only V is read from shared memory), in the
 //     channels' key order of the V tile;
-//   * warps 8-11: the packed blobs, read straight from the cache, to fp16 (V with
+//   * warps 8-15: the packed blobs, read straight from the cache, to fp16 (V with
 //     bf16 activations: bf16) tiles in the K-major 128-byte-swizzled layout, two
 //     buffers each for K and V;
-//   * warps 12, 13 and 14, 15: one thread each issues a tile's S = Q K^T and O +=
+//   * warps 16, 17 and 18, 19: one thread each issues a tile's S = Q K^T and O +=
 //     P V, 64 keys a turn; two score buffers a tile let the next turn's scores be
 //     computed while the softmax works on this one's.
 // The running maximum is raised (and O rescaled in tensor memory) only when a row
@@ -33,13 +33,18 @@
 
 namespace ggq {
 
-constexpr int kPromptThreads = 16 * 32;
-// Registers a thread: 512 threads launch with 128 each; the decoding and MMA warps
-// give some back (setmaxnreg.dec, never above 128), the softmax warps take them.
-constexpr int kSoftmaxRegs = 152, kDecodeRegs = 128, kMmaRegs = 80;
-static_assert(kSoftmaxRegs >= 128 && kDecodeRegs <= 128 && kMmaRegs <= 128 && kSoftmaxRegs % 8 == 0 &&
-                  kDecodeRegs % 8 == 0 && kMmaRegs % 8 == 0 &&
-                  256 * kSoftmaxRegs + 128 * kDecodeRegs + 128 * kMmaRegs <= kPromptThreads * 128,
+constexpr int kSoftmaxWarps = 8, kDecodeWarps = 8, kMmaWarps = 4;
+constexpr int kFirstMma = kSoftmaxWarps + kDecodeWarps;
+constexpr int kPromptThreads = (kSoftmaxWarps + kDecodeWarps + kMmaWarps) * 32;
+
+// Registers a thread: 640 threads launch with 96 each; the decoding and MMA warps
+// give some back (setmaxnreg.dec, never above 96), the softmax warps take them.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 128, kDecodeRegs = 88, kMmaRegs = 48;
+static_assert(kSoftmaxRegs >= kLaunchRegs && kDecodeRegs <= kLaunchRegs && kMmaRegs <= kLaunchRegs &&
+                  kSoftmaxRegs % 8 == 0 && kDecodeRegs % 8 == 0 && kMmaRegs % 8 == 0 &&
+                  32 * (kSoftmaxWarps * kSoftmaxRegs + kDecodeWarps * kDecodeRegs + kMmaWarps * kMmaRegs) <=
+                      kPromptThreads * kLaunchRegs &&
+                  kPromptThreads * kLaunchRegs <= 65536,
               "register split");
 
 template <int D>
@@ -251,8 +256,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(kfull + i, 128);
-            mbar_init(vfull + i, 128);
+            mbar_init(kfull + i, kDecodeWarps * 32);
+            mbar_init(vfull + i, kDecodeWarps * 32);
             mbar_init(kempty + i, static_cast<uint32_t>(ntiles));
             mbar_init(vempty + i, static_cast<uint32_t>(ntiles));
         }
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         for (int i = 0; i < NB; ++i) s_bad[2 * i] = 0x7fffffff, s_bad[2 * i + 1] = -1;
         fence_barrier_init();
     }
-    if (warp == 12) {
+    if (warp == kFirstMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -323,11 +328,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         return ok;
     };
 
-    if (warp >= 12) {
+    if (warp >= kFirstMma) {
         // ================================================================ MMA: one thread a tile
         prompt_regs<false, kMmaRegs>();
-        const int t = (warp - 12) & 1;
-        const bool scores = warp < 14;
+        const int t = (warp - kFirstMma) & 1;
+        const bool scores = warp < kFirstMma + 2;
         if (t < ntiles && lane == 0 && turns > 0) {
             const uint32_t cs = tmem + t * SH::cS, co = tmem + SH::cO + t * D;
             if (scores) {
@@ -361,19 +366,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                     if (h == kTurns - 1) tc_commit(vempty + buf);
                 }
             }
-            tc_commit(done + warp - 12);
-            mbar_wait(done + warp - 12, 0);  // every MMA has ended before tensor memory goes
+            tc_commit(done + warp - kFirstMma);
+            mbar_wait(done + warp - kFirstMma, 0);  // every MMA has ended before tensor memory goes
         }
-    } else if (warp >= 8) {
+    } else if (warp >= kSoftmaxWarps) {
         // ================================================================ packed blobs -> operand tiles
         prompt_regs<false, kDecodeRegs>();
-        const int cw = warp - 8, g8 = lane >> 2, t4 = lane & 3, gpp = p.page >> 4;
+        const int cw = warp - kSoftmaxWarps, g8 = lane >> 2, t4 = lane & 3, gpp = p.page >> 4;
         constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
-        constexpr int kPer = KG / 4;                              // groups of a step and warp (keys): 2 or 1
-        constexpr int KL = K4 ? D / 64 : D / 32;                  // 16-byte words of a lane and blob
-        constexpr int VP = KG / 2, VH = 4 / VP;                   // values: pairs of groups, parts of a pair's lines
-        constexpr int VL = (V4 ? D / 64 : D / 32) / VH;
-        const int pair = cw % VP, v_line = (cw / VP) * VL;
+        // keys: a warp takes one group of the step (64-key steps: one octet of it)
+        constexpr int KP = kDecodeWarps / KG, KO = 2 / KP;        // parts of a group, octets of a part
+        constexpr int KL = (K4 ? D / 64 : D / 32) / KP;           // 16-byte words of a lane
+        const int k_group = cw % KG, k_part = cw / KG;
+        // values: two neighbouring groups, some of the blocks of 32 channels
+        constexpr int VP = KG / 2, VB = NB / (kDecodeWarps / VP); // pairs of groups; blocks of a warp: 1 or 2
+        const int pair = cw % VP, b0 = (cw / VP) * VB;
+        const uint32_t v_sel = (VB == 1 && (b0 & 1)) ? 0x7632u : 0x5410u;
         // blobs of the step's groups, one a lane
         const auto locate = [&](int j) {
             const int g = glo + j * KG + (lane & (KG - 1));
@@ -388,22 +396,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             }
             return at;
         };
-        uint4 kq[kPer][KL], vq[2][VL];
-        uint32_t ks[kPer][2][NB / 2], vsc[2][4][NB / 2];
+        uint4 kq[KL];
+        uint32_t ks[KO][NB / 2];
+        uint4 vq[2][VB];          // a block: four words of bytes, or two of nibbles
+        uint32_t vsc[2][4];       // scales of the four keys of a word, blocks b0 and b0 + 1
         const auto load_k = [&](int64_t blobs) {
+            const int64_t at = __shfl_sync(0xffffffffu, blobs, k_group);
+            if (at < 0) return;  // past the last key: the tile keeps what it held, every row masks it
+            const uint8_t* const src = p.k + at * kKB;
 #pragma unroll
-            for (int c = 0; c < kPer; ++c) {
-                const int64_t at = __shfl_sync(0xffffffffu, blobs, cw * kPer + c);
-                if (at < 0) continue;  // past the last key: the tile keeps what it held, every row masks it
-                const uint8_t* const src = p.k + at * kKB;
+            for (int i = 0; i < KL; ++i)
+                kq[i] = __ldg(reinterpret_cast<const uint4*>(src + ((k_part * KL + i) * 32 + lane) * 16));
 #pragma unroll
-                for (int i = 0; i < KL; ++i) kq[c][i] = __ldg(reinterpret_cast<const uint4*>(src + (i * 32 + lane) * 16));
+            for (int o = 0; o < KO; ++o)
 #pragma unroll
-                for (int o = 0; o < 2; ++o)
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i)
-                        ks[c][o][i] = __ldg(reinterpret_cast<const uint32_t*>(src + kv_quant_bytes(K4, D) + (8 * o + g8) * NB * 2) + i);
-            }
+                for (int i = 0; i < NB / 2; ++i)
+                    ks[o][i] = __ldg(reinterpret_cast<const uint32_t*>(src + kv_quant_bytes(K4, D) +
+                                                                       (8 * (k_part + o) + g8) * NB * 2) + i);
         };
         const auto load_v = [&](int64_t blobs) {
 #pragma unroll
@@ -411,22 +420,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                 const int64_t at = __shfl_sync(0xffffffffu, blobs, 2 * pair + c);
                 if (at < 0) {
 #pragma unroll
-                    for (int i = 0; i < VL; ++i) vq[c][i] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = 0; i < VB; ++i) vq[c][i] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) vsc[c][r][i] = 0u;
+                    for (int r = 0; r < 4; ++r) vsc[c][r] = 0u;
                     continue;
                 }
                 const uint8_t* const src = p.v + at * kVB;
 #pragma unroll
-                for (int i = 0; i < VL; ++i) vq[c][i] = __ldg(reinterpret_cast<const uint4*>(src + ((v_line + i) * 32 + lane) * 16));
+                for (int i = 0; i < VB; ++i) {
+                    const int blk = b0 + i;
+                    if constexpr (V4) {
+                        const uint2 u = __ldg(reinterpret_cast<const uint2*>(src + ((blk >> 1) * 32 + lane) * 16 + (blk & 1) * 8));
+                        vq[c][i].x = u.x, vq[c][i].y = u.y;
+                    } else {
+                        vq[c][i] = __ldg(reinterpret_cast<const uint4*>(src + (blk * 32 + lane) * 16));
+                    }
+                }
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i)
-                        vsc[c][r][i] = __ldg(reinterpret_cast<const uint32_t*>(src + kv_quant_bytes(V4, D) +
-                                                                               (8 * (r >> 1) + 2 * t4 + (r & 1)) * NB * 2) + i);
+                    vsc[c][r] = __ldg(reinterpret_cast<const uint32_t*>(src + kv_quant_bytes(V4, D) +
+                                                                        (8 * (r >> 1) + 2 * t4 + (r & 1)) * NB * 2) + (b0 >> 1));
             }
         };
         int64_t blobs = locate(0), next = locate(1);
@@ -440,30 +453,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             next = locate(j + 2);
             // ---- keys: lane (g, t) writes 16 channels of a 64-channel atom as two chunks of its token's row
             if (j >= 2 && !wait(kempty + buf, ((j >> 1) - 1) & 1)) break;
-            uint8_t* const kt = smem + SH::oK + buf * SH::kK + (cw * kPer * 16 + g8) * 128;
+            uint8_t* const kt = smem + SH::oK + buf * SH::kK + (k_group * 16 + 8 * k_part + g8) * 128;
 #pragma unroll
-            for (int c = 0; c < kPer; ++c)
+            for (int i = 0; i < KL; ++i) {
+                const uint32_t w[4] = {kq[i].x, kq[i].y, kq[i].z, kq[i].w};
 #pragma unroll
-                for (int i = 0; i < KL; ++i) {
-                    const uint32_t w[4] = {kq[c][i].x, kq[c][i].y, kq[c][i].z, kq[c][i].w};
-#pragma unroll
-                    for (int q = 0; q < 4; q += K4 ? 1 : 2) {  // a chunk: one word of 8 nibbles or two of 4 bytes
-                        const int f = 4 * i + q, per = K4 ? NB : D / 16, o = f / per, jj = f % per;
-                        const int blk = K4 ? jj : jj >> 1, chunk = 2 * t4 + (blk & 1);
-                        const uint32_t d2 = prmt(ks[c][o][blk >> 1], 0u, (blk & 1) ? 0x3232u : 0x1010u);
-                        uint32_t h[4];
-                        if constexpr (K4) {
-                            prompt_ints4(w[q], h);
-                        } else {
-                            uint32_t a[2], e[2];
-                            prompt_ints8(w[q], a);
-                            prompt_ints8(w[q + 1 < 4 ? q + 1 : 3], e);
-                            h[0] = a[0], h[1] = a[1], h[2] = e[0], h[3] = e[1];
-                        }
-                        *reinterpret_cast<uint4*>(kt + (16 * c + 8 * o) * 128 + (blk >> 1) * (KT * 128) + ((chunk ^ g8) << 4)) =
-                            make_uint4(prompt_mul2(h[0], d2), prompt_mul2(h[1], d2), prompt_mul2(h[2], d2), prompt_mul2(h[3], d2));
+                for (int q = 0; q < 4; q += K4 ? 1 : 2) {  // a chunk: one word of 8 nibbles or two of 4 bytes
+                    const int f = 4 * i + q, per = K4 ? NB : D / 16, o = f / per, jj = f % per;
+                    const int blk = K4 ? jj : jj >> 1, chunk = 2 * t4 + (blk & 1);
+                    const uint32_t d2 = prmt(ks[o][blk >> 1], 0u, (blk & 1) ? 0x3232u : 0x1010u);
+                    uint32_t h[4];
+                    if constexpr (K4) {
+                        prompt_ints4(w[q], h);
+                    } else {
+                        uint32_t a[2], e[2];
+                        prompt_ints8(w[q], a);
+                        prompt_ints8(w[q + 1 < 4 ? q + 1 : 3], e);
+                        h[0] = a[0], h[1] = a[1], h[2] = e[0], h[3] = e[1];
                     }
+                    *reinterpret_cast<uint4*>(kt + o * (8 * 128) + (blk >> 1) * (KT * 128) + ((chunk ^ g8) << 4)) =
+                        make_uint4(prompt_mul2(h[0], d2), prompt_mul2(h[1], d2), prompt_mul2(h[2], d2), prompt_mul2(h[3], d2));
                 }
+            }
             load_k(blobs);
             fence_proxy_async_smem();
             mbar_arrive(kfull + buf);
@@ -474,72 +485,59 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i) {
-                        if (key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1) >= len) vsc[c][r][i] = 0u;
-                        odd = __vmaxu2(odd, vsc[c][r][i] & 0x7C007C00u);
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    if (key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1) >= len) vsc[c][r] = 0u;
+                    odd = __vmaxu2(odd, vsc[c][r] & 0x7C007C00u);
+                }
             if ((odd & 0xFFFFu) == 0x7C00u || (odd >> 16) == 0x7C00u) {
                 // scales that are not finite: 0 here, and the rows that see them are told
+                int* const bad = s_bad + 4 * (b0 >> 1);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) {
-                            const uint32_t u = vsc[c][r][i];
-                            const int key = key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1);
-                            const bool lo = (u & 0x7C00u) == 0x7C00u, hi = (u & 0x7C000000u) == 0x7C000000u;
-                            if (lo) atomicMin(s_bad + 4 * i, key), atomicMax(s_bad + 4 * i + 1, key);
-                            if (hi) atomicMin(s_bad + 4 * i + 2, key), atomicMax(s_bad + 4 * i + 3, key);
-                            vsc[c][r][i] = (lo ? 0u : u & 0xFFFFu) | (hi ? 0u : u & 0xFFFF0000u);
-                        }
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t u = vsc[c][r];
+                        const int key = key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1);
+                        const bool lo = (u & 0x7C00u) == 0x7C00u, hi = (u & 0x7C000000u) == 0x7C000000u;
+                        if (lo) atomicMin(bad, key), atomicMax(bad + 1, key);
+                        if (hi) atomicMin(bad + 2, key), atomicMax(bad + 3, key);
+                        vsc[c][r] = (lo ? 0u : u & 0xFFFFu) | (hi ? 0u : u & 0xFFFF0000u);
+                    }
             }
             // lane (g, t) writes 8 keys of both groups as one chunk of channel 8 n + g
-            uint8_t* const vt = smem + SH::oV + buf * SH::kV + (pair >> 1) * (D * 128) + g8 * 128 +
+            uint8_t* const vt = smem + SH::oV + buf * SH::kV + (pair >> 1) * (D * 128) + (4 * 8 * b0 + g8) * 128 +
                                 (((2 * t4 + (pair & 1)) ^ g8) << 4);
 #pragma unroll
-            for (int i = 0; i < VL; ++i) {
+            for (int i = 0; i < VB; ++i) {
+                float df[2][4];
+                uint32_t d2[2][2];
 #pragma unroll
-                for (int half = 0; half < (V4 ? 2 : 1); ++half) {  // a line: one block of 32 channels, or two
-                    float df[2][4];
-                    uint32_t d2[2][2];
-                    const auto scales = [&](int lo_blk) {
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
+                    for (int k = 0; k < 2; ++k) d2[c][k] = prmt(vsc[c][2 * k], vsc[c][2 * k + 1], i ? 0x7632u : v_sel);
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                d2[c][k] = prmt(vsc[c][2 * k][lo_blk >> 1], vsc[c][2 * k + 1][lo_blk >> 1], (lo_blk & 1) ? 0x7632u : 0x5410u);
+                    for (int k = 0; k < 4; ++k) df[c][k] = (k & 1) ? half_hi(d2[c][k >> 1]) : half_lo(d2[c][k >> 1]);
+                }
+                const uint32_t w0[4] = {vq[0][i].x, vq[0][i].y, vq[0][i].z, vq[0][i].w};
+                const uint32_t w1[4] = {vq[1][i].x, vq[1][i].y, vq[1][i].z, vq[1][i].w};
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) df[c][k] = (k & 1) ? half_hi(d2[c][k >> 1]) : half_lo(d2[c][k >> 1]);
-                        }
-                    };
-                    if (VH == 1 || v_line == 0) scales(V4 ? 2 * i + half : i);
-                    else scales(V4 ? 2 * (VL + i) + half : VL + i);
+                for (int q = 0; q < (V4 ? 2 : 4); ++q) {
                     if constexpr (V4) {
+                        uint32_t h[2][4];
+                        prompt_ints4(w0[q], h[0]);
+                        prompt_ints4(w1[q], h[1]);
 #pragma unroll
-                        for (int q = 2 * half; q < 2 * half + 2; ++q) {
-                            uint32_t h[2][4];
-                            prompt_ints4(q == 0 ? vq[0][i].x : q == 1 ? vq[0][i].y : q == 2 ? vq[0][i].z : vq[0][i].w, h[0]);
-                            prompt_ints4(q == 0 ? vq[1][i].x : q == 1 ? vq[1][i].y : q == 2 ? vq[1][i].z : vq[1][i].w, h[1]);
-                            uint8_t* const row = vt + 2 * (4 * (v_line + i) + q) * (8 * 128);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)  // even and odd eights of channels
-                                *reinterpret_cast<uint4*>(row + k * (8 * 128)) =
-                                    make_uint4(prompt_v4<BF>(h[0][k], df[0][0], df[0][1], d2[0][0]),
-                                               prompt_v4<BF>(h[0][2 + k], df[0][2], df[0][3], d2[0][1]),
-                                               prompt_v4<BF>(h[1][k], df[1][0], df[1][1], d2[1][0]),
-                                               prompt_v4<BF>(h[1][2 + k], df[1][2], df[1][3], d2[1][1]));
-                        }
+                        for (int k = 0; k < 2; ++k)  // even and odd eights of channels
+                            *reinterpret_cast<uint4*>(vt + (4 * i + 2 * q + k) * (8 * 128)) =
+                                make_uint4(prompt_v4<BF>(h[0][k], df[0][0], df[0][1], d2[0][0]),
+                                           prompt_v4<BF>(h[0][2 + k], df[0][2], df[0][3], d2[0][1]),
+                                           prompt_v4<BF>(h[1][k], df[1][0], df[1][1], d2[1][0]),
+                                           prompt_v4<BF>(h[1][2 + k], df[1][2], df[1][3], d2[1][1]));
                     } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t x[2], y[2];
-                            prompt_v8<BF>(q == 0 ? vq[0][i].x : q == 1 ? vq[0][i].y : q == 2 ? vq[0][i].z : vq[0][i].w, df[0], d2[0][0], d2[0][1], x);
-                            prompt_v8<BF>(q == 0 ? vq[1][i].x : q == 1 ? vq[1][i].y : q == 2 ? vq[1][i].z : vq[1][i].w, df[1], d2[1][0], d2[1][1], y);
-                            *reinterpret_cast<uint4*>(vt + (4 * (v_line + i) + q) * (8 * 128)) = make_uint4(x[0], x[1], y[0], y[1]);
-                        }
+                        uint32_t x[2], y[2];
+                        prompt_v8<BF>(w0[q], df[0], d2[0][0], d2[0][1], x);
+                        prompt_v8<BF>(w1[q], df[1], d2[1][0], d2[1][1], y);
+                        *reinterpret_cast<uint4*>(vt + (4 * i + q) * (8 * 128)) = make_uint4(x[0], x[1], y[0], y[1]);
                     }
                 }
             }
@@ -675,7 +673,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kFirstMma) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
@@ -691,6 +689,10 @@ cudaError_t launch_attn_prompt_one(const AttnParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!set[dev].load(std::memory_order_acquire)) {
+        cudaFuncAttributes at;
+        e = cudaFuncGetAttributes(&at, k_attn_prompt<K4, V4, D, BF>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;  // the split would not add up
         e = cudaFuncSetAttribute(k_attn_prompt<K4, V4, D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kTotal);
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_release);
