@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libggq.so")
@@ -95,6 +96,12 @@ class ggq_router(ctypes.Structure):
                                               "normalize")] + [("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
 
 
+# ggq_attn and ggq_router as packed fields: filled in place for every call
+_ATTN = struct.Struct("@iiqqPqqPqqPqPPqqffqP")
+_ROUTER = struct.Struct("@iiiiiifP")
+assert _ATTN.size == ctypes.sizeof(ggq_attn) and _ROUTER.size == ctypes.sizeof(ggq_router)
+
+
 class GGQError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -154,25 +161,6 @@ def _ptr(t, dtype: str | None = None):
     return t.data_ptr()
 
 
-def _rows(t, heads: int, dim: int):
-    """(address, ggq_dtype, token stride, head stride) of a [tokens][heads][dim]
-    CUDA tensor whose last axis is dense; the other strides are free."""
-    if not getattr(t, "is_cuda", False):
-        raise ValueError(f"libggq takes CUDA tensors (device memory), got one on {getattr(t, 'device', type(t))}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"expected a [tokens, {heads}, {dim}] tensor, got {tuple(t.shape)}")
-    token, head, one = t.stride()
-    if one != 1:
-        raise ValueError("the channels of a head have to be dense")
-    code = _DTYPE_CODES.get(str(t.dtype))
-    if code is None:
-        raise ValueError(f"expected a float32, float16 or bfloat16 tensor, got {t.dtype}")
-    return t.data_ptr(), code, token, head
-
-
-_DTYPE_CODES = {"torch." + k: v for k, v in DTYPE.items()}
-
-
 class KVCache:
     """A paged key/value cache in Q8_0 or Q4_0 blocks: two uint8 pools on the
     context's device (given, or made here), and the C structure that names them."""
@@ -194,9 +182,10 @@ class KVCache:
                 raise ValueError(f"{n_pages} pages of {size} bytes need a pool of {n_pages * size}, got {pool.numel()}")
             pools.append(pool)
         self.k, self.v = pools
+        self.device = ctx.device
         self.struct = ggq_kv_cache(TYPE[k_type], TYPE[v_type], n_kv_heads, head_dim, page_size, n_pages,
                                    pools[0].data_ptr(), pools[1].data_ptr())
-        self.ref = ctypes.byref(self.struct)
+        self.ref = ctypes.addressof(self.struct)
 
 
 class Context:
@@ -208,6 +197,14 @@ class Context:
 
         self._torch = torch
         self.device = device
+        self._dev = torch.device("cuda", device)
+        self._f32, self._i32, self._i64 = torch.float32, torch.int32, torch.int64
+        self._codes = {getattr(torch, k): v for k, v in DTYPE.items()}
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._attn_args = ctypes.create_string_buffer(_ATTN.size)
+        self._router_args = ctypes.create_string_buffer(_ROUTER.size)
+        self._attn_at, self._router_at = ctypes.addressof(self._attn_args), ctypes.addressof(self._router_args)
+        self._attn_ready = False
         h = ctypes.c_void_p()
         st = load().ggq_create(ctypes.byref(h), device)
         if st != 0:
@@ -227,8 +224,35 @@ class Context:
 
     def _stream(self, stream):
         if stream is None:
+            if self._raw_stream is not None:
+                return self._raw_stream(self.device)
             stream = self._torch.cuda.current_stream(self.device)
-        return ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
+
+    def _vec(self, t, dtype):
+        """Address of a contiguous tensor of `dtype` on the context's device (None passes NULL)."""
+        if t is None:
+            return 0
+        if t.dtype is dtype and t.get_device() == self.device and t.is_contiguous():
+            return t.data_ptr()
+        _ptr(t, str(dtype)[6:])
+        raise ValueError(f"expected a tensor on cuda:{self.device}, got one on {t.device}")
+
+    def _rows(self, t, heads, dim):
+        """(address, ggq_dtype, token stride, head stride) of a [tokens][heads][dim] tensor on the
+        context's device whose last axis is dense; the other strides are free."""
+        code = self._codes.get(t.dtype)
+        if code is None:
+            raise ValueError(f"expected a float32, float16 or bfloat16 tensor, got {t.dtype}")
+        if t.get_device() != self.device:
+            raise ValueError(f"libggq takes CUDA tensors on cuda:{self.device} (device memory), got one on {t.device}")
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+            raise ValueError(f"expected a [tokens, {heads}, {dim}] tensor, got {tuple(shape)}")
+        token, head, one = t.stride()
+        if one != 1:
+            raise ValueError("the channels of a head have to be dense")
+        return t.data_ptr(), code, token, head
 
     def _check(self, st):
         if st != 0:
@@ -315,26 +339,31 @@ class Context:
 
     def kv_store(self, cache: KVCache, k, v, slots, stream=None):
         """Quantize k and v [tokens][kv heads][D] into the cache's slots (int64 [tokens], negative: skipped)."""
-        kp, code, kt, kh = _rows(k, cache.n_kv_heads, cache.head_dim)
-        vp, vcode, vt, vh = _rows(v, cache.n_kv_heads, cache.head_dim)
-        if code != vcode or k.shape[0] != v.shape[0] or slots.numel() != k.shape[0]:
+        kp, code, kt, kh = self._rows(k, cache.n_kv_heads, cache.head_dim)
+        vp, vcode, vt, vh = self._rows(v, cache.n_kv_heads, cache.head_dim)
+        n = slots.numel()
+        if code != vcode or k.shape[0] != n or v.shape[0] != n:
             raise ValueError("k, v and slots have to agree in type and tokens")
-        self._check(load().ggq_kv_store(self.handle, cache.ref, code, kp, kt, kh, vp, vt, vh, _ptr(slots, "int64"),
-                                        k.shape[0], self._stream(stream)))
+        st = _lib.ggq_kv_store(self.handle, cache.ref, code, kp, kt, kh, vp, vt, vh, self._vec(slots, self._i64), n,
+                               self._stream(stream))
+        if st:
+            self._check(st)
 
     def kv_load(self, cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
         """Values of the cache's slots, [tokens][kv heads][D] each of K and V (float32 unless dtype says otherwise)."""
-        n, shape = slots.numel(), (slots.numel(), cache.n_kv_heads, cache.head_dim)
+        n, heads, dim = slots.numel(), cache.n_kv_heads, cache.head_dim
         if k is None:
-            k = self._torch.empty(shape, dtype=dtype or self._torch.float32, device=slots.device)
+            k = self._torch.empty((n, heads, dim), dtype=dtype or self._f32, device=self._dev)
         if v is None:
-            v = self._torch.empty(shape, dtype=dtype or self._torch.float32, device=slots.device)
-        kp, code, kt, kh = _rows(k, cache.n_kv_heads, cache.head_dim)
-        vp, vcode, vt, vh = _rows(v, cache.n_kv_heads, cache.head_dim)
+            v = self._torch.empty((n, heads, dim), dtype=dtype or self._f32, device=self._dev)
+        kp, code, kt, kh = self._rows(k, heads, dim)
+        vp, vcode, vt, vh = self._rows(v, heads, dim)
         if code != vcode or k.shape[0] != n or v.shape[0] != n:
             raise ValueError("k, v and slots have to agree in type and tokens")
-        self._check(load().ggq_kv_load(self.handle, cache.ref, code, _ptr(slots, "int64"), n, kp, kt, kh, vp, vt, vh,
-                                       self._stream(stream)))
+        st = _lib.ggq_kv_load(self.handle, cache.ref, code, self._vec(slots, self._i64), n, kp, kt, kh, vp, vt, vh,
+                              self._stream(stream))
+        if st:
+            self._check(st)
         return k, v
 
     def attention(self, cache: KVCache, q, lens, table, q_start=None, max_q=None, max_len=0, scale=None, cap=0.0,
@@ -346,9 +375,9 @@ class Context:
             raise ValueError(f"expected a [tokens, heads, {cache.head_dim}] tensor, got {tuple(q.shape)}")
         n, heads, dim = q.shape
         if out is None:
-            out = self._torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
-        qp, code, qt, qh = _rows(q, heads, cache.head_dim)
-        op, ocode, ot, oh = _rows(out, heads, cache.head_dim)
+            out = self._torch.empty((n, heads, dim), dtype=q.dtype, device=self._dev)
+        qp, code, qt, qh = self._rows(q, heads, cache.head_dim)
+        op, ocode, ot, oh = self._rows(out, heads, cache.head_dim)
         seqs = lens.numel()
         if ocode != code or out.shape[0] != n:
             raise ValueError("out has to have q's type and tokens")
@@ -358,12 +387,17 @@ class Context:
             raise ValueError(f"{n} rows for {seqs} sequences: q_start is needed")
         if slopes is not None and slopes.numel() != heads:
             raise ValueError(f"expected {heads} slopes, got {slopes.numel()}")
-        if reserve:
-            self._check(load().ggq_reserve_attention(self.handle, self._stream(stream)))
-        a = ggq_attn(code, heads, n, seqs, qp, qt, qh, op, ot, oh, _ptr(table, "int32"), table.shape[1],
-                     _ptr(lens, "int32"), _ptr(q_start, "int32"), n if max_q is None else max_q, max_len,
-                     dim ** -0.5 if scale is None else scale, cap, window, _ptr(slopes, "float32"))
-        self._check(load().ggq_attention(self.handle, cache.ref, ctypes.byref(a), self._stream(stream)))
+        raw = self._stream(stream)
+        if reserve and not self._attn_ready:
+            self._check(_lib.ggq_reserve_attention(self.handle, raw))
+            self._attn_ready = True
+        _ATTN.pack_into(self._attn_args, 0, code, heads, n, seqs, qp, qt, qh, op, ot, oh, self._vec(table, self._i32),
+                        table.shape[1], self._vec(lens, self._i32), self._vec(q_start, self._i32),
+                        n if max_q is None else max_q, max_len, dim ** -0.5 if scale is None else scale, cap, window,
+                        self._vec(slopes, self._f32))
+        st = _lib.ggq_attention(self.handle, cache.ref, self._attn_at, raw)
+        if st:
+            self._check(st)
         return out
 
     def moe_route(self, logits, top_k: int, scoring: str = "softmax", bias=None, n_groups: int = 1,
@@ -371,22 +405,25 @@ class Context:
                   weights=None, stream=None):
         """Expert ids [tokens][top_k] int32 and weights fp32 for moe_experts, of logits [tokens][experts]."""
         T, E = logits.shape
-        code = _DTYPE_CODES.get(str(logits.dtype))
+        code = self._codes.get(logits.dtype)
         if code is None:
             raise ValueError(f"expected float32, float16 or bfloat16 logits, got {logits.dtype}")
         if bias is not None and bias.numel() != E:
             raise ValueError(f"expected a bias of {E} experts, got {bias.numel()}")
-        for t in (ids, weights):
-            if t is not None and tuple(t.shape) != (T, top_k):
-                raise ValueError(f"expected a [{T}, {top_k}] output, got {tuple(t.shape)}")
         if ids is None:
-            ids = self._torch.empty((T, top_k), dtype=self._torch.int32, device=logits.device)
+            ids = self._torch.empty((T, max(top_k, 0)), dtype=self._i32, device=self._dev)
+        elif tuple(ids.shape) != (T, top_k):
+            raise ValueError(f"expected a [{T}, {top_k}] output, got {tuple(ids.shape)}")
         if weights is None:
-            weights = self._torch.empty((T, top_k), dtype=self._torch.float32, device=logits.device)
-        r = ggq_router(SCORING[scoring], n_groups, top_groups, group_best, top_k, 1 if normalize else 0, scale,
-                       _ptr(bias, "float32"))
-        self._check(load().ggq_moe_route(self.handle, ctypes.byref(r), code, _ptr(logits), T, E, _ptr(ids, "int32"),
-                                         _ptr(weights, "float32"), self._stream(stream)))
+            weights = self._torch.empty((T, max(top_k, 0)), dtype=self._f32, device=self._dev)
+        elif tuple(weights.shape) != (T, top_k):
+            raise ValueError(f"expected a [{T}, {top_k}] output, got {tuple(weights.shape)}")
+        _ROUTER.pack_into(self._router_args, 0, SCORING[scoring], n_groups, top_groups, group_best, top_k,
+                          1 if normalize else 0, scale, self._vec(bias, self._f32))
+        st = _lib.ggq_moe_route(self.handle, self._router_at, code, self._vec(logits, logits.dtype), T, E,
+                                self._vec(ids, self._i32), self._vec(weights, self._f32), self._stream(stream))
+        if st:
+            self._check(st)
         return ids, weights
 
     def moe_weights(self, gate_fmt, gate, up_fmt, up, down_fmt, down):
