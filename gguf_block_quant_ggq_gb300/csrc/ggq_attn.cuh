@@ -25,7 +25,7 @@ struct AttnParams {
     int k_q4, v_q4;
     int max_q, max_len, window;
     float scale, cap;
-    int min_share;           // 16-token groups below which a CTA's share is not cut
+    int min_share;           // units (one or two 16-token groups) below which a CTA's share is not cut
     float* parts;            // partial results [2 * kAttnMaxCtas][attn_part_floats(D)]
     int* pieces;             // pieces of an item that have arrived [kAttnMaxCtas], zero between calls
     int* err;

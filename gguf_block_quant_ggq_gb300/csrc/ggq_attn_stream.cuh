@@ -7,28 +7,28 @@
 // rows (16) by the integer quants, which fp16 holds exactly; the scales are
 // applied to its fp32 results (scores) and to the probabilities (values), so the
 // packed bytes are unpacked but never dequantized.
-//   * Scores: two k16 steps per block of 32 channels.  The quants enter as fp16
-//     subnormals u 2^-24 (a byte permutation, no arithmetic); the accumulator
-//     starts at -off 2^-24 sum_c q_c, which takes the offset out again.
+//   * Scores: two k16 steps per block of 32 channels.  For 16-bit activations the
+//     quants enter as fp16 subnormals u 2^-24 (a byte permutation, no arithmetic);
+//     -off 2^-24 sum_c q_c, added to the block's result, takes the offset out again.
+//     For fp32 the sums would lose bits to the offset: signed integers.
 //   * Values: quants as exact signed fp16 integers; the other operand is p dv
 //     times a power of two that keeps it in fp16's normal range.
 //   * fp32 activations: 8 query rows; a 16-row operand holds the high and low
-//     fp16 halves of each (22 bits), whose results add up.  16-bit activations:
+//     fp16 parts of each (22 bits of the row's largest element), whose results add up.  16-bit activations:
 //     8 or 16 rows in one fp16 operand (16-bit queries are exact in it).
-//   * Softmax statistics are fp32.  Within a group of 16 keys the probabilities
-//     are relative to the group's maximum, and the value scales are lifted by a
-//     power of two that keeps p dv below fp16's range (the second half is lifted by
-//     2^12 more); a group's result is added to the fp32 totals with its factor
-//     2^(group maximum - reference).  No sum runs longer than a group on the tensor
-//     cores (which truncate), no probability is lost for being small (those of a group
-//     that lie more than 2^28 apart take a pass each), and the totals are rescaled only when the reference rises by 2^60.
+//   * Softmax statistics are fp32.  Within a unit the probabilities are relative to
+//     the unit's maximum and lifted by a power of two that keeps p dv below fp16's
+//     range (the second half by 2^12 more); a unit's result is added to the fp32
+//     totals with its factor 2^(unit's maximum - reference).  No sum runs longer than
+//     a unit on the tensor cores (which truncate), no probability is lost for being
+//     small (those of a unit that lie more than 2^28 apart take a pass each), and the totals are rescaled only when the reference rises by 2^60.
 //
 // Bound by HBM: every attended blob is read once (17 or 9 bytes per 16
-// channels).  Work is cut in equal shares of 16-token groups over all CTAs,
+// channels).  Work is cut in equal shares of units (two 16-token groups; one for
+// heads of 256 channels) over all CTAs,
 // whatever the lengths; a CTA walks its share item by item (an item is one
-// sequence, kv head and tile of rows), its four consumer warps take every
-// fourth group, and a producer warp keeps a ring of bulk copies in flight for
-// each of them, across items.  An item that several CTAs share is joined by the
+// sequence, kv head and tile of rows), its four warps take every
+// fourth unit, each keeping a ring of bulk copies in flight, across items.  An item that several CTAs share is joined by the
 // last of them from partial results in scratch, in the order of the pieces.
 #pragma once
 #include "ggq_attn.cuh"
@@ -37,8 +37,8 @@
 
 namespace ggq {
 
-constexpr int kAttnWarps = 4;                          // consumer warps
-constexpr int kAttnThreads = (kAttnWarps + 1) * 32;    // and the producer
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr float kAttnNone = -1e30f;                    // reference maximum of a row that has seen nothing
 
 // fp32 rows (high and low halves), 8 rows or 16 rows of 16-bit activations
@@ -47,9 +47,11 @@ enum AttnMode : int { A_SPLIT8 = 0, A_HALF8 = 1, A_HALF16 = 2 };
 template <bool K4, bool V4, int D, int MODE>
 struct AttnSmem {
     static constexpr int kRows = MODE == A_HALF16 ? 16 : 8;
+    static constexpr int kUnit = D == 256 ? 1 : 2;     // 16-token groups a warp takes at once
     static constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
-    static constexpr int kStage = kKB + kVB;
-    static constexpr int kStages = (kStage <= 2304 ? 8 : kStage <= 4352 ? 5 : 3);
+    static constexpr int kStage = kUnit * (kKB + kVB); // keys of the unit's groups, then their values
+    static constexpr int kFit = (D == 64 ? 52 : 72) * 1024 / (kAttnWarps * kStage);
+    static constexpr int kStages = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
     static constexpr int kRowPitch = D + 8;            // floats of a totals row (padding: conflict-free float2 stores)
     static constexpr int oRing = 0;
     static constexpr int oTot = kAttnWarps * kStages * kStage;
@@ -57,8 +59,9 @@ struct AttnSmem {
     static constexpr int oStat = oQ + D / 16 * 32 * 16;   // m, l [warps][rows]
     static constexpr int oScan = (oStat + 2 * kAttnWarps * kRows * 4 + 7) / 8 * 8;
     static constexpr int oBar = (oScan + (128 + 4) * 8 + 15) / 16 * 16;
-    static constexpr int kTotal = oBar + 2 * kAttnWarps * kStages * 8 + 16;
-    static constexpr int kCtas = 2 * kTotal <= kSmemLimit ? 2 : 1;  // per SM
+    static constexpr int kTotal = oBar + kAttnWarps * kStages * 8 + 16;
+    // CTAs an SM: 12 warps leave 168 registers a thread (64-channel heads), 8 warps 255
+    static constexpr int kCtas = D == 64 && 3 * (kTotal + 1024) <= 228 * 1024 ? 3 : 2 * (kTotal + 1024) <= 228 * 1024 ? 2 : 1;
 };
 
 // One sequence as the plan sees it.
@@ -98,32 +101,43 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b, int tile
     if (s.items == 0) s.ghi = s.glo = 0;
     return s;
 }
-__device__ __forceinline__ int64_t attn_cost(const AttnSeq& s) { return static_cast<int64_t>(s.ghi - s.glo) * s.items; }
+// Units of UNIT groups of an item, and of the sequence's items together.
+template <int UNIT>
+__device__ __forceinline__ int attn_units(const AttnSeq& s) { return UNIT == 1 ? s.ghi - s.glo : (s.ghi - s.glo + 1) >> 1; }
+template <int UNIT>
+__device__ __forceinline__ int64_t attn_cost(const AttnSeq& s) { return static_cast<int64_t>(attn_units<UNIT>(s)) * s.items; }
 
 // A CTA's share, item by item.
+template <int UNIT>
 struct AttnWalk {
     AttnSeq s;
-    int b, item, ga;
-    int64_t left;  // groups of the share that are not yet walked
-    __device__ __forceinline__ int gb() const {  // end of the current segment
-        const int64_t e = ga + left;
-        return e < s.ghi ? static_cast<int>(e) : s.ghi;
+    int b, item, ua;
+    int64_t left;  // units of the share that are not yet walked
+    __device__ __forceinline__ int ub() const {  // end of the current segment
+        const int64_t e = ua + left;
+        const int n = attn_units<UNIT>(s);
+        return e < n ? static_cast<int>(e) : n;
     }
     __device__ __forceinline__ void next(const AttnParams& p, int tile_rows) {
-        left -= gb() - ga;
+        left -= ub() - ua;
         if (left <= 0) return;
         if (++item == s.items) {
             item = 0;
-            do s = attn_seq(p, ++b, tile_rows, false); while (attn_cost(s) == 0);
+            do s = attn_seq(p, ++b, tile_rows, false); while (attn_cost<UNIT>(s) == 0);
         }
-        ga = s.glo;
+        ua = 0;
     }
 };
 
-__device__ __forceinline__ void attn_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+// D = A B, and D += A B
+__device__ __forceinline__ void attn_mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void attn_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -145,12 +159,36 @@ __device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
                               *reinterpret_cast<const __half2*>(&c));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
-// (d0, d1) = (a0, a1) * b + (c0, c1) in one instruction
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %6};\n\t"
+// Two fp32 operations in one instruction: a b + c, a + b, a b
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
         "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(d0), "=f"(d1)
-        : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 half2_f32(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 __device__ __forceinline__ float quad_sum(float v) {
@@ -182,35 +220,34 @@ __device__ __forceinline__ void attn_out4(const AttnParams& p, const AttnSeq& s,
 
 // Position of the share [lo, ...) in the list of all groups: the runs' exclusive
 // prefix sums in s_scan (128), each run `per` sequences.
-__device__ __forceinline__ AttnWalk attn_find(const AttnParams& p, const int64_t* s_scan, int per, int64_t lo, int64_t n,
+template <int UNIT>
+__device__ __forceinline__ AttnWalk<UNIT> attn_find(const AttnParams& p, const int64_t* s_scan, int per, int64_t lo, int64_t n,
                                               int tile_rows, int lane) {
     int run = -1;
 #pragma unroll
     for (int k = 0; k < 4; ++k) run += __popc(__ballot_sync(0xffffffffu, s_scan[lane + 32 * k] <= lo));
-    AttnWalk w;
+    AttnWalk<UNIT> w;
     w.left = n;
     w.b = run * per;
     int64_t rem = lo - s_scan[run];
     for (;;) {
         w.s = attn_seq(p, w.b, tile_rows, false);
-        const int64_t c = attn_cost(w.s);
+        const int64_t c = attn_cost<UNIT>(w.s);
         if (rem < c) break;
         rem -= c;
         ++w.b;
     }
-    const int ng = w.s.ghi - w.s.glo;
-    w.item = static_cast<int>(rem / ng);
-    w.ga = w.s.glo + static_cast<int>(rem - static_cast<int64_t>(w.item) * ng);
+    const int n_units = attn_units<UNIT>(w.s);
+    w.item = static_cast<int>(rem / n_units);
+    w.ua = static_cast<int>(rem - static_cast<int64_t>(w.item) * n_units);
     return w;
 }
-
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kAttnWarps * 32) : "memory"); }
 
 template <bool K4, bool V4, int D, int MODE>
 __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas)
     k_attn_stream(const __grid_constant__ AttnParams p) {
     using SM = AttnSmem<K4, V4, D, MODE>;
-    constexpr int kRows = SM::kRows, NB = D / 32, KS = D / 16, NT = D / 8, S = SM::kStages;
+    constexpr int kRows = SM::kRows, NB = D / 32, KS = D / 16, NT = D / 8, S = SM::kStages, UNIT = SM::kUnit;
     constexpr bool TWO = MODE == A_HALF16;  // operand rows 8..15 are query rows of their own
     constexpr int RS = TWO ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -221,17 +258,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     int64_t* const s_scan = reinterpret_cast<int64_t*>(smem + SM::oScan);
     int64_t* const s_wsum = s_scan + 128;
     uint64_t* const s_full = reinterpret_cast<uint64_t*>(smem + SM::oBar);
-    uint64_t* const s_empty = s_full + kAttnWarps * S;
-    volatile int* const s_abort = reinterpret_cast<volatile int*>(s_empty + kAttnWarps * S);
+    volatile int* const s_abort = reinterpret_cast<volatile int*>(s_full + kAttnWarps * S);
     volatile int* const s_last = s_abort + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_launch_dependents();
     if (tid == 0) {
-        for (int i = 0; i < kAttnWarps * S; ++i) {
-            mbar_init(s_full + i, 1);
-            mbar_init(s_empty + i, 1);
-        }
+        for (int i = 0; i < kAttnWarps * S; ++i) mbar_init(s_full + i, 1);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -240,27 +273,25 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     // ---- plan: prefix sums of the sequences' costs over 128 runs of `per` sequences
     const int nseq = static_cast<int>(p.n_seqs), per = (nseq + 127) >> 7;
     int64_t mine = 0, incl = 0;
-    if (tid < 128) {
-        for (int b = tid * per; b < min(nseq, (tid + 1) * per); ++b) {
-            const AttnSeq s = attn_seq(p, b, kRows, blockIdx.x == 0);
-            const int64_t cost = attn_cost(s);
-            mine += cost;
-            if (cost == 0 && b % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x)) {
-                for (int r = 0; r < min(s.rows, p.max_q) * p.H; ++r)  // nothing cached: zeros
-                    for (int d = 0; d < D; d += 4)
-                        attn_out4(p, s, (r % p.H) / p.G, (r / p.H) * p.G + (r % p.H) % p.G, d, make_float4(0.f, 0.f, 0.f, 0.f));
-            }
+    for (int b = tid * per; b < min(nseq, (tid + 1) * per); ++b) {
+        const AttnSeq s = attn_seq(p, b, kRows, blockIdx.x == 0);
+        const int64_t cost = attn_cost<UNIT>(s);
+        mine += cost;
+        if (cost == 0 && b % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x)) {
+            for (int r = 0; r < min(s.rows, p.max_q) * p.H; ++r)  // nothing cached: zeros
+                for (int d = 0; d < D; d += 4)
+                    attn_out4(p, s, (r % p.H) / p.G, (r / p.H) * p.G + (r % p.H) % p.G, d, make_float4(0.f, 0.f, 0.f, 0.f));
         }
-        incl = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-        }
-        if (lane == 31) s_wsum[warp] = incl;
     }
+    incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) s_wsum[warp] = incl;
     __syncthreads();
-    if (tid < 128) {
+    {
         int64_t base = 0;
         for (int w = 0; w < warp; ++w) base += s_wsum[w];
         s_scan[tid] = base + incl - mine;
@@ -272,67 +303,55 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     const int c = static_cast<int>(blockIdx.x);
     if (c >= C) return;
     const int64_t lo = N * c / C, hi = N * (c + 1) / C;
-    AttnWalk w = attn_find(p, s_scan, per, lo, hi - lo, kRows, lane);
+    AttnWalk<UNIT> w = attn_find<UNIT>(p, s_scan, per, lo, hi - lo, kRows, lane);
 
-    if (warp == kAttnWarps) {
-        // ---- producer: lane l fills consumer l's ring, a round of four groups at a time
-        const uint64_t policy = policy_evict_first();
-        const int gpp = p.page >> 4;
-        int n = 0, base = w.ga;
-        const auto page_of = [&](const AttnWalk& x, int g) {
-            int pg = 0;
-            if (lane < kAttnWarps && g < x.gb()) {
-                pg = p.table[x.b * p.table_stride + g / gpp];
-                if (pg < 0 || pg >= p.n_pages) {
-                    set_error(p.err, DEV_ERR_BAD_PLACE);
-                    pg = 0;
-                }
-            }
-            return pg;
-        };
-        int pg = page_of(w, base + lane);
-        bool ok = true;
-        while (w.left > 0) {
-            const int g = base + lane, gb = w.gb(), hk = w.item / (w.s.items / p.Hkv);
-            const bool mine_g = lane < kAttnWarps && g < gb;
-            const int pg_now = pg;
-            base += kAttnWarps;
-            if (base >= gb) {
-                w.next(p, kRows);
-                base = w.ga;
-            }
-            if (w.left > 0) pg = page_of(w, base + lane);  // on its way while this round waits for room
-            if (mine_g) {
-                const int slot = n % S, at = lane * S + slot;
-                if (n >= S) ok = !*s_abort && mbar_wait(s_empty + at, ((n / S) - 1) & 1);
-                if (ok) {
-                    const int64_t blob = (static_cast<int64_t>(pg_now) * p.Hkv + hk) * gpp + g % gpp;
-                    uint8_t* const dst = smem + SM::oRing + at * SM::kStage;
-                    mbar_arrive_expect_tx(s_full + at, SM::kStage);
-                    bulk_g2s(dst, p.k + blob * SM::kKB, SM::kKB, s_full + at, policy);
-                    bulk_g2s(dst + SM::kKB, p.v + blob * SM::kVB, SM::kVB, s_full + at, policy);
-                    ++n;
-                }
-            }
-            if (!__all_sync(0xffffffffu, ok)) break;
+    // ---- this warp's ring: it takes every fourth unit of the segments; a unit's copies start as
+    // soon as the warp has done with the place's last one, the page id having been read a turn before
+    const uint64_t policy = policy_evict_first();
+    const int gpp = p.page >> 4;
+    AttnWalk<UNIT> fw = w;  // the unit that is fetched next: fu of segment fw
+    int fu = fw.ua + warp, fpage = -1;
+    const auto seek = [&]() {
+        while (fw.left > 0 && fu >= fw.ub()) {
+            fw.next(p, kRows);
+            fu = fw.ua + warp;
         }
-        if (!__all_sync(0xffffffffu, ok)) {
-            *s_abort = 1;
-            set_error(p.err, DEV_ERR_TIMEOUT);
-            if (lane < kAttnWarps)  // let the copies in flight land before the CTA ends
-                for (int i = n > S ? n - S : 0; i < n; ++i) mbar_wait(s_full + lane * S + i % S, (i / S) & 1);
+        fpage = -1;
+        const int g = fw.s.glo + UNIT * fu + lane;
+        if (fw.left > 0 && lane < UNIT && g < fw.s.ghi) {
+            fpage = p.table[fw.b * p.table_stride + g / gpp];
+            if (fpage < 0 || fpage >= p.n_pages) {
+                set_error(p.err, DEV_ERR_BAD_PLACE);
+                fpage = 0;
+            }
         }
-        return;
-    }
+    };
+    const auto fetch = [&](int at) {
+        if (fw.left <= 0) return;
+        const int g = fw.s.glo + UNIT * fu + lane;
+        if (lane == 0) mbar_arrive_expect_tx(s_full + at, UNIT == 2 && g + 1 < fw.s.ghi ? SM::kStage : SM::kStage / UNIT);
+        __syncwarp();
+        if (fpage >= 0) {
+            const int hk = fw.item / (fw.s.items / p.Hkv);
+            const int64_t blob = (static_cast<int64_t>(fpage) * p.Hkv + hk) * gpp + g % gpp;
+            uint8_t* const dst = smem + SM::oRing + at * SM::kStage;
+            bulk_g2s(dst + lane * SM::kKB, p.k + blob * SM::kKB, SM::kKB, s_full + at, policy);
+            bulk_g2s(dst + UNIT * SM::kKB + lane * SM::kVB, p.v + blob * SM::kVB, SM::kVB, s_full + at, policy);
+        }
+        fu += kAttnWarps;
+        seek();
+    };
+    seek();
+    for (int i = 0; i < S; ++i) fetch(warp * S + i);
 
-    // ---- consumers
+    // ---- segments
     const int g8 = lane >> 2, t4 = lane & 3;
     int slot = 0;
     uint32_t phase = 0;
     while (w.left > 0) {
         const AttnSeq sq = w.s;
-        const int ga = w.ga, gb = w.gb(), item = w.item;
-        const int64_t at0 = hi - w.left;               // position of the segment's first group
+        const int ua = w.ua, ub = w.ub(), item = w.item;
+        const int64_t at0 = hi - w.left;               // position of the segment's first unit
         const int shown = min(sq.rows, p.max_q), tiles = sq.items / p.Hkv, hk = item / tiles;
         const int r0 = (item - hk * tiles) * kRows, r_end = min(shown * p.G, r0 + kRows);
         const int from = sq.len - sq.rows;
@@ -340,57 +359,66 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         // query rows -> operand registers (through shared memory, each warp a part of the k-steps)
         float xs[RS];                                   // score of an accumulator unit, times log2 e
         int pos[RS], first_key[RS];
-        float init[RS][NB], slope[RS];
+        float offset[RS][NB], slope[RS];
         {
-            uint32_t frag[KS][4];
+            float up[RS];
+            int row[RS];
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs) {
-                const int r = min(r0 + g8 + 8 * rs, r_end - 1);  // rows past the end repeat the last one
-                float4 x[KS];
+                row[rs] = min(r0 + g8 + 8 * rs, r_end - 1);  // rows past the end repeat the last one
                 float amax = 0.0f;
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
-                    x[j] = attn_q4(p, sq, hk, r, 16 * j + 4 * t4);
-                    amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x[j].x), fabsf(x[j].y))), fmaxf(fabsf(x[j].z), fabsf(x[j].w)));
+                    const float4 x = attn_q4(p, sq, hk, row[rs], 16 * j + 4 * t4);
+                    amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
                 }
                 amax = quad_max(amax);
                 const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-                const int sh = ex == 128 ? 0 : min(13 - ex, 100);  // largest element in [2^13, 2^14)
-                const float up = pow2f(sh);
-                xs[rs] = p.scale * scalbnf(1.0f, 24 - sh);
-                pos[rs] = from + r / p.G;
+                // largest element in [2^13, 2^14); fp32 rows: in [2^10, 2^11), the high halves being integers,
+                // whose products and sums of a block the matrix unit holds exactly
+                const int sh = ex == 128 ? 0 : min((MODE == A_SPLIT8 ? 10 : 13) - ex, 100);
+                up[rs] = copysignf(pow2f(sh), p.scale);
+                xs[rs] = fabsf(p.scale) * scalbnf(1.0f, (MODE == A_SPLIT8 ? 0 : 24) - sh);
+                pos[rs] = from + row[rs] / p.G;
                 first_key[rs] = p.window > 0 ? pos[rs] - p.window + 1 : 0;
-                slope[rs] = p.slopes ? p.slopes[hk * p.G + r % p.G] : 0.0f;
+                slope[rs] = p.slopes ? p.slopes[hk * p.G + row[rs] % p.G] : 0.0f;
+            }
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float sum = 0.0f;
+            for (int b = 0; b < NB; ++b) {
+                float sum[RS];
 #pragma unroll
-                    for (int j = 2 * b; j < 2 * b + 2; ++j) {
-                        const float v[4] = {x[j].x * up, x[j].y * up, x[j].z * up, x[j].w * up};
+                for (int rs = 0; rs < RS; ++rs) sum[rs] = 0.0f;
+#pragma unroll
+                for (int j = 2 * b; j < 2 * b + 2; ++j) {
+                    uint32_t frag[4];
+#pragma unroll
+                    for (int rs = 0; rs < RS; ++rs) {
+                        const float4 x = attn_q4(p, sq, hk, row[rs], 16 * j + 4 * t4);
+                        const float v[4] = {x.x * up[rs], x.y * up[rs], x.z * up[rs], x.w * up[rs]};
                         float h[4], l[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            h[i] = __half2float(__float2half_rn(v[i]));
+                            h[i] = MODE == A_SPLIT8 ? rintf(v[i]) : __half2float(__float2half_rn(v[i]));
                             l[i] = __half2float(__float2half_rn(v[i] - h[i]));
-                            sum += MODE == A_SPLIT8 ? h[i] + l[i] : h[i];
+                            sum[rs] += h[i];
                         }
                         // 4-bit quants of channels 2, 3 of four enter 16 times too large
-                        const float k16 = K4 ? 0.0625f : 1.0f;
-                        frag[j][rs] = pack_h2(h[0], h[1]);
-                        frag[j][2 + rs] = pack_h2(h[2] * k16, h[3] * k16);
+                        const float k16 = K4 && MODE != A_SPLIT8 ? 0.0625f : 1.0f;
+                        frag[rs] = pack_h2(h[0], h[1]);
+                        frag[2 + rs] = pack_h2(h[2] * k16, h[3] * k16);
                         if (!TWO) {
-                            frag[j][1] = MODE == A_SPLIT8 ? pack_h2(l[0], l[1]) : 0u;
-                            frag[j][3] = MODE == A_SPLIT8 ? pack_h2(l[2] * k16, l[3] * k16) : 0u;
+                            frag[1] = MODE == A_SPLIT8 ? pack_h2(l[0], l[1]) : 0u;
+                            frag[3] = MODE == A_SPLIT8 ? pack_h2(l[2] * k16, l[3] * k16) : 0u;
                         }
                     }
-                    init[rs][b] = quad_sum(sum) * (K4 ? -8.0f : -128.0f) * 5.9604644775390625e-8f;  // 2^-24
+                    if ((j & (kAttnWarps - 1)) == warp) s_q[j * 32 + lane] = make_uint4(frag[0], frag[1], frag[2], frag[3]);
                 }
-            }
 #pragma unroll
-            for (int j = 0; j < KS; ++j)
-                if ((j & (kAttnWarps - 1)) == warp) s_q[j * 32 + lane] = make_uint4(frag[j][0], frag[j][1], frag[j][2], frag[j][3]);
+                for (int rs = 0; rs < RS; ++rs)
+                    offset[rs][b] = quad_sum(sum[rs]) * (K4 ? -8.0f : -128.0f) * 5.9604644775390625e-8f;  // 2^-24
+            }
         }
-        consumer_sync();
+        __syncthreads();
         const bool plain = p.cap <= 0.0f && !p.slopes;
         constexpr float kLog2e = 1.44269504088896340736f;
         if (plain)
@@ -400,17 +428,21 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         const int last_first = p.window > 0 ? from + (r_end - 1) / p.G - p.window + 1 : 0;
         const int whole_begin = last_first > 0 ? (last_first + 15) >> 4 : 0;
 
-        float m[RS], l[RS], tot[RS][NT][2];
+        float m[RS], l[RS];
+        float2 tot[RS][NT];
 #pragma unroll
         for (int rs = 0; rs < RS; ++rs) {
             m[rs] = kAttnNone, l[rs] = 0.0f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) tot[rs][n][0] = tot[rs][n][1] = 0.0f;
+            for (int n = 0; n < NT; ++n) tot[rs][n] = both(0.0f);
         }
-        float vs = 0x1p40f;  // power of two on the value scales
+        // power of two that lifts the probabilities: p * lift * (largest value scale) stays below 32000;
+        // fp16 probabilities (16-bit activations) must not pass 2^15 themselves
+        constexpr float kMaxLift = MODE == A_SPLIT8 ? 40.0f : 15.0f;
+        float lift = kMaxLift, dlimit = 32000.0f * pow2f(-static_cast<int>(kMaxLift));
 
-        for (int g = ga + warp; g < gb; g += kAttnWarps) {
-            const int at = warp * S + slot;
+        for (int u = ua + warp; u < ub; u += kAttnWarps) {
+            const int at = warp * S + slot, g = sq.glo + UNIT * u;
             bool ok = !*s_abort && mbar_wait(s_full + at, phase);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
@@ -419,272 +451,304 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                 break;
             }
             const uint8_t* const kb = smem + SM::oRing + at * SM::kStage;
-            const uint8_t* const vb = kb + SM::kKB;
+            const uint8_t* const vb = kb + UNIT * SM::kKB;
 
-            // scores of two octets of keys
-            float sc[2][4];
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sc[o][i] = 0.0f;
+            // ---- scores of two octets of keys a group: x[rs][2 * (2 group + octet)] and + 1, keys 2 t and 2 t + 1
             constexpr int KW = K4 ? NB : KS;  // words of an octet
-            uint32_t kw[2 * KW];
+            float2 sc[RS][2 * UNIT];
+            uint32_t kw[UNIT][2 * KW], kd[UNIT][2][2][NB / 2];
 #pragma unroll
-            for (int v = 0; v < KW / 2; ++v) {
-                const uint4 u = *reinterpret_cast<const uint4*>(kb + (v * 32 + lane) * 16);
-                kw[4 * v] = u.x, kw[4 * v + 1] = u.y, kw[4 * v + 2] = u.z, kw[4 * v + 3] = u.w;
-            }
-            uint32_t kd[2][2][NB / 2];  // scales of keys 8 o + 2 t + e
+            for (int c = 0; c < UNIT; ++c) {
+                const uint8_t* const blob = kb + c * SM::kKB;
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const uint32_t* const d = reinterpret_cast<const uint32_t*>(
-                    kb + kv_quant_bytes(K4, D) + (8 * o + 2 * t4) * NB * 2);
+                for (int v = 0; v < KW / 2; ++v) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(blob + (v * 32 + lane) * 16);
+                    kw[c][4 * v] = q.x, kw[c][4 * v + 1] = q.y, kw[c][4 * v + 2] = q.z, kw[c][4 * v + 3] = q.w;
+                }
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int o = 0; o < 2; ++o) {
+                    const uint32_t* const d = reinterpret_cast<const uint32_t*>(
+                        blob + kv_quant_bytes(K4, D) + (8 * o + 2 * t4) * NB * 2);
 #pragma unroll
-                    for (int i = 0; i < NB / 2; ++i) kd[o][e][i] = d[e * (NB / 2) + i];
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < NB / 2; ++i) kd[c][o][e][i] = d[e * (NB / 2) + i];
+                }
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 const uint4 qa = s_q[(2 * b) * 32 + lane], qb = s_q[(2 * b + 1) * 32 + lane];
                 const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w}, fb[4] = {qb.x, qb.y, qb.z, qb.w};
 #pragma unroll
+                for (int c = 0; c < UNIT; ++c)
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        float cc[4];
+                        if constexpr (K4 && MODE == A_SPLIT8) {
+                            const uint32_t q = kw[c][o * NB + b], y = q >> 8;
+                            attn_mma0(cc, fa, h2_sub((q & 0x000F000Fu) | 0x64006400u, 0x64086408u),
+                                      h2_fma((q & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u));
+                            attn_mma(cc, fb, h2_sub((y & 0x000F000Fu) | 0x64006400u, 0x64086408u),
+                                     h2_fma((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u));
+                        } else if constexpr (MODE == A_SPLIT8) {
+                            const uint32_t q = kw[c][o * KS + 2 * b], y = kw[c][o * KS + 2 * b + 1];
+                            attn_mma0(cc, fa, h2_sub(prmt(q, 0x64646464u, 0x4140u), 0x64806480u),
+                                      h2_sub(prmt(q, 0x64646464u, 0x4342u), 0x64806480u));
+                            attn_mma(cc, fb, h2_sub(prmt(y, 0x64646464u, 0x4140u), 0x64806480u),
+                                     h2_sub(prmt(y, 0x64646464u, 0x4342u), 0x64806480u));
+                        } else if constexpr (K4) {
+                            const uint32_t q = kw[c][o * NB + b], y = q >> 8;
+                            attn_mma0(cc, fa, q & 0x000F000Fu, q & 0x00F000F0u);
+                            attn_mma(cc, fb, y & 0x000F000Fu, y & 0x00F000F0u);
+                        } else {
+                            const uint32_t q = kw[c][o * KS + 2 * b], y = kw[c][o * KS + 2 * b + 1];
+                            attn_mma0(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u));
+                            attn_mma(cc, fb, prmt(y, 0u, 0x4140u), prmt(y, 0u, 0x4342u));
+                        }
+                        const float2 d = half2_f32(prmt(kd[c][o][0][b >> 1], kd[c][o][1][b >> 1], (b & 1) ? 0x7632u : 0x5410u));
+                        const float2 r = add2(make_float2(cc[0], cc[1]),
+                                              MODE == A_SPLIT8 ? make_float2(cc[2], cc[3]) : both(offset[0][b]));
+                        sc[0][2 * c + o] = b ? fma2(d, r, sc[0][2 * c + o]) : mul2(d, r);
+                        if constexpr (TWO) {
+                            const float2 r2 = add2(make_float2(cc[2], cc[3]), both(offset[RS - 1][b]));
+                            sc[RS - 1][2 * c + o] = b ? fma2(d, r2, sc[RS - 1][2 * c + o]) : mul2(d, r2);
+                        }
+                    }
+            }
+            uint32_t vd[UNIT][4][NB / 2];  // value scales of keys 8 o + 2 t + e, index 2 o + e
+#pragma unroll
+            for (int c = 0; c < UNIT; ++c)
+#pragma unroll
                 for (int o = 0; o < 2; ++o) {
-                    float cc[4] = {init[0][b], init[0][b], TWO ? init[RS - 1][b] : 0.0f, TWO ? init[RS - 1][b] : 0.0f};
-                    if constexpr (K4) {
-                        const uint32_t u = kw[o * NB + b], y = u >> 8;
-                        attn_mma(cc, fa, u & 0x000F000Fu, u & 0x00F000F0u);
-                        attn_mma(cc, fb, y & 0x000F000Fu, y & 0x00F000F0u);
-                    } else {
-                        const uint32_t u = kw[o * KS + 2 * b], y = kw[o * KS + 2 * b + 1];
-                        attn_mma(cc, fa, prmt(u, 0u, 0x4140u), prmt(u, 0u, 0x4342u));
-                        attn_mma(cc, fb, prmt(y, 0u, 0x4140u), prmt(y, 0u, 0x4342u));
-                    }
-                    const float d0 = (b & 1) ? half_hi(kd[o][0][b >> 1]) : half_lo(kd[o][0][b >> 1]);
-                    const float d1 = (b & 1) ? half_hi(kd[o][1][b >> 1]) : half_lo(kd[o][1][b >> 1]);
-                    if constexpr (MODE == A_SPLIT8) cc[0] += cc[2], cc[1] += cc[3];
-                    sc[o][0] = fmaf(d0, cc[0], sc[o][0]);
-                    sc[o][1] = fmaf(d1, cc[1], sc[o][1]);
-                    if constexpr (TWO) {
-                        sc[o][2] = fmaf(d0, cc[2], sc[o][2]);
-                        sc[o][3] = fmaf(d1, cc[3], sc[o][3]);
-                    }
+                    const uint32_t* const d = reinterpret_cast<const uint32_t*>(
+                        vb + c * SM::kVB + kv_quant_bytes(V4, D) + (8 * o + 2 * t4) * NB * 2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < NB / 2; ++i) vd[c][2 * o + e][i] = d[e * (NB / 2) + i];
                 }
-            }
-            uint32_t vd[2][2][NB / 2];
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                const uint32_t* const d = reinterpret_cast<const uint32_t*>(
-                    vb + kv_quant_bytes(V4, D) + (8 * o + 2 * t4) * NB * 2);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int i = 0; i < NB / 2; ++i) vd[o][e][i] = d[e * (NB / 2) + i];
-            }
 
-            // logits in units of log2, masks
-            float x[RS][4];
+            // ---- logits in units of log2, masks
+            float x[RS][4 * UNIT];
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[rs][i] = sc[i >> 1][2 * rs + (i & 1)] * xs[rs];
+                for (int i = 0; i < 4 * UNIT; ++i) x[rs][i] = ((i & 1) ? sc[rs][i >> 1].y : sc[rs][i >> 1].x) * xs[rs];
             if (!plain) {
 #pragma unroll
                 for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 4 * UNIT; ++i) {
                         const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
                         float y = x[rs][i];
                         if (p.cap > 0.0f) y = p.cap * tanhf(__fdividef(y, p.cap));
                         x[rs][i] = fmaf(slope[rs], static_cast<float>(key - pos[rs]), y) * kLog2e;
                     }
             }
-            if (g < whole_begin || g >= whole_end) {
+            if (g < whole_begin || g + UNIT > whole_end) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4 * UNIT; ++i) {
                     const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
 #pragma unroll
                     for (int rs = 0; rs < RS; ++rs)
                         if (key > pos[rs] || key < first_key[rs]) x[rs][i] = -INFINITY;
                     if (key >= sq.len)  // never written: whatever the place holds
 #pragma unroll
-                        for (int k = 0; k < NB / 2; ++k) vd[i >> 1][i & 1][k] = 0u;
+                        for (int k = 0; k < NB / 2; ++k) vd[i >> 2][i & 3][k] = 0u;
                 }
             }
 
-            // the group's maximum is its probabilities' reference
-            float pr[RS][4], f[RS];
+            // ---- the unit's maximum is its probabilities' reference
+            float top[RS];
             bool raise = false;
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs) {
-                f[rs] = quad_max(fmaxf(fmaxf(x[rs][0], x[rs][1]), fmaxf(x[rs][2], x[rs][3])));
-                raise |= f[rs] > m[rs] + 60.0f ||
-                         fminf(fminf(x[rs][0], x[rs][1]), fminf(x[rs][2], x[rs][3])) < f[rs] - 28.0f;
+                float hi_x = x[rs][0], lo_x = x[rs][0];
+#pragma unroll
+                for (int i = 1; i < 4 * UNIT; ++i) hi_x = fmaxf(hi_x, x[rs][i]), lo_x = fminf(lo_x, x[rs][i]);
+                top[rs] = quad_max(hi_x);
+                raise |= top[rs] > m[rs] + 60.0f || lo_x < top[rs] - 28.0f;
             }
             uint32_t dm = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int k = 0; k < NB / 2; ++k) dm = __vmaxu2(dm, vd[i >> 1][i & 1][k] & 0x7FFF7FFFu);
-            raise |= !(fmaxf(half_lo(dm), half_hi(dm)) * vs <= 46341.0f) || (dm & 0x7FFFu) >= 0x7C00u || (dm >> 16) >= 0x7C00u;
-            bool dirty = false;  // a value scale is not finite
-            bool more = false;   // some probabilities are too small for fp16 beside the group's largest
-            if (__any_sync(0xffffffffu, raise)) {
-                float dfin = 0.0f;
+            for (int c = 0; c < UNIT; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int k = 0; k < NB / 2; ++k) {
-                        const uint32_t u = vd[i >> 1][i & 1][k] & 0x7FFF7FFFu;
-                        if ((u & 0xFFFFu) < 0x7C00u) dfin = fmaxf(dfin, half_lo(u)); else dirty = true;
-                        if ((u >> 16) < 0x7C00u) dfin = fmaxf(dfin, half_hi(u)); else dirty = true;
-                    }
-                dirty = __any_sync(0xffffffffu, dirty);
+                    for (int k = 0; k < NB / 2; ++k) dm = __vmaxu2(dm, V4 ? vd[c][i][k] & 0x7FFF7FFFu : vd[c][i][k]);
+            raise |= !(half_lo(dm) <= dlimit && half_hi(dm) <= dlimit);  // larger, or not a number
+            bool more = false;   // some probabilities are too small for fp16 beside the unit's largest
+            if (__any_sync(0xffffffffu, raise)) {
+                float dfin = 0.0f;
+                uint32_t spoilt[RS] = {};  // blocks of 32 channels in which a row sees a scale that is not finite
+#pragma unroll
+                for (int c = 0; c < UNIT; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const uint32_t d = (vd[c][i][b >> 1] >> (16 * (b & 1))) & 0x7FFFu;
+                            if (d < 0x7C00u) {
+                                dfin = fmaxf(dfin, half_lo(d));
+                            } else {
+                                vd[c][i][b >> 1] &= (b & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+                                for (int rs = 0; rs < RS; ++rs)
+                                    if (x[rs][4 * c + i] != -INFINITY) spoilt[rs] |= 1u << b;
+                            }
+                        }
                 dfin = warp_max(dfin);
-                if (dfin * vs > 46341.0f)  // the largest to [2^13, 2^14)
-                    vs = pow2f(13 - (static_cast<int>(__float_as_uint(dfin) >> 23) - 127));
+                if (dfin > dlimit) {  // the largest times the lift to [2^13, 2^14)
+                    const int e = 13 - (static_cast<int>(__float_as_uint(dfin) >> 23) - 127);
+                    lift = fminf(static_cast<float>(e), kMaxLift);
+                    dlimit = 32000.0f * pow2f(-static_cast<int>(lift));
+                }
 #pragma unroll
-                for (int rs = 0; rs < RS; ++rs)
-                    if (f[rs] > m[rs] + 60.0f) {
-                        const float a = ex2(m[rs] - f[rs]);
-                        m[rs] = f[rs];
-                        l[rs] *= a;
+                for (int rs = 0; rs < RS; ++rs) {
+                    spoilt[rs] |= __shfl_xor_sync(0xffffffffu, spoilt[rs], 1);
+                    spoilt[rs] |= __shfl_xor_sync(0xffffffffu, spoilt[rs], 2);
+                    const bool up = top[rs] > m[rs] + 60.0f;
+                    const float a = up ? ex2(m[rs] - top[rs]) : 1.0f;
+                    if (up) m[rs] = top[rs];
+                    l[rs] *= a;
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) tot[rs][n][0] *= a, tot[rs][n][1] *= a;
-                    }
+                    for (int n = 0; n < NT; ++n) tot[rs][n] = mul2(tot[rs][n], both(((spoilt[rs] >> (n >> 2)) & 1u) ? NAN : a));
 #pragma unroll
-                for (int rs = 0; rs < RS; ++rs)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) more |= x[rs][i] < f[rs] - 28.0f && x[rs][i] > m[rs] - 126.0f;
+                    for (int i = 0; i < 4 * UNIT; ++i) more |= x[rs][i] < top[rs] - 28.0f && x[rs][i] > m[rs] - 126.0f;
+                }
                 more = __any_sync(0xffffffffu, more);
             }
             for (;;) {  // once, but for probabilities more than 2^28 apart: those below wait for a pass of their own
-                float rest[RS];
+                float rest[RS], f[RS], pr[RS][4 * UNIT];
 #pragma unroll
                 for (int rs = 0; rs < RS; ++rs) {
-                    const float top = fmaxf(f[rs], kAttnNone);  // a group that the row does not see: all probabilities 0
-                    float sum = 0.0f;
+                    const float ref = fmaxf(top[rs], kAttnNone);  // a unit that the row does not see: all probabilities 0
+                    const float sub = ref - lift;
                     rest[rs] = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        pr[rs][i] = ex2(x[rs][i] - top);
+                    for (int i = 0; i < 4 * UNIT; ++i) {
+                        pr[rs][i] = ex2(x[rs][i] - sub);
                         if (more) {
-                            if (x[rs][i] < top - 28.0f) {
+                            if (x[rs][i] < ref - 28.0f) {
                                 pr[rs][i] = 0.0f;
                                 rest[rs] = fmaxf(rest[rs], x[rs][i]);
                             } else {
                                 x[rs][i] = -INFINITY;
                             }
                         }
-                        sum += pr[rs][i];
-                        pr[rs][i] *= vs;
                     }
-                    const float w = ex2(top - m[rs]);
-                    l[rs] = fmaf(sum, w, l[rs]);
-                    f[rs] = w * (1.0f / vs);
+                    float2 sum = make_float2(pr[rs][0], pr[rs][1]);
+#pragma unroll
+                    for (int i = 2; i < 4 * UNIT; i += 2) sum = add2(sum, make_float2(pr[rs][i], pr[rs][i + 1]));
+                    f[rs] = ex2(sub - m[rs]);
+                    l[rs] = fmaf(sum.x + sum.y, f[rs], l[rs]);
                 }
+                uint32_t ph[RS][2 * UNIT];  // 16-bit activations: the probabilities in fp16
+#pragma unroll
+                for (int rs = 0; rs < RS; ++rs)
+#pragma unroll
+                    for (int i = 0; i < 2 * UNIT; ++i) ph[rs][i] = MODE == A_SPLIT8 ? 0u : pack_h2(pr[rs][2 * i], pr[rs][2 * i + 1]);
 
-                // values, block by block of 32 channels
+                // ---- values, block by block of 32 channels
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
-                    uint32_t a[4];
-                    float dv[4], acc[4][4];
+                    float acc[4][4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[k][i] = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dv[i] = (b & 1) ? half_hi(vd[i >> 1][i & 1][b >> 1]) : half_lo(vd[i >> 1][i & 1][b >> 1]);
-                    float pd[RS][4];
-#pragma unroll
-                    for (int rs = 0; rs < RS; ++rs)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            pd[rs][i] = pr[rs][i] * dv[i];
-                            if (dirty && pr[rs][i] == 0.0f) pd[rs][i] = 0.0f;  // an infinite scale that the row does not see
-                        }
-                    if constexpr (MODE == A_SPLIT8) {
+                    for (int c = 0; c < UNIT; ++c) {
+                        uint32_t a[4];
 #pragma unroll
                         for (int o = 0; o < 2; ++o) {
-                            // rounded to fp16, and 2^12 times what that leaves
-                            const uint32_t h = pack_h2(pd[0][2 * o], pd[0][2 * o + 1]);
-                            a[2 * o] = h;
-                            a[2 * o + 1] = pack_h2((pd[0][2 * o] - half_lo(h)) * 4096.0f, (pd[0][2 * o + 1] - half_hi(h)) * 4096.0f);
+                            const uint32_t d2 = prmt(vd[c][2 * o][b >> 1], vd[c][2 * o + 1][b >> 1], (b & 1) ? 0x7632u : 0x5410u);
+                            if constexpr (MODE == A_SPLIT8) {
+                                // rounded to fp16, and 2^12 times what that leaves
+                                const float2 v = mul2(make_float2(pr[0][4 * c + 2 * o], pr[0][4 * c + 2 * o + 1]), half2_f32(d2));
+                                const uint32_t h = pack_h2(v.x, v.y);
+                                const float2 hv = half2_f32(h);
+                                const float2 r = mul2(add2(v, make_float2(-hv.x, -hv.y)), both(4096.0f));
+                                a[2 * o] = h;
+                                a[2 * o + 1] = pack_h2(r.x, r.y);
+                            } else {
+                                a[2 * o] = h2_mul(ph[0][2 * c + o], d2);
+                                a[2 * o + 1] = TWO ? h2_mul(ph[RS - 1][2 * c + o], d2) : 0u;
+                            }
                         }
-                    } else {
+                        const uint8_t* const blob = vb + c * SM::kVB;
+                        if constexpr (V4) {
+                            const uint2 u2 = *reinterpret_cast<const uint2*>(blob + ((b >> 1) * 32 + lane) * 16 + (b & 1) * 8);
+                            const uint32_t uw[2] = {u2.x, u2.y};
 #pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            a[2 * o] = pack_h2(pd[0][2 * o], pd[0][2 * o + 1]);
-                            a[2 * o + 1] = TWO ? pack_h2(pd[RS - 1][2 * o], pd[RS - 1][2 * o + 1]) : 0u;
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t q = uw[k], y = q >> 8;
+                                // 1024 + q - 1032, and (1024 + 16 q) / 16 - 72
+                                const uint32_t e0 = h2_sub((q & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+                                const uint32_t e1 = h2_sub((y & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+                                const uint32_t o0 = h2_fma((q & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+                                const uint32_t o1 = h2_fma((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+                                if (c == 0) attn_mma0(acc[2 * k], a, e0, e1), attn_mma0(acc[2 * k + 1], a, o0, o1);
+                                else attn_mma(acc[2 * k], a, e0, e1), attn_mma(acc[2 * k + 1], a, o0, o1);
+                            }
+                        } else {
+                            const uint4 u4 = *reinterpret_cast<const uint4*>(blob + (b * 32 + lane) * 16);
+                            const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {  // 1024 + (q + 128) - 1152
+                                const uint32_t e0 = h2_sub(prmt(uw[k], 0x64646464u, 0x4140u), 0x64806480u);
+                                const uint32_t e1 = h2_sub(prmt(uw[k], 0x64646464u, 0x4342u), 0x64806480u);
+                                if (c == 0) attn_mma0(acc[k], a, e0, e1);
+                                else attn_mma(acc[k], a, e0, e1);
+                            }
                         }
-                    }
-                    if constexpr (V4) {
-                        const uint2 u2 = *reinterpret_cast<const uint2*>(vb + ((b >> 1) * 32 + lane) * 16 + (b & 1) * 8);
-                        const uint32_t uw[2] = {u2.x, u2.y};
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t u = uw[k], y = u >> 8;
-                            // 1024 + q - 1032, and (1024 + 16 q) / 16 - 72
-                            attn_mma(acc[2 * k], a, h2_sub((u & 0x000F000Fu) | 0x64006400u, 0x64086408u),
-                                     h2_sub((y & 0x000F000Fu) | 0x64006400u, 0x64086408u));
-                            attn_mma(acc[2 * k + 1], a, h2_fma((u & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u),
-                                     h2_fma((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u));
-                        }
-                    } else {
-                        const uint4 u4 = *reinterpret_cast<const uint4*>(vb + (b * 32 + lane) * 16);
-                        const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 1024 + (q + 128) - 1152
-                            attn_mma(acc[k], a, h2_sub(prmt(uw[k], 0x64646464u, 0x4140u), 0x64806480u),
-                                     h2_sub(prmt(uw[k], 0x64646464u, 0x4342u), 0x64806480u));
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float(&o)[2] = tot[0][4 * b + k];
-                        if constexpr (MODE == A_SPLIT8) fma2(acc[k][0], acc[k][1], acc[k][2], acc[k][3], 0x1p-12f, acc[k][0], acc[k][1]);
-                        fma2(o[0], o[1], acc[k][0], acc[k][1], f[0], o[0], o[1]);
-                        if constexpr (TWO) {
-                            float(&o2)[2] = tot[RS - 1][4 * b + k];
-                            fma2(o2[0], o2[1], acc[k][2], acc[k][3], f[RS - 1], o2[0], o2[1]);
-                        }
+                        float2 r = make_float2(acc[k][0], acc[k][1]);
+                        if constexpr (MODE == A_SPLIT8) r = fma2(make_float2(acc[k][2], acc[k][3]), both(0x1p-12f), r);
+                        tot[0][4 * b + k] = fma2(r, both(f[0]), tot[0][4 * b + k]);
+                        if constexpr (TWO)
+                            tot[RS - 1][4 * b + k] = fma2(make_float2(acc[k][2], acc[k][3]), both(f[RS - 1]), tot[RS - 1][4 * b + k]);
                     }
                 }
                 if (!more) break;
                 more = false;
 #pragma unroll
                 for (int rs = 0; rs < RS; ++rs) {
-                    f[rs] = quad_max(rest[rs]);
-                    more |= f[rs] > m[rs] - 126.0f;
+                    top[rs] = quad_max(rest[rs]);
+                    more |= top[rs] > m[rs] - 126.0f;
                 }
                 more = __any_sync(0xffffffffu, more);
                 if (!more) break;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(s_empty + at);
+            fetch(at);
             if (++slot == S) slot = 0, phase ^= 1u;
         }
+        // the reference moves to the sum's power of two (it may lag the largest score by 2^60)
         float* const s_mine = s_tot + warp * kRows * SM::kRowPitch;
 #pragma unroll
-        for (int rs = 0; rs < RS; ++rs)
+        for (int rs = 0; rs < RS; ++rs) {
+            float sum = quad_sum(l[rs]);
+            const int e = static_cast<int>(__float_as_uint(sum) >> 23) - 127;
+            float a = 1.0f;
+            if (sum > 0.0f && e < 127) {
+                a = pow2f(-e);
+                sum *= a;
+                m[rs] += static_cast<float>(e);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<float2*>(s_mine + (g8 + 8 * rs) * SM::kRowPitch + 8 * n + 2 * t4) =
-                    make_float2(tot[rs][n][0], tot[rs][n][1]);
-#pragma unroll
-        for (int rs = 0; rs < RS; ++rs) {
-            const float sum = quad_sum(l[rs]);
+                *reinterpret_cast<float2*>(s_mine + (g8 + 8 * rs) * SM::kRowPitch + 8 * n + 2 * t4) = mul2(tot[rs][n], both(a));
             if (t4 == 0) {
                 s_m[warp * kRows + g8 + 8 * rs] = m[rs];
                 s_l[warp * kRows + g8 + 8 * rs] = sum;
             }
         }
-        consumer_sync();
+        __syncthreads();
 
         // ---- the segment's result: the four warps' parts
-        const bool whole = ga == sq.glo && gb == sq.ghi;
+        const int n_units = attn_units<UNIT>(sq);
+        const bool whole = ua == 0 && ub == n_units;
         float* const part = p.parts + (static_cast<int64_t>(c) * 2 + (at0 == lo ? 0 : 1)) * attn_part_floats(D);
-        for (int i = tid; i < kRows * D / 4; i += kAttnWarps * 32) {
+        for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
             const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
             if (r0 + row >= r_end) break;
             float M = kAttnNone, L = 0.0f;
@@ -708,21 +772,21 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         }
         if (!whole) {
             // pieces of this item: the CTAs c0 .. c1 whose shares it crosses
-            const int64_t p0 = at0 - (ga - sq.glo), p1 = p0 + (sq.ghi - sq.glo);  // the item's positions [p0, p1)
+            const int64_t p0 = at0 - ua, p1 = p0 + n_units;  // the item's positions [p0, p1)
             const int c0 = static_cast<int>(((p0 + 1) * C - 1) / N), c1 = static_cast<int>((p1 * C - 1) / N);
             __threadfence();
-            consumer_sync();
+            __syncthreads();
             if (tid == 0) {
                 const int before = atomicAdd(p.pieces + c0, 1);
                 *s_last = before == c1 - c0;
                 if (before == c1 - c0) p.pieces[c0] = 0;
                 __threadfence();
             }
-            consumer_sync();
+            __syncthreads();
             if (*s_last) {
                 const int64_t size = attn_part_floats(D);
                 const int slot0 = N * c0 / C == p0 ? 0 : 1;  // the first piece; every other piece begins its CTA's share
-                for (int i = tid; i < kRows * D / 4; i += kAttnWarps * 32) {
+                for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
                     const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
                     if (r0 + row >= r_end) break;
                     float M = kAttnNone, L = 0.0f;
@@ -742,7 +806,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                 }
             }
         }
-        consumer_sync();  // the totals and the query operand are free again
+        __syncthreads();  // the totals and the query operand are free again
         w.next(p, kRows);
     }
 }
@@ -761,8 +825,8 @@ cudaError_t launch_attn_stream(const AttnParams& p, int nsm, cudaStream_t s) {
         if (dev < kMaxDevices) set[dev] = true;
     }
     const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.G + SM::kRows - 1) / SM::kRows;
-    const int64_t groups = p.n_seqs * p.Hkv * tiles * ((static_cast<int64_t>(p.max_len) + 15) / 16);
-    int64_t grid = (groups + p.min_share - 1) / p.min_share;
+    const int64_t units = p.n_seqs * p.Hkv * tiles * ((static_cast<int64_t>(p.max_len) + 16 * SM::kUnit - 1) / (16 * SM::kUnit) + 1);
+    int64_t grid = (units + p.min_share - 1) / p.min_share;
     if (grid > static_cast<int64_t>(nsm) * SM::kCtas) grid = static_cast<int64_t>(nsm) * SM::kCtas;
     if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
     if (grid < 1) grid = 1;
