@@ -155,6 +155,7 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     p.G = a->n_heads / kv->n_kv_heads;
     p.D = kv->head_dim;
     p.page = kv->page_size;
+    p.page_magic = static_cast<uint32_t>((1ull << 32) / (kv->page_size / 16) + 1);
     p.k_q4 = kv->k_type == GGQ_TYPE_Q4_0;
     p.v_q4 = kv->v_type == GGQ_TYPE_Q4_0;
     p.max_q = static_cast<int>(!a->q_start ? 1 : a->max_q < a->n_tokens ? a->max_q : a->n_tokens);

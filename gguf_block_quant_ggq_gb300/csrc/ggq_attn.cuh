@@ -22,6 +22,7 @@ struct AttnParams {
     int64_t n_tokens, n_seqs;
     int dtype;               // 0 f32, 1 f16, 2 bf16
     int H, Hkv, G, D, page;
+    uint32_t page_magic;     // 2^32 / (page / 16) + 1
     int k_q4, v_q4;
     int max_q, max_len, window;
     float scale, cap;

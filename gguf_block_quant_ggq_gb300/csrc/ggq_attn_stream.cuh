@@ -205,10 +205,17 @@ __device__ __forceinline__ const T* attn_q_row(const AttnParams& p, const AttnSe
     const int i = r / p.G, h = hk * p.G + r - i * p.G;
     return static_cast<const T*>(p.q) + (s.first + i) * p.q_token + h * p.q_head;
 }
-__device__ __forceinline__ float4 attn_q4(const AttnParams& p, const AttnSeq& s, int hk, int r, int d) {
-    if (p.dtype == 0) return ld4(attn_q_row<float>(p, s, hk, r) + d);
-    if (p.dtype == 1) return ld4(attn_q_row<__half>(p, s, hk, r) + d);
-    return ld4(attn_q_row<__nv_bfloat16>(p, s, hk, r) + d);
+// Elements 16 j + 4 t .. + 3 of a row: all loads in flight at once.
+template <typename T, int KS>
+__device__ __forceinline__ void attn_load_row(const T* q, float4 (&x)[KS]) {
+#pragma unroll
+    for (int j = 0; j < KS; ++j) x[j] = ld4(q + 16 * j);
+}
+template <int KS>
+__device__ __forceinline__ void attn_row(const AttnParams& p, const AttnSeq& s, int hk, int r, int t4, float4 (&x)[KS]) {
+    if (p.dtype == 0) attn_load_row(attn_q_row<float>(p, s, hk, r) + 4 * t4, x);
+    else if (p.dtype == 1) attn_load_row(attn_q_row<__half>(p, s, hk, r) + 4 * t4, x);
+    else attn_load_row(attn_q_row<__nv_bfloat16>(p, s, hk, r) + 4 * t4, x);
 }
 __device__ __forceinline__ void attn_out4(const AttnParams& p, const AttnSeq& s, int hk, int r, int d, float4 v) {
     const int i = r / p.G, h = hk * p.G + r - i * p.G;
@@ -308,39 +315,59 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     // ---- this warp's ring: it takes every fourth unit of the segments; a unit's copies start as
     // soon as the warp has done with the place's last one, the page id having been read a turn before
     const uint64_t policy = policy_evict_first();
-    const int gpp = p.page >> 4;
-    AttnWalk<UNIT> fw = w;  // the unit that is fetched next: fu of segment fw
-    int fu = fw.ua + warp, fpage = -1;
-    const auto seek = [&]() {
+    const int gpp = p.page >> 4;  // groups of a page
+    AttnWalk<UNIT> fw = w;        // the segment whose units are fetched
+    int fu = fw.ua + warp, fend = 0, fglo = 0, fghi = 0, fhk = 0;
+    const int32_t* ftable = nullptr;
+    const auto enter = [&]() {  // what the units of segment fw share; empty segments are passed over
         while (fw.left > 0 && fu >= fw.ub()) {
             fw.next(p, kRows);
             fu = fw.ua + warp;
         }
+        fend = fw.left > 0 ? fw.ub() : 0;
+        fglo = fw.s.glo;
+        fghi = fw.s.ghi;
+        fhk = fw.item / (fw.s.items / p.Hkv);
+        ftable = p.table + fw.b * p.table_stride;
+    };
+    // page and place of a group: division by gpp as a multiplication that is at most one too large
+    int fpage = 0, fplace = 0;
+    const auto seek = [&]() {
+        const int g = fglo + UNIT * fu + (lane < UNIT ? lane : 0);
+        int q = g;
+        fplace = 0;
+        if (gpp > 1) {
+            q = static_cast<int>(__umulhi(static_cast<uint32_t>(g), p.page_magic));
+            fplace = g - q * gpp;
+            if (fplace < 0) --q, fplace += gpp;
+        }
         fpage = -1;
-        const int g = fw.s.glo + UNIT * fu + lane;
-        if (fw.left > 0 && lane < UNIT && g < fw.s.ghi) {
-            fpage = p.table[fw.b * p.table_stride + g / gpp];
+        if (lane < UNIT && fu < fend && g < fghi) fpage = ftable[q];
+    };
+    const auto fetch = [&](int at) {
+        if (fu >= fend) return;
+        const bool two = UNIT == 2 && fglo + UNIT * fu + 1 < fghi;
+        if (lane == 0) mbar_arrive_expect_tx(s_full + at, two ? SM::kStage : SM::kStage / UNIT);
+        __syncwarp();
+        // neighbouring groups of a page are one copy
+        const int next_place = __shfl_sync(0xffffffffu, fplace, UNIT - 1);
+        const bool joined = two && next_place != 0;
+        const int copies = lane == 0 ? (joined ? 2 : 1) : (two && !joined && lane < UNIT ? 1 : 0);
+        if (copies > 0) {
             if (fpage < 0 || fpage >= p.n_pages) {
                 set_error(p.err, DEV_ERR_BAD_PLACE);
                 fpage = 0;
             }
-        }
-    };
-    const auto fetch = [&](int at) {
-        if (fw.left <= 0) return;
-        const int g = fw.s.glo + UNIT * fu + lane;
-        if (lane == 0) mbar_arrive_expect_tx(s_full + at, UNIT == 2 && g + 1 < fw.s.ghi ? SM::kStage : SM::kStage / UNIT);
-        __syncwarp();
-        if (fpage >= 0) {
-            const int hk = fw.item / (fw.s.items / p.Hkv);
-            const int64_t blob = (static_cast<int64_t>(fpage) * p.Hkv + hk) * gpp + g % gpp;
+            const int64_t blob = (static_cast<int64_t>(fpage) * p.Hkv + fhk) * gpp + fplace;
             uint8_t* const dst = smem + SM::oRing + at * SM::kStage;
-            bulk_g2s(dst + lane * SM::kKB, p.k + blob * SM::kKB, SM::kKB, s_full + at, policy);
-            bulk_g2s(dst + UNIT * SM::kKB + lane * SM::kVB, p.v + blob * SM::kVB, SM::kVB, s_full + at, policy);
+            bulk_g2s(dst + lane * SM::kKB, p.k + blob * SM::kKB, copies * SM::kKB, s_full + at, policy);
+            bulk_g2s(dst + UNIT * SM::kKB + lane * SM::kVB, p.v + blob * SM::kVB, copies * SM::kVB, s_full + at, policy);
         }
         fu += kAttnWarps;
+        if (fu >= fend) enter();
         seek();
     };
+    enter();
     seek();
     for (int i = 0; i < S; ++i) fetch(warp * S + i);
 
@@ -363,14 +390,19 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         {
             float up[RS];
             int row[RS];
+            float4 x[RS][KS];
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs) {
                 row[rs] = min(r0 + g8 + 8 * rs, r_end - 1);  // rows past the end repeat the last one
+                attn_row<KS>(p, sq, hk, row[rs], t4, x[rs]);
+            }
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) {
                 float amax = 0.0f;
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
-                    const float4 x = attn_q4(p, sq, hk, row[rs], 16 * j + 4 * t4);
-                    amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+                    const float4 y = x[rs][j];
+                    amax = fmaxf(fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y))), fmaxf(fabsf(y.z), fabsf(y.w)));
                 }
                 amax = quad_max(amax);
                 const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
@@ -393,8 +425,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                     uint32_t frag[4];
 #pragma unroll
                     for (int rs = 0; rs < RS; ++rs) {
-                        const float4 x = attn_q4(p, sq, hk, row[rs], 16 * j + 4 * t4);
-                        const float v[4] = {x.x * up[rs], x.y * up[rs], x.z * up[rs], x.w * up[rs]};
+                        const float4 y = x[rs][j];
+                        const float v[4] = {y.x * up[rs], y.y * up[rs], y.z * up[rs], y.w * up[rs]};
                         float h[4], l[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -443,12 +475,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
 
         for (int u = ua + warp; u < ub; u += kAttnWarps) {
             const int at = warp * S + slot, g = sq.glo + UNIT * u;
-            bool ok = !*s_abort && mbar_wait(s_full + at, phase);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {
-                *s_abort = 1;
-                set_error(p.err, DEV_ERR_TIMEOUT);
-                break;
+            if (!__all_sync(0xffffffffu, mbar_test(s_full + at, phase))) {
+                bool ok = !*s_abort && mbar_wait(s_full + at, phase);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) {
+                    *s_abort = 1;
+                    set_error(p.err, DEV_ERR_TIMEOUT);
+                    break;
+                }
             }
             const uint8_t* const kb = smem + SM::oRing + at * SM::kStage;
             const uint8_t* const vb = kb + UNIT * SM::kKB;
@@ -456,7 +490,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             // ---- scores of two octets of keys a group: x[rs][2 * (2 group + octet)] and + 1, keys 2 t and 2 t + 1
             constexpr int KW = K4 ? NB : KS;  // words of an octet
             float2 sc[RS][2 * UNIT];
-            uint32_t kw[UNIT][2 * KW], kd[UNIT][2][2][NB / 2];
+            uint32_t kw[UNIT][2 * KW];
+            float kd[UNIT][2][2][NB];  // scales of keys 8 o + 2 t + e
 #pragma unroll
             for (int c = 0; c < UNIT; ++c) {
                 const uint8_t* const blob = kb + c * SM::kKB;
@@ -472,7 +507,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) kd[c][o][e][i] = d[e * (NB / 2) + i];
+                        for (int i = 0; i < NB / 2; ++i) {
+                            const float2 f = half2_f32(d[e * (NB / 2) + i]);
+                            kd[c][o][e][2 * i] = f.x, kd[c][o][e][2 * i + 1] = f.y;
+                        }
                 }
             }
 #pragma unroll
@@ -505,7 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                             attn_mma0(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u));
                             attn_mma(cc, fb, prmt(y, 0u, 0x4140u), prmt(y, 0u, 0x4342u));
                         }
-                        const float2 d = half2_f32(prmt(kd[c][o][0][b >> 1], kd[c][o][1][b >> 1], (b & 1) ? 0x7632u : 0x5410u));
+                        const float2 d = make_float2(kd[c][o][0][b], kd[c][o][1][b]);
                         const float2 r = add2(make_float2(cc[0], cc[1]),
                                               MODE == A_SPLIT8 ? make_float2(cc[2], cc[3]) : both(offset[0][b]));
                         sc[0][2 * c + o] = b ? fma2(d, r, sc[0][2 * c + o]) : mul2(d, r);
