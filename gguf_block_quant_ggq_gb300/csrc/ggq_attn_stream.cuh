@@ -104,20 +104,31 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b, int tile
 // Units of UNIT groups of an item, and of the sequence's items together.
 template <int UNIT>
 __device__ __forceinline__ int attn_units(const AttnSeq& s) { return UNIT == 1 ? s.ghi - s.glo : (s.ghi - s.glo + 1) >> 1; }
+// What an item counts in the shares: its units, and kItemCost for its queries, its
+// merge and its output (they take a CTA about as long as six units: 5000 cycles).
+// The first kItemCost positions of an item stand for no unit.
+constexpr int kItemCost = 6;
 template <int UNIT>
-__device__ __forceinline__ int64_t attn_cost(const AttnSeq& s) { return static_cast<int64_t>(attn_units<UNIT>(s)) * s.items; }
+__device__ __forceinline__ int attn_span(const AttnSeq& s) {
+    const int n = attn_units<UNIT>(s);
+    return n > 0 ? n + kItemCost : 0;
+}
+template <int UNIT>
+__device__ __forceinline__ int64_t attn_cost(const AttnSeq& s) { return static_cast<int64_t>(attn_span<UNIT>(s)) * s.items; }
 
 // A CTA's share, item by item.
 template <int UNIT>
 struct AttnWalk {
     AttnSeq s;
     int b, item, ua;
-    int64_t left;  // units of the share that are not yet walked
+    int64_t left;  // positions of the share that are not yet walked
     __device__ __forceinline__ int ub() const {  // end of the current segment
         const int64_t e = ua + left;
-        const int n = attn_units<UNIT>(s);
+        const int n = attn_span<UNIT>(s);
         return e < n ? static_cast<int>(e) : n;
     }
+    __device__ __forceinline__ int first() const { return ua > kItemCost ? ua - kItemCost : 0; }  // its units
+    __device__ __forceinline__ int last() const { return ub() - kItemCost; }
     __device__ __forceinline__ void next(const AttnParams& p, int tile_rows) {
         left -= ub() - ua;
         if (left <= 0) return;
@@ -244,9 +255,9 @@ __device__ __forceinline__ AttnWalk<UNIT> attn_find(const AttnParams& p, const i
         rem -= c;
         ++w.b;
     }
-    const int n_units = attn_units<UNIT>(w.s);
-    w.item = static_cast<int>(rem / n_units);
-    w.ua = static_cast<int>(rem - static_cast<int64_t>(w.item) * n_units);
+    const int span = attn_span<UNIT>(w.s);
+    w.item = static_cast<int>(rem / span);
+    w.ua = static_cast<int>(rem - static_cast<int64_t>(w.item) * span);
     return w;
 }
 
@@ -317,14 +328,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     const uint64_t policy = policy_evict_first();
     const int gpp = p.page >> 4;  // groups of a page
     AttnWalk<UNIT> fw = w;        // the segment whose units are fetched
-    int fu = fw.ua + warp, fend = 0, fglo = 0, fghi = 0, fhk = 0;
+    int fu = fw.first() + warp, fend = 0, fglo = 0, fghi = 0, fhk = 0;
     const int32_t* ftable = nullptr;
     const auto enter = [&]() {  // what the units of segment fw share; empty segments are passed over
-        while (fw.left > 0 && fu >= fw.ub()) {
+        while (fw.left > 0 && fu >= fw.last()) {
             fw.next(p, kRows);
-            fu = fw.ua + warp;
+            fu = fw.first() + warp;
         }
-        fend = fw.left > 0 ? fw.ub() : 0;
+        fend = fw.left > 0 ? fw.last() : 0;
         fglo = fw.s.glo;
         fghi = fw.s.ghi;
         fhk = fw.item / (fw.s.items / p.Hkv);
@@ -377,8 +388,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     uint32_t phase = 0;
     while (w.left > 0) {
         const AttnSeq sq = w.s;
-        const int ua = w.ua, ub = w.ub(), item = w.item;
-        const int64_t at0 = hi - w.left;               // position of the segment's first unit
+        const int ua = w.first(), ub = w.last(), item = w.item;
+        const int64_t at0 = hi - w.left;               // the segment's first position
+        if (ub <= 0) {  // the share ends before the item's units
+            w.next(p, kRows);
+            continue;
+        }
         const int shown = min(sq.rows, p.max_q), tiles = sq.items / p.Hkv, hk = item / tiles;
         const int r0 = (item - hk * tiles) * kRows, r_end = min(shown * p.G, r0 + kRows);
         const int from = sq.len - sq.rows;
@@ -810,8 +825,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         }
         if (!whole) {
             // pieces of this item: the CTAs c0 .. c1 whose shares it crosses
-            const int64_t p0 = at0 - ua, p1 = p0 + n_units;  // the item's positions [p0, p1)
-            const int c0 = static_cast<int>(((p0 + 1) * C - 1) / N), c1 = static_cast<int>((p1 * C - 1) / N);
+            const int64_t p0 = at0 - w.ua, p1 = p0 + n_units + kItemCost;  // the item's positions [p0, p1)
+            const int c0 = static_cast<int>(((p0 + kItemCost + 1) * C - 1) / N), c1 = static_cast<int>((p1 * C - 1) / N);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -823,7 +838,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             __syncthreads();
             if (*s_last) {
                 const int64_t size = attn_part_floats(D);
-                const int slot0 = N * c0 / C == p0 ? 0 : 1;  // the first piece; every other piece begins its CTA's share
+                const int slot0 = N * c0 / C >= p0 ? 0 : 1;  // the first piece; every other piece begins its CTA's share
                 for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
                     const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
                     if (r0 + row >= r_end) break;
@@ -863,7 +878,7 @@ cudaError_t launch_attn_stream(const AttnParams& p, int nsm, cudaStream_t s) {
         if (dev < kMaxDevices) set[dev] = true;
     }
     const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.G + SM::kRows - 1) / SM::kRows;
-    const int64_t units = p.n_seqs * p.Hkv * tiles * ((static_cast<int64_t>(p.max_len) + 16 * SM::kUnit - 1) / (16 * SM::kUnit) + 1);
+    const int64_t units = p.n_seqs * p.Hkv * tiles * ((static_cast<int64_t>(p.max_len) + 16 * SM::kUnit - 1) / (16 * SM::kUnit) + 1 + kItemCost);
     int64_t grid = (units + p.min_share - 1) / p.min_share;
     if (grid > static_cast<int64_t>(nsm) * SM::kCtas) grid = static_cast<int64_t>(nsm) * SM::kCtas;
     if (grid > kAttnMaxCtas) grid = kAttnMaxCtas;
