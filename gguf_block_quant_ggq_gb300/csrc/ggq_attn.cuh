@@ -28,7 +28,7 @@ struct AttnParams {
     float scale, cap;
     int min_share;           // units (one or two 16-token groups) below which a CTA's share is not cut
     float* parts;            // partial results [2 * kAttnMaxCtas][attn_part_floats(D)]
-    int* pieces;             // pieces of an item that have arrived [kAttnMaxCtas], zero between calls
+    int* pieces;             // pieces, and groups of pieces, that have arrived [2][kAttnMaxCtas], zero between calls
     int* err;
 };
 

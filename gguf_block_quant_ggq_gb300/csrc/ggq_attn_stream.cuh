@@ -9,7 +9,7 @@
 // packed bytes are unpacked but never dequantized.
 //   * Scores: two k16 steps per block of 32 channels.  For 16-bit activations the
 //     quants enter as fp16 subnormals u 2^-24 (a byte permutation, no arithmetic);
-//     -off 2^-24 sum_c q_c, added to the block's result, takes the offset out again.
+//     the accumulator starts at -off 2^-24 sum_c q_c, which takes the offset out again.
 //     For fp32 the sums would lose bits to the offset: signed integers.
 //   * Values: quants as exact signed fp16 integers; the other operand is p dv
 //     times a power of two that keeps it in fp16's normal range.
@@ -140,7 +140,18 @@ struct AttnWalk {
     }
 };
 
-// D = A B, and D += A B
+// D = A B, D = A B + C, and D += A B
+__device__ __forceinline__ void attn_mma_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// A register of any content: operand rows whose results nobody reads.
+__device__ __forceinline__ uint32_t attn_any() {
+    uint32_t r;
+    asm volatile("" : "=r"(r));
+    return r;
+}
 __device__ __forceinline__ void attn_mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -211,6 +222,19 @@ __device__ __forceinline__ float quad_max(float v) {
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
+// The rows of an item: kv head, first row and end of its tile.
+struct AttnTile {
+    int hk, r0, r_end;
+};
+__device__ __forceinline__ AttnTile attn_tile(const AttnParams& p, const AttnSeq& s, int item, int tile_rows) {
+    const int tiles = s.items / p.Hkv;
+    AttnTile t;
+    t.hk = item / tiles;
+    t.r0 = (item - t.hk * tiles) * tile_rows;
+    t.r_end = min(min(s.rows, p.max_q) * p.G, t.r0 + tile_rows);
+    return t;
+}
+
 template <typename T>
 __device__ __forceinline__ const T* attn_q_row(const AttnParams& p, const AttnSeq& s, int hk, int r) {
     const int i = r / p.G, h = hk * p.G + r - i * p.G;
@@ -259,6 +283,120 @@ __device__ __forceinline__ AttnWalk<UNIT> attn_find(const AttnParams& p, const i
     w.item = static_cast<int>(rem / span);
     w.ua = static_cast<int>(rem - static_cast<int64_t>(w.item) * span);
     return w;
+}
+
+// ---- items that several CTAs share.  The pieces of the item at position p0 belong
+// to the CTAs c0 .. c1 (c0: where its units begin); each piece is a partial result in
+// its CTA's slot 0 if the CTA's share begins with it, else in slot 1 (c0's only).
+// Sixteen neighbouring pieces are joined by the last of them, then these results by
+// the last of the groups, always in the order of the pieces.
+constexpr int kJoin = 16;
+
+template <int UNIT>
+struct AttnPieces {
+    int c0, c1, slot0;
+    __device__ __forceinline__ AttnPieces(const AttnWalk<UNIT>& w, int64_t p0, int64_t N, int C) {
+        c0 = static_cast<int>(((p0 + kItemCost + 1) * C - 1) / N);
+        c1 = static_cast<int>(((p0 + attn_span<UNIT>(w.s)) * C - 1) / N);
+        slot0 = N * c0 / C >= p0 ? 0 : 1;
+    }
+    template <int D>
+    __device__ __forceinline__ float* at(const AttnParams& p, int k) const {
+        return p.parts + (2 * static_cast<int64_t>(k) + (k == c0 ? slot0 : 0)) * attn_part_floats(D);
+    }
+};
+
+__device__ __forceinline__ int atomic_add_acq_rel(int* p, int v) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
+// One thread, after the CTA's barrier: this CTA's piece has arrived.  *last: 1 if it
+// completes its group of kJoin pieces.
+template <int UNIT>
+__device__ __forceinline__ void attn_arrive(const AttnParams& p, const AttnWalk<UNIT>& w, int64_t p0, int64_t N, int C,
+                                            volatile int* last) {
+    const AttnPieces<UNIT> q(w, p0, N, C);
+    const int g0 = q.c0 + (static_cast<int>(blockIdx.x) - q.c0) / kJoin * kJoin, n = min(kJoin, q.c1 - g0 + 1);
+    const bool is_last = atomic_add_acq_rel(p.pieces + g0, 1) == n - 1;
+    if (is_last) p.pieces[g0] = 0;
+    *last = is_last;
+}
+
+// The whole CTA, after the barrier that follows attn_arrive.
+template <int D, int ROWS, int UNIT>
+__device__ __noinline__ void attn_join(const AttnParams& p, const AttnWalk<UNIT>& w, int64_t p0, int64_t N, int C, int tid,
+                                       volatile int* last) {
+    if (!*last) return;
+    const AttnPieces<UNIT> q(w, p0, N, C);
+    const AttnTile tile = attn_tile(p, w.s, w.item, ROWS);
+    const int g0 = q.c0 + (static_cast<int>(blockIdx.x) - q.c0) / kJoin * kJoin;
+    const bool groups = q.c1 - q.c0 >= kJoin;
+    for (int level = 0; level < 2; ++level) {
+        const int from = level ? q.c0 : g0, step = level ? kJoin : 1, to = level ? q.c1 : min(g0 + kJoin - 1, q.c1);
+        const bool done = level == 1 || !groups;
+        constexpr int kQuads = (ROWS * D / 4 + kAttnThreads - 1) / kAttnThreads;
+        float4 o[kQuads];
+        float M[kQuads], L[kQuads];
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const int i = tid + k * kAttnThreads, row = i / (D / 4), d = 4 * (i - row * (D / 4));
+            M[k] = kAttnNone, L[k] = 0.0f;
+            o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row >= ROWS) continue;
+            for (int b = from; b <= to; b += 4 * step) {  // four pieces' loads in flight
+                float pm[4], pl[4];
+                float4 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float* const a = q.template at<D>(p, min(b + e * step, to - (to - from) % step));
+                    pm[e] = __ldcg(a + row), pl[e] = __ldcg(a + 16 + row);
+                    v[e] = __ldcg(reinterpret_cast<const float4*>(a + 32 + row * D + d));
+                }
+                float top = M[k];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (b + e * step <= to) top = fmaxf(top, pm[e]);
+                const float f0 = ex2(M[k] - top);
+                M[k] = top;
+                L[k] *= f0, o[k].x *= f0, o[k].y *= f0, o[k].z *= f0, o[k].w *= f0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (b + e * step <= to) {
+                        const float f = ex2(pm[e] - top);
+                        L[k] = fmaf(pl[e], f, L[k]);
+                        o[k].x = fmaf(v[e].x, f, o[k].x), o[k].y = fmaf(v[e].y, f, o[k].y);
+                        o[k].z = fmaf(v[e].z, f, o[k].z), o[k].w = fmaf(v[e].w, f, o[k].w);
+                    }
+            }
+        }
+        float* const to_part = q.template at<D>(p, g0);
+        if (!done) __syncthreads();  // the group's first piece is read: its place takes the result
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const int i = tid + k * kAttnThreads, row = i / (D / 4), d = 4 * (i - row * (D / 4));
+            if (row >= ROWS) continue;
+            if (done) {
+                const float inv = L[k] != 0.0f ? 1.0f / L[k] : 0.0f;
+                if (tile.r0 + row < tile.r_end)
+                    attn_out4(p, w.s, tile.hk, tile.r0 + row, d, make_float4(o[k].x * inv, o[k].y * inv, o[k].z * inv, o[k].w * inv));
+            } else {
+                if (d == 0) to_part[row] = M[k], to_part[16 + row] = L[k];
+                *reinterpret_cast<float4*>(to_part + 32 + row * D + d) = o[k];
+            }
+        }
+        if (done) return;
+        __syncthreads();
+        if (tid == 0) {
+            const int n = (q.c1 - q.c0) / kJoin + 1;
+            const bool is_last = atomic_add_acq_rel(p.pieces + kAttnMaxCtas + q.c0, 1) == n - 1;
+            if (is_last) p.pieces[kAttnMaxCtas + q.c0] = 0;
+            *last = is_last;
+        }
+        __syncthreads();
+        if (!*last) return;
+    }
 }
 
 template <bool K4, bool V4, int D, int MODE>
@@ -341,10 +479,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         fhk = fw.item / (fw.s.items / p.Hkv);
         ftable = p.table + fw.b * p.table_stride;
     };
-    // page and place of a group: division by gpp as a multiplication that is at most one too large
-    int fpage = 0, fplace = 0;
+    // lane 0: page and place of the unit's first group (division by gpp as a multiplication that is
+    // at most one too large), and of the second one where it begins a page of its own
+    int fplace = 0, fpage = 0, fpage2 = 0;
+    bool bad_page = false;
     const auto seek = [&]() {
-        const int g = fglo + UNIT * fu + (lane < UNIT ? lane : 0);
+        if (lane != 0 || fu >= fend) return;
+        const int g = fglo + UNIT * fu;
         int q = g;
         fplace = 0;
         if (gpp > 1) {
@@ -352,27 +493,27 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             fplace = g - q * gpp;
             if (fplace < 0) --q, fplace += gpp;
         }
-        fpage = -1;
-        if (lane < UNIT && fu < fend && g < fghi) fpage = ftable[q];
+        fpage = ftable[q];
+        if (UNIT == 2 && fplace + 1 == gpp && g + 1 < fghi) fpage2 = ftable[q + 1];
     };
     const auto fetch = [&](int at) {
         if (fu >= fend) return;
-        const bool two = UNIT == 2 && fglo + UNIT * fu + 1 < fghi;
-        if (lane == 0) mbar_arrive_expect_tx(s_full + at, two ? SM::kStage : SM::kStage / UNIT);
-        __syncwarp();
-        // neighbouring groups of a page are one copy
-        const int next_place = __shfl_sync(0xffffffffu, fplace, UNIT - 1);
-        const bool joined = two && next_place != 0;
-        const int copies = lane == 0 ? (joined ? 2 : 1) : (two && !joined && lane < UNIT ? 1 : 0);
-        if (copies > 0) {
-            if (fpage < 0 || fpage >= p.n_pages) {
-                set_error(p.err, DEV_ERR_BAD_PLACE);
-                fpage = 0;
-            }
-            const int64_t blob = (static_cast<int64_t>(fpage) * p.Hkv + fhk) * gpp + fplace;
+        if (lane == 0) {
+            const bool two = UNIT == 2 && fglo + UNIT * fu + 1 < fghi, apart = two && fplace + 1 == gpp;
+            const int n = two && !apart ? 2 : 1;  // neighbouring groups of a page are one copy
+            mbar_arrive_expect_tx(s_full + at, two ? SM::kStage : SM::kStage / UNIT);
             uint8_t* const dst = smem + SM::oRing + at * SM::kStage;
-            bulk_g2s(dst + lane * SM::kKB, p.k + blob * SM::kKB, copies * SM::kKB, s_full + at, policy);
-            bulk_g2s(dst + UNIT * SM::kKB + lane * SM::kVB, p.v + blob * SM::kVB, copies * SM::kVB, s_full + at, policy);
+            const uint32_t pages = static_cast<uint32_t>(p.n_pages);
+            if (static_cast<uint32_t>(fpage) >= pages) fpage = 0, bad_page = true;
+            const int64_t blob = (static_cast<int64_t>(fpage) * p.Hkv + fhk) * gpp + fplace;
+            bulk_g2s(dst, p.k + blob * SM::kKB, n * SM::kKB, s_full + at, policy);
+            bulk_g2s(dst + UNIT * SM::kKB, p.v + blob * SM::kVB, n * SM::kVB, s_full + at, policy);
+            if (apart) {
+                if (static_cast<uint32_t>(fpage2) >= pages) fpage2 = 0, bad_page = true;
+                const int64_t blob2 = (static_cast<int64_t>(fpage2) * p.Hkv + fhk) * gpp;
+                bulk_g2s(dst + SM::kKB, p.k + blob2 * SM::kKB, SM::kKB, s_full + at, policy);
+                bulk_g2s(dst + UNIT * SM::kKB + SM::kVB, p.v + blob2 * SM::kVB, SM::kVB, s_full + at, policy);
+            }
         }
         fu += kAttnWarps;
         if (fu >= fend) enter();
@@ -382,35 +523,47 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     seek();
     for (int i = 0; i < S; ++i) fetch(warp * S + i);
 
-    // ---- segments
+    // ---- segments; a segment's query rows are on their way while the one before is finished
     const int g8 = lane >> 2, t4 = lane & 3;
     int slot = 0;
     uint32_t phase = 0;
+    float4 x[RS][KS];
+    const auto load_rows = [&](const AttnWalk<UNIT>& at) {
+        const AttnTile t = attn_tile(p, at.s, at.item, kRows);
+#pragma unroll
+        for (int rs = 0; rs < RS; ++rs)  // rows past the end repeat the last one
+            attn_row<KS>(p, at.s, t.hk, min(t.r0 + g8 + 8 * rs, t.r_end - 1), t4, x[rs]);
+    };
+    const auto skip_empty = [&](AttnWalk<UNIT>& at) {  // a share may end before an item's units
+        while (at.left > 0 && at.last() <= 0) at.next(p, kRows);
+    };
+    // an item that this CTA has added a piece to: whether it was the last one is known after the next barrier
+    bool pending = false;
+    AttnWalk<UNIT> pw = w;
+    int64_t pp0 = 0;
+    const auto settle = [&]() {
+        if (!pending) return;
+        pending = false;
+        attn_join<D, kRows, UNIT>(p, pw, pp0, N, C, tid, s_last);
+    };
+    skip_empty(w);
+    constexpr bool kAhead = RS * KS <= 8;  // there are registers to hold them
+    if (kAhead && w.left > 0) load_rows(w);
     while (w.left > 0) {
+        if (!kAhead) load_rows(w);
         const AttnSeq sq = w.s;
-        const int ua = w.first(), ub = w.last(), item = w.item;
+        const int ua = w.first(), ub = w.last();
         const int64_t at0 = hi - w.left;               // the segment's first position
-        if (ub <= 0) {  // the share ends before the item's units
-            w.next(p, kRows);
-            continue;
-        }
-        const int shown = min(sq.rows, p.max_q), tiles = sq.items / p.Hkv, hk = item / tiles;
-        const int r0 = (item - hk * tiles) * kRows, r_end = min(shown * p.G, r0 + kRows);
+        const AttnTile tile = attn_tile(p, sq, w.item, kRows);
+        const int hk = tile.hk, r0 = tile.r0, r_end = tile.r_end;
         const int from = sq.len - sq.rows;
 
         // query rows -> operand registers (through shared memory, each warp a part of the k-steps)
         float xs[RS];                                   // score of an accumulator unit, times log2 e
         int pos[RS], first_key[RS];
-        float offset[RS][NB], slope[RS];
+        float offset[NB][4], slope[RS];                 // -offset * sum of the queries of a block, as an accumulator
         {
             float up[RS];
-            int row[RS];
-            float4 x[RS][KS];
-#pragma unroll
-            for (int rs = 0; rs < RS; ++rs) {
-                row[rs] = min(r0 + g8 + 8 * rs, r_end - 1);  // rows past the end repeat the last one
-                attn_row<KS>(p, sq, hk, row[rs], t4, x[rs]);
-            }
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs) {
                 float amax = 0.0f;
@@ -426,9 +579,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                 const int sh = ex == 128 ? 0 : min((MODE == A_SPLIT8 ? 10 : 13) - ex, 100);
                 up[rs] = copysignf(pow2f(sh), p.scale);
                 xs[rs] = fabsf(p.scale) * scalbnf(1.0f, (MODE == A_SPLIT8 ? 0 : 24) - sh);
-                pos[rs] = from + row[rs] / p.G;
+                const int r = min(r0 + g8 + 8 * rs, r_end - 1);
+                pos[rs] = from + r / p.G;
                 first_key[rs] = p.window > 0 ? pos[rs] - p.window + 1 : 0;
-                slope[rs] = p.slopes ? p.slopes[hk * p.G + row[rs] % p.G] : 0.0f;
+                slope[rs] = p.slopes ? p.slopes[hk * p.G + r % p.G] : 0.0f;
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
@@ -461,11 +615,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                     if ((j & (kAttnWarps - 1)) == warp) s_q[j * 32 + lane] = make_uint4(frag[0], frag[1], frag[2], frag[3]);
                 }
 #pragma unroll
-                for (int rs = 0; rs < RS; ++rs)
-                    offset[rs][b] = quad_sum(sum[rs]) * (K4 ? -8.0f : -128.0f) * 5.9604644775390625e-8f;  // 2^-24
+                for (int rs = 0; rs < 2; ++rs)
+                    offset[b][2 * rs] = offset[b][2 * rs + 1] = quad_sum(sum[rs < RS ? rs : 0]) * (K4 ? -8.0f : -128.0f) * 0x1p-24f;
             }
         }
         __syncthreads();
+        settle();
         const bool plain = p.cap <= 0.0f && !p.slopes;
         constexpr float kLog2e = 1.44269504088896340736f;
         if (plain)
@@ -502,9 +657,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             const uint8_t* const kb = smem + SM::oRing + at * SM::kStage;
             const uint8_t* const vb = kb + UNIT * SM::kKB;
 
-            // ---- scores of two octets of keys a group: x[rs][2 * (2 group + octet)] and + 1, keys 2 t and 2 t + 1
+            // ---- scores, index 4 group + 2 octet + e: keys 2 t + e of the octet
             constexpr int KW = K4 ? NB : KS;  // words of an octet
-            float2 sc[RS][2 * UNIT];
+            float sc[RS][4 * UNIT];
             uint32_t kw[UNIT][2 * KW];
             float kd[UNIT][2][2][NB];  // scales of keys 8 o + 2 t + e
 #pragma unroll
@@ -551,21 +706,21 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                                      h2_sub(prmt(y, 0x64646464u, 0x4342u), 0x64806480u));
                         } else if constexpr (K4) {
                             const uint32_t q = kw[c][o * NB + b], y = q >> 8;
-                            attn_mma0(cc, fa, q & 0x000F000Fu, q & 0x00F000F0u);
+                            attn_mma_c(cc, fa, q & 0x000F000Fu, q & 0x00F000F0u, offset[b]);
                             attn_mma(cc, fb, y & 0x000F000Fu, y & 0x00F000F0u);
                         } else {
                             const uint32_t q = kw[c][o * KS + 2 * b], y = kw[c][o * KS + 2 * b + 1];
-                            attn_mma0(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u));
+                            attn_mma_c(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u), offset[b]);
                             attn_mma(cc, fb, prmt(y, 0u, 0x4140u), prmt(y, 0u, 0x4342u));
                         }
-                        const float2 d = make_float2(kd[c][o][0][b], kd[c][o][1][b]);
-                        const float2 r = add2(make_float2(cc[0], cc[1]),
-                                              MODE == A_SPLIT8 ? make_float2(cc[2], cc[3]) : both(offset[0][b]));
-                        sc[0][2 * c + o] = b ? fma2(d, r, sc[0][2 * c + o]) : mul2(d, r);
-                        if constexpr (TWO) {
-                            const float2 r2 = add2(make_float2(cc[2], cc[3]), both(offset[RS - 1][b]));
-                            sc[RS - 1][2 * c + o] = b ? fma2(d, r2, sc[RS - 1][2 * c + o]) : mul2(d, r2);
-                        }
+                        if constexpr (MODE == A_SPLIT8) cc[0] += cc[2], cc[1] += cc[3];
+#pragma unroll
+                        for (int rs = 0; rs < RS; ++rs)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float& to = sc[rs][4 * c + 2 * o + e];
+                                to = b ? fmaf(kd[c][o][e][b], cc[2 * rs + e], to) : kd[c][o][e][b] * cc[2 * rs + e];
+                            }
                     }
             }
             uint32_t vd[UNIT][4][NB / 2];  // value scales of keys 8 o + 2 t + e, index 2 o + e
@@ -582,20 +737,20 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                 }
 
             // ---- logits in units of log2, masks
-            float x[RS][4 * UNIT];
+            float lg[RS][4 * UNIT];
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
-                for (int i = 0; i < 4 * UNIT; ++i) x[rs][i] = ((i & 1) ? sc[rs][i >> 1].y : sc[rs][i >> 1].x) * xs[rs];
+                for (int i = 0; i < 4 * UNIT; ++i) lg[rs][i] = sc[rs][i] * xs[rs];
             if (!plain) {
 #pragma unroll
                 for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
                     for (int i = 0; i < 4 * UNIT; ++i) {
                         const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
-                        float y = x[rs][i];
+                        float y = lg[rs][i];
                         if (p.cap > 0.0f) y = p.cap * tanhf(__fdividef(y, p.cap));
-                        x[rs][i] = fmaf(slope[rs], static_cast<float>(key - pos[rs]), y) * kLog2e;
+                        lg[rs][i] = fmaf(slope[rs], static_cast<float>(key - pos[rs]), y) * kLog2e;
                     }
             }
             if (g < whole_begin || g + UNIT > whole_end) {
@@ -604,7 +759,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                     const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
 #pragma unroll
                     for (int rs = 0; rs < RS; ++rs)
-                        if (key > pos[rs] || key < first_key[rs]) x[rs][i] = -INFINITY;
+                        if (key > pos[rs] || key < first_key[rs]) lg[rs][i] = -INFINITY;
                     if (key >= sq.len)  // never written: whatever the place holds
 #pragma unroll
                         for (int k = 0; k < NB / 2; ++k) vd[i >> 2][i & 3][k] = 0u;
@@ -616,9 +771,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             bool raise = false;
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs) {
-                float hi_x = x[rs][0], lo_x = x[rs][0];
+                float hi_x = lg[rs][0], lo_x = lg[rs][0];
 #pragma unroll
-                for (int i = 1; i < 4 * UNIT; ++i) hi_x = fmaxf(hi_x, x[rs][i]), lo_x = fminf(lo_x, x[rs][i]);
+                for (int i = 1; i < 4 * UNIT; ++i) hi_x = fmaxf(hi_x, lg[rs][i]), lo_x = fminf(lo_x, lg[rs][i]);
                 top[rs] = quad_max(hi_x);
                 raise |= top[rs] > m[rs] + 60.0f || lo_x < top[rs] - 28.0f;
             }
@@ -647,7 +802,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                                 vd[c][i][b >> 1] &= (b & 1) ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
                                 for (int rs = 0; rs < RS; ++rs)
-                                    if (x[rs][4 * c + i] != -INFINITY) spoilt[rs] |= 1u << b;
+                                    if (lg[rs][4 * c + i] != -INFINITY) spoilt[rs] |= 1u << b;
                             }
                         }
                 dfin = warp_max(dfin);
@@ -667,7 +822,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
 #pragma unroll
                     for (int n = 0; n < NT; ++n) tot[rs][n] = mul2(tot[rs][n], both(((spoilt[rs] >> (n >> 2)) & 1u) ? NAN : a));
 #pragma unroll
-                    for (int i = 0; i < 4 * UNIT; ++i) more |= x[rs][i] < top[rs] - 28.0f && x[rs][i] > m[rs] - 126.0f;
+                    for (int i = 0; i < 4 * UNIT; ++i) more |= lg[rs][i] < top[rs] - 28.0f && lg[rs][i] > m[rs] - 126.0f;
                 }
                 more = __any_sync(0xffffffffu, more);
             }
@@ -680,13 +835,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                     rest[rs] = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 4 * UNIT; ++i) {
-                        pr[rs][i] = ex2(x[rs][i] - sub);
+                        pr[rs][i] = ex2(lg[rs][i] - sub);
                         if (more) {
-                            if (x[rs][i] < ref - 28.0f) {
+                            if (lg[rs][i] < ref - 28.0f) {
                                 pr[rs][i] = 0.0f;
-                                rest[rs] = fmaxf(rest[rs], x[rs][i]);
+                                rest[rs] = fmaxf(rest[rs], lg[rs][i]);
                             } else {
-                                x[rs][i] = -INFINITY;
+                                lg[rs][i] = -INFINITY;
                             }
                         }
                     }
@@ -722,7 +877,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                                 a[2 * o + 1] = pack_h2(r.x, r.y);
                             } else {
                                 a[2 * o] = h2_mul(ph[0][2 * c + o], d2);
-                                a[2 * o + 1] = TWO ? h2_mul(ph[RS - 1][2 * c + o], d2) : 0u;
+                                a[2 * o + 1] = TWO ? h2_mul(ph[RS - 1][2 * c + o], d2) : attn_any();
                             }
                         }
                         const uint8_t* const blob = vb + c * SM::kVB;
@@ -775,6 +930,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             fetch(at);
             if (++slot == S) slot = 0, phase ^= 1u;
         }
+        AttnWalk<UNIT> next = w;
+        next.next(p, kRows);
+        skip_empty(next);
+        if (kAhead && next.left > 0) load_rows(next);
         // the reference moves to the sum's power of two (it may lag the largest score by 2^60)
         float* const s_mine = s_tot + warp * kRows * SM::kRowPitch;
 #pragma unroll
@@ -803,7 +962,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         float* const part = p.parts + (static_cast<int64_t>(c) * 2 + (at0 == lo ? 0 : 1)) * attn_part_floats(D);
         for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
             const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
-            if (r0 + row >= r_end) break;
+            if (whole && r0 + row >= r_end) break;
             float M = kAttnNone, L = 0.0f;
 #pragma unroll
             for (int k = 0; k < kAttnWarps; ++k) M = fmaxf(M, s_m[k * kRows + row]);
@@ -824,44 +983,17 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             }
         }
         if (!whole) {
-            // pieces of this item: the CTAs c0 .. c1 whose shares it crosses
-            const int64_t p0 = at0 - w.ua, p1 = p0 + n_units + kItemCost;  // the item's positions [p0, p1)
-            const int c0 = static_cast<int>(((p0 + kItemCost + 1) * C - 1) / N), c1 = static_cast<int>((p1 * C - 1) / N);
-            __threadfence();
+            pending = true;
+            pw = w;
+            pp0 = at0 - w.ua;  // the item's first position
             __syncthreads();
-            if (tid == 0) {
-                const int before = atomicAdd(p.pieces + c0, 1);
-                *s_last = before == c1 - c0;
-                if (before == c1 - c0) p.pieces[c0] = 0;
-                __threadfence();
-            }
-            __syncthreads();
-            if (*s_last) {
-                const int64_t size = attn_part_floats(D);
-                const int slot0 = N * c0 / C >= p0 ? 0 : 1;  // the first piece; every other piece begins its CTA's share
-                for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
-                    const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
-                    if (r0 + row >= r_end) break;
-                    float M = kAttnNone, L = 0.0f;
-                    for (int k = c0; k <= c1; ++k)
-                        M = fmaxf(M, __ldcg(p.parts + (2 * k + (k == c0 ? slot0 : 0)) * size + row));
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int k = c0; k <= c1; ++k) {
-                        const float* const q = p.parts + (2 * k + (k == c0 ? slot0 : 0)) * size;
-                        const float f = ex2(__ldcg(q + row) - M);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + 32 + row * D + d));
-                        L = fmaf(__ldcg(q + 16 + row), f, L);
-                        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-                    }
-                    const float inv = L != 0.0f ? 1.0f / L : 0.0f;
-                    attn_out4(p, sq, hk, r0 + row, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-                }
-            }
+            if (tid == 0) attn_arrive<UNIT>(p, pw, pp0, N, C, s_last);
         }
-        __syncthreads();  // the totals and the query operand are free again
-        w.next(p, kRows);
+        w = next;
     }
+    if (bad_page) set_error(p.err, DEV_ERR_BAD_PLACE);
+    __syncthreads();
+    settle();
 }
 
 // Launch of one (K format, V format, D, mode); the grid fills the SMs once.

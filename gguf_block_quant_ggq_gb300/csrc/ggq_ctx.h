@@ -20,7 +20,7 @@ inline size_t align_up(size_t v, size_t a = kAlign) { return (v + a - 1) / a * a
 struct Ctrl {
     int err;
     int pad[63];
-    int attn_pieces[1024];  // attention: arrived pieces of shared items, zero between calls
+    int attn_pieces[2 * 1024];  // attention: arrived pieces and groups of pieces of shared items, zero between calls
 };
 
 }  // namespace ggq
