@@ -44,6 +44,18 @@ constexpr float kAttnNone = -1e30f;                    // reference maximum of a
 // fp32 rows (high and low halves), 8 rows or 16 rows of 16-bit activations
 enum AttnMode : int { A_SPLIT8 = 0, A_HALF8 = 1, A_HALF16 = 2 };
 
+// cap * tanh(y / cap).  For fp32 rows tanhf; else 1 - 2 / (1 + exp(2 z)), whose error
+// of a few 2^-23 cap is far below the roundings of 16-bit activations.
+template <int MODE>
+__device__ __forceinline__ float attn_cap(float y, float cap) {
+    const float z = __fdividef(y, cap);
+    if (MODE == A_SPLIT8) return cap * tanhf(z);
+    const float e = z * 2.88539008177792681f;  // 2 log2 e
+    float x;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(e > 120.0f ? 120.0f : e));
+    return cap - __fdividef(2.0f * cap, 1.0f + x);
+}
+
 template <bool K4, bool V4, int D, int MODE>
 struct AttnSmem {
     static constexpr int kRows = MODE == A_HALF16 ? 16 : 8;
@@ -749,9 +761,16 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                     for (int i = 0; i < 4 * UNIT; ++i) {
                         const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
                         float y = lg[rs][i];
-                        if (p.cap > 0.0f) y = p.cap * tanhf(__fdividef(y, p.cap));
+                        if (p.cap > 0.0f) y = attn_cap<MODE>(y, p.cap);
                         lg[rs][i] = fmaf(slope[rs], static_cast<float>(key - pos[rs]), y) * kLog2e;
                     }
+            }
+            float lowest[RS];  // before the masks: a bound
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) {
+                lowest[rs] = lg[rs][0];
+#pragma unroll
+                for (int i = 1; i < 4 * UNIT; ++i) lowest[rs] = fminf(lowest[rs], lg[rs][i]);
             }
             if (g < whole_begin || g + UNIT > whole_end) {
 #pragma unroll
@@ -771,11 +790,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             bool raise = false;
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs) {
-                float hi_x = lg[rs][0], lo_x = lg[rs][0];
+                float highest = lg[rs][0];
 #pragma unroll
-                for (int i = 1; i < 4 * UNIT; ++i) hi_x = fmaxf(hi_x, lg[rs][i]), lo_x = fminf(lo_x, lg[rs][i]);
-                top[rs] = quad_max(hi_x);
-                raise |= top[rs] > m[rs] + 60.0f || lo_x < top[rs] - 28.0f;
+                for (int i = 1; i < 4 * UNIT; ++i) highest = fmaxf(highest, lg[rs][i]);
+                top[rs] = quad_max(highest);
+                raise |= top[rs] > m[rs] + 60.0f || lowest[rs] < top[rs] - 28.0f;
             }
             uint32_t dm = 0u;
 #pragma unroll
