@@ -59,7 +59,7 @@ __device__ __forceinline__ float attn_cap(float y, float cap) {
 template <bool K4, bool V4, int D, int MODE>
 struct AttnSmem {
     static constexpr int kRows = MODE == A_HALF16 ? 16 : 8;
-    static constexpr int kUnit = D == 256 ? 1 : 2;     // 16-token groups a warp takes at once
+    static constexpr int kUnit = D == 256 ? 1 : D == 64 && (K4 || V4) ? 4 : 2;  // 16-token groups a warp takes at once
     static constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
     static constexpr int kStage = kUnit * (kKB + kVB); // keys of the unit's groups, then their values
     static constexpr int kFit = (D == 64 ? 52 : 72) * 1024 / (kAttnWarps * kStage);
@@ -67,9 +67,9 @@ struct AttnSmem {
     static constexpr int kRowPitch = D + 8;            // floats of a totals row (padding: conflict-free float2 stores)
     static constexpr int oRing = 0;
     static constexpr int oTot = kAttnWarps * kStages * kStage;
-    static constexpr int oQ = oTot + kAttnWarps * kRows * kRowPitch * 4;
-    static constexpr int oStat = oQ + D / 16 * 32 * 16;   // m, l [warps][rows]
-    static constexpr int oScan = (oStat + 2 * kAttnWarps * kRows * 4 + 7) / 8 * 8;
+    static constexpr int oQ = oTot + kAttnWarps * 8 * kRowPitch * 4;  // totals of 8 rows a warp
+    static constexpr int oStat = oQ + D / 16 * 32 * 16;   // m, l [warps][8]
+    static constexpr int oScan = (oStat + 2 * kAttnWarps * 8 * 4 + 7) / 8 * 8;
     static constexpr int oBar = (oScan + (128 + 4) * 8 + 15) / 16 * 16;
     static constexpr int kTotal = oBar + kAttnWarps * kStages * 8 + 16;
     // CTAs an SM: 12 warps leave 168 registers a thread (64-channel heads), 8 warps 255
@@ -115,11 +115,12 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b, int tile
 }
 // Units of UNIT groups of an item, and of the sequence's items together.
 template <int UNIT>
-__device__ __forceinline__ int attn_units(const AttnSeq& s) { return UNIT == 1 ? s.ghi - s.glo : (s.ghi - s.glo + 1) >> 1; }
+__device__ __forceinline__ int attn_units(const AttnSeq& s) { return (s.ghi - s.glo + UNIT - 1) / UNIT; }
 // What an item counts in the shares: its units, and kItemCost for its queries, its
-// merge and its output (they take a CTA about as long as six units: 5000 cycles).
+// merge and its output (measured on 64 ragged sequences of up to 4096 tokens: 82 us
+// at 0, 68 at 6, 63 at 13).
 // The first kItemCost positions of an item stand for no unit.
-constexpr int kItemCost = 6;
+constexpr int kItemCost = 12;
 template <int UNIT>
 __device__ __forceinline__ int attn_span(const AttnSeq& s) {
     const int n = attn_units<UNIT>(s);
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     float* const s_tot = reinterpret_cast<float*>(smem + SM::oTot);
     uint4* const s_q = reinterpret_cast<uint4*>(smem + SM::oQ);
     float* const s_m = reinterpret_cast<float*>(smem + SM::oStat);
-    float* const s_l = s_m + kAttnWarps * kRows;
+    float* const s_l = s_m + kAttnWarps * 8;
     int64_t* const s_scan = reinterpret_cast<int64_t*>(smem + SM::oScan);
     int64_t* const s_wsum = s_scan + 128;
     uint64_t* const s_full = reinterpret_cast<uint64_t*>(smem + SM::oBar);
@@ -491,13 +492,13 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         fhk = fw.item / (fw.s.items / p.Hkv);
         ftable = p.table + fw.b * p.table_stride;
     };
-    // lane 0: page and place of the unit's first group (division by gpp as a multiplication that is
-    // at most one too large), and of the second one where it begins a page of its own
-    int fplace = 0, fpage = 0, fpage2 = 0;
+    // lane l: page and place of the unit's group l (division by gpp as a multiplication that is at most
+    // one too large)
+    int fplace = 0, fpage = 0;
     bool bad_page = false;
     const auto seek = [&]() {
-        if (lane != 0 || fu >= fend) return;
-        const int g = fglo + UNIT * fu;
+        const int g = fglo + UNIT * fu + lane;
+        if (lane >= UNIT || fu >= fend || g >= fghi) return;
         int q = g;
         fplace = 0;
         if (gpp > 1) {
@@ -506,26 +507,20 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             if (fplace < 0) --q, fplace += gpp;
         }
         fpage = ftable[q];
-        if (UNIT == 2 && fplace + 1 == gpp && g + 1 < fghi) fpage2 = ftable[q + 1];
     };
     const auto fetch = [&](int at) {
         if (fu >= fend) return;
-        if (lane == 0) {
-            const bool two = UNIT == 2 && fglo + UNIT * fu + 1 < fghi, apart = two && fplace + 1 == gpp;
-            const int n = two && !apart ? 2 : 1;  // neighbouring groups of a page are one copy
-            mbar_arrive_expect_tx(s_full + at, two ? SM::kStage : SM::kStage / UNIT);
-            uint8_t* const dst = smem + SM::oRing + at * SM::kStage;
-            const uint32_t pages = static_cast<uint32_t>(p.n_pages);
-            if (static_cast<uint32_t>(fpage) >= pages) fpage = 0, bad_page = true;
+        const int n = min(UNIT, fghi - fglo - UNIT * fu);  // groups of the unit
+        const bool joined = __shfl_sync(0xffffffffu, fplace, 0) + n <= gpp;  // of one page: one copy
+        if (lane == 0) mbar_arrive_expect_tx(s_full + at, n * (SM::kStage / UNIT));
+        __syncwarp();
+        if (lane < (joined ? 1 : n)) {
+            const int copies = joined ? n : 1;
+            if (static_cast<uint32_t>(fpage) >= static_cast<uint32_t>(p.n_pages)) fpage = 0, bad_page = true;
             const int64_t blob = (static_cast<int64_t>(fpage) * p.Hkv + fhk) * gpp + fplace;
-            bulk_g2s(dst, p.k + blob * SM::kKB, n * SM::kKB, s_full + at, policy);
-            bulk_g2s(dst + UNIT * SM::kKB, p.v + blob * SM::kVB, n * SM::kVB, s_full + at, policy);
-            if (apart) {
-                if (static_cast<uint32_t>(fpage2) >= pages) fpage2 = 0, bad_page = true;
-                const int64_t blob2 = (static_cast<int64_t>(fpage2) * p.Hkv + fhk) * gpp;
-                bulk_g2s(dst + SM::kKB, p.k + blob2 * SM::kKB, SM::kKB, s_full + at, policy);
-                bulk_g2s(dst + UNIT * SM::kKB + SM::kVB, p.v + blob2 * SM::kVB, SM::kVB, s_full + at, policy);
-            }
+            uint8_t* const dst = smem + SM::oRing + at * SM::kStage;
+            bulk_g2s(dst + lane * SM::kKB, p.k + blob * SM::kKB, copies * SM::kKB, s_full + at, policy);
+            bulk_g2s(dst + UNIT * SM::kKB + lane * SM::kVB, p.v + blob * SM::kVB, copies * SM::kVB, s_full + at, policy);
         }
         fu += kAttnWarps;
         if (fu >= fend) enter();
@@ -535,17 +530,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     seek();
     for (int i = 0; i < S; ++i) fetch(warp * S + i);
 
-    // ---- segments; a segment's query rows are on their way while the one before is finished
+    // ---- segments
     const int g8 = lane >> 2, t4 = lane & 3;
     int slot = 0;
     uint32_t phase = 0;
-    float4 x[RS][KS];
-    const auto load_rows = [&](const AttnWalk<UNIT>& at) {
-        const AttnTile t = attn_tile(p, at.s, at.item, kRows);
-#pragma unroll
-        for (int rs = 0; rs < RS; ++rs)  // rows past the end repeat the last one
-            attn_row<KS>(p, at.s, t.hk, min(t.r0 + g8 + 8 * rs, t.r_end - 1), t4, x[rs]);
-    };
     const auto skip_empty = [&](AttnWalk<UNIT>& at) {  // a share may end before an item's units
         while (at.left > 0 && at.last() <= 0) at.next(p, kRows);
     };
@@ -559,10 +547,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         attn_join<D, kRows, UNIT>(p, pw, pp0, N, C, tid, s_last);
     };
     skip_empty(w);
-    constexpr bool kAhead = RS * KS <= 8;  // there are registers to hold them
-    if (kAhead && w.left > 0) load_rows(w);
     while (w.left > 0) {
-        if (!kAhead) load_rows(w);
         const AttnSeq sq = w.s;
         const int ua = w.first(), ub = w.last();
         const int64_t at0 = hi - w.left;               // the segment's first position
@@ -575,6 +560,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         int pos[RS], first_key[RS];
         float offset[NB][4], slope[RS];                 // -offset * sum of the queries of a block, as an accumulator
         {
+            float4 x[RS][KS];
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs)  // rows past the end repeat the last one
+                attn_row<KS>(p, sq, hk, min(r0 + g8 + 8 * rs, r_end - 1), t4, x[rs]);
             float up[RS];
 #pragma unroll
             for (int rs = 0; rs < RS; ++rs) {
@@ -949,14 +938,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             fetch(at);
             if (++slot == S) slot = 0, phase ^= 1u;
         }
-        AttnWalk<UNIT> next = w;
-        next.next(p, kRows);
-        skip_empty(next);
-        if (kAhead && next.left > 0) load_rows(next);
-        // the reference moves to the sum's power of two (it may lag the largest score by 2^60)
-        float* const s_mine = s_tot + warp * kRows * SM::kRowPitch;
+        // ---- the segment's result: the four warps' parts, 8 rows at a time
+        const int n_units = attn_units<UNIT>(sq);
+        const bool whole = ua == 0 && ub == n_units;
+        float* const part = p.parts + (static_cast<int64_t>(c) * 2 + (at0 == lo ? 0 : 1)) * attn_part_floats(D);
+        float* const s_mine = s_tot + warp * 8 * SM::kRowPitch;
 #pragma unroll
         for (int rs = 0; rs < RS; ++rs) {
+            // the reference moves to the sum's power of two (it may lag the largest score by 2^60)
             float sum = quad_sum(l[rs]);
             const int e = static_cast<int>(__float_as_uint(sum) >> 23) - 127;
             float a = 1.0f;
@@ -965,40 +954,36 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
                 sum *= a;
                 m[rs] += static_cast<float>(e);
             }
+            if (rs > 0) __syncthreads();
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<float2*>(s_mine + (g8 + 8 * rs) * SM::kRowPitch + 8 * n + 2 * t4) = mul2(tot[rs][n], both(a));
+                *reinterpret_cast<float2*>(s_mine + g8 * SM::kRowPitch + 8 * n + 2 * t4) = mul2(tot[rs][n], both(a));
             if (t4 == 0) {
-                s_m[warp * kRows + g8 + 8 * rs] = m[rs];
-                s_l[warp * kRows + g8 + 8 * rs] = sum;
+                s_m[warp * 8 + g8] = m[rs];
+                s_l[warp * 8 + g8] = sum;
             }
-        }
-        __syncthreads();
-
-        // ---- the segment's result: the four warps' parts
-        const int n_units = attn_units<UNIT>(sq);
-        const bool whole = ua == 0 && ub == n_units;
-        float* const part = p.parts + (static_cast<int64_t>(c) * 2 + (at0 == lo ? 0 : 1)) * attn_part_floats(D);
-        for (int i = tid; i < kRows * D / 4; i += kAttnThreads) {
-            const int row = i / (D / 4), d = 4 * (i - row * (D / 4));
-            if (whole && r0 + row >= r_end) break;
-            float M = kAttnNone, L = 0.0f;
+            __syncthreads();
+            for (int i = tid; i < 8 * D / 4; i += kAttnThreads) {
+                const int r8 = i / (D / 4), d = 4 * (i - r8 * (D / 4)), row = 8 * rs + r8;
+                if (whole && r0 + row >= r_end) break;
+                float M = kAttnNone, L = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kAttnWarps; ++k) M = fmaxf(M, s_m[k * kRows + row]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < kAttnWarps; ++k) M = fmaxf(M, s_m[k * 8 + r8]);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < kAttnWarps; ++k) {
-                const float f = ex2(s_m[k * kRows + row] - M);
-                const float4 v = *reinterpret_cast<const float4*>(s_tot + (k * kRows + row) * SM::kRowPitch + d);
-                L = fmaf(s_l[k * kRows + row], f, L);
-                o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-            }
-            if (whole) {
-                const float inv = L != 0.0f ? 1.0f / L : 0.0f;
-                attn_out4(p, sq, hk, r0 + row, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-            } else {
-                if (d == 0) part[row] = M, part[16 + row] = L;
-                *reinterpret_cast<float4*>(part + 32 + row * D + d) = o;
+                for (int k = 0; k < kAttnWarps; ++k) {
+                    const float f = ex2(s_m[k * 8 + r8] - M);
+                    const float4 v = *reinterpret_cast<const float4*>(s_tot + (k * 8 + r8) * SM::kRowPitch + d);
+                    L = fmaf(s_l[k * 8 + r8], f, L);
+                    o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+                }
+                if (whole) {
+                    const float inv = L != 0.0f ? 1.0f / L : 0.0f;
+                    attn_out4(p, sq, hk, r0 + row, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                } else {
+                    if (d == 0) part[row] = M, part[16 + row] = L;
+                    *reinterpret_cast<float4*>(part + 32 + row * D + d) = o;
+                }
             }
         }
         if (!whole) {
@@ -1008,7 +993,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             __syncthreads();
             if (tid == 0) attn_arrive<UNIT>(p, pw, pp0, N, C, s_last);
         }
-        w = next;
+        w.next(p, kRows);
+        skip_empty(w);
     }
     if (bad_page) set_error(p.err, DEV_ERR_BAD_PLACE);
     __syncthreads();
