@@ -25,7 +25,7 @@ ggq_status cache_checks(ggq_ctx* c, const ggq_kv_cache* kv, const char* op) {
     if (!kv_type_ok(kv->k_type) || !kv_type_ok(kv->v_type))
         return fail(c, GGQ_ERR_UNSUPPORTED, "%s: cache types %d and %d; supported: Q8_0, Q4_0", op, kv->k_type, kv->v_type);
     if (kv->n_kv_heads < 1 || kv->n_kv_heads > 16384 || (kv->head_dim != 64 && kv->head_dim != 128 && kv->head_dim != 256) ||
-        kv->page_size < 16 || kv->page_size % 16 || kv->n_pages < 1 || kv->n_pages > INT32_MAX)
+        kv->page_size < 16 || kv->page_size % 16 || kv->n_pages < 1 || kv->n_pages > INT32_MAX / (kv->page_size / 16))
         return fail(c, GGQ_ERR_SHAPE,
                     "%s: %d kv heads of %d channels in %lld pages of %d tokens (head_dim 64, 128 or 256, pages of a "
                     "multiple of 16 tokens)",
@@ -35,6 +35,9 @@ ggq_status cache_checks(ggq_ctx* c, const ggq_kv_cache* kv, const char* op) {
         return fail(c, GGQ_ERR_INVALID_ARG, "%s: cache pools must be 16-byte aligned", op);
     return GGQ_OK;
 }
+
+// A page's 16-token groups as a multiplier for division (exact or one too large).
+uint32_t page_magic(int page_size) { return static_cast<uint32_t>((1ull << 32) / (page_size / 16) + 1); }
 
 // Partial results of items that two or more CTAs share, for the widest heads.
 size_t attn_scratch() { return align_up(2ull * kAttnMaxCtas * attn_part_floats(256) * sizeof(float)); }
@@ -61,7 +64,7 @@ ggq_status kv_params(ggq_ctx* c, const ggq_kv_cache* kv, int dtype, const void* 
         return fail(c, GGQ_ERR_INVALID_ARG, "%s: rows must start at multiples of 4 elements (pointers and strides)", op);
     *p = KvParams{{static_cast<uint8_t*>(kv->k), kv->k_type == GGQ_TYPE_Q4_0},
                   {static_cast<uint8_t*>(kv->v), kv->v_type == GGQ_TYPE_Q4_0},
-                  kv->n_kv_heads, kv->head_dim, kv->page_size, kv->n_pages * kv->page_size,
+                  kv->n_kv_heads, kv->head_dim, kv->page_size, page_magic(kv->page_size), 1, kv->n_pages * kv->page_size,
                   slots, T, k, v, k_token, k_head, v_token, v_head, &c->ctrl->err};
     return GGQ_OK;
 }
@@ -155,7 +158,7 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     p.G = a->n_heads / kv->n_kv_heads;
     p.D = kv->head_dim;
     p.page = kv->page_size;
-    p.page_magic = static_cast<uint32_t>((1ull << 32) / (kv->page_size / 16) + 1);
+    p.page_magic = page_magic(kv->page_size);
     p.k_q4 = kv->k_type == GGQ_TYPE_Q4_0;
     p.v_q4 = kv->v_type == GGQ_TYPE_Q4_0;
     p.max_q = static_cast<int>(!a->q_start ? 1 : a->max_q < a->n_tokens ? a->max_q : a->n_tokens);

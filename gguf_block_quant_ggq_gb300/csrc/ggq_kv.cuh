@@ -27,6 +27,8 @@ struct KvPool {
 struct KvParams {
     KvPool k, v;
     int H, D, page;
+    uint32_t page_magic;         // 2^32 / (page / 16) + 1
+    int heads_at_once;           // heads of a CTA
     int64_t n_slots;             // pages * page_size
     const int64_t* slots;
     int64_t n;
