@@ -14,6 +14,11 @@ cudaError_t launch_attention(const AttnParams& p, int nsm, cudaStream_t s) {
         if (p.D == 128) return launch_attn_prompt_128(p, s);
         return launch_attn_prompt_256(p, s);
     }
+    if (p.dtype == 0 && rows >= kPromptRows && rows <= 64ll * 65535) {
+        if (p.D == 64) return launch_attn_rows_64(p, s);
+        if (p.D == 128) return launch_attn_rows_128(p, s);
+        return launch_attn_rows_256(p, s);
+    }
     if (p.D == 64) return launch_attn_stream_64(p, nsm, s);
     if (p.D == 128) return launch_attn_stream_128(p, nsm, s);
     return launch_attn_stream_256(p, nsm, s);

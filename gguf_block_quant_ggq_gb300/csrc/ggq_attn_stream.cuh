@@ -273,6 +273,406 @@ __device__ __forceinline__ void attn_out4(const AttnParams& p, const AttnSeq& s,
     else st4(static_cast<__nv_bfloat16*>(p.out) + at, v);
 }
 
+// A warp's query rows (8, or 16) against units of the cache: what a thread keeps of
+// them, and one step.  A thread's rows: g (16 rows: and g + 8).
+template <bool K4, bool V4, int D, int MODE, int UNIT>
+struct AttnRows {
+    static constexpr bool TWO = MODE == A_HALF16;  // operand rows 8..15 are query rows of their own
+    static constexpr int RS = TWO ? 2 : 1, NB = D / 32, KS = D / 16, NT = D / 8;
+    static constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
+    static constexpr float kLog2e = 1.44269504088896340736f;
+    // power of two that lifts the probabilities: p * lift * (largest value scale) stays below 32000;
+    // fp16 probabilities (16-bit activations) must not pass 2^15 themselves
+    static constexpr float kMaxLift = MODE == A_SPLIT8 ? 40.0f : 15.0f;
+
+    float xs[RS];                    // score of an accumulator unit (plain: times log2 e)
+    int pos[RS], first_key[RS];
+    float offset[NB][4], slope[RS];  // -offset * sum of the queries of a block, as an accumulator
+    int whole_begin, whole_end;      // groups that every row sees whole
+    bool plain;                      // no cap, no slopes
+    float m[RS], l[RS];              // reference maximum and sum
+    float2 tot[RS][NT];              // channels 8 n + 2 t, + 1
+    float lift, dlimit;
+
+    // Query rows r0 .. of an item -> operand fragments in s_q (k-steps j with j % PARTS == part) and what a
+    // thread keeps of its rows; nothing seen yet.
+    template <int PARTS>
+    __device__ __forceinline__ void begin(const AttnParams& p, const AttnSeq& sq, int hk, int r0, int r_end, uint4* s_q,
+                                          int part, int lane) {
+        const int g8 = lane >> 2, t4 = lane & 3, from = sq.len - sq.rows;
+        {
+            float4 x[RS][KS];
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs)  // rows past the end repeat the last one
+                attn_row<KS>(p, sq, hk, min(r0 + g8 + 8 * rs, r_end - 1), t4, x[rs]);
+            float up[RS];
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    const float4 y = x[rs][j];
+                    amax = fmaxf(fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y))), fmaxf(fabsf(y.z), fabsf(y.w)));
+                }
+                amax = quad_max(amax);
+                const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+                // largest element in [2^13, 2^14); fp32 rows: in [2^10, 2^11), the high halves being integers,
+                // whose products and sums of a block the matrix unit holds exactly
+                const int sh = ex == 128 ? 0 : min((MODE == A_SPLIT8 ? 10 : 13) - ex, 100);
+                up[rs] = copysignf(pow2f(sh), p.scale);
+                xs[rs] = fabsf(p.scale) * scalbnf(1.0f, (MODE == A_SPLIT8 ? 0 : 24) - sh);
+                const int r = min(r0 + g8 + 8 * rs, r_end - 1);
+                pos[rs] = from + r / p.G;
+                first_key[rs] = p.window > 0 ? pos[rs] - p.window + 1 : 0;
+                slope[rs] = p.slopes ? p.slopes[hk * p.G + r % p.G] : 0.0f;
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float sum[RS];
+#pragma unroll
+                for (int rs = 0; rs < RS; ++rs) sum[rs] = 0.0f;
+#pragma unroll
+                for (int j = 2 * b; j < 2 * b + 2; ++j) {
+                    uint32_t frag[4];
+#pragma unroll
+                    for (int rs = 0; rs < RS; ++rs) {
+                        const float4 y = x[rs][j];
+                        const float v[4] = {y.x * up[rs], y.y * up[rs], y.z * up[rs], y.w * up[rs]};
+                        float h[4], l[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            h[i] = MODE == A_SPLIT8 ? rintf(v[i]) : __half2float(__float2half_rn(v[i]));
+                            l[i] = __half2float(__float2half_rn(v[i] - h[i]));
+                            sum[rs] += h[i];
+                        }
+                        // 4-bit quants of channels 2, 3 of four enter 16 times too large
+                        const float k16 = K4 && MODE != A_SPLIT8 ? 0.0625f : 1.0f;
+                        frag[rs] = pack_h2(h[0], h[1]);
+                        frag[2 + rs] = pack_h2(h[2] * k16, h[3] * k16);
+                        if (!TWO) {
+                            frag[1] = MODE == A_SPLIT8 ? pack_h2(l[0], l[1]) : 0u;
+                            frag[3] = MODE == A_SPLIT8 ? pack_h2(l[2] * k16, l[3] * k16) : 0u;
+                        }
+                    }
+                    if ((j & (PARTS - 1)) == part) s_q[j * 32 + lane] = make_uint4(frag[0], frag[1], frag[2], frag[3]);
+                }
+#pragma unroll
+                for (int rs = 0; rs < 2; ++rs)
+                    offset[b][2 * rs] = offset[b][2 * rs + 1] = quad_sum(sum[rs < RS ? rs : 0]) * (K4 ? -8.0f : -128.0f) * 0x1p-24f;
+            }
+        }
+        plain = p.cap <= 0.0f && !p.slopes;
+        if (plain)
+            for (int rs = 0; rs < RS; ++rs) xs[rs] *= kLog2e;
+        whole_end = (from + r0 / p.G + 1) >> 4;
+        const int last_first = p.window > 0 ? from + (r_end - 1) / p.G - p.window + 1 : 0;
+        whole_begin = last_first > 0 ? (last_first + 15) >> 4 : 0;
+#pragma unroll
+        for (int rs = 0; rs < RS; ++rs) {
+            m[rs] = kAttnNone, l[rs] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) tot[rs][n] = both(0.0f);
+        }
+        lift = kMaxLift;
+        dlimit = 32000.0f * pow2f(-static_cast<int>(kMaxLift));
+    }
+
+    // A unit: groups g .. g + UNIT - 1, their key blobs at kb and value blobs at vb.
+    __device__ __forceinline__ void unit(const AttnParams& p, const uint4* s_q, const uint8_t* kb, const uint8_t* vb, int g,
+                                         int len, int lane) {
+        const int t4 = lane & 3;
+        // ---- scores, index 4 group + 2 octet + e: keys 2 t + e of the octet
+        constexpr int KW = K4 ? NB : KS;  // words of an octet
+        float sc[RS][4 * UNIT];
+        uint32_t kw[UNIT][2 * KW];
+        float kd[UNIT][2][2][NB];  // scales of keys 8 o + 2 t + e
+#pragma unroll
+        for (int c = 0; c < UNIT; ++c) {
+            const uint8_t* const blob = kb + c * kKB;
+#pragma unroll
+            for (int v = 0; v < KW / 2; ++v) {
+                const uint4 q = *reinterpret_cast<const uint4*>(blob + (v * 32 + lane) * 16);
+                kw[c][4 * v] = q.x, kw[c][4 * v + 1] = q.y, kw[c][4 * v + 2] = q.z, kw[c][4 * v + 3] = q.w;
+            }
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const uint32_t* const d = reinterpret_cast<const uint32_t*>(
+                    blob + kv_quant_bytes(K4, D) + (8 * o + 2 * t4) * NB * 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i) {
+                        const float2 f = half2_f32(d[e * (NB / 2) + i]);
+                        kd[c][o][e][2 * i] = f.x, kd[c][o][e][2 * i + 1] = f.y;
+                    }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint4 qa = s_q[(2 * b) * 32 + lane], qb = s_q[(2 * b + 1) * 32 + lane];
+            const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w}, fb[4] = {qb.x, qb.y, qb.z, qb.w};
+#pragma unroll
+            for (int c = 0; c < UNIT; ++c)
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    float cc[4];
+                    if constexpr (K4 && MODE == A_SPLIT8) {
+                        const uint32_t q = kw[c][o * NB + b], y = q >> 8;
+                        attn_mma0(cc, fa, h2_sub((q & 0x000F000Fu) | 0x64006400u, 0x64086408u),
+                                  h2_fma((q & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u));
+                        attn_mma(cc, fb, h2_sub((y & 0x000F000Fu) | 0x64006400u, 0x64086408u),
+                                 h2_fma((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u));
+                    } else if constexpr (MODE == A_SPLIT8) {
+                        const uint32_t q = kw[c][o * KS + 2 * b], y = kw[c][o * KS + 2 * b + 1];
+                        attn_mma0(cc, fa, h2_sub(prmt(q, 0x64646464u, 0x4140u), 0x64806480u),
+                                  h2_sub(prmt(q, 0x64646464u, 0x4342u), 0x64806480u));
+                        attn_mma(cc, fb, h2_sub(prmt(y, 0x64646464u, 0x4140u), 0x64806480u),
+                                 h2_sub(prmt(y, 0x64646464u, 0x4342u), 0x64806480u));
+                    } else if constexpr (K4) {
+                        const uint32_t q = kw[c][o * NB + b], y = q >> 8;
+                        attn_mma_c(cc, fa, q & 0x000F000Fu, q & 0x00F000F0u, offset[b]);
+                        attn_mma(cc, fb, y & 0x000F000Fu, y & 0x00F000F0u);
+                    } else {
+                        const uint32_t q = kw[c][o * KS + 2 * b], y = kw[c][o * KS + 2 * b + 1];
+                        attn_mma_c(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u), offset[b]);
+                        attn_mma(cc, fb, prmt(y, 0u, 0x4140u), prmt(y, 0u, 0x4342u));
+                    }
+                    if constexpr (MODE == A_SPLIT8) cc[0] += cc[2], cc[1] += cc[3];
+#pragma unroll
+                    for (int rs = 0; rs < RS; ++rs)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& to = sc[rs][4 * c + 2 * o + e];
+                            to = b ? fmaf(kd[c][o][e][b], cc[2 * rs + e], to) : kd[c][o][e][b] * cc[2 * rs + e];
+                        }
+                }
+        }
+        uint32_t vd[UNIT][4][NB / 2];  // value scales of keys 8 o + 2 t + e, index 2 o + e
+#pragma unroll
+        for (int c = 0; c < UNIT; ++c)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const uint32_t* const d = reinterpret_cast<const uint32_t*>(
+                    vb + c * kVB + kv_quant_bytes(V4, D) + (8 * o + 2 * t4) * NB * 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < NB / 2; ++i) vd[c][2 * o + e][i] = d[e * (NB / 2) + i];
+            }
+
+        // ---- logits in units of log2, masks
+        float lg[RS][4 * UNIT];
+#pragma unroll
+        for (int rs = 0; rs < RS; ++rs)
+#pragma unroll
+            for (int i = 0; i < 4 * UNIT; ++i) lg[rs][i] = sc[rs][i] * xs[rs];
+        if (!plain) {
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs)
+#pragma unroll
+                for (int i = 0; i < 4 * UNIT; ++i) {
+                    const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
+                    float y = lg[rs][i];
+                    if (p.cap > 0.0f) y = attn_cap<MODE>(y, p.cap);
+                    lg[rs][i] = fmaf(slope[rs], static_cast<float>(key - pos[rs]), y) * kLog2e;
+                }
+        }
+        float lowest[RS];  // before the masks: a bound
+#pragma unroll
+        for (int rs = 0; rs < RS; ++rs) {
+            lowest[rs] = lg[rs][0];
+#pragma unroll
+            for (int i = 1; i < 4 * UNIT; ++i) lowest[rs] = fminf(lowest[rs], lg[rs][i]);
+        }
+        if (g < whole_begin || g + UNIT > whole_end) {
+#pragma unroll
+            for (int i = 0; i < 4 * UNIT; ++i) {
+                const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
+#pragma unroll
+                for (int rs = 0; rs < RS; ++rs)
+                    if (key > pos[rs] || key < first_key[rs]) lg[rs][i] = -INFINITY;
+                if (key >= len)  // never written: whatever the place holds
+#pragma unroll
+                    for (int k = 0; k < NB / 2; ++k) vd[i >> 2][i & 3][k] = 0u;
+            }
+        }
+
+        // ---- the unit's maximum is its probabilities' reference
+        float top[RS];
+        bool raise = false;
+#pragma unroll
+        for (int rs = 0; rs < RS; ++rs) {
+            float highest = lg[rs][0];
+#pragma unroll
+            for (int i = 1; i < 4 * UNIT; ++i) highest = fmaxf(highest, lg[rs][i]);
+            top[rs] = quad_max(highest);
+            raise |= top[rs] > m[rs] + 60.0f || lowest[rs] < top[rs] - 28.0f;
+        }
+        uint32_t dm = 0u;
+#pragma unroll
+        for (int c = 0; c < UNIT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < NB / 2; ++k) dm = __vmaxu2(dm, V4 ? vd[c][i][k] & 0x7FFF7FFFu : vd[c][i][k]);
+        raise |= !(half_lo(dm) <= dlimit && half_hi(dm) <= dlimit);  // larger, or not a number
+        bool more = false;   // some probabilities are too small for fp16 beside the unit's largest
+        if (__any_sync(0xffffffffu, raise)) {
+            float dfin = 0.0f;
+            uint32_t spoilt[RS] = {};  // blocks of 32 channels in which a row sees a scale that is not finite
+#pragma unroll
+            for (int c = 0; c < UNIT; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint32_t d = (vd[c][i][b >> 1] >> (16 * (b & 1))) & 0x7FFFu;
+                        if (d < 0x7C00u) {
+                            dfin = fmaxf(dfin, half_lo(d));
+                        } else {
+                            vd[c][i][b >> 1] &= (b & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+                            for (int rs = 0; rs < RS; ++rs)
+                                if (lg[rs][4 * c + i] != -INFINITY) spoilt[rs] |= 1u << b;
+                        }
+                    }
+            dfin = warp_max(dfin);
+            if (dfin > dlimit) {  // the largest times the lift to [2^13, 2^14)
+                const int e = 13 - (static_cast<int>(__float_as_uint(dfin) >> 23) - 127);
+                lift = fminf(static_cast<float>(e), kMaxLift);
+                dlimit = 32000.0f * pow2f(-static_cast<int>(lift));
+            }
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) {
+                spoilt[rs] |= __shfl_xor_sync(0xffffffffu, spoilt[rs], 1);
+                spoilt[rs] |= __shfl_xor_sync(0xffffffffu, spoilt[rs], 2);
+                const bool up = top[rs] > m[rs] + 60.0f;
+                const float a = up ? ex2(m[rs] - top[rs]) : 1.0f;
+                if (up) m[rs] = top[rs];
+                l[rs] *= a;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) tot[rs][n] = mul2(tot[rs][n], both(((spoilt[rs] >> (n >> 2)) & 1u) ? NAN : a));
+#pragma unroll
+                for (int i = 0; i < 4 * UNIT; ++i) more |= lg[rs][i] < top[rs] - 28.0f && lg[rs][i] > m[rs] - 126.0f;
+            }
+            more = __any_sync(0xffffffffu, more);
+        }
+        for (;;) {  // once, but for probabilities more than 2^28 apart: those below wait for a pass of their own
+            float rest[RS], f[RS], pr[RS][4 * UNIT];
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) {
+                const float ref = fmaxf(top[rs], kAttnNone);  // a unit that the row does not see: all probabilities 0
+                const float sub = ref - lift;
+                rest[rs] = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 4 * UNIT; ++i) {
+                    pr[rs][i] = ex2(lg[rs][i] - sub);
+                    if (more) {
+                        if (lg[rs][i] < ref - 28.0f) {
+                            pr[rs][i] = 0.0f;
+                            rest[rs] = fmaxf(rest[rs], lg[rs][i]);
+                        } else {
+                            lg[rs][i] = -INFINITY;
+                        }
+                    }
+                }
+                float2 sum = make_float2(pr[rs][0], pr[rs][1]);
+#pragma unroll
+                for (int i = 2; i < 4 * UNIT; i += 2) sum = add2(sum, make_float2(pr[rs][i], pr[rs][i + 1]));
+                f[rs] = ex2(sub - m[rs]);
+                l[rs] = fmaf(sum.x + sum.y, f[rs], l[rs]);
+            }
+            uint32_t ph[RS][2 * UNIT];  // 16-bit activations: the probabilities in fp16
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs)
+#pragma unroll
+                for (int i = 0; i < 2 * UNIT; ++i) ph[rs][i] = MODE == A_SPLIT8 ? 0u : pack_h2(pr[rs][2 * i], pr[rs][2 * i + 1]);
+
+            // ---- values, block by block of 32 channels
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float acc[4][4];
+#pragma unroll
+                for (int c = 0; c < UNIT; ++c) {
+                    uint32_t a[4];
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const uint32_t d2 = prmt(vd[c][2 * o][b >> 1], vd[c][2 * o + 1][b >> 1], (b & 1) ? 0x7632u : 0x5410u);
+                        if constexpr (MODE == A_SPLIT8) {
+                            // rounded to fp16, and 2^12 times what that leaves
+                            const float2 v = mul2(make_float2(pr[0][4 * c + 2 * o], pr[0][4 * c + 2 * o + 1]), half2_f32(d2));
+                            const uint32_t h = pack_h2(v.x, v.y);
+                            const float2 hv = half2_f32(h);
+                            const float2 r = mul2(add2(v, make_float2(-hv.x, -hv.y)), both(4096.0f));
+                            a[2 * o] = h;
+                            a[2 * o + 1] = pack_h2(r.x, r.y);
+                        } else {
+                            a[2 * o] = h2_mul(ph[0][2 * c + o], d2);
+                            a[2 * o + 1] = TWO ? h2_mul(ph[RS - 1][2 * c + o], d2) : attn_any();
+                        }
+                    }
+                    const uint8_t* const blob = vb + c * kVB;
+                    if constexpr (V4) {
+                        const uint2 u2 = *reinterpret_cast<const uint2*>(blob + ((b >> 1) * 32 + lane) * 16 + (b & 1) * 8);
+                        const uint32_t uw[2] = {u2.x, u2.y};
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t q = uw[k], y = q >> 8;
+                            // 1024 + q - 1032, and (1024 + 16 q) / 16 - 72
+                            const uint32_t e0 = h2_sub((q & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+                            const uint32_t e1 = h2_sub((y & 0x000F000Fu) | 0x64006400u, 0x64086408u);
+                            const uint32_t o0 = h2_fma((q & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+                            const uint32_t o1 = h2_fma((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
+                            if (c == 0) attn_mma0(acc[2 * k], a, e0, e1), attn_mma0(acc[2 * k + 1], a, o0, o1);
+                            else attn_mma(acc[2 * k], a, e0, e1), attn_mma(acc[2 * k + 1], a, o0, o1);
+                        }
+                    } else {
+                        const uint4 u4 = *reinterpret_cast<const uint4*>(blob + (b * 32 + lane) * 16);
+                        const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {  // 1024 + (q + 128) - 1152
+                            const uint32_t e0 = h2_sub(prmt(uw[k], 0x64646464u, 0x4140u), 0x64806480u);
+                            const uint32_t e1 = h2_sub(prmt(uw[k], 0x64646464u, 0x4342u), 0x64806480u);
+                            if (c == 0) attn_mma0(acc[k], a, e0, e1);
+                            else attn_mma(acc[k], a, e0, e1);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float2 r = make_float2(acc[k][0], acc[k][1]);
+                    if constexpr (MODE == A_SPLIT8) r = fma2(make_float2(acc[k][2], acc[k][3]), both(0x1p-12f), r);
+                    tot[0][4 * b + k] = fma2(r, both(f[0]), tot[0][4 * b + k]);
+                    if constexpr (TWO)
+                        tot[RS - 1][4 * b + k] = fma2(make_float2(acc[k][2], acc[k][3]), both(f[RS - 1]), tot[RS - 1][4 * b + k]);
+                }
+            }
+            if (!more) break;
+            more = false;
+#pragma unroll
+            for (int rs = 0; rs < RS; ++rs) {
+                top[rs] = quad_max(rest[rs]);
+                more |= top[rs] > m[rs] - 126.0f;
+            }
+            more = __any_sync(0xffffffffu, more);
+            if (!more) break;
+        }
+    }
+
+    // The reference moves to the sum's power of two (it may lag the largest score by 2^60); the row's sum.
+    __device__ __forceinline__ float settle_reference(int rs, float* factor) {
+        float sum = quad_sum(l[rs]);
+        const int e = static_cast<int>(__float_as_uint(sum) >> 23) - 127;
+        *factor = 1.0f;
+        if (sum > 0.0f && e < 127) {
+            *factor = pow2f(-e);
+            sum *= *factor;
+            m[rs] += static_cast<float>(e);
+        }
+        return sum;
+    }
+};
+
 // Position of the share [lo, ...) in the list of all groups: the runs' exclusive
 // prefix sums in s_scan (128), each run `per` sequences.
 template <int UNIT>
@@ -416,9 +816,7 @@ template <bool K4, bool V4, int D, int MODE>
 __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas)
     k_attn_stream(const __grid_constant__ AttnParams p) {
     using SM = AttnSmem<K4, V4, D, MODE>;
-    constexpr int kRows = SM::kRows, NB = D / 32, KS = D / 16, NT = D / 8, S = SM::kStages, UNIT = SM::kUnit;
-    constexpr bool TWO = MODE == A_HALF16;  // operand rows 8..15 are query rows of their own
-    constexpr int RS = TWO ? 2 : 1;
+    constexpr int kRows = SM::kRows, NT = D / 8, S = SM::kStages, UNIT = SM::kUnit, RS = MODE == A_HALF16 ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
     float* const s_tot = reinterpret_cast<float*>(smem + SM::oTot);
     uint4* const s_q = reinterpret_cast<uint4*>(smem + SM::oQ);
@@ -553,97 +951,10 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         const int64_t at0 = hi - w.left;               // the segment's first position
         const AttnTile tile = attn_tile(p, sq, w.item, kRows);
         const int hk = tile.hk, r0 = tile.r0, r_end = tile.r_end;
-        const int from = sq.len - sq.rows;
-
-        // query rows -> operand registers (through shared memory, each warp a part of the k-steps)
-        float xs[RS];                                   // score of an accumulator unit, times log2 e
-        int pos[RS], first_key[RS];
-        float offset[NB][4], slope[RS];                 // -offset * sum of the queries of a block, as an accumulator
-        {
-            float4 x[RS][KS];
-#pragma unroll
-            for (int rs = 0; rs < RS; ++rs)  // rows past the end repeat the last one
-                attn_row<KS>(p, sq, hk, min(r0 + g8 + 8 * rs, r_end - 1), t4, x[rs]);
-            float up[RS];
-#pragma unroll
-            for (int rs = 0; rs < RS; ++rs) {
-                float amax = 0.0f;
-#pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                    const float4 y = x[rs][j];
-                    amax = fmaxf(fmaxf(amax, fmaxf(fabsf(y.x), fabsf(y.y))), fmaxf(fabsf(y.z), fabsf(y.w)));
-                }
-                amax = quad_max(amax);
-                const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-                // largest element in [2^13, 2^14); fp32 rows: in [2^10, 2^11), the high halves being integers,
-                // whose products and sums of a block the matrix unit holds exactly
-                const int sh = ex == 128 ? 0 : min((MODE == A_SPLIT8 ? 10 : 13) - ex, 100);
-                up[rs] = copysignf(pow2f(sh), p.scale);
-                xs[rs] = fabsf(p.scale) * scalbnf(1.0f, (MODE == A_SPLIT8 ? 0 : 24) - sh);
-                const int r = min(r0 + g8 + 8 * rs, r_end - 1);
-                pos[rs] = from + r / p.G;
-                first_key[rs] = p.window > 0 ? pos[rs] - p.window + 1 : 0;
-                slope[rs] = p.slopes ? p.slopes[hk * p.G + r % p.G] : 0.0f;
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                float sum[RS];
-#pragma unroll
-                for (int rs = 0; rs < RS; ++rs) sum[rs] = 0.0f;
-#pragma unroll
-                for (int j = 2 * b; j < 2 * b + 2; ++j) {
-                    uint32_t frag[4];
-#pragma unroll
-                    for (int rs = 0; rs < RS; ++rs) {
-                        const float4 y = x[rs][j];
-                        const float v[4] = {y.x * up[rs], y.y * up[rs], y.z * up[rs], y.w * up[rs]};
-                        float h[4], l[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            h[i] = MODE == A_SPLIT8 ? rintf(v[i]) : __half2float(__float2half_rn(v[i]));
-                            l[i] = __half2float(__float2half_rn(v[i] - h[i]));
-                            sum[rs] += h[i];
-                        }
-                        // 4-bit quants of channels 2, 3 of four enter 16 times too large
-                        const float k16 = K4 && MODE != A_SPLIT8 ? 0.0625f : 1.0f;
-                        frag[rs] = pack_h2(h[0], h[1]);
-                        frag[2 + rs] = pack_h2(h[2] * k16, h[3] * k16);
-                        if (!TWO) {
-                            frag[1] = MODE == A_SPLIT8 ? pack_h2(l[0], l[1]) : 0u;
-                            frag[3] = MODE == A_SPLIT8 ? pack_h2(l[2] * k16, l[3] * k16) : 0u;
-                        }
-                    }
-                    if ((j & (kAttnWarps - 1)) == warp) s_q[j * 32 + lane] = make_uint4(frag[0], frag[1], frag[2], frag[3]);
-                }
-#pragma unroll
-                for (int rs = 0; rs < 2; ++rs)
-                    offset[b][2 * rs] = offset[b][2 * rs + 1] = quad_sum(sum[rs < RS ? rs : 0]) * (K4 ? -8.0f : -128.0f) * 0x1p-24f;
-            }
-        }
+        AttnRows<K4, V4, D, MODE, UNIT> rows;
+        rows.template begin<kAttnWarps>(p, sq, hk, r0, r_end, s_q, warp, lane);
         __syncthreads();
         settle();
-        const bool plain = p.cap <= 0.0f && !p.slopes;
-        constexpr float kLog2e = 1.44269504088896340736f;
-        if (plain)
-            for (int rs = 0; rs < RS; ++rs) xs[rs] *= kLog2e;
-        // groups that every row of the tile sees whole
-        const int whole_end = (from + r0 / p.G + 1) >> 4;
-        const int last_first = p.window > 0 ? from + (r_end - 1) / p.G - p.window + 1 : 0;
-        const int whole_begin = last_first > 0 ? (last_first + 15) >> 4 : 0;
-
-        float m[RS], l[RS];
-        float2 tot[RS][NT];
-#pragma unroll
-        for (int rs = 0; rs < RS; ++rs) {
-            m[rs] = kAttnNone, l[rs] = 0.0f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) tot[rs][n] = both(0.0f);
-        }
-        // power of two that lifts the probabilities: p * lift * (largest value scale) stays below 32000;
-        // fp16 probabilities (16-bit activations) must not pass 2^15 themselves
-        constexpr float kMaxLift = MODE == A_SPLIT8 ? 40.0f : 15.0f;
-        float lift = kMaxLift, dlimit = 32000.0f * pow2f(-static_cast<int>(kMaxLift));
-
         for (int u = ua + warp; u < ub; u += kAttnWarps) {
             const int at = warp * S + slot, g = sq.glo + UNIT * u;
             if (!__all_sync(0xffffffffu, mbar_test(s_full + at, phase))) {
@@ -658,282 +969,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             const uint8_t* const kb = smem + SM::oRing + at * SM::kStage;
             const uint8_t* const vb = kb + UNIT * SM::kKB;
 
-            // ---- scores, index 4 group + 2 octet + e: keys 2 t + e of the octet
-            constexpr int KW = K4 ? NB : KS;  // words of an octet
-            float sc[RS][4 * UNIT];
-            uint32_t kw[UNIT][2 * KW];
-            float kd[UNIT][2][2][NB];  // scales of keys 8 o + 2 t + e
-#pragma unroll
-            for (int c = 0; c < UNIT; ++c) {
-                const uint8_t* const blob = kb + c * SM::kKB;
-#pragma unroll
-                for (int v = 0; v < KW / 2; ++v) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(blob + (v * 32 + lane) * 16);
-                    kw[c][4 * v] = q.x, kw[c][4 * v + 1] = q.y, kw[c][4 * v + 2] = q.z, kw[c][4 * v + 3] = q.w;
-                }
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const uint32_t* const d = reinterpret_cast<const uint32_t*>(
-                        blob + kv_quant_bytes(K4, D) + (8 * o + 2 * t4) * NB * 2);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) {
-                            const float2 f = half2_f32(d[e * (NB / 2) + i]);
-                            kd[c][o][e][2 * i] = f.x, kd[c][o][e][2 * i + 1] = f.y;
-                        }
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const uint4 qa = s_q[(2 * b) * 32 + lane], qb = s_q[(2 * b + 1) * 32 + lane];
-                const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w}, fb[4] = {qb.x, qb.y, qb.z, qb.w};
-#pragma unroll
-                for (int c = 0; c < UNIT; ++c)
-#pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        float cc[4];
-                        if constexpr (K4 && MODE == A_SPLIT8) {
-                            const uint32_t q = kw[c][o * NB + b], y = q >> 8;
-                            attn_mma0(cc, fa, h2_sub((q & 0x000F000Fu) | 0x64006400u, 0x64086408u),
-                                      h2_fma((q & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u));
-                            attn_mma(cc, fb, h2_sub((y & 0x000F000Fu) | 0x64006400u, 0x64086408u),
-                                     h2_fma((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u));
-                        } else if constexpr (MODE == A_SPLIT8) {
-                            const uint32_t q = kw[c][o * KS + 2 * b], y = kw[c][o * KS + 2 * b + 1];
-                            attn_mma0(cc, fa, h2_sub(prmt(q, 0x64646464u, 0x4140u), 0x64806480u),
-                                      h2_sub(prmt(q, 0x64646464u, 0x4342u), 0x64806480u));
-                            attn_mma(cc, fb, h2_sub(prmt(y, 0x64646464u, 0x4140u), 0x64806480u),
-                                     h2_sub(prmt(y, 0x64646464u, 0x4342u), 0x64806480u));
-                        } else if constexpr (K4) {
-                            const uint32_t q = kw[c][o * NB + b], y = q >> 8;
-                            attn_mma_c(cc, fa, q & 0x000F000Fu, q & 0x00F000F0u, offset[b]);
-                            attn_mma(cc, fb, y & 0x000F000Fu, y & 0x00F000F0u);
-                        } else {
-                            const uint32_t q = kw[c][o * KS + 2 * b], y = kw[c][o * KS + 2 * b + 1];
-                            attn_mma_c(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u), offset[b]);
-                            attn_mma(cc, fb, prmt(y, 0u, 0x4140u), prmt(y, 0u, 0x4342u));
-                        }
-                        if constexpr (MODE == A_SPLIT8) cc[0] += cc[2], cc[1] += cc[3];
-#pragma unroll
-                        for (int rs = 0; rs < RS; ++rs)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float& to = sc[rs][4 * c + 2 * o + e];
-                                to = b ? fmaf(kd[c][o][e][b], cc[2 * rs + e], to) : kd[c][o][e][b] * cc[2 * rs + e];
-                            }
-                    }
-            }
-            uint32_t vd[UNIT][4][NB / 2];  // value scales of keys 8 o + 2 t + e, index 2 o + e
-#pragma unroll
-            for (int c = 0; c < UNIT; ++c)
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const uint32_t* const d = reinterpret_cast<const uint32_t*>(
-                        vb + c * SM::kVB + kv_quant_bytes(V4, D) + (8 * o + 2 * t4) * NB * 2);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int i = 0; i < NB / 2; ++i) vd[c][2 * o + e][i] = d[e * (NB / 2) + i];
-                }
-
-            // ---- logits in units of log2, masks
-            float lg[RS][4 * UNIT];
-#pragma unroll
-            for (int rs = 0; rs < RS; ++rs)
-#pragma unroll
-                for (int i = 0; i < 4 * UNIT; ++i) lg[rs][i] = sc[rs][i] * xs[rs];
-            if (!plain) {
-#pragma unroll
-                for (int rs = 0; rs < RS; ++rs)
-#pragma unroll
-                    for (int i = 0; i < 4 * UNIT; ++i) {
-                        const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
-                        float y = lg[rs][i];
-                        if (p.cap > 0.0f) y = attn_cap<MODE>(y, p.cap);
-                        lg[rs][i] = fmaf(slope[rs], static_cast<float>(key - pos[rs]), y) * kLog2e;
-                    }
-            }
-            float lowest[RS];  // before the masks: a bound
-#pragma unroll
-            for (int rs = 0; rs < RS; ++rs) {
-                lowest[rs] = lg[rs][0];
-#pragma unroll
-                for (int i = 1; i < 4 * UNIT; ++i) lowest[rs] = fminf(lowest[rs], lg[rs][i]);
-            }
-            if (g < whole_begin || g + UNIT > whole_end) {
-#pragma unroll
-                for (int i = 0; i < 4 * UNIT; ++i) {
-                    const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
-#pragma unroll
-                    for (int rs = 0; rs < RS; ++rs)
-                        if (key > pos[rs] || key < first_key[rs]) lg[rs][i] = -INFINITY;
-                    if (key >= sq.len)  // never written: whatever the place holds
-#pragma unroll
-                        for (int k = 0; k < NB / 2; ++k) vd[i >> 2][i & 3][k] = 0u;
-                }
-            }
-
-            // ---- the unit's maximum is its probabilities' reference
-            float top[RS];
-            bool raise = false;
-#pragma unroll
-            for (int rs = 0; rs < RS; ++rs) {
-                float highest = lg[rs][0];
-#pragma unroll
-                for (int i = 1; i < 4 * UNIT; ++i) highest = fmaxf(highest, lg[rs][i]);
-                top[rs] = quad_max(highest);
-                raise |= top[rs] > m[rs] + 60.0f || lowest[rs] < top[rs] - 28.0f;
-            }
-            uint32_t dm = 0u;
-#pragma unroll
-            for (int c = 0; c < UNIT; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int k = 0; k < NB / 2; ++k) dm = __vmaxu2(dm, V4 ? vd[c][i][k] & 0x7FFF7FFFu : vd[c][i][k]);
-            raise |= !(half_lo(dm) <= dlimit && half_hi(dm) <= dlimit);  // larger, or not a number
-            bool more = false;   // some probabilities are too small for fp16 beside the unit's largest
-            if (__any_sync(0xffffffffu, raise)) {
-                float dfin = 0.0f;
-                uint32_t spoilt[RS] = {};  // blocks of 32 channels in which a row sees a scale that is not finite
-#pragma unroll
-                for (int c = 0; c < UNIT; ++c)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            const uint32_t d = (vd[c][i][b >> 1] >> (16 * (b & 1))) & 0x7FFFu;
-                            if (d < 0x7C00u) {
-                                dfin = fmaxf(dfin, half_lo(d));
-                            } else {
-                                vd[c][i][b >> 1] &= (b & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-#pragma unroll
-                                for (int rs = 0; rs < RS; ++rs)
-                                    if (lg[rs][4 * c + i] != -INFINITY) spoilt[rs] |= 1u << b;
-                            }
-                        }
-                dfin = warp_max(dfin);
-                if (dfin > dlimit) {  // the largest times the lift to [2^13, 2^14)
-                    const int e = 13 - (static_cast<int>(__float_as_uint(dfin) >> 23) - 127);
-                    lift = fminf(static_cast<float>(e), kMaxLift);
-                    dlimit = 32000.0f * pow2f(-static_cast<int>(lift));
-                }
-#pragma unroll
-                for (int rs = 0; rs < RS; ++rs) {
-                    spoilt[rs] |= __shfl_xor_sync(0xffffffffu, spoilt[rs], 1);
-                    spoilt[rs] |= __shfl_xor_sync(0xffffffffu, spoilt[rs], 2);
-                    const bool up = top[rs] > m[rs] + 60.0f;
-                    const float a = up ? ex2(m[rs] - top[rs]) : 1.0f;
-                    if (up) m[rs] = top[rs];
-                    l[rs] *= a;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) tot[rs][n] = mul2(tot[rs][n], both(((spoilt[rs] >> (n >> 2)) & 1u) ? NAN : a));
-#pragma unroll
-                    for (int i = 0; i < 4 * UNIT; ++i) more |= lg[rs][i] < top[rs] - 28.0f && lg[rs][i] > m[rs] - 126.0f;
-                }
-                more = __any_sync(0xffffffffu, more);
-            }
-            for (;;) {  // once, but for probabilities more than 2^28 apart: those below wait for a pass of their own
-                float rest[RS], f[RS], pr[RS][4 * UNIT];
-#pragma unroll
-                for (int rs = 0; rs < RS; ++rs) {
-                    const float ref = fmaxf(top[rs], kAttnNone);  // a unit that the row does not see: all probabilities 0
-                    const float sub = ref - lift;
-                    rest[rs] = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 4 * UNIT; ++i) {
-                        pr[rs][i] = ex2(lg[rs][i] - sub);
-                        if (more) {
-                            if (lg[rs][i] < ref - 28.0f) {
-                                pr[rs][i] = 0.0f;
-                                rest[rs] = fmaxf(rest[rs], lg[rs][i]);
-                            } else {
-                                lg[rs][i] = -INFINITY;
-                            }
-                        }
-                    }
-                    float2 sum = make_float2(pr[rs][0], pr[rs][1]);
-#pragma unroll
-                    for (int i = 2; i < 4 * UNIT; i += 2) sum = add2(sum, make_float2(pr[rs][i], pr[rs][i + 1]));
-                    f[rs] = ex2(sub - m[rs]);
-                    l[rs] = fmaf(sum.x + sum.y, f[rs], l[rs]);
-                }
-                uint32_t ph[RS][2 * UNIT];  // 16-bit activations: the probabilities in fp16
-#pragma unroll
-                for (int rs = 0; rs < RS; ++rs)
-#pragma unroll
-                    for (int i = 0; i < 2 * UNIT; ++i) ph[rs][i] = MODE == A_SPLIT8 ? 0u : pack_h2(pr[rs][2 * i], pr[rs][2 * i + 1]);
-
-                // ---- values, block by block of 32 channels
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float acc[4][4];
-#pragma unroll
-                    for (int c = 0; c < UNIT; ++c) {
-                        uint32_t a[4];
-#pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            const uint32_t d2 = prmt(vd[c][2 * o][b >> 1], vd[c][2 * o + 1][b >> 1], (b & 1) ? 0x7632u : 0x5410u);
-                            if constexpr (MODE == A_SPLIT8) {
-                                // rounded to fp16, and 2^12 times what that leaves
-                                const float2 v = mul2(make_float2(pr[0][4 * c + 2 * o], pr[0][4 * c + 2 * o + 1]), half2_f32(d2));
-                                const uint32_t h = pack_h2(v.x, v.y);
-                                const float2 hv = half2_f32(h);
-                                const float2 r = mul2(add2(v, make_float2(-hv.x, -hv.y)), both(4096.0f));
-                                a[2 * o] = h;
-                                a[2 * o + 1] = pack_h2(r.x, r.y);
-                            } else {
-                                a[2 * o] = h2_mul(ph[0][2 * c + o], d2);
-                                a[2 * o + 1] = TWO ? h2_mul(ph[RS - 1][2 * c + o], d2) : attn_any();
-                            }
-                        }
-                        const uint8_t* const blob = vb + c * SM::kVB;
-                        if constexpr (V4) {
-                            const uint2 u2 = *reinterpret_cast<const uint2*>(blob + ((b >> 1) * 32 + lane) * 16 + (b & 1) * 8);
-                            const uint32_t uw[2] = {u2.x, u2.y};
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const uint32_t q = uw[k], y = q >> 8;
-                                // 1024 + q - 1032, and (1024 + 16 q) / 16 - 72
-                                const uint32_t e0 = h2_sub((q & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-                                const uint32_t e1 = h2_sub((y & 0x000F000Fu) | 0x64006400u, 0x64086408u);
-                                const uint32_t o0 = h2_fma((q & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
-                                const uint32_t o1 = h2_fma((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD480D480u);
-                                if (c == 0) attn_mma0(acc[2 * k], a, e0, e1), attn_mma0(acc[2 * k + 1], a, o0, o1);
-                                else attn_mma(acc[2 * k], a, e0, e1), attn_mma(acc[2 * k + 1], a, o0, o1);
-                            }
-                        } else {
-                            const uint4 u4 = *reinterpret_cast<const uint4*>(blob + (b * 32 + lane) * 16);
-                            const uint32_t uw[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {  // 1024 + (q + 128) - 1152
-                                const uint32_t e0 = h2_sub(prmt(uw[k], 0x64646464u, 0x4140u), 0x64806480u);
-                                const uint32_t e1 = h2_sub(prmt(uw[k], 0x64646464u, 0x4342u), 0x64806480u);
-                                if (c == 0) attn_mma0(acc[k], a, e0, e1);
-                                else attn_mma(acc[k], a, e0, e1);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float2 r = make_float2(acc[k][0], acc[k][1]);
-                        if constexpr (MODE == A_SPLIT8) r = fma2(make_float2(acc[k][2], acc[k][3]), both(0x1p-12f), r);
-                        tot[0][4 * b + k] = fma2(r, both(f[0]), tot[0][4 * b + k]);
-                        if constexpr (TWO)
-                            tot[RS - 1][4 * b + k] = fma2(make_float2(acc[k][2], acc[k][3]), both(f[RS - 1]), tot[RS - 1][4 * b + k]);
-                    }
-                }
-                if (!more) break;
-                more = false;
-#pragma unroll
-                for (int rs = 0; rs < RS; ++rs) {
-                    top[rs] = quad_max(rest[rs]);
-                    more |= top[rs] > m[rs] - 126.0f;
-                }
-                more = __any_sync(0xffffffffu, more);
-                if (!more) break;
-            }
+            rows.unit(p, s_q, kb, vb, g, sq.len, lane);
             __syncwarp();
             fetch(at);
             if (++slot == S) slot = 0, phase ^= 1u;
@@ -945,21 +981,14 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         float* const s_mine = s_tot + warp * 8 * SM::kRowPitch;
 #pragma unroll
         for (int rs = 0; rs < RS; ++rs) {
-            // the reference moves to the sum's power of two (it may lag the largest score by 2^60)
-            float sum = quad_sum(l[rs]);
-            const int e = static_cast<int>(__float_as_uint(sum) >> 23) - 127;
-            float a = 1.0f;
-            if (sum > 0.0f && e < 127) {
-                a = pow2f(-e);
-                sum *= a;
-                m[rs] += static_cast<float>(e);
-            }
+            float a;
+            const float sum = rows.settle_reference(rs, &a);
             if (rs > 0) __syncthreads();
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<float2*>(s_mine + g8 * SM::kRowPitch + 8 * n + 2 * t4) = mul2(tot[rs][n], both(a));
+                *reinterpret_cast<float2*>(s_mine + g8 * SM::kRowPitch + 8 * n + 2 * t4) = mul2(rows.tot[rs][n], both(a));
             if (t4 == 0) {
-                s_m[warp * 8 + g8] = m[rs];
+                s_m[warp * 8 + g8] = rows.m[rs];
                 s_l[warp * 8 + g8] = sum;
             }
             __syncthreads();
