@@ -207,7 +207,7 @@ ggq_status ggq_moe_route(ggq_ctx* c, const ggq_router* r, int dtype, const void*
         ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(r->bias)) & 3))
         return fail(c, GGQ_ERR_INVALID_ARG, "moe_route: misaligned pointer");
     const RouteParams p{logits, r->bias, T, static_cast<int>(E), r->top_k, r->n_groups, r->top_groups, r->group_best,
-                        r->scoring == GGQ_SCORE_SIGMOID, r->normalize != 0, r->scale, ids, weights};
+                        r->scoring == GGQ_SCORE_SIGMOID, r->normalize != 0, 0, r->scale, ids, weights};
     const cudaError_t e = launch_route(p, dt, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GGQ_OK : cuda_fail(c, e, "moe_route launch");
 }

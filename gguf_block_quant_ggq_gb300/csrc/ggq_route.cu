@@ -7,9 +7,14 @@
 // thousand tokens bound by the k dependent rounds of the selection, not by
 // bytes.
 //
-// One warp a token: lane l holds experts l, l + 32, ... as order-preserving
-// 32-bit keys, in registers.  A round is a maximum over the lane's keys, one
-// redux for the warp's largest key and one for the lowest expert that has it.
+// One warp a token: lane l holds experts NV l .. NV l + NV - 1 as order-preserving
+// 32-bit keys, in registers, so that lanes and places in them follow the experts'
+// order.  A round of the choice is one redux for the warp's largest key, one ballot
+// for the first lane that has it, and that lane's own search; groups of whole lanes
+// are scored by butterflies over all groups at once.  Bound by its instructions at
+// many tokens (4096 tokens of 256 experts in 8 groups: 11 us, 1250 instructions a
+// token, where the logits' 4 MB take under 1 us; with the experts interleaved over the
+// lanes and groups scored one after another 16 us and 2000), by the launch at few (4 us).
 #include "ggq_device.cuh"
 #include "ggq_internal.h"
 #include "ggq_kv.cuh"
@@ -33,9 +38,14 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 
 // score of logit x; m: the row's maximum (softmax numerators).  A NaN scores 0.
 __device__ __forceinline__ float score_of(float x, bool sigmoid, float m) {
-    if (x != x) return 0.0f;
-    if (sigmoid) return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
-    return x == m ? 1.0f : expf(__fsub_rn(x, m));
+    const float e = expf(sigmoid ? -x : __fsub_rn(x, m));
+    const float s = sigmoid ? __frcp_rn(__fadd_rn(1.0f, e)) : x == m ? 1.0f : e;
+    return x != x ? 0.0f : s;
+}
+
+// The sum of a group's two largest keys' values, or the largest value, as a key.
+__device__ __forceinline__ uint32_t group_key(uint32_t a, uint32_t b, bool two) {
+    return key_of(two ? __fadd_rn(value_of(a), value_of(b)) : value_of(a));
 }
 
 // NV: keys a lane holds in registers (E <= 32 NV).
@@ -43,14 +53,24 @@ template <int NV, typename T>
 __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RouteParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    __shared__ uint32_t s_keys[NV <= 16 ? 4 * 32 * NV : 1];  // groups that are not whole lanes
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + warp;
     if (t >= p.T) return;
     const T* const row = static_cast<const T*>(p.logits) + t * p.E;
     const bool sigmoid = p.sigmoid != 0;
+    const int e0 = lane * NV;
     float x[NV];
+    if (p.quads) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] = lane + 32 * i < p.E ? ld1(row + lane + 32 * i) : -INFINITY;
+        for (int i = 0; i < NV; i += 4) {
+            const float4 v = e0 + i < p.E ? ld4(row + e0 + i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i] = e0 + i < p.E ? ld1(row + e0 + i) : -INFINITY;
+    }
     float m = 0.0f, inv = 1.0f;
     if (!sigmoid) {
         m = -INFINITY;
@@ -67,67 +87,99 @@ __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RoutePara
             inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
         }
     }
-    uint32_t key[NV];
+    uint32_t key[NV], best = kTaken;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
         float c = x[i];
-        if (c == c && (p.bias || sigmoid)) {
+        if (p.bias || sigmoid) {
             c = __fmul_rn(score_of(c, sigmoid, m), inv);
-            if (p.bias) c = __fadd_rn(c, e < p.E ? p.bias[e] : 0.0f);
+            if (p.bias) c = __fadd_rn(c, e0 + i < p.E ? p.bias[e0 + i] : 0.0f);
+            if (x[i] != x[i]) c = x[i];
         }
-        key[i] = e < p.E ? key_of(c) : kTaken;
+        key[i] = e0 + i < p.E ? key_of(c) : kTaken;
     }
     if (p.n_groups > 1) {
-        const int per = p.E / p.n_groups;
-        uint32_t mine = kTaken;  // lane g: group g's score
-        for (int g = 0; g < p.n_groups; ++g) {
-            uint32_t a = kTaken, b = kTaken;  // this lane's two largest keys of the group
+        const int per = p.E / p.n_groups, lanes = per / NV;  // lanes of a group
+        const bool two = p.group_best == 2, whole = lanes * NV == per && (lanes & (lanes - 1)) == 0;
+        uint32_t mine = kTaken;  // this lane's group's score; lanes that are not a group's first one: none
+        if (whole) {
+            uint32_t a = kTaken, b = kTaken;  // the two largest keys
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int e = lane + 32 * i;
-                if (e >= g * per && e < (g + 1) * per) {
-                    b = max(b, min(a, key[i]));
-                    a = max(a, key[i]);
-                }
+                b = max(b, min(a, key[i]));
+                a = max(a, key[i]);
             }
-            const uint32_t first = __reduce_max_sync(kFull, a);
-            float s = value_of(first);
-            if (p.group_best == 2) {
-                const uint32_t who = __ballot_sync(kFull, a == first);
-                if (lane == __ffs(who) - 1) a = b;
-                s = __fadd_rn(s, value_of(__reduce_max_sync(kFull, a)));
+            for (int d = 1; d < lanes; d <<= 1) {
+                const uint32_t oa = __shfl_xor_sync(kFull, a, d), ob = __shfl_xor_sync(kFull, b, d);
+                b = max(max(b, ob), min(a, oa));
+                a = max(a, oa);
             }
-            if (lane == g) mine = key_of(s);
-        }
-        uint32_t open = 0u;
-        for (int j = 0; j < p.top_groups; ++j) {
-            const uint32_t best = __reduce_max_sync(kFull, mine);
-            const int g = __ffs(__ballot_sync(kFull, mine == best && lane < p.n_groups && !((open >> lane) & 1u))) - 1;
-            open |= 1u << g;
-            if (lane == g) mine = kTaken;
-        }
+            if ((lane & (lanes - 1)) == 0 && e0 < p.E) mine = group_key(a, b, two);
+        } else if constexpr (NV <= 16) {
+            uint32_t* const keys = s_keys + warp * 32 * NV;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = lane + 32 * i;
-            if (e < p.E && !((open >> (e / per)) & 1u)) key[i] = kTaken;
+            for (int i = 0; i < NV; ++i) keys[e0 + i] = key[i];
+            __syncwarp();
+            if (lane < p.n_groups) {
+                uint32_t a = kTaken, b = kTaken;
+                for (int i = 0; i < per; ++i) {
+                    const uint32_t k = keys[lane * per + i];
+                    b = max(b, min(a, k));
+                    a = max(a, k);
+                }
+                mine = group_key(a, b, two);
+            }
+        } else {
+            for (int g = 0; g < p.n_groups; ++g) {
+                uint32_t a = kTaken, b = kTaken;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (e0 + i >= g * per && e0 + i < (g + 1) * per) {
+                        b = max(b, min(a, key[i]));
+                        a = max(a, key[i]);
+                    }
+                const uint32_t first = __reduce_max_sync(kFull, a);
+                if (lane == __ffs(__ballot_sync(kFull, a == first)) - 1) a = b;
+                const uint32_t second = __reduce_max_sync(kFull, a);
+                if (lane == g) mine = group_key(first, second, two);
+            }
+        }
+        uint32_t open = 0u;  // bit l: the group that lane l scored stays open
+        for (int j = 0; j < p.top_groups; ++j) {
+            const uint32_t top = __reduce_max_sync(kFull, mine);
+            const int l = __ffs(__ballot_sync(kFull, mine == top)) - 1;
+            open |= 1u << l;
+            if (lane == l) mine = kTaken;
+        }
+        if (whole) {
+            if (!((open >> (lane & ~(lanes - 1))) & 1u))
+#pragma unroll
+                for (int i = 0; i < NV; ++i) key[i] = kTaken;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (e0 + i < p.E && !((open >> ((e0 + i) / per)) & 1u)) key[i] = kTaken;
         }
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) best = max(best, key[i]);
     int id = 0;  // lane j: the j-th choice
     for (int j = 0; j < p.k; ++j) {
-        uint32_t a = kTaken;
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        const int l = __ffs(__ballot_sync(kFull, best == top)) - 1;
+        int at = 0;
+        if (lane == l) {  // its first key of that size is taken
+            best = kTaken;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) a = max(a, key[i]);
-        const uint32_t best = __reduce_max_sync(kFull, a);
-        int e = 0x7fffffff;
+            for (int i = NV - 1; i >= 0; --i) at = key[i] == top ? i : at;
 #pragma unroll
-        for (int i = NV - 1; i >= 0; --i)
-            if (key[i] == best) e = lane + 32 * i;
-        e = __reduce_min_sync(kFull, e);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (lane + 32 * i == e) key[i] = kTaken;
-        if (lane == j) id = e;
+            for (int i = 0; i < NV; ++i) {
+                if (i == at) key[i] = kTaken;
+                best = max(best, key[i]);
+            }
+        }
+        at = __shfl_sync(kFull, at, l);
+        if (lane == j) id = l * NV + at;
     }
     const float w = lane < p.k ? __fmul_rn(score_of(ld1(row + id), sigmoid, m), inv) : 0.0f;
     float sum = w;
@@ -140,7 +192,8 @@ __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RoutePara
 }
 
 template <typename T>
-cudaError_t launch(const RouteParams& p, cudaStream_t s) {
+cudaError_t launch(RouteParams p, cudaStream_t s) {
+    p.quads = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.logits) % (4 * sizeof(T)) == 0;
     const dim3 grid(static_cast<unsigned>((p.T + 3) / 4));
     if (p.E <= 128) return launch_pdl(k_route<4, T>, grid, dim3(128), 0, s, p);
     if (p.E <= 256) return launch_pdl(k_route<8, T>, grid, dim3(128), 0, s, p);

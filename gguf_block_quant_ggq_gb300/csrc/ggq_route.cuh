@@ -13,6 +13,7 @@ struct RouteParams {
     int64_t T;
     int E, k, n_groups, top_groups, group_best;
     int sigmoid, normalize;
+    int quads;  // rows of whole aligned quads (set by the launch)
     float scale;
     int32_t* ids;
     float* weights;
