@@ -15,8 +15,8 @@ cudaError_t launch_attention(const AttnParams& p, int nsm, cudaStream_t s) {
         return launch_attn_prompt_256(p, s);
     }
     if (p.dtype == 0 && rows >= kPromptRows && rows <= 64ll * 65535) {
-        if (p.D == 64) return launch_attn_rows_64(p, s);
-        if (p.D == 128) return launch_attn_rows_128(p, s);
+        if (p.D == 64) return launch_attn_promptf_64(p, s);
+        if (p.D == 128) return launch_attn_promptf_128(p, s);
         return launch_attn_rows_256(p, s);
     }
     if (p.D == 64) return launch_attn_stream_64(p, nsm, s);

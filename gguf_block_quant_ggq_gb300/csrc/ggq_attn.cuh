@@ -41,9 +41,9 @@ cudaError_t launch_attention(const AttnParams& p, int nsm, cudaStream_t s);
 cudaError_t launch_attn_stream_64(const AttnParams& p, int nsm, cudaStream_t s);
 cudaError_t launch_attn_stream_128(const AttnParams& p, int nsm, cudaStream_t s);
 cudaError_t launch_attn_stream_256(const AttnParams& p, int nsm, cudaStream_t s);
-cudaError_t launch_attn_rows_64(const AttnParams& p, cudaStream_t s);
-cudaError_t launch_attn_rows_128(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_rows_256(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_promptf_64(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_promptf_128(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_prompt_64(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_prompt_128(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_prompt_256(const AttnParams& p, cudaStream_t s);
