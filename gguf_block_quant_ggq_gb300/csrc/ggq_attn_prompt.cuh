@@ -555,10 +555,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         const uint32_t cs = tmem + t * SH::cS + lanes, co = tmem + SH::cO + t * D + lanes;
         const int i_row = r / p.G, h = hk * p.G + r - i_row * p.G, pos = from + i_row;
         const int first_key = p.window > 0 ? pos - p.window + 1 : 0;
-        const float slope = p.slopes ? p.slopes[h] : 0.0f;
         const bool plain = p.cap <= 0.0f && !p.slopes && rscale > 0.0f;
         constexpr float kLog2e = 1.44269504088896340736f;
-        const float sx = plain ? rscale * kLog2e : rscale;
+        const float sx = p.cap > 0.0f ? rscale : rscale * kLog2e, slope = p.slopes ? p.slopes[h] * kLog2e : 0.0f;
         const float inv_cap = p.cap > 0.0f ? 2.0f * kLog2e / p.cap : 0.0f;
         // steps that every row of the tile sees whole
         const int t_first = from + (r_begin + 128 * t) / p.G, t_last = from + (min(r_end, r_begin + 128 * t + 128) - 1) / p.G;
@@ -578,15 +577,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             prompt_tie32(x + 32);
             // logits in units of log2 (plain: still to be multiplied by sx)
             if (!plain) {
+                const float rel = static_cast<float>(key0 - pos);
 #pragma unroll
                 for (int k = 0; k < 64; ++k) {
                     float y = x[k] * sx;
                     // tanh(z) = 1 - 2 / (1 + exp(2 z))
                     if (p.cap > 0.0f) {
                         const float z = y * inv_cap;
-                        y = p.cap - __fdividef(2.0f * p.cap, 1.0f + prompt_ex2(z > 120.0f ? 120.0f : z));
+                        y = kLog2e * (p.cap - __fdividef(2.0f * p.cap, 1.0f + prompt_ex2(z > 120.0f ? 120.0f : z)));
                     }
-                    x[k] = fmaf(slope, static_cast<float>(key0 + k - pos), y) * kLog2e;
+                    x[k] = fmaf(slope, rel + static_cast<float>(k), y);
                 }
             }
             if (!whole) {

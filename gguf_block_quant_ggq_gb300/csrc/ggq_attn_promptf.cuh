@@ -395,10 +395,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
         const uint32_t cs = tmem + lanes, co = tmem + SH::cO + half * HD + lanes;
         const int i_row = r / p.G, h = hk * p.G + r - i_row * p.G, pos = from + i_row;
         const int first_key = p.window > 0 ? pos - p.window + 1 : 0;
-        const float slope = p.slopes ? p.slopes[h] : 0.0f, rscale = s_top[3 * 128 + rr];
+        const float rscale = s_top[3 * 128 + rr];
         const bool plain = p.cap <= 0.0f && !p.slopes && rscale > 0.0f;
         constexpr float kLog2e = 1.44269504088896340736f;
-        const float sx = plain ? rscale * kLog2e : rscale, mul = plain ? sx : 1.0f;
+        const float slope = p.slopes ? p.slopes[h] * kLog2e : 0.0f;
+        const float sx = p.cap > 0.0f ? rscale : rscale * kLog2e, mul = plain ? sx : 1.0f;
         // steps that every row of the tile sees whole
         const int seen_from = p.window > 0 ? pos_last - p.window + 1 : 0;
         float tot[HD], m = -1e30f, l = 0.0f;
@@ -459,11 +460,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
             // logits in units of log2 (plain: still to be multiplied by sx)
             constexpr auto key_at = [](int k) { return 16 * ((k >> 2) & 1) + 8 * ((k >> 1) & 1) + 2 * (k >> 3) + (k & 1); };
             if (!plain) {
+                const float rel = static_cast<float>(mine - pos);
 #pragma unroll
                 for (int k = 0; k < HK; ++k) {
                     float y = x[k] * sx;
-                    if (p.cap > 0.0f) y = p.cap * tanhf(y / p.cap);
-                    x[k] = fmaf(slope, static_cast<float>(mine + key_at(k) - pos), y) * kLog2e;
+                    if (p.cap > 0.0f) y = kLog2e * (p.cap * tanhf(y / p.cap));
+                    x[k] = fmaf(slope, rel + static_cast<float>(key_at(k)), y);
                 }
             }
             if (!whole) {
