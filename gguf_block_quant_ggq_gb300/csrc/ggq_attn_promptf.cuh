@@ -15,7 +15,8 @@
 //     channels; they agree on the row's maximum through shared memory;
 //   * warps 8-15: the packed blobs to fp16 (keys) and bf16 (values) integers, K-major
 //     128-byte-swizzled tiles of 128 keys, and their scales to fp32;
-//   * warps 16 and 17: one thread each issues the scores' and the outputs' MMAs.
+//   * warps 16, 17 and 18, 19: one thread each issues the scores' and the outputs' MMAs
+//     of half the blocks (the instructions are small: one thread's issue would bound them).
 // Keys lie in tiles, scores and probabilities in the order in which a V word's lanes
 // hold them: key 16 c + 8 o + 2 t + e of 32 at place 8 t + 4 c + 2 o + e.
 #pragma once
@@ -74,8 +75,7 @@ __device__ __forceinline__ void pf_ld16(uint32_t taddr, float* v) {
 }
 __device__ __forceinline__ void pf_st8(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
 }
 __device__ __forceinline__ float pf_half(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
 __device__ __forceinline__ void pf_pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory"); }
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + SH::oBar);
     uint64_t *const kfull = bars, *const kempty = bars + 2, *const vfull = bars + 4, *const vempty = bars + 6;
     uint64_t *const sfull = bars + 8, *const pfull = bars + 10, *const pdone = bars + 12, *const done = bars + 14;
-    uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 16);
+    uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 18);
     volatile int* const abort = reinterpret_cast<volatile int*>(tslot + 1);
     int* const s_bad = reinterpret_cast<int*>(tslot + 2);  // [NB][2] first and last key whose value scale is not finite
 
@@ -123,12 +123,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
         for (int i = 0; i < 2; ++i) {
             mbar_init(kfull + i, kDecodeWarps * 32);
             mbar_init(vfull + i, kDecodeWarps * 32);
-            mbar_init(kempty + i, 1 + kSoftmaxWarps);
-            mbar_init(vempty + i, 1 + kSoftmaxWarps);
-            mbar_init(sfull + i, 1);
+            mbar_init(kempty + i, 2 + kSoftmaxWarps);
+            mbar_init(vempty + i, 2 + kSoftmaxWarps);
+            mbar_init(sfull + i, 2);
             mbar_init(pfull + i, kSoftmaxWarps * 32);
-            mbar_init(pdone + i, 1);
+            mbar_init(pdone + i, 2);
             mbar_init(done + i, 1);
+            mbar_init(done + 2 + i, 1);
         }
         *abort = 0;
         for (int i = 0; i < NB; ++i) s_bad[2 * i] = 0x7fffffff, s_bad[2 * i + 1] = -1;
@@ -200,8 +201,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
     if (warp >= kFirstMma) {
         // ================================================================ MMA
         prompt_regs<false, kPfMmaRegs>();
-        if (warp < kFirstMma + 2 && lane == 0 && steps > 0) {
-            if (warp == kFirstMma) {
+        const int b0 = (warp & 1) * (NB / 2);  // its blocks
+        if (lane == 0 && steps > 0) {
+            if (warp < kFirstMma + 2) {
                 const uint64_t qd = umma_desc_sw128(smem_addr(smem));
                 constexpr uint32_t id = prompt_idesc(KEYS, false);
                 for (int i = 0; i < steps; ++i) {
@@ -211,10 +213,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
                     tc_fence_after();
                     const uint64_t kd = umma_desc_sw128(smem_addr(smem + SH::oK + buf * SH::kK + h * (KEYS * 128)));
 #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk)
+                    for (int e = 0; e < NB / 2; ++e)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {  // the low term's 32 channels, then the high one's
-                            const int at = (blk & 1) * 4 + 2 * (k & 1);
+                            const int blk = b0 + e, at = (blk & 1) * 4 + 2 * (k & 1);
                             tc_mma(tmem + SH::cBuf * sb + blk * KEYS, qd + (k < 2 ? SH::kQ / 16 : 0) + (blk >> 1) * (128 * 128 / 16) + at,
                                    kd + (blk >> 1) * (KT * 128 / 16) + at, id, k > 0);
                         }
@@ -233,14 +235,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
                     const uint64_t vd = umma_desc_sw128(smem_addr(smem + SH::oV + buf * SH::kV + (h * KEYS / 64) * (D * 128))) +
                                         (KEYS == 32 ? 4 * (h & 1) : 0);
 #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk)
+                    for (int e = 0; e < NB / 2; ++e)
 #pragma unroll
                         for (int term = 2; term >= 0; --term)
 #pragma unroll
-                            for (int k = 0; k < 2 * KS; ++k)
+                            for (int k = 0; k < 2 * KS; ++k) {
+                                const int blk = b0 + e;
                                 tc_mma_ts(tmem + SH::cO + 32 * blk,
                                           tmem + SH::cBuf * sb + 96 * (k / KS) + (3 * blk + term) * (HK / 2) + 8 * (k % KS),
                                           vd + blk * (32 * 128 / 16) + 2 * k, id, h > 0 || term < 2 || k > 0);
+                            }
                     tc_commit(pdone + sb);
                     if (h == STEPS - 1) tc_commit(vempty + buf);
                 }
@@ -513,12 +517,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
                     for (int z = 0; z < 4; z += 2)
 #pragma unroll
                         for (int term = 0; term < 3; ++term) {
-                            const uint32_t u0 = __float_as_uint(y[z]), u1 = __float_as_uint(y[z + 1]);
-                            w[term * (HK / 2) + (k + z) / 2] = prmt(u0, u1, 0x7632u);
-                            if (term < 2) {
-                                y[z] -= __uint_as_float(u0 & 0xFFFF0000u);
-                                y[z + 1] -= __uint_as_float(u1 & 0xFFFF0000u);
-                            }
+                            const uint32_t u = prmt(__float_as_uint(y[z]), __float_as_uint(y[z + 1]), 0x7632u);
+                            w[term * (HK / 2) + (k + z) / 2] = u;
+                            if (term < 2)
+                                ffma2(y[z], y[z + 1], __uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u), -1.0f, y[z], y[z + 1]);
                         }
                 }
                 const uint32_t to = cs + SH::cBuf * sb + 96 * half + blk * (3 * HK / 2);
