@@ -55,7 +55,8 @@ struct PromptShape {
     static constexpr int kQ = 128 * D * 2;             // bytes of a tile's queries
     static constexpr int kK = kKeys * D * 2, kV = kK;  // bytes of a step's keys, values
     static constexpr int oK = kTiles * kQ, oV = oK + 2 * kK, oBar = oV + 2 * kV;
-    static constexpr int kTotal = oBar + 384 + 1024;   // + alignment of the tiles
+    static constexpr int oScale = oBar + 384;          // of the rows
+    static constexpr int kTotal = oScale + kRows * 4 + 1024;  // + alignment of the tiles
     // tensor-memory columns: two 64-key score buffers of each tile (probabilities over
     // them), then the outputs
     static constexpr uint32_t cS = 128, cO = kTiles * cS;
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
     constexpr int TILES = SH::kTiles, KT = SH::kKeys, NB = D / 32, KG = KT / 16;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // warp: uniform
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + SH::oBar);
     uint64_t *const kfull = bars, *const kempty = bars + 2, *const vfull = bars + 4, *const vempty = bars + 6;
     // per tile and score buffer: scores there, probabilities there, P V done; per MMA thread: all done
@@ -276,39 +277,52 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // ---- queries: thread a row, fp16 with the row's largest element in [2^13, 2^14)
-    float rscale = 0.0f;
+    // ---- queries: whole rows at a time, 8 channels a lane, as fp16 with the row's largest element in [2^13, 2^14)
+    float* const s_scale = reinterpret_cast<float*>(smem + SH::oScale);
     if (warp < 4 * TILES && (warp >> 2) < ntiles) {
-        const int r = min(r_begin + tid, r_end - 1), i = r / p.G, h = hk * p.G + r - i * p.G;
-        const int64_t at = (first + i) * p.q_token + h * p.q_head;
-        const auto q4 = [&](int d) {
-            return BF ? ld4(static_cast<const __nv_bfloat16*>(p.q) + at + d) : ld4(static_cast<const __half*>(p.q) + at + d);
-        };
-        float amax = 0.0f;
-#pragma unroll 8
-        for (int d = 0; d < D; d += 4) {
-            const float4 x = q4(d);
-            amax = fmaxf(fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
-        }
-        const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-        const int sh = ex == 128 ? 0 : min(13 - ex, 100);
-        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(sh + 127) << 23), p.scale);
-        rscale = fabsf(p.scale) * scalbnf(1.0f, -sh);  // not negative: the largest product is the largest logit
-        uint8_t* const row = smem + (tid >> 7) * SH::kQ + (tid & 127) * 128;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {  // the K tile's channel order: 16 t + 4 j + i holds 16 j + 4 t + i of 64
-            const int d = 64 * (c >> 3) + 32 * (c & 1) + 4 * ((c & 7) >> 1);
-            const float4 x = q4(d), y = q4(d + 16);
-            const uint4 u = make_uint4(prompt_pack<false>(x.x * up, x.y * up), prompt_pack<false>(x.z * up, x.w * up),
-                                       prompt_pack<false>(y.x * up, y.y * up), prompt_pack<false>(y.z * up, y.w * up));
-            *reinterpret_cast<uint4*>(row + (c >> 3) * (128 * 128) + (((c & 7) ^ (tid & 7)) << 4)) = u;
+        constexpr int LR = D / 8, RL = 32 / LR;  // lanes of a row, rows of a load
+        const int d = 8 * (lane % LR);
+        // the K tile's channel order: 16 t + 4 j + i holds 16 j + 4 t + i of 64
+        uint8_t* const to = smem + (warp >> 2) * SH::kQ + (d >> 6) * (128 * 128) + 8 * ((d >> 4) & 1);
+        const int chunk = 2 * ((d >> 2) & 3) + ((d >> 5) & 1);
+#pragma unroll 1
+        for (int k0 = 0; k0 < 32; k0 += 8 * RL) {
+            float4 x[8][2];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = min(r_begin + 32 * warp + k0 + k * RL + lane / LR, r_end - 1), i = r / p.G;
+                const int64_t at = (first + i) * p.q_token + (hk * p.G + r - i * p.G) * p.q_head + d;
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                    x[k][z] = BF ? ld4(static_cast<const __nv_bfloat16*>(p.q) + at + 4 * z)
+                                 : ld4(static_cast<const __half*>(p.q) + at + 4 * z);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int row = 32 * warp + k0 + k * RL + lane / LR, rr = row & 127;
+                float amax = 0.0f;
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(x[k][z].x), fabsf(x[k][z].y)), fmaxf(fabsf(x[k][z].z), fabsf(x[k][z].w))));
+#pragma unroll
+                for (int m = 1; m < LR; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+                const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+                const int sh = ex == 128 ? 0 : min(13 - ex, 100);
+                const float up = copysignf(__uint_as_float(static_cast<uint32_t>(sh + 127) << 23), p.scale);
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                    *reinterpret_cast<uint2*>(to + rr * 128 + (((chunk + 2 * z) ^ (rr & 7)) << 4)) =
+                        make_uint2(prompt_pack<false>(x[k][z].x * up, x[k][z].y * up), prompt_pack<false>(x[k][z].z * up, x[k][z].w * up));
+                // not negative: the largest product is the largest logit
+                if (lane % LR == 0) s_scale[row] = fabsf(p.scale) * scalbnf(1.0f, -sh);
+            }
         }
         fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
 
     const auto wait1 = [&](uint64_t* bar, uint32_t parity) {
         const bool ok = !*abort && mbar_wait(bar, parity);
@@ -333,7 +347,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         prompt_regs<false, kMmaRegs>();
         const int t = (warp - kFirstMma) & 1;
         const bool scores = warp < kFirstMma + 2;
-        if (t < ntiles && lane == 0 && turns > 0) {
+        if (t < ntiles && elect_one() && turns > 0) {
             const uint32_t cs = tmem + t * SH::cS, co = tmem + SH::cO + t * D;
             if (scores) {
                 const uint64_t qd = umma_desc_sw128(smem_addr(smem + t * SH::kQ));
@@ -555,6 +569,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         const uint32_t cs = tmem + t * SH::cS + lanes, co = tmem + SH::cO + t * D + lanes;
         const int i_row = r / p.G, h = hk * p.G + r - i_row * p.G, pos = from + i_row;
         const int first_key = p.window > 0 ? pos - p.window + 1 : 0;
+        const float rscale = s_scale[tid];
         const bool plain = p.cap <= 0.0f && !p.slopes && rscale > 0.0f;
         constexpr float kLog2e = 1.44269504088896340736f;
         const float sx = p.cap > 0.0f ? rscale : rscale * kLog2e, slope = p.slopes ? p.slopes[h] * kLog2e : 0.0f;

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
     constexpr int HK = KEYS / 2, HD = D / 2;  // keys and channels of a softmax thread
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // warp: uniform
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + SH::oBar);
     uint64_t *const kfull = bars, *const kempty = bars + 2, *const vfull = bars + 4, *const vempty = bars + 6;
     uint64_t *const sfull = bars + 8, *const pfull = bars + 10, *const pdone = bars + 12, *const done = bars + 14;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tslot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
 
     const auto wait1 = [&](uint64_t* bar, uint32_t parity) {
         const bool ok = !*abort && mbar_wait(bar, parity);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
         // ================================================================ MMA
         prompt_regs<false, kPfMmaRegs>();
         const int b0 = (warp & 1) * (NB / 2);  // its blocks
-        if (lane == 0 && steps > 0) {
+        if (elect_one() && steps > 0) {
             if (warp < kFirstMma + 2) {
                 const uint64_t qd = umma_desc_sw128(smem_addr(smem));
                 constexpr uint32_t id = prompt_idesc(KEYS, false);
