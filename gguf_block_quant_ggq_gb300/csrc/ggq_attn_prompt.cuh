@@ -632,10 +632,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                     }
                 }
             }
+            // fp16: 2^7 times the probabilities, at most 2^15, so that fewer are subnormal
+            const float ref = BF ? m : m - 7.0f;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < 64; k += 2) {
-                ffma2(x[k], x[k + 1], x[k], x[k + 1], mul, -m, -m);
+                ffma2(x[k], x[k + 1], x[k], x[k + 1], mul, -ref, -ref);
                 x[k] = prompt_ex2(x[k]);
                 x[k + 1] = prompt_ex2(x[k + 1]);
                 add2(sum[k & 2], sum[(k & 2) + 1], sum[k & 2], sum[(k & 2) + 1], x[k], x[k + 1]);

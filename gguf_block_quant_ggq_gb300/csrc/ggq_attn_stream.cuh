@@ -31,6 +31,8 @@
 // fourth unit, each keeping a ring of bulk copies in flight, across items.  An item that several CTAs share is joined by the
 // last of them from partial results in scratch, in the order of the pieces.
 #pragma once
+#include <atomic>
+
 #include "ggq_attn.cuh"
 #include "ggq_device.cuh"
 #include "ggq_internal.h"
@@ -178,6 +180,12 @@ __device__ __forceinline__ void attn_mma(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// the same with subnormal results: factors of sums that the unit's lift has raised
+__device__ __forceinline__ float ex2_small(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -514,7 +522,7 @@ struct AttnRows {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int k = 0; k < NB / 2; ++k) dm = __vmaxu2(dm, V4 ? vd[c][i][k] & 0x7FFF7FFFu : vd[c][i][k]);
+                for (int k = 0; k < NB / 2; ++k) dm = __vmaxu2(dm, vd[c][i][k] & 0x7FFF7FFFu);
         raise |= !(half_lo(dm) <= dlimit && half_hi(dm) <= dlimit);  // larger, or not a number
         bool more = false;   // some probabilities are too small for fp16 beside the unit's largest
         if (__any_sync(0xffffffffu, raise)) {
@@ -547,11 +555,13 @@ struct AttnRows {
                 spoilt[rs] |= __shfl_xor_sync(0xffffffffu, spoilt[rs], 1);
                 spoilt[rs] |= __shfl_xor_sync(0xffffffffu, spoilt[rs], 2);
                 const bool up = top[rs] > m[rs] + 60.0f;
-                const float a = up ? ex2(m[rs] - top[rs]) : 1.0f;
+                // in two halves: the totals may be 2^60 above the old reference, the new one 2^126 and more
+                const float a = up ? ex2(0.5f * (m[rs] - top[rs])) : 1.0f;
                 if (up) m[rs] = top[rs];
-                l[rs] *= a;
+                l[rs] = l[rs] * a * a;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) tot[rs][n] = mul2(tot[rs][n], both(((spoilt[rs] >> (n >> 2)) & 1u) ? NAN : a));
+                for (int n = 0; n < NT; ++n)
+                    tot[rs][n] = mul2(mul2(tot[rs][n], both(((spoilt[rs] >> (n >> 2)) & 1u) ? NAN : a)), both(a));
 #pragma unroll
                 for (int i = 0; i < 4 * UNIT; ++i) more |= lg[rs][i] < top[rs] - 28.0f && lg[rs][i] > m[rs] - 126.0f;
             }
@@ -579,7 +589,7 @@ struct AttnRows {
                 float2 sum = make_float2(pr[rs][0], pr[rs][1]);
 #pragma unroll
                 for (int i = 2; i < 4 * UNIT; i += 2) sum = add2(sum, make_float2(pr[rs][i], pr[rs][i + 1]));
-                f[rs] = ex2(sub - m[rs]);
+                f[rs] = ex2_small(sub - m[rs]);
                 l[rs] = fmaf(sum.x + sum.y, f[rs], l[rs]);
             }
             uint32_t ph[RS][2 * UNIT];  // 16-bit activations: the probabilities in fp16
@@ -1034,14 +1044,15 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
 template <bool K4, bool V4, int D, int MODE>
 cudaError_t launch_attn_stream(const AttnParams& p, int nsm, cudaStream_t s) {
     using SM = AttnSmem<K4, V4, D, MODE>;
-    static bool set[kMaxDevices] = {};
+    static std::atomic<bool> set[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= kMaxDevices || !set[dev]) {
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!set[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(k_attn_stream<K4, V4, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kTotal);
         if (e != cudaSuccess) return e;
-        if (dev < kMaxDevices) set[dev] = true;
+        set[dev].store(true, std::memory_order_release);
     }
     const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.G + SM::kRows - 1) / SM::kRows;
     const int64_t units = p.n_seqs * p.Hkv * tiles * ((static_cast<int64_t>(p.max_len) + 16 * SM::kUnit - 1) / (16 * SM::kUnit) + 1 + kItemCost);
