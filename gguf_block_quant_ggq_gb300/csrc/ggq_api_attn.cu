@@ -169,7 +169,7 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     p.err = &c->ctrl->err;
     s = need_scratch(c, attn_scratch());
     if (s != GGQ_OK) return s;
-    p.min_share = 4;
+    p.min_share = 4;  // one sequence of 777 tokens, 8 kv heads: 11.8 us; 13.6 at 2, 12.6 at 8, 15.1 at 16
     p.parts = reinterpret_cast<float*>(c->pool);
     p.pieces = c->ctrl->attn_pieces;
     const cudaError_t e = launch_attention(p, c->nsm, static_cast<cudaStream_t>(stream));

@@ -3,8 +3,11 @@
 //
 // Mathematics: S = Q K^T and O = P V per kv head, the rows being the head
 // group's query heads of consecutive tokens, with the softmax's running maximum
-// and sum.  Bound by the tensor cores: 4 D operations per (row, key), 2 kt D bytes
-// of packed cache per 128-row tile and step of kt keys.
+// and sum.  4 D operations per (row, key); the packed cache is a small part.  Measured:
+// the last 4096 of 8192 causal bf16 rows, 32 heads on 8 of 128 channels: 431 us, 956
+// TFLOP/s, half the rate of a plain 16-bit product; the tensor pipe is busy 39% of the
+// time, the issue slots 65%: bound by the instructions of the softmax and of unpacking
+// the blobs (done once for 256 rows) and the waits between them.
 //
 // A CTA takes one kv head of one sequence and one or two tiles of 128 rows that
 // share its steps of keys (heads of 256 channels: one tile, whose O fills half of
@@ -21,8 +24,10 @@
 //     computed while the softmax works on this one's.
 // The running maximum is raised (and O rescaled in tensor memory) only when a row
 // passes it by 2^8.  fp16 queries are exact; bf16 ones too (rows are scaled by a
-// power of two).  K is rounded to fp16; V and P to the activations' type, so that
-// with bf16 no probability is lost for being small.
+// power of two).  K is rounded to fp16 (2^-12 of each value); V and P to the
+// activations' type: with bf16 2^-9 of each, as much as the output's own rounding, but
+// no probability is lost for being small and no value for being large; with fp16 2^-12,
+// P being kept at 2^7 times its value.  Each row's sum is fp32.
 #pragma once
 #include <atomic>
 

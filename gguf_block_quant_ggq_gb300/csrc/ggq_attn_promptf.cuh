@@ -10,6 +10,12 @@
 // lost for being small; with two terms the outputs were 6 times further off).  Tensor memory sums 128 keys; the sums of those are added up
 // in registers, in fp32 with rounding to nearest.
 //
+// Measured (28 heads on 4 of 128 channels, distance bias, 5 ragged prompts of up to 1000
+// rows): 191 us, 95 TFLOP/s of the formula's operations (on mma.sync with the scales in
+// the accumulators: 321 us); 4096 causal rows of 32 heads on 8: 728 us (1716).  A step of
+// 32 keys takes 128 rows 1.5 us: 40 MMAs of 32 columns, some 60 cycles each with their
+// issue, and about 500 instructions of each of the softmax's eight warps; both alternate.
+//
 // A CTA takes 128 rows of one kv head of one sequence.  Roles:
 //   * warps 0-7: two threads a row, each half of a step's keys and half of the output's
 //     channels; they agree on the row's maximum through shared memory;

@@ -1,11 +1,13 @@
 // ggq_attn_rows.cuh -- attention of many fp32 query rows (prompts) over the packed
-// cache on mma.sync.
+// cache on mma.sync, for heads of 256 channels (whose scores, probabilities and outputs
+// tensor memory does not hold at once).
 //
 // The same step as the streaming kernel's (a warp's 8 rows against a unit of keys,
 // operands split so that 22 bits of the products count), laid out for many rows: a
 // CTA takes 64 rows of one kv head of one sequence, 8 a warp, and all its warps read
 // the same ring of units in shared memory, up to the last key that a row sees.
-// Bound by instructions (unpacking and scaling, about 1000 a warp, unit and 8 rows).
+// Bound by instructions (unpacking and scaling, about 1000 a warp, unit and 8 rows):
+// 4096 causal rows, 16 heads on 8: 1.73 ms (the streaming kernel: 3.5 ms), 40 TFLOP/s.
 #pragma once
 #include <atomic>
 
@@ -17,7 +19,7 @@ constexpr int kRowsWarps = 8, kRowsThreads = kRowsWarps * 32, kRowsTile = 8 * kR
 
 template <bool K4, bool V4, int D>
 struct RowsSmem {
-    static constexpr int kUnit = D == 256 ? 1 : 2;
+    static constexpr int kUnit = 1;  // 16 keys: a warp's 8 rows of outputs leave no registers for more
     static constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D), kStage = kUnit * (kKB + kVB);
     static constexpr int kStages = 6;
     static constexpr int kQ = D / 16 * 32 * 16;  // bytes of a warp's query operand

@@ -10,7 +10,9 @@
 // has eight channels of a row, four threads a block.  Rows whose slots fill an
 // aligned group (the tokens of a prompt) pass through the group's blob in shared
 // memory, which is written or read in whole lines; other rows (one token of each
-// sequence) go to or come from their blob directly.
+// sequence) go to or come from their blob directly.  Bound at 16384 tokens of 8 heads of
+// 128 channels by instructions (store 33 us, issue slots 66% used; load 30 us; their
+// 128 MB each take 19 us), at a decode step's by latency (5 us for both).
 #include "ggq_device.cuh"
 #include "ggq_internal.h"
 #include "ggq_kv.cuh"
@@ -291,8 +293,10 @@ template <bool STORE, int D>
 cudaError_t launch_kv_dim(KvParams p, int dtype, cudaStream_t s) {
     // the first window may begin up to 15 rows before the first row
     const int64_t windows = (p.n + 2 * kKvRows - 2) / kKvRows;
-    // a head at a time while that leaves SMs without work, then several (the slots are looked at once)
-    p.heads_at_once = windows * 2 * p.H < 4096 ? 1 : 4;
+    // One head a CTA while the CTAs are few, four once there are plenty (store and load
+    // of 8 heads of 128 channels, us, one / four: 64 tokens 5.0 / 8.8, 1024 7.8 / 13.5,
+    // 4096 18.6 / 19.5, 16384 70 / 60).
+    p.heads_at_once = windows * 2 * p.H < 8192 ? 1 : 4;
     const int parts = (p.H + p.heads_at_once - 1) / p.heads_at_once;
     const dim3 grid(static_cast<unsigned>(windows), static_cast<unsigned>(2 * parts));
     if (dtype == 0) return launch_pdl(k_kv<STORE, D, float>, grid, dim3(kKvThreads), 0, s, p);
