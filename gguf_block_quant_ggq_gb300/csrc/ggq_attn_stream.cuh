@@ -70,12 +70,19 @@ __device__ __forceinline__ float attn_cap(float y, float cap) {
 template <bool K4, bool V4, int D, int MODE>
 struct AttnSmem {
     static constexpr int kRows = MODE == A_HALF16 ? 16 : 8;
-    static constexpr int kUnit = D == 256 ? 1 : D == 64 && (K4 || V4) ? 4 : 2;  // 16-token groups a warp takes at once
+    // 16-token groups a warp takes at once: what the registers hold.  (8 rows of 64 4-bit
+    // channels, 33 ragged sequences of up to 8192: 43 us at 4, 47 at 2; 16 rows 184 and
+    // 133, fp32 57 and 53, 16 rows with one 8-bit side 219 and 137.)
+    static constexpr int kUnit = D == 256 ? 1 : D == 64 && K4 && V4 && MODE == A_HALF8 ? 4 : 2;
     static constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
     static constexpr int kStage = kUnit * (kKB + kVB); // keys of the unit's groups, then their values
-    static constexpr int kFit = (D == 64 ? 52 : 72) * 1024 / (kAttnWarps * kStage);
+    // Ring bytes that leave an SM its CTAs, and heads of 256 channels some first-level cache
+    // for what their registers do not hold (Q4_0, 33 ragged sequences of up to 8192: 72 KB
+    // 211 us with one CTA an SM, 64 KB 154).
+    static constexpr int kFit = (D == 64 ? 52 : D == 128 ? 72 : 64) * 1024 / (kAttnWarps * kStage);
     static constexpr int kStages = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
-    static constexpr int kRowPitch = D + 8;            // floats of a totals row (padding: conflict-free float2 stores)
+    static constexpr int kMerge = D == 256 ? 128 : D;  // channels that the warps' totals are merged by
+    static constexpr int kRowPitch = kMerge + 8;       // floats of a totals row (padding: conflict-free float2 stores)
     static constexpr int oRing = 0;
     static constexpr int oTot = kAttnWarps * kStages * kStage;
     static constexpr int oQ = oTot + kAttnWarps * 8 * kRowPitch * 4;  // totals of 8 rows a warp
@@ -300,6 +307,10 @@ struct AttnRows {
     static constexpr float kLog2e = 1.44269504088896340736f;
     // power of two that lifts the probabilities: p * lift * (largest value scale) stays below 32000;
     // fp16 probabilities (16-bit activations) must not pass 2^15 themselves
+    // 8 rows of 256 channels: the offsets are added to the results, one register a block
+    // instead of an accumulator's four (Q8_0: 182 -> 139 us; 16 rows, which spill either
+    // way: 283 -> 287)
+    static constexpr bool kOffsetLater = D == 256 && MODE == A_HALF8;
     static constexpr float kMaxLift = MODE == A_SPLIT8 ? 40.0f : 15.0f;
 
     float xs[RS];                    // score of an accumulator unit (plain: times log2 e)
@@ -447,14 +458,17 @@ struct AttnRows {
                                  h2_sub(prmt(y, 0x64646464u, 0x4342u), 0x64806480u));
                     } else if constexpr (K4) {
                         const uint32_t q = kw[c][o * NB + b], y = q >> 8;
-                        attn_mma_c(cc, fa, q & 0x000F000Fu, q & 0x00F000F0u, offset[b]);
+                        if constexpr (kOffsetLater) attn_mma0(cc, fa, q & 0x000F000Fu, q & 0x00F000F0u);
+                        else attn_mma_c(cc, fa, q & 0x000F000Fu, q & 0x00F000F0u, offset[b]);
                         attn_mma(cc, fb, y & 0x000F000Fu, y & 0x00F000F0u);
                     } else {
                         const uint32_t q = kw[c][o * KS + 2 * b], y = kw[c][o * KS + 2 * b + 1];
-                        attn_mma_c(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u), offset[b]);
+                        if constexpr (kOffsetLater) attn_mma0(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u));
+                        else attn_mma_c(cc, fa, prmt(q, 0u, 0x4140u), prmt(q, 0u, 0x4342u), offset[b]);
                         attn_mma(cc, fb, prmt(y, 0u, 0x4140u), prmt(y, 0u, 0x4342u));
                     }
                     if constexpr (MODE == A_SPLIT8) cc[0] += cc[2], cc[1] += cc[3];
+                    else if constexpr (kOffsetLater) cc[0] += offset[b][0], cc[1] += offset[b][0];
 #pragma unroll
                     for (int rs = 0; rs < RS; ++rs)
 #pragma unroll
@@ -1002,35 +1016,38 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         for (int rs = 0; rs < RS; ++rs) {
             float a;
             const float sum = rows.settle_reference(rs, &a);
-            if (rs > 0) __syncthreads();
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<float2*>(s_mine + g8 * SM::kRowPitch + 8 * n + 2 * t4) = mul2(rows.tot[rs][n], both(a));
-            if (t4 == 0) {
-                s_m[warp * 8 + g8] = rows.m[rs];
-                s_l[warp * 8 + g8] = sum;
-            }
-            __syncthreads();
-            for (int i = tid; i < 8 * D / 4; i += kAttnThreads) {
-                const int r8 = i / (D / 4), d = 4 * (i - r8 * (D / 4)), row = 8 * rs + r8;
-                if (whole && r0 + row >= r_end) break;
-                float M = kAttnNone, L = 0.0f;
+            for (int c0 = 0; c0 < D; c0 += SM::kMerge) {
+                if (rs > 0 || c0 > 0) __syncthreads();
 #pragma unroll
-                for (int k = 0; k < kAttnWarps; ++k) M = fmaxf(M, s_m[k * 8 + r8]);
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < kAttnWarps; ++k) {
-                    const float f = ex2(s_m[k * 8 + r8] - M);
-                    const float4 v = *reinterpret_cast<const float4*>(s_tot + (k * 8 + r8) * SM::kRowPitch + d);
-                    L = fmaf(s_l[k * 8 + r8], f, L);
-                    o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+                for (int n = 0; n < SM::kMerge / 8; ++n)
+                    *reinterpret_cast<float2*>(s_mine + g8 * SM::kRowPitch + 8 * n + 2 * t4) = mul2(rows.tot[rs][c0 / 8 + n], both(a));
+                if (t4 == 0) {
+                    s_m[warp * 8 + g8] = rows.m[rs];
+                    s_l[warp * 8 + g8] = sum;
                 }
-                if (whole) {
-                    const float inv = L != 0.0f ? 1.0f / L : 0.0f;
-                    attn_out4(p, sq, hk, r0 + row, d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-                } else {
-                    if (d == 0) part[row] = M, part[16 + row] = L;
-                    *reinterpret_cast<float4*>(part + 32 + row * D + d) = o;
+                __syncthreads();
+                for (int i = tid; i < 8 * SM::kMerge / 4; i += kAttnThreads) {
+                    const int r8 = i / (SM::kMerge / 4), d = 4 * (i - r8 * (SM::kMerge / 4)), row = 8 * rs + r8;
+                    if (whole && r0 + row >= r_end) break;
+                    float M = kAttnNone, L = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kAttnWarps; ++k) M = fmaxf(M, s_m[k * 8 + r8]);
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < kAttnWarps; ++k) {
+                        const float f = ex2(s_m[k * 8 + r8] - M);
+                        const float4 v = *reinterpret_cast<const float4*>(s_tot + (k * 8 + r8) * SM::kRowPitch + d);
+                        L = fmaf(s_l[k * 8 + r8], f, L);
+                        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+                    }
+                    if (whole) {
+                        const float inv = L != 0.0f ? 1.0f / L : 0.0f;
+                        attn_out4(p, sq, hk, r0 + row, c0 + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                    } else {
+                        if (c0 + d == 0) part[row] = M, part[16 + row] = L;
+                        *reinterpret_cast<float4*>(part + 32 + row * D + c0 + d) = o;
+                    }
                 }
             }
         }
