@@ -38,7 +38,7 @@
 // bf16: 64 us, 4.9 TB/s (shares end together, but an item's start and join cost what 12
 // units do); one of 777, fp32: 11.6 us, all latency.  64 heads on 8 of 64 channels, Q4_0,
 // 33 of up to 16384, f16: 66 us, 2.6 TB/s, bound by instructions (half the bytes a
-// value, the same unpacking), as are 5 rows of 16 heads on 8 of 256 channels (91 us).
+// value, the same unpacking), as are 5 rows of 16 heads on 8 of 256 channels (86 us).
 #pragma once
 #include <atomic>
 
@@ -77,8 +77,9 @@ struct AttnSmem {
     static constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
     static constexpr int kStage = kUnit * (kKB + kVB); // keys of the unit's groups, then their values
     // Ring bytes that leave an SM its CTAs, and heads of 256 channels some first-level cache
-    // for what their registers do not hold (Q4_0, 33 ragged sequences of up to 8192: 72 KB
-    // 211 us with one CTA an SM, 64 KB 154).
+    // for what their registers do not hold (Q4_0, 33 ragged sequences of up to 8192, 16
+    // rows: 186 us, with 72 KB 300; 128 channels, Q8_0: 147, with 104 KB and so one CTA an
+    // SM 227).
     static constexpr int kFit = (D == 64 ? 52 : D == 128 ? 72 : 64) * 1024 / (kAttnWarps * kStage);
     static constexpr int kStages = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
     static constexpr int kMerge = D == 256 ? 128 : D;  // channels that the warps' totals are merged by
@@ -308,8 +309,8 @@ struct AttnRows {
     // power of two that lifts the probabilities: p * lift * (largest value scale) stays below 32000;
     // fp16 probabilities (16-bit activations) must not pass 2^15 themselves
     // 8 rows of 256 channels: the offsets are added to the results, one register a block
-    // instead of an accumulator's four (Q8_0: 182 -> 139 us; 16 rows, which spill either
-    // way: 283 -> 287)
+    // instead of an accumulator's four (Q8_0, 33 ragged sequences of up to 8192: 129 -> 123
+    // us; 16 rows, which spill either way: 182 -> 184)
     static constexpr bool kOffsetLater = D == 256 && MODE == A_HALF8;
     static constexpr float kMaxLift = MODE == A_SPLIT8 ? 40.0f : 15.0f;
 
