@@ -307,11 +307,11 @@ struct AttnRows {
     static constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
     static constexpr float kLog2e = 1.44269504088896340736f;
     // power of two that lifts the probabilities: p * lift * (largest value scale) stays below 32000;
-    // fp16 probabilities (16-bit activations) must not pass 2^15 themselves
     // 8 rows of 256 channels: the offsets are added to the results, one register a block
     // instead of an accumulator's four (Q8_0, 33 ragged sequences of up to 8192: 129 -> 123
     // us; 16 rows, which spill either way: 182 -> 184)
     static constexpr bool kOffsetLater = D == 256 && MODE == A_HALF8;
+    // fp16 probabilities (16-bit activations) must not pass 2^15 themselves
     static constexpr float kMaxLift = MODE == A_SPLIT8 ? 40.0f : 15.0f;
 
     float xs[RS];                    // score of an accumulator unit (plain: times log2 e)
