@@ -123,7 +123,7 @@ if __name__ == "__main__":
                     "tokens, dump>, k_attn_stream<K is 4-bit, V is 4-bit, channels, rows (0 8 of fp32, 1 8 and 2 16 of 16 "
                     "bits)>, k_attn_prompt<K, V, channels, bf16>, k_attn_promptf<K, V, channels>, k_attn_rows<K, V, "
                     "channels>, k_kv<store, channels> and k_route<keys a lane> (one row an element type); "
-                    "k_attn_prompt and k_attn_promptf launch with 96 registers and split them by warp role; formats 0 Q4_0, 1 Q8_0, 2 Q4_K, 3 Q5_K, 4 Q6_K, 5 MXFP4, 6 Q2_K, 7 Q3_K.\n\n")
+                    "k_attn_prompt and k_attn_promptf launch with 96 and 72 registers and split them by warp role; formats 0 Q4_0, 1 Q8_0, 2 Q4_K, 3 Q5_K, 4 Q6_K, 5 MXFP4, 6 Q2_K, 7 Q3_K.\n\n")
             f.write(ptxas_summary())
     else:
         print(build(force=True))

@@ -11,17 +11,17 @@
 // in registers, in fp32 with rounding to nearest.
 //
 // Measured (28 heads on 4 of 128 channels, distance bias, 5 ragged prompts of up to 1000
-// rows): 191 us, 95 TFLOP/s of the formula's operations (on mma.sync with the scales in
-// the accumulators: 321 us); 4096 causal rows of 32 heads on 8: 728 us (1716).  A step of
-// 32 keys takes 128 rows 1.5 us: 40 MMAs of 32 columns, some 60 cycles each with their
-// issue, and about 500 instructions of each of the softmax's eight warps; both alternate.
+// rows): 175 us, 104 TFLOP/s of the formula's operations (on mma.sync with the scales in
+// the accumulators: 321 us); 4096 causal rows of 32 heads on 8: 737 us (1716).  Bound by
+// its small MMAs: a step of 32 keys takes 128 rows 1.5 us for 40 MMAs of 32 columns, some
+// 70 cycles each whatever their width.
 //
 // A CTA takes 128 rows of one kv head of one sequence.  Roles:
-//   * warps 0-7: two threads a row, each half of a step's keys and half of the output's
+//   * warps 0-15: four threads a row, each a quarter of a step's keys and of the output's
 //     channels; they agree on the row's maximum through shared memory;
-//   * warps 8-15: the packed blobs to fp16 (keys) and bf16 (values) integers, K-major
+//   * warps 16-23: the packed blobs to fp16 (keys) and bf16 (values) integers, K-major
 //     128-byte-swizzled tiles of 128 keys, and their scales to fp32;
-//   * warps 16, 17 and 18, 19: one thread each issues the scores' and the outputs' MMAs
+//   * warps 24, 25 and 26, 27: one thread each issues the scores' and the outputs' MMAs
 //     of half the blocks (the instructions are small: one thread's issue would bound them).
 // Keys lie in tiles, scores and probabilities in the order in which a V word's lanes
 // hold them: key 16 c + 8 o + 2 t + e of 32 at place 8 t + 4 c + 2 o + e.
@@ -32,10 +32,16 @@
 
 namespace ggq {
 
-constexpr int kPfSoftmaxRegs = 160, kPfDecodeRegs = 64, kPfMmaRegs = 32;
-static_assert(kPfSoftmaxRegs >= kLaunchRegs && kPfDecodeRegs <= kLaunchRegs && kPfMmaRegs <= kLaunchRegs &&
-                  32 * (kSoftmaxWarps * kPfSoftmaxRegs + kDecodeWarps * kPfDecodeRegs + kMmaWarps * kPfMmaRegs) <=
-                      kPromptThreads * kLaunchRegs,
+// Four threads a row: 16 softmax warps, four a scheduler (5 ragged prompts of up to 1000
+// rows with a distance bias: 175 us; two threads a row with 160 registers each: 191.  4096
+// causal rows without one: 737 and 727).
+constexpr int kPfParts = 4, kPfSoftmaxWarps = 4 * kPfParts, kPfFirstMma = kPfSoftmaxWarps + kDecodeWarps;
+constexpr int kPfThreads = (kPfFirstMma + kMmaWarps) * 32;
+constexpr int kPfLaunchRegs = 72, kPfSoftmaxRegs = 88, kPfDecodeRegs = 56, kPfMmaRegs = 40;
+static_assert(kPfSoftmaxRegs >= kPfLaunchRegs && kPfDecodeRegs <= kPfLaunchRegs && kPfMmaRegs <= kPfLaunchRegs &&
+                  32 * (kPfSoftmaxWarps * kPfSoftmaxRegs + kDecodeWarps * kPfDecodeRegs + kMmaWarps * kPfMmaRegs) <=
+                      kPfThreads * kPfLaunchRegs &&
+                  kPfThreads * kPfLaunchRegs <= 65536,
               "register split");
 
 template <int D>
@@ -46,7 +52,7 @@ struct PromptfShape {
     static constexpr int kSteps = kTile / kKeys;  // steps of a tile; tensor memory sums over a tile
     static constexpr int kQ = 128 * D * 2, kK = kTile * D * 2, kV = kK, kS = kTile * NB * 4;
     static constexpr int oK = 2 * kQ, oV = oK + 2 * kK, oSK = oV + 2 * kV, oSV = oSK + 2 * kS, oTop = oSV + 2 * kS;
-    static constexpr int oBar = oTop + 4 * 128 * 4, kTotal = oBar + 256 + 1024;
+    static constexpr int oBar = oTop + 2 * kPfParts * 128 * 4, kTotal = oBar + 256 + 1024;
     static constexpr uint32_t cBuf = 192, cO = 2 * cBuf;  // columns: two buffers (scores 128, probabilities 192), then the output
     static_assert(cO + D <= 512, "tensor memory");
 };
@@ -71,26 +77,34 @@ __device__ __forceinline__ void pf_nibbles(uint32_t w, uint32_t (&h)[4]) {
         h[i] = *reinterpret_cast<const uint32_t*>(&r);
     }
 }
-// 16 columns, to be used after prompt_wait_ld on the same registers
-__device__ __forceinline__ void pf_ld16(uint32_t taddr, float* v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-        : "r"(taddr));
+// 8 columns, to be used after prompt_wait_ld on the same registers
+__device__ __forceinline__ void pf_ld8(uint32_t taddr, float* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr));
+}
+// keeps uses of v behind the wait
+__device__ __forceinline__ void pf_tie8(float* v) {
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
+}
+__device__ __forceinline__ void pf_st4(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]));
 }
 __device__ __forceinline__ void pf_st8(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]));
 }
 __device__ __forceinline__ float pf_half(uint32_t bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); }
-__device__ __forceinline__ void pf_pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory"); }
+// the warps of 32 rows
+__device__ __forceinline__ void pf_rows_sync(int quarter) { asm volatile("bar.sync %0, %1;" ::"r"(quarter + 1), "n"(32 * kPfParts) : "memory"); }
 
 template <bool K4, bool V4, int D>
-__global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kPfThreads, 1) k_attn_promptf(const __grid_constant__ AttnParams p) {
     using SH = PromptfShape<D>;
     constexpr int NB = SH::NB, KT = SH::kTile, KEYS = SH::kKeys, STEPS = SH::kSteps, KG = KT / 16;
-    constexpr int HK = KEYS / 2, HD = D / 2;  // keys and channels of a softmax thread
+    constexpr int HK = KEYS / kPfParts, HD = D / kPfParts;  // keys and channels of a softmax thread
+    constexpr int KS = KEYS / 16, PC = 192 / KS;             // MMA depths of a step's keys, columns of one's probabilities
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;  // warp: uniform
@@ -129,10 +143,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
         for (int i = 0; i < 2; ++i) {
             mbar_init(kfull + i, kDecodeWarps * 32);
             mbar_init(vfull + i, kDecodeWarps * 32);
-            mbar_init(kempty + i, 2 + kSoftmaxWarps);
-            mbar_init(vempty + i, 2 + kSoftmaxWarps);
+            mbar_init(kempty + i, 2 + kPfSoftmaxWarps);
+            mbar_init(vempty + i, 2 + kPfSoftmaxWarps);
             mbar_init(sfull + i, 2);
-            mbar_init(pfull + i, kSoftmaxWarps * 32);
+            mbar_init(pfull + i, kPfSoftmaxWarps * 32);
             mbar_init(pdone + i, 2);
             mbar_init(done + i, 1);
             mbar_init(done + 2 + i, 1);
@@ -141,20 +155,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
         for (int i = 0; i < NB; ++i) s_bad[2 * i] = 0x7fffffff, s_bad[2 * i + 1] = -1;
         fence_barrier_init();
     }
-    if (warp == kFirstMma) {
+    if (warp == kPfFirstMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tslot)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // ---- queries: a warp takes 16 rows, whole rows at a time, the row's largest element in [2^13, 2^14)
-    float* const s_top = reinterpret_cast<float*>(smem + SH::oTop);  // [2][2][128]; before the first step: [3 * 128 + row] scale
-    if (warp < kSoftmaxWarps) {
-        constexpr int LR = D / 4, RL = 32 / LR, NL = 16 / RL;  // lanes of a row, rows of a load, loads
+    // ---- queries: a warp takes 8 rows, whole rows at a time, the row's largest element in [2^13, 2^14)
+    float* const s_top = reinterpret_cast<float*>(smem + SH::oTop);  // [2][parts][128]; before the first step: [7 * 128 + row] scale
+    if (warp < kPfSoftmaxWarps) {
+        constexpr int LR = D / 4, RL = 32 / LR, NL = 8 / RL;  // lanes of a row, rows of a load, loads
         const int d = 4 * (lane % LR);
         float4 x[NL];
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
-            const int r = min(r_begin + warp * 16 + k * RL + lane / LR, r_end - 1), i = r / p.G;
+            const int r = min(r_begin + warp * 8 + k * RL + lane / LR, r_end - 1), i = r / p.G;
             x[k] = ld4(static_cast<const float*>(p.q) + (first + i) * p.q_token + (hk * p.G + r - i * p.G) * p.q_head + d);
         }
         // the K tile's channel order: chunk t of block b holds 32 b + 16 j + 4 t + i
@@ -162,7 +176,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
         const int chunk = 4 * ((d >> 5) & 1) + ((d >> 2) & 3);
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
-            const int rr = warp * 16 + k * RL + lane / LR;
+            const int rr = warp * 8 + k * RL + lane / LR;
             float amax = fmaxf(fmaxf(fabsf(x[k].x), fabsf(x[k].y)), fmaxf(fabsf(x[k].z), fabsf(x[k].w)));
 #pragma unroll
             for (int m = 1; m < LR; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
@@ -177,7 +191,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
             *reinterpret_cast<uint2*>(at) = hi;
             *reinterpret_cast<uint2*>(at + SH::kQ) = lo;
             // not negative: the largest product is the largest logit
-            if (lane % LR == 0) s_top[3 * 128 + rr] = fabsf(p.scale) * scalbnf(1.0f, -sh);
+            if (lane % LR == 0) s_top[7 * 128 + rr] = fabsf(p.scale) * scalbnf(1.0f, -sh);
         }
         fence_proxy_async_smem();
     }
@@ -204,12 +218,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
         return ok;
     };
 
-    if (warp >= kFirstMma) {
+    if (warp >= kPfFirstMma) {
         // ================================================================ MMA
         prompt_regs<false, kPfMmaRegs>();
         const int b0 = (warp & 1) * (NB / 2);  // its blocks
         if (elect_one() && steps > 0) {
-            if (warp < kFirstMma + 2) {
+            if (warp < kPfFirstMma + 2) {
                 const uint64_t qd = umma_desc_sw128(smem_addr(smem));
                 constexpr uint32_t id = prompt_idesc(KEYS, false);
                 for (int i = 0; i < steps; ++i) {
@@ -231,7 +245,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
                 }
             } else {
                 constexpr uint32_t id = prompt_idesc(32, true);
-                constexpr int KS = HK / 16;  // MMA depths of a thread's keys
                 for (int i = 0; i < steps; ++i) {
                     const int j = i / STEPS, h = i % STEPS, buf = j & 1, sb = i & 1;
                     if (h == 0 && !wait1(vfull + buf, (j >> 1) & 1)) break;
@@ -245,23 +258,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
 #pragma unroll
                         for (int term = 2; term >= 0; --term)
 #pragma unroll
-                            for (int k = 0; k < 2 * KS; ++k) {
+                            for (int k = 0; k < KS; ++k) {
                                 const int blk = b0 + e;
                                 tc_mma_ts(tmem + SH::cO + 32 * blk,
-                                          tmem + SH::cBuf * sb + 96 * (k / KS) + (3 * blk + term) * (HK / 2) + 8 * (k % KS),
+                                          tmem + SH::cBuf * sb + PC * k + (3 * blk + term) * 8,
                                           vd + blk * (32 * 128 / 16) + 2 * k, id, h > 0 || term < 2 || k > 0);
                             }
                     tc_commit(pdone + sb);
                     if (h == STEPS - 1) tc_commit(vempty + buf);
                 }
             }
-            tc_commit(done + warp - kFirstMma);
-            mbar_wait(done + warp - kFirstMma, 0);  // every MMA has ended before tensor memory goes
+            tc_commit(done + warp - kPfFirstMma);
+            mbar_wait(done + warp - kPfFirstMma, 0);  // every MMA has ended before tensor memory goes
         }
-    } else if (warp >= kSoftmaxWarps) {
+    } else if (warp >= kPfSoftmaxWarps) {
         // ================================================================ packed blobs -> operand tiles and scales
         prompt_regs<false, kPfDecodeRegs>();
-        const int cw = warp - kSoftmaxWarps, g8 = lane >> 2, t4 = lane & 3, gpp = p.page >> 4;
+        const int cw = warp - kPfSoftmaxWarps, g8 = lane >> 2, t4 = lane & 3, gpp = p.page >> 4;
         constexpr int kKB = kv_blob_bytes(K4, D), kVB = kv_blob_bytes(V4, D);
         static_assert(KG == kDecodeWarps, "a warp takes one group of a tile's keys");
         constexpr int KL = K4 ? D / 64 : D / 32, VB = NB / 2;  // 16-byte words of a lane; blocks of values of a warp
@@ -398,14 +411,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
             mbar_arrive(vfull + buf);
         }
     } else {
-        // ================================================================ softmax: two threads a row
+        // ================================================================ softmax: four threads a row
         prompt_regs<true, kPfSoftmaxRegs>();
-        const int rr = tid & 127, half = tid >> 7, r = min(r_begin + rr, r_end - 1);
+        const int rr = tid & 127, part = tid >> 7, r = min(r_begin + rr, r_end - 1);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t cs = tmem + lanes, co = tmem + SH::cO + half * HD + lanes;
+        const uint32_t cs = tmem + lanes, co = tmem + SH::cO + part * HD + lanes;
         const int i_row = r / p.G, h = hk * p.G + r - i_row * p.G, pos = from + i_row;
         const int first_key = p.window > 0 ? pos - p.window + 1 : 0;
-        const float rscale = s_top[3 * 128 + rr];
+        const float rscale = s_top[7 * 128 + rr];
         const bool plain = p.cap <= 0.0f && !p.slopes && rscale > 0.0f;
         constexpr float kLog2e = 1.44269504088896340736f;
         const float slope = p.slopes ? p.slopes[h] * kLog2e : 0.0f;
@@ -420,40 +433,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
             wait(pdone + (last & 1), (last >> 1) & 1);
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < HD; c += 32) {
-                float o[32];
-                prompt_ld32(co + c, o);
+            for (int c = 0; c < HD; c += 16) {
+                float o[16];
+                pf_ld8(co + c, o);
+                pf_ld8(co + c + 8, o + 8);
                 prompt_wait_ld();
-                prompt_tie32(o);
+                pf_tie8(o);
+                pf_tie8(o + 8);
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) add2(tot[c + k], tot[c + k + 1], tot[c + k], tot[c + k + 1], o[k], o[k + 1]);
+                for (int k = 0; k < 16; k += 2) add2(tot[c + k], tot[c + k + 1], tot[c + k], tot[c + k + 1], o[k], o[k + 1]);
             }
         };
-        // A wait that gave up does not leave the loop: the other warp of the rows waits at the pair's barrier.
+        // A wait that gave up does not leave the loop: the other warps of the rows wait at their barrier.
         for (int i = 0; i < steps; ++i) {
-            const int j = i / STEPS, at = (i % STEPS) * KEYS + half * HK, buf = j & 1, sb = i & 1;
+            const int j = i / STEPS, at = (i % STEPS) * KEYS + part * HK, buf = j & 1, sb = i & 1;
             if (i % STEPS == 0) wait(kfull + buf, (j >> 1) & 1);
             wait(sfull + sb, (i >> 1) & 1);
             tc_fence_after();
-            const int key0 = 16 * glo + i * KEYS, mine = key0 + (KEYS == 32 ? 4 : 32) * half;
+            const int key0 = 16 * glo + i * KEYS, mine = key0 + (KEYS == 32 ? 2 * part : 32 * (part >> 1) + 4 * (part & 1));
             const bool whole = key0 + KEYS - 1 <= pos_first && key0 >= seen_from;
             float x[HK];
-            {
-                float s[64];
+            const float* const sk = reinterpret_cast<const float*>(smem + SH::oSK + buf * SH::kS) + at;
 #pragma unroll
-                for (int blk = 0; blk < NB; ++blk)
-                    if constexpr (HK == 32) prompt_ld32(cs + SH::cBuf * sb + blk * KEYS + half * HK, s + blk * HK);
-                    else pf_ld16(cs + SH::cBuf * sb + blk * KEYS + half * HK, s + blk * HK);
+            for (int b2 = 0; b2 < NB; b2 += 2) {  // two blocks at a time
+                float s[2 * HK];
+#pragma unroll
+                for (int k = 0; k < 2 * HK; k += 8)
+                    pf_ld8(cs + SH::cBuf * sb + (b2 + k / HK) * KEYS + part * HK + k % HK, s + k);
                 prompt_wait_ld();
-                prompt_tie32(s);
-                prompt_tie32(s + 32);
-                const float* const sk = reinterpret_cast<const float*>(smem + SH::oSK + buf * SH::kS) + at;
 #pragma unroll
-                for (int blk = 0; blk < NB; ++blk)
+                for (int k = 0; k < 2 * HK; k += 8) pf_tie8(s + k);
+#pragma unroll
+                for (int blk = b2; blk < b2 + 2; ++blk)
 #pragma unroll
                     for (int k = 0; k < HK; k += 4) {
                         const float4 d = *reinterpret_cast<const float4*>(sk + blk * KT + k);
-                        const float* const y = s + blk * HK + k;
+                        const float* const y = s + (blk - b2) * HK + k;
                         if (blk == 0) {
                             mul2(x[k], x[k + 1], y[0], y[1], d.x, d.y);
                             mul2(x[k + 2], x[k + 3], y[2], y[3], d.z, d.w);
@@ -487,11 +502,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
 #pragma unroll
             for (int k = 0; k < HK; ++k) tops[k & 3] = fmaxf(tops[k & 3], x[k]);
             float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;
-            s_top[(sb * 2 + half) * 128 + rr] = top;
-            tc_fence_before();  // both halves of the scores are read before probabilities go over them
-            pf_pair_sync(warp & 3);
+            s_top[(sb * kPfParts + part) * 128 + rr] = top;
+            tc_fence_before();  // all of the rows' scores are read before probabilities go over them
+            pf_rows_sync(warp & 3);
             tc_fence_after();
-            top = fmaxf(top, s_top[(sb * 2 + (half ^ 1)) * 128 + rr]);
+#pragma unroll
+            for (int k = 0; k < kPfParts; ++k) top = fmaxf(top, s_top[(sb * kPfParts + k) * 128 + rr]);
             const bool raise = top > m + 8.0f, raised = __any_sync(0xffffffffu, raise), fresh = i % STEPS == 0;
             float a = 1.0f;
             if (raise) {
@@ -529,9 +545,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
                                 ffma2(y[z], y[z + 1], __uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u), -1.0f, y[z], y[z + 1]);
                         }
                 }
-                const uint32_t to = cs + SH::cBuf * sb + 96 * half + blk * (3 * HK / 2);
 #pragma unroll
-                for (int k = 0; k < 3 * HK / 2; k += 8) pf_st8(to + k, w + k);
+                for (int term = 0; term < 3; ++term) {
+                    const uint32_t to = cs + SH::cBuf * sb + (3 * blk + term) * 8;
+                    if constexpr (HK == 16) pf_st8(to + PC * part, w + 8 * term);
+                    else pf_st4(to + PC * (part >> 1) + 4 * (part & 1), w + 4 * term);
+                }
             }
             if (i % STEPS == STEPS - 1) {
                 __syncwarp();
@@ -543,11 +562,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
 #pragma unroll
                     for (int k = 0; k < HD; ++k) tot[k] *= a;
                     if (!fresh) {
-                        uint32_t zero[32];
+                        const uint32_t zero[8] = {};
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) zero[k] = 0u;
-#pragma unroll
-                        for (int c = 0; c < HD; c += 32) prompt_st32(co + c, zero);
+                        for (int c = 0; c < HD; c += 8) pf_st8(co + c, zero);
                     }
                 }
             }
@@ -557,28 +574,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_promptf(const __grid
         }
         // ---- output rows
         if (steps > 0) fold(steps - 1);
-        s_top[half * 128 + rr] = l;
-        pf_pair_sync(warp & 3);
-        l = s_top[rr] + s_top[128 + rr];
+        s_top[part * 128 + rr] = l;
+        pf_rows_sync(warp & 3);
+        l = (s_top[rr] + s_top[128 + rr]) + (s_top[256 + rr] + s_top[384 + rr]);
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         if (r_begin + rr < r_end) {
-            float* const out = static_cast<float*>(p.out) + (first + i_row) * p.out_token + h * p.out_head + half * HD;
+            float* const out = static_cast<float*>(p.out) + (first + i_row) * p.out_token + h * p.out_head + part * HD;
+            // an infinite or NaN value among those that the row sees
+            const int* const sp = s_bad + 2 * (part * HD / 32);
+            const bool spoilt = sp[0] <= pos && sp[1] >= first_key && sp[1] >= 0;
+            const float f = spoilt ? NAN : inv;
 #pragma unroll
-            for (int c = 0; c < HD; c += 32) {
-                // an infinite or NaN value among those that the row sees
-                const int* const sp = s_bad + 2 * (half * (HD / 32) + c / 32);
-                const bool spoilt = sp[0] <= pos && sp[1] >= first_key && sp[1] >= 0;
-                const float f = spoilt ? NAN : inv;
-#pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                    *reinterpret_cast<float4*>(out + c + k) =
-                        make_float4(tot[c + k] * f, tot[c + k + 1] * f, tot[c + k + 2] * f, tot[c + k + 3] * f);
-            }
+            for (int k = 0; k < HD; k += 4)
+                *reinterpret_cast<float4*>(out + k) = make_float4(tot[k] * f, tot[k + 1] * f, tot[k + 2] * f, tot[k + 3] * f);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kFirstMma) {
+    if (warp == kPfFirstMma) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
@@ -597,14 +610,14 @@ cudaError_t launch_attn_promptf_one(const AttnParams& p, cudaStream_t s) {
         cudaFuncAttributes at;
         e = cudaFuncGetAttributes(&at, k_attn_promptf<K4, V4, D>);
         if (e != cudaSuccess) return e;
-        if (at.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;  // the split would not add up
+        if (at.numRegs != kPfLaunchRegs) return cudaErrorInvalidConfiguration;  // the split would not add up
         e = cudaFuncSetAttribute(k_attn_promptf<K4, V4, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kTotal);
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_release);
     }
     const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.G + 127) / 128;
     return launch_pdl(k_attn_promptf<K4, V4, D>,
-                      dim3(static_cast<unsigned>(p.n_seqs * p.Hkv), static_cast<unsigned>(tiles)), dim3(kPromptThreads),
+                      dim3(static_cast<unsigned>(p.n_seqs * p.Hkv), static_cast<unsigned>(tiles)), dim3(kPfThreads),
                       SH::kTotal, s, p);
 }
 
