@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ggq_attn_plan.h"
 #include "ggq_kv.cuh"
 
 namespace ggq {
@@ -28,11 +29,9 @@ struct AttnParams {
     float scale, cap;
     int min_share;           // units (one or two 16-token groups) below which a CTA's share is not cut
     float* parts;            // partial results [2 * kAttnMaxCtas][attn_part_floats(D)]
-    int* pieces;             // pieces, and groups of pieces, that have arrived [2][kAttnMaxCtas], zero between calls
+    int* pieces;             // arrival counters [kAttnCounters], zero between calls
     int* err;
 };
-
-constexpr int kAttnMaxCtas = 1024;
 
 // A partial result: reference maxima [16], sums [16], values [16][D].
 __host__ __device__ constexpr int attn_part_floats(int D) { return 32 + 16 * D; }

@@ -135,11 +135,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b, int tile
 // Units of UNIT groups of an item, and of the sequence's items together.
 template <int UNIT>
 __device__ __forceinline__ int attn_units(const AttnSeq& s) { return (s.ghi - s.glo + UNIT - 1) / UNIT; }
-// What an item counts in the shares: its units, and kItemCost for its queries, its
-// merge and its output (measured on 64 ragged sequences of up to 4096 tokens: 82 us
-// at 0, 68 at 6, 63.6 at 12, 65 at 20).
-// The first kItemCost positions of an item stand for no unit.
-constexpr int kItemCost = 12;
+// Positions of an item in the list of all items: kItemCost, then its units.
 template <int UNIT>
 __device__ __forceinline__ int attn_span(const AttnSeq& s) {
     const int n = attn_units<UNIT>(s);
@@ -732,26 +728,11 @@ __device__ __forceinline__ AttnWalk<UNIT> attn_find(const AttnParams& p, const i
     return w;
 }
 
-// ---- items that several CTAs share.  The pieces of the item at position p0 belong
-// to the CTAs c0 .. c1 (c0: where its units begin); each piece is a partial result in
-// its CTA's slot 0 if the CTA's share begins with it, else in slot 1 (c0's only).
-// Sixteen neighbouring pieces are joined by the last of them, then these results by
-// the last of the groups, always in the order of the pieces.
-constexpr int kJoin = 16;
-
-template <int UNIT>
-struct AttnPieces {
-    int c0, c1, slot0;
-    __device__ __forceinline__ AttnPieces(const AttnWalk<UNIT>& w, int64_t p0, int64_t N, int C) {
-        c0 = static_cast<int>(((p0 + kItemCost + 1) * C - 1) / N);
-        c1 = static_cast<int>(((p0 + attn_span<UNIT>(w.s)) * C - 1) / N);
-        slot0 = N * c0 / C >= p0 ? 0 : 1;
-    }
-    template <int D>
-    __device__ __forceinline__ float* at(const AttnParams& p, int k) const {
-        return p.parts + (2 * static_cast<int64_t>(k) + (k == c0 ? slot0 : 0)) * attn_part_floats(D);
-    }
-};
+// ---- items that several CTAs share (ggq_attn_plan.h)
+template <int D>
+__device__ __forceinline__ float* attn_part(const AttnParams& p, int c, int slot) {
+    return p.parts + (2 * static_cast<int64_t>(c) + slot) * attn_part_floats(D);
+}
 
 __device__ __forceinline__ int atomic_add_acq_rel(int* p, int v) {
     int old;
@@ -764,10 +745,11 @@ __device__ __forceinline__ int atomic_add_acq_rel(int* p, int v) {
 template <int UNIT>
 __device__ __forceinline__ void attn_arrive(const AttnParams& p, const AttnWalk<UNIT>& w, int64_t p0, int64_t N, int C,
                                             volatile int* last) {
-    const AttnPieces<UNIT> q(w, p0, N, C);
-    const int g0 = q.c0 + (static_cast<int>(blockIdx.x) - q.c0) / kJoin * kJoin, n = min(kJoin, q.c1 - g0 + 1);
-    const bool is_last = atomic_add_acq_rel(p.pieces + g0, 1) == n - 1;
-    if (is_last) p.pieces[g0] = 0;
+    const AttnPieces q(p0, attn_span<UNIT>(w.s), N, C);
+    const int g0 = q.group(static_cast<int>(blockIdx.x));
+    int* const counter = p.pieces + q.piece_counter(g0);
+    const bool is_last = atomic_add_acq_rel(counter, 1) == q.group_pieces(g0) - 1;
+    if (is_last) *counter = 0;
     *last = is_last;
 }
 
@@ -776,12 +758,12 @@ template <int D, int ROWS, int UNIT>
 __device__ __noinline__ void attn_join(const AttnParams& p, const AttnWalk<UNIT>& w, int64_t p0, int64_t N, int C, int tid,
                                        volatile int* last) {
     if (!*last) return;
-    const AttnPieces<UNIT> q(w, p0, N, C);
+    const AttnPieces q(p0, attn_span<UNIT>(w.s), N, C);
     const AttnTile tile = attn_tile(p, w.s, w.item, ROWS);
-    const int g0 = q.c0 + (static_cast<int>(blockIdx.x) - q.c0) / kJoin * kJoin;
-    const bool groups = q.c1 - q.c0 >= kJoin;
+    const int g0 = q.group(static_cast<int>(blockIdx.x));
+    const bool groups = q.groups() > 1;
     for (int level = 0; level < 2; ++level) {
-        const int from = level ? q.c0 : g0, step = level ? kJoin : 1, to = level ? q.c1 : min(g0 + kJoin - 1, q.c1);
+        const int from = level ? q.c0 : g0, step = level ? kJoin : 1, to = level ? q.c1 : g0 + q.group_pieces(g0) - 1;
         const bool done = level == 1 || !groups;
         constexpr int kQuads = (ROWS * D / 4 + kAttnThreads - 1) / kAttnThreads;
         float4 o[kQuads];
@@ -797,7 +779,8 @@ __device__ __noinline__ void attn_join(const AttnParams& p, const AttnWalk<UNIT>
                 float4 v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float* const a = q.template at<D>(p, min(b + e * step, to - (to - from) % step));
+                    const int c = min(b + e * step, to - (to - from) % step);
+                    const float* const a = attn_part<D>(p, c, q.slot(c));
                     pm[e] = __ldcg(a + row), pl[e] = __ldcg(a + 16 + row);
                     v[e] = __ldcg(reinterpret_cast<const float4*>(a + 32 + row * D + d));
                 }
@@ -818,7 +801,7 @@ __device__ __noinline__ void attn_join(const AttnParams& p, const AttnWalk<UNIT>
                     }
             }
         }
-        float* const to_part = q.template at<D>(p, g0);
+        float* const to_part = attn_part<D>(p, g0, q.slot(g0));
         if (!done) __syncthreads();  // the group's first piece is read: its place takes the result
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
@@ -836,9 +819,9 @@ __device__ __noinline__ void attn_join(const AttnParams& p, const AttnWalk<UNIT>
         if (done) return;
         __syncthreads();
         if (tid == 0) {
-            const int n = (q.c1 - q.c0) / kJoin + 1;
-            const bool is_last = atomic_add_acq_rel(p.pieces + kAttnMaxCtas + q.c0, 1) == n - 1;
-            if (is_last) p.pieces[kAttnMaxCtas + q.c0] = 0;
+            int* const counter = p.pieces + q.group_counter();
+            const bool is_last = atomic_add_acq_rel(counter, 1) == q.groups() - 1;
+            if (is_last) *counter = 0;
             *last = is_last;
         }
         __syncthreads();
@@ -1011,7 +994,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         // ---- the segment's result: the four warps' parts, 8 rows at a time
         const int n_units = attn_units<UNIT>(sq);
         const bool whole = ua == 0 && ub == n_units;
-        float* const part = p.parts + (static_cast<int64_t>(c) * 2 + (at0 == lo ? 0 : 1)) * attn_part_floats(D);
+        float* const part = attn_part<D>(p, c, at0 == lo ? 0 : 1);
         float* const s_mine = s_tot + warp * 8 * SM::kRowPitch;
 #pragma unroll
         for (int rs = 0; rs < RS; ++rs) {

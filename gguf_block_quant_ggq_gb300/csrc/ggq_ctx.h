@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "../../include/ggq.h"
+#include "ggq_attn_plan.h"
 
 namespace ggq {
 
@@ -20,7 +21,7 @@ inline size_t align_up(size_t v, size_t a = kAlign) { return (v + a - 1) / a * a
 struct Ctrl {
     int err;
     int pad[63];
-    int attn_pieces[2 * 1024];  // attention: arrived pieces and groups of pieces of shared items, zero between calls
+    int attn_pieces[kAttnCounters];  // attention: arrived pieces and groups of pieces of shared items, zero between calls
 };
 
 }  // namespace ggq
