@@ -1,9 +1,9 @@
 // ggq_route.cu -- the expert router: scores, choice, groups, top-k, weights.
 //
 // Mathematics: score = softmax(l) or sigmoid(l); choice = score + bias (softmax
-// without bias: the logits, whose order is the scores'); only the best groups'
-// experts stay; the top_k choices in order, ties to the lower id; weights are
-// the chosen scores, renormalised and scaled.  Reads each logit once; at a few
+// without bias: the logits, whose order is the scores'; sums of a group's two best
+// are of scores always); only the best groups' experts stay; the top_k choices in
+// order, ties to the lower id; weights are the chosen scores, renormalised and scaled.  Reads each logit once; at a few
 // thousand tokens bound by the k dependent rounds of the selection, not by
 // bytes.
 //
@@ -43,10 +43,20 @@ __device__ __forceinline__ float score_of(float x, bool sigmoid, float m) {
     return x != x ? 0.0f : s;
 }
 
-// The sum of a group's two largest keys' values, or the largest value, as a key.
-__device__ __forceinline__ uint32_t group_key(uint32_t a, uint32_t b, bool two) {
-    return key_of(two ? __fadd_rn(value_of(a), value_of(b)) : value_of(a));
-}
+// A group's score as a key: the value of its largest key, or the sum of its two largest
+// ones'.  Keys of logits (softmax without bias) stand in the order of the scores, but
+// their sums do not: the scores are added then.
+struct GroupScore {
+    bool two, logits;
+    float m, inv;
+    __device__ __forceinline__ float value(uint32_t key) const {
+        const float x = value_of(key);
+        return logits && key > kNaN ? __fmul_rn(score_of(x, false, m), inv) : x;
+    }
+    __device__ __forceinline__ uint32_t key(uint32_t a, uint32_t b) const {
+        return key_of(two ? __fadd_rn(value(a), value(b)) : value_of(a));
+    }
+};
 
 // NV: keys a lane holds in registers (E <= 32 NV).
 template <int NV, typename T>
@@ -78,7 +88,8 @@ __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RoutePara
         for (int i = 0; i < NV; ++i) m = fmaxf(m, x[i]);
         m = warp_max(m);
         if (m == -INFINITY) m = 0.0f;  // a row of -inf: every score 0
-        if (p.bias || !p.normalize) {  // the scores themselves are needed, not only their ratios
+        // the scores themselves are needed, not only their ratios (the sums of two: the same with a bias of 0)
+        if (p.bias || !p.normalize || (p.n_groups > 1 && p.group_best == 2)) {
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) s += score_of(x[i], false, m);
@@ -100,7 +111,8 @@ __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RoutePara
     }
     if (p.n_groups > 1) {
         const int per = p.E / p.n_groups, lanes = per / NV;  // lanes of a group
-        const bool two = p.group_best == 2, whole = lanes * NV == per && (lanes & (lanes - 1)) == 0;
+        const GroupScore score{p.group_best == 2, !sigmoid && !p.bias, m, inv};
+        const bool whole = lanes * NV == per && (lanes & (lanes - 1)) == 0;
         uint32_t mine = kTaken;  // this lane's group's score; lanes that are not a group's first one: none
         if (whole) {
             uint32_t a = kTaken, b = kTaken;  // the two largest keys
@@ -114,7 +126,7 @@ __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RoutePara
                 b = max(max(b, ob), min(a, oa));
                 a = max(a, oa);
             }
-            if ((lane & (lanes - 1)) == 0 && e0 < p.E) mine = group_key(a, b, two);
+            if ((lane & (lanes - 1)) == 0 && e0 < p.E) mine = score.key(a, b);
         } else if constexpr (NV <= 16) {
             uint32_t* const keys = s_keys + warp * 32 * NV;
 #pragma unroll
@@ -127,7 +139,7 @@ __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RoutePara
                     b = max(b, min(a, k));
                     a = max(a, k);
                 }
-                mine = group_key(a, b, two);
+                mine = score.key(a, b);
             }
         } else {
             for (int g = 0; g < p.n_groups; ++g) {
@@ -141,7 +153,7 @@ __global__ void __launch_bounds__(128) k_route(const __grid_constant__ RoutePara
                 const uint32_t first = __reduce_max_sync(kFull, a);
                 if (lane == __ffs(__ballot_sync(kFull, a == first)) - 1) a = b;
                 const uint32_t second = __reduce_max_sync(kFull, a);
-                if (lane == g) mine = group_key(first, second, two);
+                if (lane == g) mine = score.key(first, second);
             }
         }
         uint32_t open = 0u;  // bit l: the group that lane l scored stays open

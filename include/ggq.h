@@ -456,8 +456,8 @@ ggq_status ggq_reserve_attention(ggq_ctx* ctx, void* stream);
  *   ids = the top_k open experts by choice, best first (ties to the lower id);
  *   weights = their scores (without the bias), with `normalize` divided by their
  *     sum (a sum of 0 leaves zeros), times scale.
- * Softmax without bias compares the logits themselves.  A NaN logit is chosen
- * last and weighs 0.  1 <= top_k <= 32, E <= 4096, n_groups <= 32 dividing E, top_k <=
+ * Softmax without bias orders experts, and groups of group_best = 1, by the logits
+ * themselves.  A NaN logit is chosen last and weighs 0.  1 <= top_k <= 32, E <= 4096, n_groups <= 32 dividing E, top_k <=
  * top_groups * E / n_groups.  ids and weights [T][top_k] are what
  * ggq_moe_experts_routed takes.  Needs no scratch. */
 ggq_status ggq_moe_route(ggq_ctx* ctx, const ggq_router* router, int dtype, const void* logits, int64_t T, int64_t E,
