@@ -44,7 +44,7 @@ __device__ __forceinline__ float score_of(float x, bool sigmoid, float m) {
 }
 
 // A group's score as a key: the value of its largest key, or the sum of its two largest
-// ones'.  Keys of logits (softmax without bias) stand in the order of the scores, but
+// ones' (of one where the group has no second).  Keys of logits (softmax without bias) stand in the order of the scores, but
 // their sums do not: the scores are added then.
 struct GroupScore {
     bool two, logits;
@@ -54,7 +54,7 @@ struct GroupScore {
         return logits && key > kNaN ? __fmul_rn(score_of(x, false, m), inv) : x;
     }
     __device__ __forceinline__ uint32_t key(uint32_t a, uint32_t b) const {
-        return key_of(two ? __fadd_rn(value(a), value(b)) : value_of(a));
+        return key_of(!two ? value_of(a) : b == kTaken ? value(a) : __fadd_rn(value(a), value(b)));
     }
 };
 

@@ -193,7 +193,7 @@ typedef struct ggq_router {
     int32_t scoring;    /* ggq_scoring                                           */
     int32_t n_groups;   /* groups of E / n_groups neighbouring experts; 1: none  */
     int32_t top_groups; /* groups that stay open                                 */
-    int32_t group_best; /* a group's score: the sum of its best 1 or 2 choices   */
+    int32_t group_best; /* a group's score: the sum of its best 1 or 2 choices (of its only one) */
     int32_t top_k;
     int32_t normalize;  /* weights divided by their sum                          */
     float scale;        /* then multiplied by this                               */

@@ -50,3 +50,19 @@ def test_softmax_groups(ctx, T, E, groups, top, k, dtype):  # noqa: F811
     with_bias, _ = ctx.moe_route(x.cuda(), k, n_groups=groups, top_groups=top, group_best=2, bias=torch.zeros(E, device="cuda"))
     assert torch.equal(ids, with_bias)
     ctx.sync_status()
+
+
+@pytest.mark.parametrize("T,E,top,k", [(6, 32, 5, 5), (9, 8, 3, 2), (4, 17, 16, 16)])
+@pytest.mark.parametrize("scoring,bias", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+def test_groups_of_one_expert(ctx, T, E, top, k, scoring, bias):  # noqa: F811
+    """No second choice to add: the group's score is its expert's."""
+    x = grid(T, E, E, "f32")
+    b = torch.randperm(E, generator=torch.Generator().manual_seed(E)).float() / 4 if bias else None
+    want, weights, gap = reference(x, k, E, top, 2, scoring, b)
+    assert gap > 2.0 ** -20
+    args = dict(scoring=scoring, n_groups=E, top_groups=top, bias=None if b is None else b.cuda())
+    ids, w = ctx.moe_route(x.cuda(), k, group_best=2, **args)
+    assert torch.equal(ids.cpu().long(), want)
+    assert ((w.cpu().double() - weights).abs() <= (10 + k + E ** 0.5) * 2.0 ** -23 * weights).all()
+    assert torch.equal(ids, ctx.moe_route(x.cuda(), k, group_best=1, **args)[0])
+    ctx.sync_status()
