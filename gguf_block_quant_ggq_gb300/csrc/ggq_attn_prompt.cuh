@@ -213,6 +213,34 @@ __device__ __forceinline__ uint32_t prompt_v4(uint32_t h, float d0, float d1, ui
     return prompt_mul2(h, d2);
 }
 
+// Whether a value scale of block blk is not finite among the keys first_key .. pos.  The
+// tile kernels keep the first and last such key that they meet; a row whose window lies
+// between the two looks for itself.
+template <bool V4, int D>
+__device__ __noinline__ bool prompt_bad_value(const AttnParams& p, int b, int hk, int blk, int first_key, int pos) {
+    const int gpp = p.page >> 4;
+    const uint16_t* scales = nullptr;
+    for (int key = first_key; key <= pos; ++key) {
+        if (scales == nullptr || (key & 15) == 0) {
+            const int g = key >> 4;
+            int pg = p.table[b * p.table_stride + g / gpp];
+            if (pg < 0 || pg >= p.n_pages) pg = 0;
+            const int64_t at = (static_cast<int64_t>(pg) * p.Hkv + hk) * gpp + g % gpp;
+            scales = reinterpret_cast<const uint16_t*>(p.v + at * kv_blob_bytes(V4, D) + kv_quant_bytes(V4, D)) + blk;
+        }
+        if ((__ldg(scales + (key & 15) * (D / 32)) & 0x7C00u) == 0x7C00u) return true;
+    }
+    return false;
+}
+// A row sees a value scale of block blk that is not finite; s_bad: the first and last key of those.
+template <bool V4, int D>
+__device__ __forceinline__ bool prompt_spoilt(const AttnParams& p, const int* s_bad, int b, int hk, int blk, int first_key, int pos) {
+    const int lo = s_bad[2 * blk], hi = s_bad[2 * blk + 1];
+    if (lo > pos || hi < first_key || hi < 0) return false;
+    if (lo >= first_key || hi <= pos) return true;
+    return prompt_bad_value<V4, D>(p, b, hk, blk, first_key, pos);
+}
+
 template <bool REGS_UP, int N>
 __device__ __forceinline__ void prompt_regs() {
     if (REGS_UP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -669,13 +697,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         tc_fence_after();
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         const int64_t at = (first + i_row) * p.out_token + h * p.out_head;
+        bool spoilt = false;  // an infinite or NaN value of the block among those that the row sees
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
             float o[16];
+            if ((c & 1) == 0) {
+                spoilt = prompt_spoilt<V4, D>(p, s_bad, b, hk, c >> 1, first_key, pos);
+                __syncwarp();
+            }
             if (steps > 0) prompt_ld16(co + 16 * c, o);
-            // an infinite or NaN value among those that the row sees
-            const int* const sb = s_bad + 2 * (c >> 1);
-            const bool spoilt = sb[0] <= pos && sb[1] >= first_key && sb[1] >= 0;
             if (there) {
 #pragma unroll
                 for (int k = 0; k < 16; k += 8) {

@@ -581,9 +581,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) k_attn_promptf(const __grid_con
         if (r_begin + rr < r_end) {
             float* const out = static_cast<float*>(p.out) + (first + i_row) * p.out_token + h * p.out_head + part * HD;
             // an infinite or NaN value among those that the row sees
-            const int* const sp = s_bad + 2 * (part * HD / 32);
-            const bool spoilt = sp[0] <= pos && sp[1] >= first_key && sp[1] >= 0;
-            const float f = spoilt ? NAN : inv;
+            const float f = prompt_spoilt<V4, D>(p, s_bad, b, hk, part * HD / 32, first_key, pos) ? NAN : inv;
 #pragma unroll
             for (int k = 0; k < HD; k += 4)
                 *reinterpret_cast<float4*>(out + k) = make_float4(tot[k] * f, tot[k + 1] * f, tot[k + 2] * f, tot[k + 3] * f);

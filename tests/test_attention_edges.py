@@ -26,3 +26,50 @@ def test_long_sequences_beside_short_ones(ctx, lens, dtype, news):  # noqa: F811
         c.call(out=again)
         assert torch.equal(out, again)
     ctx.sync_status()
+
+
+# prompts from nothing, so that rows lie before, at, between and behind two places of a sequence
+PROMPTS = [300, 400, 257, 129, 90, 350, 200, 310, 33, 16, 399, 17] * 2
+
+
+def set_scale(c, pool, type_, page, place, block, bits):
+    """Writes `bits` as the scale of one block of 32 channels of the cache's slot `place`, of every kv head."""
+    per = (17 if type_ == "Q8_0" else 9) * c.D
+    blobs = pool.view(-1, per)
+    first = (place // page * c.Hkv + torch.arange(c.Hkv, device="cuda")) * (page // 16) + place % page // 16
+    at = per - c.D + 2 * (place % 16 * (c.D // 32) + block)
+    blobs[first, at] = bits & 0xFF
+    blobs[first, at + 1] = bits >> 8
+
+
+@pytest.mark.parametrize("bits", [0x7E00, 0x7C00, 0xFC00])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("D,v_type,page", [(64, "Q8_0", 16), (128, "Q4_0", 48), (128, "Q8_0", 64), (256, "Q8_0", 16)])
+@pytest.mark.parametrize("window", [0, 1, 40])
+def test_rows_between_two_bad_values(ctx, D, v_type, page, dtype, window, bits):  # noqa: F811
+    """Two value scales of a sequence that are not finite: rows that see neither keep their results bit by
+    bit, those that see one have its 32 channels spoilt."""
+    for news in (PROMPTS, [min(3, x) for x in PROMPTS]):
+        c = Case(ctx, PROMPTS, news, 16, 8, D, v_type=v_type, dtype=dtype, page=page, seed=11)
+        clean = c.call(window=window)
+        k0, bad = 0, []
+        for length in PROMPTS:
+            bad.append([length // 4, length - 2 - length // 4])
+            for at in bad[-1]:
+                set_scale(c, c.cache.v, v_type, page, int(c.slots[k0 + at]), 1, bits)
+            k0 += length
+        out = c.call(window=window)
+        ctx.sync_status()
+        r0 = between = 0
+        for length, new, two in zip(PROMPTS, news, bad):
+            pos = torch.arange(length - new, length, device="cuda")
+            sees = torch.zeros(new, dtype=torch.bool, device="cuda")
+            for at in two:
+                sees |= (pos >= at) & (pos < at + window if window else True)
+            between += int((~sees & (pos > two[0]) & (pos < two[1])).sum())
+            got, want = out[r0:r0 + new], clean[r0:r0 + new]
+            assert torch.equal(got[~sees], want[~sees])
+            assert not torch.isfinite(got[sees][..., 32:64].float()).any()
+            assert torch.equal(got[sees][..., :32], want[sees][..., :32])
+            r0 += new
+        assert between > 0 or window == 0 or news is not PROMPTS
