@@ -428,8 +428,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) k_attn_promptf(const __grid_con
         float tot[HD], m = -1e30f, l = 0.0f;
 #pragma unroll
         for (int k = 0; k < HD; ++k) tot[k] = 0.0f;
-        // adds the sums in tensor memory to the totals
-        const auto fold = [&](int last) {
+        // adds the sums in tensor memory to the totals, or (SCALE) multiplies them by the row's factor where
+        // they are, which is 1 for rows that others of the warp take along: a row's roundings are its own
+        const auto fold = [&](auto SCALE, int last, float a) {
             wait(pdone + (last & 1), (last >> 1) & 1);
             tc_fence_after();
 #pragma unroll
@@ -440,8 +441,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) k_attn_promptf(const __grid_con
                 prompt_wait_ld();
                 pf_tie8(o);
                 pf_tie8(o + 8);
+                if constexpr (SCALE.value) {
+                    uint32_t scaled[16];
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) add2(tot[c + k], tot[c + k + 1], tot[c + k], tot[c + k + 1], o[k], o[k + 1]);
+                    for (int k = 0; k < 16; ++k) scaled[k] = __float_as_uint(o[k] * a);
+                    pf_st8(co + c, scaled);
+                    pf_st8(co + c + 8, scaled + 8);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) add2(tot[c + k], tot[c + k + 1], tot[c + k], tot[c + k + 1], o[k], o[k + 1]);
+                }
             }
         };
         // A wait that gave up does not leave the loop: the other warps of the rows wait at their barrier.
@@ -557,15 +566,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) k_attn_promptf(const __grid_con
                 if (lane == 0) mbar_arrive(vempty + buf);
             }
             if (i > 0 && (raised || fresh)) {
-                fold(i - 1);
+                if (fresh) fold(std::false_type{}, i - 1, 1.0f);
+                else fold(std::true_type{}, i - 1, a);
                 if (raised) {
 #pragma unroll
                     for (int k = 0; k < HD; ++k) tot[k] *= a;
-                    if (!fresh) {
-                        const uint32_t zero[8] = {};
-#pragma unroll
-                        for (int c = 0; c < HD; c += 8) pf_st8(co + c, zero);
-                    }
                 }
             }
             tmem_wait_st();
@@ -573,7 +578,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) k_attn_promptf(const __grid_con
             mbar_arrive(pfull + sb);
         }
         // ---- output rows
-        if (steps > 0) fold(steps - 1);
+        if (steps > 0) fold(std::false_type{}, steps - 1, 1.0f);
         s_top[part * 128 + rr] = l;
         pf_rows_sync(warp & 3);
         l = (s_top[rr] + s_top[128 + rr]) + (s_top[256 + rr] + s_top[384 + rr]);

@@ -73,3 +73,38 @@ def test_rows_between_two_bad_values(ctx, D, v_type, page, dtype, window, bits):
             assert torch.equal(got[sees][..., :32], want[sees][..., :32])
             r0 += new
         assert between > 0 or window == 0 or news is not PROMPTS
+
+
+WIDE = [("k", "Q8_0", 512.0), ("k", "Q8_0", 516.0), ("k", "Q8_0", 60000.0), ("k", "Q4_0", 8192.0), ("k", "Q4_0", 60000.0),
+        ("v", "Q8_0", 511.5), ("v", "Q8_0", 512.0), ("v", "Q8_0", 600.0), ("v", "Q4_0", 8192.0)]
+
+
+@pytest.mark.parametrize("dtype,what,type_,scale", [("f32", *w) for w in WIDE if w[0] == "k"])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 48), (256, 16)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_keys_and_values_beyond_fp16(ctx, dtype, what, type_, scale, D, page, window):  # noqa: F811
+    """One block of each sequence with a large finite scale, whose products leave fp16's range (an fp16 value
+    of 65504 is stored with the scale 516): rows of prompts that do not see it keep their results bit by bit,
+    those that see it, and single rows, are as close to 64 bits as any."""
+    types = {"k": dict(k_type=type_), "v": dict(v_type=type_)}[what]
+    # scores of a few units beside a key of that size, nearly equal weights beside such a value
+    q_mul = 0.08 / scale * (1.0 if type_ == "Q8_0" else 16.0) if what == "k" else 0.3
+    for news in (PROMPTS, [min(3, x) for x in PROMPTS]):
+        c = Case(ctx, PROMPTS, news, 16, 8, D, dtype=dtype, page=page, seed=13, q_mul=q_mul, **types)
+        clean = c.call(window=window)
+        bits = int(torch.tensor(scale, dtype=torch.float16).view(torch.int16))
+        k0 = 0
+        for length in PROMPTS:
+            set_scale(c, c.cache.k if what == "k" else c.cache.v, type_, page, int(c.slots[k0 + length // 3]), 1, bits)
+            k0 += length
+        c.k, c.v = (x.double() for x in ctx.kv_load(c.cache, c.slots))
+        out = c.call(window=window)
+        ctx.sync_status()
+        check(c, out, window=window)
+        if news is PROMPTS:
+            r0 = 0
+            for length, new in zip(PROMPTS, news):
+                pos = torch.arange(new, device="cuda")
+                sees = (pos >= length // 3) & (pos < length // 3 + window if window else True)
+                assert torch.equal(out[r0:r0 + new][~sees], clean[r0:r0 + new][~sees])
+                r0 += new
