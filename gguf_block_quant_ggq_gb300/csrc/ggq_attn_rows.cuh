@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_attn_rows(const __grid_cons
     uint4* const s_q = reinterpret_cast<uint4*>(smem + SM::oQ + warp * SM::kQ);
     rows.template begin<1>(p, sq, hk, r0, r_end, s_q, 0, lane);
     __syncwarp();
-    const int my_lo = group_of(r0), my_hi = end_of(r_end - 1), loaded = min(sq.len, 16 * ghi);  // keys that the ring holds
+    const int my_lo = group_of(r0), my_hi = end_of(r_end - 1);
     for (int u = 0; u < units; ++u) {
         const int at = u % S, g = glo + UNIT * u;
         if (!__all_sync(0xffffffffu, mbar_test(s_full + at, (u / S) & 1))) {
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_attn_rows(const __grid_cons
             }
         }
         const uint8_t* const kb = smem + at * SM::kStage;
-        if (g < my_hi && g + UNIT > my_lo) rows.unit(p, s_q, kb, kb + UNIT * SM::kKB, g, loaded, lane);
+        if (g < my_hi && g + UNIT > my_lo) rows.unit(p, s_q, kb, kb + UNIT * SM::kKB, g, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty + at);
         // the place of the unit before this one: every warp has left it, or soon will

@@ -404,7 +404,7 @@ struct AttnRows {
 
     // A unit: groups g .. g + UNIT - 1, their key blobs at kb and value blobs at vb.
     __device__ __forceinline__ void unit(const AttnParams& p, const uint4* s_q, const uint8_t* kb, const uint8_t* vb, int g,
-                                         int len, int lane) {
+                                         int lane) {
         const int t4 = lane & 3;
         // ---- scores, index 4 group + 2 octet + e: keys 2 t + e of the octet
         constexpr int KW = K4 ? NB : KS;  // words of an octet
@@ -516,10 +516,13 @@ struct AttnRows {
 #pragma unroll
             for (int i = 0; i < 4 * UNIT; ++i) {
                 const int key = 16 * g + 8 * (i >> 1) + 2 * t4 + (i & 1);
+                bool seen = false;
 #pragma unroll
-                for (int rs = 0; rs < RS; ++rs)
+                for (int rs = 0; rs < RS; ++rs) {
                     if (key > pos[rs] || key < first_key[rs]) lg[rs][i] = -INFINITY;
-                if (key >= len)  // never written: whatever the place holds
+                    else seen = true;
+                }
+                if (!seen)  // whatever the place holds (it may never have been written) takes no part in the lift
 #pragma unroll
                     for (int k = 0; k < NB / 2; ++k) vd[i >> 2][i & 3][k] = 0u;
             }
@@ -564,7 +567,7 @@ struct AttnRows {
                                 if (lg[rs][4 * c + i] != -INFINITY) spoilt[rs] |= 1u << b;
                         }
                     }
-            dfin = warp_max(dfin);
+            dfin = quad_max(dfin);  // of the rows' own keys
             if (dfin > dlimit) {  // the largest times the lift to [2^13, 2^14)
                 const int e = 13 - (static_cast<int>(__float_as_uint(dfin) >> 23) - 127);
                 lift = fminf(static_cast<float>(e), kMaxLift);
@@ -986,7 +989,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             const uint8_t* const kb = smem + SM::oRing + at * SM::kStage;
             const uint8_t* const vb = kb + UNIT * SM::kKB;
 
-            rows.unit(p, s_q, kb, vb, g, sq.len, lane);
+            rows.unit(p, s_q, kb, vb, g, lane);
             __syncwarp();
             fetch(at);
             if (++slot == S) slot = 0, phase ^= 1u;

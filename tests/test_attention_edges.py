@@ -79,7 +79,7 @@ WIDE = [("k", "Q8_0", 512.0), ("k", "Q8_0", 516.0), ("k", "Q8_0", 60000.0), ("k"
         ("v", "Q8_0", 511.5), ("v", "Q8_0", 512.0), ("v", "Q8_0", 600.0), ("v", "Q4_0", 8192.0)]
 
 
-@pytest.mark.parametrize("dtype,what,type_,scale", [("f32", *w) for w in WIDE if w[0] == "k"])
+@pytest.mark.parametrize("dtype,what,type_,scale", [("f32", *w) for w in WIDE])
 @pytest.mark.parametrize("D,page", [(64, 16), (128, 48), (256, 16)])
 @pytest.mark.parametrize("window", [0, 40])
 def test_keys_and_values_beyond_fp16(ctx, dtype, what, type_, scale, D, page, window):  # noqa: F811
