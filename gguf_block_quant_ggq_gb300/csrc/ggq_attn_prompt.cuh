@@ -24,14 +24,19 @@
 //     computed while the softmax works on this one's.
 // The running maximum is raised (and O rescaled in tensor memory) only when a row
 // passes it by 2^8.  fp16 queries are exact; bf16 ones too (rows are scaled by a
-// power of two).  K is rounded to fp16 (2^-12 of each value); V and P to the
-// activations' type: with bf16 2^-9 of each, as much as the output's own rounding, but
-// no probability is lost for being small and no value for being large; with fp16 2^-12,
-// P being kept at 2^7 times its value.  Each row's sum is fp32.
+// power of two).  K is rounded to fp16 (2^-11 of each value at most); V and P to the
+// activations' type: with bf16 2^-8 of each at most, as much as the output's own rounding,
+// but no probability is lost for being small (fp16 would lose those below 2^-31 of the
+// largest, which are all of an output whose channel the large ones leave at 0) and no value
+// for being large; with fp16 2^-11, P being kept at 2^7 times its value.  Each row's sum is fp32.  Keys, and values of fp16
+// rows, that leave fp16's range count as 0 here, and the rows that see them are computed
+// again in fp32 (ggq_attn_exact.cuh).
 #pragma once
 #include <atomic>
+#include <type_traits>
 
 #include "ggq_attn.cuh"
+#include "ggq_attn_exact.cuh"
 #include "ggq_device.cuh"
 #include "ggq_internal.h"
 #include "ggq_tcgen05.cuh"
@@ -261,6 +266,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
     uint32_t* const tslot = reinterpret_cast<uint32_t*>(bars + 24);
     volatile int* const abort = reinterpret_cast<volatile int*>(tslot + 1);
     int* const s_bad = reinterpret_cast<int*>(tslot + 2);  // [NB][2] first and last key whose value scale is not finite
+    int* const s_wide = s_bad + 2 * NB;                    // first and last key that fp16 tiles cannot hold
 
     pdl_launch_dependents();
     pdl_wait();
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             mbar_init(done + i, 1);
         }
         *abort = 0;
-        for (int i = 0; i < NB; ++i) s_bad[2 * i] = 0x7fffffff, s_bad[2 * i + 1] = -1;
+        for (int i = 0; i <= NB; ++i) s_bad[2 * i] = 0x7fffffff, s_bad[2 * i + 1] = -1;  // and s_wide
         fence_barrier_init();
     }
     if (warp == kFirstMma) {
@@ -501,6 +507,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             // ---- keys: lane (g, t) writes 16 channels of a 64-channel atom as two chunks of its token's row
             if (j >= 2 && !wait(kempty + buf, ((j >> 1) - 1) & 1)) break;
             uint8_t* const kt = smem + SH::oK + buf * SH::kK + (k_group * 16 + 8 * k_part + g8) * 128;
+            uint32_t most = 0u;
+#pragma unroll
+            for (int o = 0; o < KO; ++o)
+#pragma unroll
+                for (int q = 0; q < NB / 2; ++q) most = __vmaxu2(most, ks[o][q] & 0x7FFF7FFFu);
+            if ((most & 0xFFFFu) > attn_half_limit<K4>() || (most >> 16) > attn_half_limit<K4>()) {
+                // scales whose products leave fp16: 0 here, and the rows that see them are told
+#pragma unroll
+                for (int o = 0; o < KO; ++o)
+#pragma unroll
+                    for (int q = 0; q < NB / 2; ++q) {
+                        const int key = 16 * (glo + j * KG + k_group) + 8 * (k_part + o) + g8;
+                        const bool lo = attn_wide<K4>(ks[o][q]), hi = attn_wide<K4>(ks[o][q] >> 16);
+                        if ((lo || hi) && key < len) atomicMin(s_wide, key), atomicMax(s_wide + 1, key);
+                        ks[o][q] = (lo ? 0u : ks[o][q] & 0xFFFFu) | (hi ? 0u : ks[o][q] & 0xFFFF0000u);
+                    }
+            }
 #pragma unroll
             for (int i = 0; i < KL; ++i) {
                 const uint32_t w[4] = {kq[i].x, kq[i].y, kq[i].z, kq[i].w};
@@ -534,10 +557,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     if (key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1) >= len) vsc[c][r] = 0u;
-                    odd = __vmaxu2(odd, vsc[c][r] & 0x7C007C00u);
+                    odd = __vmaxu2(odd, vsc[c][r] & 0x7FFF7FFFu);
                 }
-            if ((odd & 0xFFFFu) == 0x7C00u || (odd >> 16) == 0x7C00u) {
-                // scales that are not finite: 0 here, and the rows that see them are told
+            constexpr uint32_t kLimit = BF ? 0x7BFFu : attn_half_limit<V4>();
+            if ((odd & 0xFFFFu) > kLimit || (odd >> 16) > kLimit) {
+                // scales that are not finite, or (fp16 rows) whose products are not: 0 here, and the rows that
+                // see them are told
                 int* const bad = s_bad + 4 * (b0 >> 1);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
@@ -545,9 +570,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                     for (int r = 0; r < 4; ++r) {
                         const uint32_t u = vsc[c][r];
                         const int key = key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1);
-                        const bool lo = (u & 0x7C00u) == 0x7C00u, hi = (u & 0x7C000000u) == 0x7C000000u;
+                        bool lo = (u & 0x7C00u) == 0x7C00u, hi = (u & 0x7C000000u) == 0x7C000000u;
                         if (lo) atomicMin(bad, key), atomicMax(bad + 1, key);
                         if (hi) atomicMin(bad + 2, key), atomicMax(bad + 3, key);
+                        if constexpr (!BF) {
+                            const bool wide_lo = attn_wide<V4>(u), wide_hi = attn_wide<V4>(u >> 16);
+                            if (wide_lo || wide_hi) atomicMin(s_wide, key), atomicMax(s_wide + 1, key);
+                            lo |= wide_lo, hi |= wide_hi;
+                        }
                         vsc[c][r] = (lo ? 0u : u & 0xFFFFu) | (hi ? 0u : u & 0xFFFF0000u);
                     }
             }
@@ -720,6 +750,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                     dst[1] = make_uint2(w[2], w[3]);
                 }
             }
+        }
+        // ---- rows that may see keys or values which the tiles left out
+        __syncwarp();  // their outputs, written above by their own lanes, are written again by the warp
+        uint32_t again = __ballot_sync(0xffffffffu, there && s_wide[0] <= pos && s_wide[1] >= first_key && s_wide[1] >= 0);
+        for (; again; again &= again - 1u) {
+            const int from_lane = __ffs(again) - 1;
+            attn_exact_row<K4, V4, D, std::conditional_t<BF, __nv_bfloat16, __half>, !BF>(
+                p, b, hk, __shfl_sync(0xffffffffu, h, from_lane), first + __shfl_sync(0xffffffffu, i_row, from_lane),
+                __shfl_sync(0xffffffffu, first_key, from_lane), __shfl_sync(0xffffffffu, pos, from_lane));
         }
         }
     }
