@@ -1117,13 +1117,19 @@ ggq_status ggq_sync_status(ggq_ctx* c, void* stream) {
     DeviceScope scope;
     ggq_status s = check_ctx(c, scope);
     if (s != GGQ_OK) return s;
-    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(c, e, "sync_status: stream");
+    // read and cleared in the stream's order: the caller's next call on it finds the block as it is left here
     int word = 0;
-    e = cudaMemcpy(&word, &c->ctrl->err, sizeof(int), cudaMemcpyDeviceToHost);
+    e = cudaMemcpyAsync(&word, &c->ctrl->err, sizeof(int), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(c, e, "sync_status: read");
     if (word != 0) {
-        cudaMemset(c->ctrl, 0, sizeof(Ctrl));  // the word, and what a kernel that gave up may have left
+        // a kernel that gave up may have left arrivals; after any other error the counters are zero
+        e = cudaMemsetAsync(c->ctrl, 0, word == DEV_ERR_TIMEOUT ? sizeof(Ctrl) : sizeof(c->ctrl->err), st);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+        if (e != cudaSuccess) return cuda_fail(c, e, "sync_status: clear");
         return fail(c, GGQ_ERR_DEVICE, "device error word %d (%s)", word,
                     word == DEV_ERR_TIMEOUT   ? "a bounded wait ran out"
                     : word == DEV_ERR_BAD_IDS ? "a routed expert id out of range"

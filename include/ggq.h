@@ -464,8 +464,9 @@ ggq_status ggq_moe_route(ggq_ctx* ctx, const ggq_router* router, int dtype, cons
                          int32_t* ids, float* weights, void* stream);
 
 /* Synchronise `stream` and read the device error word: GGQ_OK, or
- * GGQ_ERR_DEVICE (a bounded wait inside a kernel ran out; the word is cleared),
- * or GGQ_ERR_CUDA. */
+ * GGQ_ERR_DEVICE (a bounded wait inside a kernel ran out, or an expert id, slot,
+ * page, length or row range was out of bounds; the word is cleared in the stream's
+ * order), or GGQ_ERR_CUDA.  No other stream is waited for. */
 ggq_status ggq_sync_status(ggq_ctx* ctx, void* stream);
 
 #ifdef __cplusplus

@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+import gguf_block_quant_ggq_gb300 as ggq  # noqa: E402
 from test_attention import Case, ctx  # noqa: E402,F401
 from test_attention_tiles import check  # noqa: E402
 
@@ -127,3 +128,31 @@ def test_fp16_rows_at_the_end_of_their_range(ctx):  # noqa: F811
     before[last] = False
     assert torch.equal(out[before], clean[before])
     assert torch.isfinite(out).all()
+
+
+def test_status_is_read_and_cleared_in_the_streams_order(ctx):  # noqa: F811
+    """sync_status of a side stream neither waits for another stream's work nor leaves the clearing of the
+    error word to it: calls that follow on the side stream are whole."""
+    c = Case(ctx, [30000, 7, 900], [1, 1, 1], 8, 1, 128, page=64, seed=4)
+    want = c.call()
+    s, busy = torch.cuda.Stream(), torch.cuda.Event()
+    outside = torch.full_like(c.slots[:1], c.cache.n_pages * c.cache.page_size)
+    k, v = c.k[:1].float(), c.v[:1].float()
+    outs = torch.zeros((20, *want.shape), device="cuda")
+    torch.cuda.synchronize()
+    for busily in (False, True):  # first a round in which nothing else runs: kernels are loaded
+        outs.zero_()
+        torch.cuda.synchronize()
+        if busily:
+            torch.cuda._sleep(2 * 10 ** 9)  # about a second of the default stream's time
+            busy.record()
+        with torch.cuda.stream(s):
+            ctx.kv_store(c.cache, k, v, outside)
+            with pytest.raises(ggq.GGQError, match="outside the key/value cache"):
+                ctx.sync_status()
+            for out in outs:
+                c.call(out=out)
+            ctx.sync_status()
+            assert not busily or not busy.query()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for out in outs)
