@@ -163,7 +163,9 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     p.v_q4 = kv->v_type == GGQ_TYPE_Q4_0;
     p.max_q = static_cast<int>(!a->q_start ? 1 : a->max_q < a->n_tokens ? a->max_q : a->n_tokens);
     p.max_len = static_cast<int>(room);
-    p.window = static_cast<int>(a->window <= 0 ? 0 : a->window < INT32_MAX ? a->window : INT32_MAX);
+    // a window of all that a sequence can hold is none: positions minus windows stay in range, the rows
+    // before the first key (position -1 and below) included
+    p.window = static_cast<int>(a->window <= 0 || a->window >= room ? 0 : a->window);
     p.scale = a->scale;
     p.cap = a->cap > 0.0f ? a->cap : 0.0f;
     p.err = &c->ctrl->err;

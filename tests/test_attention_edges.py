@@ -156,3 +156,16 @@ def test_status_is_read_and_cleared_in_the_streams_order(ctx):  # noqa: F811
             assert not busily or not busy.query()
         torch.cuda.synchronize()
         assert all(torch.equal(out, want) for out in outs)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 3, 2 ** 31 - 1, 2 ** 31, 2 ** 40])
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 256), ("bf16", 128), ("f16", 256)])
+def test_windows_of_any_size(ctx, dtype, D, window):  # noqa: F811
+    """More new rows than cached tokens, and a window that stands for none: rows before the first key are zeros,
+    the others see what they see without a window."""
+    for lens, news in (([3, 17, 1], [6, 17, 5]), ([3, 17, 300, 5] * 6, [90, 170, 300, 6] * 6)):
+        c = Case(ctx, lens, news, 16, 8, D, dtype=dtype, seed=D)
+        out = c.call(window=window)
+        ctx.sync_status()
+        assert torch.equal(out, c.call())
+        check(c, out)
