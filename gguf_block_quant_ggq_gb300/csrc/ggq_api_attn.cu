@@ -117,7 +117,7 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     if (dt < 0) return fail(c, GGQ_ERR_UNSUPPORTED, "attention: element type %d; supported: F32, F16, BF16", a->dtype);
     if (a->n_heads < 1 || a->n_heads % kv->n_kv_heads || a->n_heads > 16384)
         return fail(c, GGQ_ERR_SHAPE, "attention: %d query heads on %d kv heads", a->n_heads, kv->n_kv_heads);
-    if (a->n_tokens < 0 || a->n_tokens > (1 << 24) || a->n_seqs < 0 || a->n_seqs > (1 << 20) ||
+    if (a->n_tokens < 0 || a->n_tokens > kAttnMaxRows || a->n_seqs < 0 || a->n_seqs > (1 << 20) ||
         (!a->q_start && a->n_tokens != a->n_seqs) || a->table_stride < 0 || a->max_len < 0 || a->max_q < 0)
         return fail(c, GGQ_ERR_SHAPE, "attention: %lld rows of %lld sequences, max_q=%lld, max_len=%lld",
                     static_cast<long long>(a->n_tokens), static_cast<long long>(a->n_seqs),
@@ -134,7 +134,7 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
         return fail(c, GGQ_ERR_INVALID_ARG, "attention: lens, q_start, table and slopes must be 4-byte aligned");
     int64_t room = a->table_stride * kv->page_size;  // what a table row can name
     if (a->max_len > 0 && a->max_len < room) room = a->max_len;
-    if (room > INT32_MAX) room = INT32_MAX;
+    if (room > kAttnMaxLen) room = kAttnMaxLen;
     AttnParams p{};
     p.q = a->q;
     p.out = a->out;

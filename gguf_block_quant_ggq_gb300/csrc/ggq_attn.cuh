@@ -33,6 +33,11 @@ struct AttnParams {
     int* err;
 };
 
+// Bounds of a call: a sequence's tokens and the call's rows.  Positions are 32-bit: a key
+// behind a sequence's last tile, and a position (at least -rows) minus a window (less than the
+// longest sequence), stay in range.
+constexpr int64_t kAttnMaxRows = 1 << 24, kAttnMaxLen = (1ll << 31) - (1 << 25);
+
 // A partial result: reference maxima [16], sums [16], values [16][D].
 __host__ __device__ constexpr int attn_part_floats(int D) { return 32 + 16 * D; }
 

@@ -180,7 +180,7 @@ typedef struct ggq_attn {
     const int32_t* lens;    /* [n_seqs] cached tokens, the new ones included            */
     const int32_t* q_start; /* [n_seqs + 1] first row of each sequence; NULL: row b is sequence b's one new token */
     int64_t max_q;          /* upper bound of a sequence's rows (ignored without q_start) */
-    int64_t max_len;        /* upper bound of lens (0: table_stride * page_size)        */
+    int64_t max_len;        /* upper bound of lens (0: table_stride * page_size; at most 2^31 - 2^25 counts) */
     float scale;            /* of q . k                                                 */
     float cap;              /* > 0: cap * tanh(score / cap)                             */
     int64_t window;         /* > 0: a token sees the last `window` tokens, itself included */

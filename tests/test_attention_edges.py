@@ -169,3 +169,29 @@ def test_windows_of_any_size(ctx, dtype, D, window):  # noqa: F811
         ctx.sync_status()
         assert torch.equal(out, c.call())
         check(c, out)
+
+
+@pytest.mark.parametrize("rows", [1, 300])
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 256), ("bf16", 128)])
+def test_lengths_up_to_the_bound(ctx, dtype, D, rows):  # noqa: F811
+    """The longest sequence there is, on one page that its table names again and again, behind a window: the rows
+    see what those of a short sequence see whose last tokens stand in the same places.  A longer one is cut to
+    it and reported."""
+    page, longest = 4096, 2 ** 31 - 2 ** 25
+    c = Case(ctx, [page], [rows], 32, 8, D, dtype=dtype, page=page, seed=rows, spare_pages=0)
+    start = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+
+    def call(length, **kw):
+        table = torch.zeros((1, (length + page - 1) // page), dtype=torch.int32, device="cuda")
+        lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+        return ctx.attention(c.cache, c.q, lens, table, q_start=start, window=100, **kw)
+
+    want = call(page)
+    out = call(longest)
+    ctx.sync_status()
+    check(c, want, window=100)
+    check(c, out, window=100)
+    cut = call(2 ** 31 - 1)
+    with pytest.raises(ggq.GGQError, match="outside the key/value cache"):
+        ctx.sync_status()
+    assert torch.equal(cut, out)
