@@ -178,6 +178,8 @@ class KVCache:
             if pool is None:
                 pool = torch.zeros(n_pages * size, dtype=torch.uint8, device=f"cuda:{ctx.device}")
             _ptr(pool, "uint8")
+            if pool.get_device() != ctx.device:
+                raise ValueError(f"expected a pool on cuda:{ctx.device}, got one on {pool.device}")
             if pool.numel() != n_pages * size:
                 raise ValueError(f"{n_pages} pages of {size} bytes need a pool of {n_pages * size}, got {pool.numel()}")
             pools.append(pool)
@@ -253,6 +255,10 @@ class Context:
         if one != 1:
             raise ValueError("the channels of a head have to be dense")
         return t.data_ptr(), code, token, head
+
+    def _own(self, cache):
+        if cache.device != self.device:
+            raise ValueError(f"the cache lies on cuda:{cache.device}, this context works on cuda:{self.device}")
 
     def _check(self, st):
         if st != 0:
@@ -339,6 +345,7 @@ class Context:
 
     def kv_store(self, cache: KVCache, k, v, slots, stream=None):
         """Quantize k and v [tokens][kv heads][D] into the cache's slots (int64 [tokens], negative: skipped)."""
+        self._own(cache)
         kp, code, kt, kh = self._rows(k, cache.n_kv_heads, cache.head_dim)
         vp, vcode, vt, vh = self._rows(v, cache.n_kv_heads, cache.head_dim)
         n = slots.numel()
@@ -351,6 +358,7 @@ class Context:
 
     def kv_load(self, cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
         """Values of the cache's slots, [tokens][kv heads][D] each of K and V (float32 unless dtype says otherwise)."""
+        self._own(cache)
         n, heads, dim = slots.numel(), cache.n_kv_heads, cache.head_dim
         if k is None:
             k = self._torch.empty((n, heads, dim), dtype=dtype or self._f32, device=self._dev)
@@ -371,6 +379,7 @@ class Context:
         """Attention of q [tokens][heads][D] over the cache: lens int32 [sequences] (new tokens included), table
         int32 [sequences][pages], q_start int32 [sequences + 1] unless every sequence has one token; max_q and
         max_len bound a sequence's rows and length (default: all rows, the table's capacity)."""
+        self._own(cache)
         if q.dim() != 3:
             raise ValueError(f"expected a [tokens, heads, {cache.head_dim}] tensor, got {tuple(q.shape)}")
         n, heads, dim = q.shape
