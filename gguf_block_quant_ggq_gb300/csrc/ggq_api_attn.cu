@@ -42,10 +42,10 @@ uint32_t page_magic(int page_size) { return static_cast<uint32_t>((1ull << 32) /
 // Partial results of items that two or more CTAs share, for the widest heads.
 size_t attn_scratch() { return align_up(2ull * kAttnMaxCtas * attn_part_floats(256) * sizeof(float)); }
 
-// Rows of four elements at a time: pointer and strides are multiples of 4.
-bool rows4(const void* p, int64_t token, int64_t head, int dtype) {
-    return (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(4 * dtype_bytes(dtype))) == 0 && token % 4 == 0 &&
-           head % 4 == 0;
+// Rows of four elements at a time: the pointer and the strides of axes of more than one element are multiples of 4.
+bool rows4(const void* p, int64_t tokens, int64_t token, int heads, int64_t head, int dtype) {
+    return (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(4 * dtype_bytes(dtype))) == 0 &&
+           (tokens < 2 || token % 4 == 0) && (heads < 2 || head % 4 == 0);
 }
 
 ggq_status kv_params(ggq_ctx* c, const ggq_kv_cache* kv, int dtype, const void* k, int64_t k_token, int64_t k_head,
@@ -60,7 +60,7 @@ ggq_status kv_params(ggq_ctx* c, const ggq_kv_cache* kv, int dtype, const void* 
     if (!k || !v || !slots) return fail(c, GGQ_ERR_INVALID_ARG, "%s: null pointer", op);
     if (reinterpret_cast<uintptr_t>(slots) & 7)
         return fail(c, GGQ_ERR_INVALID_ARG, "%s: slots must be 8-byte aligned", op);
-    if (!rows4(k, k_token, k_head, *dt) || !rows4(v, v_token, v_head, *dt))
+    if (!rows4(k, T, k_token, kv->n_kv_heads, k_head, *dt) || !rows4(v, T, v_token, kv->n_kv_heads, v_head, *dt))
         return fail(c, GGQ_ERR_INVALID_ARG, "%s: rows must start at multiples of 4 elements (pointers and strides)", op);
     *p = KvParams{{static_cast<uint8_t*>(kv->k), kv->k_type == GGQ_TYPE_Q4_0},
                   {static_cast<uint8_t*>(kv->v), kv->v_type == GGQ_TYPE_Q4_0},
@@ -127,7 +127,8 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     if (a->n_tokens == 0 || a->n_seqs == 0) return GGQ_OK;
     if (!a->q || !a->out || !a->lens || (!a->table && a->table_stride > 0))
         return fail(c, GGQ_ERR_INVALID_ARG, "attention: null pointer");
-    if (!rows4(a->q, a->q_token, a->q_head, dt) || !rows4(a->out, a->out_token, a->out_head, dt))
+    if (!rows4(a->q, a->n_tokens, a->q_token, a->n_heads, a->q_head, dt) ||
+        !rows4(a->out, a->n_tokens, a->out_token, a->n_heads, a->out_head, dt))
         return fail(c, GGQ_ERR_INVALID_ARG, "attention: rows must start at multiples of 4 elements (pointers and strides)");
     if ((reinterpret_cast<uintptr_t>(a->lens) | reinterpret_cast<uintptr_t>(a->q_start) |
          reinterpret_cast<uintptr_t>(a->table) | reinterpret_cast<uintptr_t>(a->slopes)) & 3)

@@ -413,8 +413,8 @@ ggq_status ggq_set_moe_counters(ggq_ctx* ctx, int64_t* pairs, int64_t n_experts,
 size_t ggq_kv_page_bytes(int type, int n_kv_heads, int head_dim, int page_size);
 
 /* Quantize T tokens' keys and values into the cache: k and v [T][n_kv_heads][D]
- * of dtype, token and head strides in elements (multiples of 4, pointers aligned
- * to 4 elements), go to the slots [T] (int64: page * page_size + place; a
+ * of dtype, token and head strides in elements (multiples of 4 where the axis has
+ * more than one element, pointers aligned to 4 elements), go to the slots [T] (int64: page * page_size + place; a
  * negative slot is skipped; two tokens with one slot leave it undefined).
  *   Q8_0: d = amax * (1/127) (an fp32 product with the rounded reciprocal), q =
  *     round-half-away(x * (1/d)) clamped to +-127;

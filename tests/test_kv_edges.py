@@ -26,3 +26,23 @@ def test_pools_and_caches_of_another_device_are_refused(ctx):  # noqa: F811
         ctx.kv_load(mine, slots)
     with pytest.raises(ValueError, match="cuda:1"):
         ctx.attention(mine, rows, lens, table)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_strides_of_axes_of_one_element(ctx, dtype):  # noqa: F811
+    """One token, or one head, whose stride no address depends on: any is taken."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    for tokens, heads in ((1, 4), (6, 1), (1, 1)):
+        cache, want = (ctx.kv_cache("Q8_0", "Q8_0", 2, 16, heads, 64) for _ in range(2))
+        x = torch.randn((3, tokens, heads, 64), device="cuda", generator=g).to(dtype)
+        slots = torch.arange(tokens, device="cuda")
+        # odd strides of the axes of one element
+        odd = [t.as_strided(t.shape, (t.stride(0) if tokens > 1 else 4097, t.stride(1) if heads > 1 else 33, 1)) for t in x]
+        ctx.kv_store(cache, odd[0], odd[1], slots)
+        ctx.kv_store(want, x[0], x[1], slots)
+        assert torch.equal(cache.k, want.k) and torch.equal(cache.v, want.v)
+        lens = torch.full((tokens,), tokens, dtype=torch.int32, device="cuda")
+        table = torch.zeros((tokens, 1), dtype=torch.int32, device="cuda")
+        assert torch.equal(ctx.attention(cache, odd[2], lens, table), ctx.attention(cache, x[2], lens, table))
+    ctx.sync_status()
