@@ -357,13 +357,16 @@ class Context:
             self._check(st)
 
     def kv_load(self, cache: KVCache, slots, dtype=None, k=None, v=None, stream=None):
-        """Values of the cache's slots, [tokens][kv heads][D] each of K and V (float32 unless dtype says otherwise)."""
+        """Values of the cache's slots, [tokens][kv heads][D] each of K and V (float32 unless dtype or a given
+        buffer says otherwise)."""
         self._own(cache)
         n, heads, dim = slots.numel(), cache.n_kv_heads, cache.head_dim
+        if dtype is None:
+            dtype = k.dtype if k is not None else v.dtype if v is not None else self._f32
         if k is None:
-            k = self._torch.empty((n, heads, dim), dtype=dtype or self._f32, device=self._dev)
+            k = self._torch.empty((n, heads, dim), dtype=dtype, device=self._dev)
         if v is None:
-            v = self._torch.empty((n, heads, dim), dtype=dtype or self._f32, device=self._dev)
+            v = self._torch.empty((n, heads, dim), dtype=dtype, device=self._dev)
         kp, code, kt, kh = self._rows(k, heads, dim)
         vp, vcode, vt, vh = self._rows(v, heads, dim)
         if code != vcode or k.shape[0] != n or v.shape[0] != n:

@@ -46,3 +46,14 @@ def test_strides_of_axes_of_one_element(ctx, dtype):  # noqa: F811
         table = torch.zeros((tokens, 1), dtype=torch.int32, device="cuda")
         assert torch.equal(ctx.attention(cache, odd[2], lens, table), ctx.attention(cache, x[2], lens, table))
     ctx.sync_status()
+
+
+def test_one_given_buffer_sets_the_type_of_both(ctx):  # noqa: F811
+    c = Case(ctx, [21], [1], 2, 2, 64)
+    want = ctx.kv_load(c.cache, c.slots, dtype=torch.bfloat16)
+    for name in ("k", "v"):
+        given = torch.empty_like(want[0])
+        got = ctx.kv_load(c.cache, c.slots, **{name: given})
+        assert got["kv".index(name)] is given
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ctx.sync_status()
