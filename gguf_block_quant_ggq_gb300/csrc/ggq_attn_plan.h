@@ -47,4 +47,20 @@ struct AttnPieces {
     __host__ __device__ __forceinline__ int group_counter() const { return kAttnMaxCtas + c0; }
 };
 
+// The copies of a warp's ring, place by place: the parity of the barrier phase that a
+// place's last copy completes (kNoCopy: none yet).  A warp that leaves its units early
+// waits for these before its CTA's shared memory goes to another one.
+constexpr int kNoCopy = -1;
+struct AttnRing {
+    int* turns;
+    __host__ __device__ __forceinline__ void clear(int at) const { turns[at] = kNoCopy; }
+    __host__ __device__ __forceinline__ void issue(int at, uint32_t parity) const { turns[at] = static_cast<int>(parity); }
+    // wait(place, parity) for every place that holds or awaits a copy
+    template <typename WAIT>
+    __host__ __device__ __forceinline__ void drain(int from, int places, WAIT wait) const {
+        for (int at = from; at < from + places; ++at)
+            if (turns[at] != kNoCopy) wait(at, static_cast<uint32_t>(turns[at]));
+    }
+};
+
 }  // namespace ggq

@@ -90,7 +90,8 @@ struct AttnSmem {
     static constexpr int oStat = oQ + D / 16 * 32 * 16;   // m, l [warps][8]
     static constexpr int oScan = (oStat + 2 * kAttnWarps * 8 * 4 + 7) / 8 * 8;
     static constexpr int oBar = (oScan + (128 + 4) * 8 + 15) / 16 * 16;
-    static constexpr int kTotal = oBar + kAttnWarps * kStages * 8 + 16;
+    static constexpr int oTurns = oBar + kAttnWarps * kStages * 8 + 16;
+    static constexpr int kTotal = oTurns + kAttnWarps * kStages * 4;
     // CTAs an SM: 12 warps leave 168 registers a thread (64-channel heads), 8 warps 255
     static constexpr int kCtas = D == 64 && 3 * (kTotal + 1024) <= 228 * 1024 ? 3 : 2 * (kTotal + 1024) <= 228 * 1024 ? 2 : 1;
 };
@@ -847,11 +848,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     uint64_t* const s_full = reinterpret_cast<uint64_t*>(smem + SM::oBar);
     volatile int* const s_abort = reinterpret_cast<volatile int*>(s_full + kAttnWarps * S);
     volatile int* const s_last = s_abort + 1;
+    const AttnRing ring{reinterpret_cast<int*>(smem + SM::oTurns)};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_launch_dependents();
     if (tid == 0) {
-        for (int i = 0; i < kAttnWarps * S; ++i) mbar_init(s_full + i, 1);
+        for (int i = 0; i < kAttnWarps * S; ++i) mbar_init(s_full + i, 1), ring.clear(i);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -926,11 +928,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         }
         fpage = ftable[q];
     };
-    const auto fetch = [&](int at) {
+    const auto fetch = [&](int at, uint32_t parity) {
         if (fu >= fend) return;
         const int n = min(UNIT, fghi - fglo - UNIT * fu);  // groups of the unit
         const bool joined = __shfl_sync(0xffffffffu, fplace, 0) + n <= gpp;  // of one page: one copy
-        if (lane == 0) mbar_arrive_expect_tx(s_full + at, n * (SM::kStage / UNIT));
+        if (lane == 0) mbar_arrive_expect_tx(s_full + at, n * (SM::kStage / UNIT)), ring.issue(at, parity);
         __syncwarp();
         if (lane < (joined ? 1 : n)) {
             const int copies = joined ? n : 1;
@@ -946,7 +948,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     };
     enter();
     seek();
-    for (int i = 0; i < S; ++i) fetch(warp * S + i);
+    for (int i = 0; i < S; ++i) fetch(warp * S + i, 0u);
 
     // ---- segments
     const int g8 = lane >> 2, t4 = lane & 3;
@@ -991,7 +993,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
 
             rows.unit(p, s_q, kb, vb, g, lane);
             __syncwarp();
-            fetch(at);
+            fetch(at, phase ^ 1u);
             if (++slot == S) slot = 0, phase ^= 1u;
         }
         // ---- the segment's result: the four warps' parts, 8 rows at a time
@@ -1049,6 +1051,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         skip_empty(w);
     }
     if (bad_page) set_error(p.err, DEV_ERR_BAD_PLACE);
+    // a wait gave up: let the copies in flight land before the CTA ends
+    if (*s_abort && lane == 0) ring.drain(warp * S, S, [&](int at, uint32_t parity) { mbar_wait(s_full + at, parity); });
     __syncthreads();
     settle();
 }

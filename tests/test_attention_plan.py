@@ -8,6 +8,10 @@ in one place of a CTA, every group of pieces and every item that is joined in gr
 an arrival counter of its own, and the places whose results a join reads are the ones
 that were written.  The counters' rule of one array for all groups, by the group's first
 CTA alone, is counted beside it: the batches have to reach the case where it fails.
+
+A second program gives up a warp's ring of copies at every point of its work, with the copies
+landing late or not at all until then, and checks that the drain waits for each that is on its
+way, and for nothing else.
 """
 import os
 import shutil
@@ -110,6 +114,63 @@ int main() {
 }
 """
 
+RING = r"""
+#include <cstdio>
+#include <random>
+#include "ggq_attn_plan.h"
+using namespace ggq;
+
+// A barrier of one arrival and its copy's bytes: `done` phases are over.
+struct Barrier {
+    int issued = 0, done = 0;
+    bool test(uint32_t parity) const { return (static_cast<uint32_t>(done) & 1u) != parity; }  // the phase of that parity is over
+};
+
+int main() {
+    std::mt19937 rng(3);
+    long waits = 0, violations = 0;
+    for (int round = 0; round < 20000; ++round) {
+        const int S = 2 + rng() % 5, units = rng() % 20, from = S * (rng() % 4), leave = rng() % (units + 1);
+        int turns[4 * 6];
+        Barrier bars[4 * 6];
+        const AttnRing ring{turns};
+        for (int i = 0; i < 4 * S; ++i) ring.clear(i);
+        int fetched = 0;
+        const auto fetch = [&](int at, uint32_t parity) {  // as the kernel's: one unit into a place whose last copy is over
+            if (fetched >= units) return;
+            ++fetched;
+            if (bars[at].issued != bars[at].done) ++violations;
+            ++bars[at].issued;
+            ring.issue(at, parity);
+        };
+        for (int i = 0; i < S; ++i) fetch(from + i, 0u);
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int u = 0; u < leave; ++u) {
+            const int at = from + slot;
+            bars[at].done = bars[at].issued;  // the copy lands
+            if (!bars[at].test(phase)) ++violations;
+            fetch(at, phase ^ 1u);
+            if (++slot == S) slot = 0, phase ^= 1u;
+        }
+        for (int i = 0; i < S; ++i)  // some of the others have landed, some are on their way
+            if (rng() % 2) bars[from + i].done = bars[from + i].issued;
+        ring.drain(from, S, [&](int at, uint32_t parity) {
+            if (at < from || at >= from + S || bars[at].issued == 0) ++violations;
+            const bool pending = bars[at].issued != bars[at].done;
+            if (bars[at].test(parity) == pending) ++violations;  // a copy on its way is waited for, no other one
+            bars[at].done = bars[at].issued;
+            if (!bars[at].test(parity)) ++violations;            // and the wait ends with it
+            ++waits;
+        });
+        for (const Barrier& b : bars)
+            if (b.issued != b.done) ++violations;
+    }
+    std::printf("waits %ld violations %ld\n", waits, violations);
+    return violations == 0 ? 0 : 1;
+}
+"""
+
 
 def _nvcc():
     for cand in (shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
@@ -118,18 +179,27 @@ def _nvcc():
     return None
 
 
-def test_every_group_of_pieces_has_a_counter_and_a_place(tmp_path):
+def run(program, tmp_path):
     nvcc = _nvcc()
     if nvcc is None:
         pytest.skip("nvcc not available")
     src = tmp_path / "attn_plan_check.cu"
-    src.write_text(PROGRAM)
+    src.write_text(program)
     exe = tmp_path / "attn_plan_check"
     r = subprocess.run([nvcc, "-std=c++17", "-O1", "-gencode", "arch=compute_103a,code=sm_103a", "-I", CSRC,
                         str(src), "-o", str(exe)], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-3000:]
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stdout[-3000:]
-    known, rest = r.stdout.splitlines()
+    return r.stdout
+
+
+def test_every_group_of_pieces_has_a_counter_and_a_place(tmp_path):
+    known, rest = run(PROGRAM, tmp_path).splitlines()
     assert int(known.split()[1]) >= 3  # the named batches bring two groups to one CTA
     assert int(rest.split()[5]) >= 100 and rest.endswith("violations 0")
+
+
+def test_a_ring_that_gives_up_waits_for_its_copies(tmp_path):
+    out = run(RING, tmp_path).split()
+    assert int(out[1]) > 1000 and out[2:] == ["violations", "0"]
