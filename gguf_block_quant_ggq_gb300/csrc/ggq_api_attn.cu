@@ -2,6 +2,7 @@
 // the expert router (include/ggq.h): argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/ggq.h"
@@ -168,7 +169,8 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     // before the first key (position -1 and below) included
     p.window = static_cast<int>(a->window <= 0 || a->window >= room ? 0 : a->window);
     p.scale = a->scale;
-    p.cap = a->cap > 0.0f ? a->cap : 0.0f;
+    // beyond 2^+-100 the quotients by the cap leave fp32, and a larger (smaller) cap changes no result
+    p.cap = a->cap > 0.0f ? std::min(std::max(a->cap, 0x1p-100f), 0x1p100f) : 0.0f;
     p.err = &c->ctrl->err;
     s = need_scratch(c, attn_scratch());
     if (s != GGQ_OK) return s;

@@ -37,7 +37,8 @@ static bool tiles_pay(const AttnParams& p, int nsm) {
 
 cudaError_t launch_attention(const AttnParams& p, int nsm, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
-    const bool fits = rows <= 64ll * 65535 && p.n_seqs * p.Hkv <= INT32_MAX;  // the tile kernels' grids
+    const bool fits = rows <= 64ll * 65535 && p.n_seqs * p.Hkv <= INT32_MAX &&  // the tile kernels' grids
+                      (p.dtype == 0 || p.cap <= kWideCap);
     if (fits && tiles_pay(p, nsm)) {
         if (p.dtype == 0) {
             if (p.D == 64) return launch_attn_promptf_64(p, s);

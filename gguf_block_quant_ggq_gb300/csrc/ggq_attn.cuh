@@ -38,6 +38,11 @@ struct AttnParams {
 // longest sequence), stay in range.
 constexpr int64_t kAttnMaxRows = 1 << 24, kAttnMaxLen = (1ll << 31) - (1 << 25);
 
+// The kernels of 16-bit rows form cap * tanh(z) as cap - 2 cap / (1 + exp(2 z)), whose error is
+// a few 2^-23 cap.  Beyond this cap that would show beside the scores' own roundings: such
+// calls take the streaming kernel of fp32 rows, which has tanhf, at about its times for fp32.
+constexpr float kWideCap = 1024.0f;
+
 // A partial result: reference maxima [16], sums [16], values [16][D].
 __host__ __device__ constexpr int attn_part_floats(int D) { return 32 + 16 * D; }
 

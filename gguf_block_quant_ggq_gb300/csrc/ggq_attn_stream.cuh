@@ -56,7 +56,7 @@ constexpr float kAttnNone = -1e30f;                    // reference maximum of a
 enum AttnMode : int { A_SPLIT8 = 0, A_HALF8 = 1, A_HALF16 = 2 };
 
 // cap * tanh(y / cap).  For fp32 rows tanhf; else 1 - 2 / (1 + exp(2 z)), whose error
-// of a few 2^-23 cap is far below the roundings of 16-bit activations.
+// of a few 2^-23 cap (cap <= kWideCap) is below the roundings of 16-bit activations.
 template <int MODE>
 __device__ __forceinline__ float attn_cap(float y, float cap) {
     const float z = __fdividef(y, cap);
@@ -1082,7 +1082,7 @@ cudaError_t launch_attn_stream(const AttnParams& p, int nsm, cudaStream_t s) {
 
 template <bool K4, bool V4, int D>
 cudaError_t launch_attn_stream_mode(const AttnParams& p, int nsm, cudaStream_t s) {
-    if (p.dtype == 0) return launch_attn_stream<K4, V4, D, A_SPLIT8>(p, nsm, s);
+    if (p.dtype == 0 || p.cap > kWideCap) return launch_attn_stream<K4, V4, D, A_SPLIT8>(p, nsm, s);
     if (static_cast<int64_t>(p.max_q) * p.G <= 8) return launch_attn_stream<K4, V4, D, A_HALF8>(p, nsm, s);
     return launch_attn_stream<K4, V4, D, A_HALF16>(p, nsm, s);
 }

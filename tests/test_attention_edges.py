@@ -195,3 +195,19 @@ def test_lengths_up_to_the_bound(ctx, dtype, D, rows):  # noqa: F811
     with pytest.raises(ggq.GGQError, match="outside the key/value cache"):
         ctx.sync_status()
     assert torch.equal(cut, out)
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 1000.0, 3000.0, 1e5, 1e9, 1e30, 3e38])
+@pytest.mark.parametrize("dtype,D,slopes", [("f32", 64, False), ("f32", 256, False), ("f16", 64, True), ("bf16", 128, False),
+                                            ("f16", 256, False)])
+def test_caps_of_any_size(ctx, dtype, D, slopes, cap):  # noqa: F811
+    """A large cap leaves the scores as they are, a tiny one makes them equal; scores of both signs up to some hundreds."""
+    for news in (PROMPTS, [min(3, x) for x in PROMPTS]):
+        for q_mul in (1.0, 30.0):
+            c = Case(ctx, PROMPTS, news, 16, 8, D, dtype=dtype, seed=21, q_mul=q_mul)
+            opts = dict(cap=cap)
+            if slopes:
+                opts["slopes"] = torch.exp2(-1.0 - torch.arange(16, device="cuda") / 2)
+            out = c.call(**opts)
+            ctx.sync_status()
+            check(c, out, **opts)
