@@ -47,20 +47,23 @@ struct AttnPieces {
     __host__ __device__ __forceinline__ int group_counter() const { return kAttnMaxCtas + c0; }
 };
 
-// The copies of a warp's ring, place by place: the parity of the barrier phase that a
-// place's last copy completes (kNoCopy: none yet).  A warp that leaves its units early
-// waits for these before its CTA's shared memory goes to another one.
-constexpr int kNoCopy = -1;
-struct AttnRing {
-    int* turns;
-    __host__ __device__ __forceinline__ void clear(int at) const { turns[at] = kNoCopy; }
-    __host__ __device__ __forceinline__ void issue(int at, uint32_t parity) const { turns[at] = static_cast<int>(parity); }
-    // wait(place, parity) for every place that holds or awaits a copy
-    template <typename WAIT>
-    __host__ __device__ __forceinline__ void drain(int from, int places, WAIT wait) const {
-        for (int at = from; at < from + places; ++at)
-            if (turns[at] != kNoCopy) wait(at, static_cast<uint32_t>(turns[at]));
+// The copies of a warp's ring that are on their way when it leaves its units early, for
+// which it waits before its CTA's shared memory goes to another one.  A warp fills its
+// places in turn and takes them in turn; the next one it would take is `slot`, whose copy
+// completes the barrier phase of parity `phase` (the places before it: of the other
+// parity).  All places hold or await a copy until the share's last one, which is noted.
+constexpr int kMoreCopies = -1, kNoCopies = -2;
+__host__ __device__ constexpr int attn_last_copy(int slot, uint32_t parity) { return 2 * slot + static_cast<int>(parity); }
+template <typename WAIT>
+__host__ __device__ __forceinline__ void attn_drain(int last, int places, int slot, uint32_t phase, WAIT wait) {
+    const auto parity = [&](int at) { return at >= slot ? phase : phase ^ 1u; };
+    int n = places;
+    if (last != kMoreCopies) {
+        const int at = last >> 1;
+        if (last == kNoCopies || static_cast<uint32_t>(last & 1) != parity(at)) return;  // all taken
+        n = (at >= slot ? at - slot : at - slot + places) + 1;
     }
-};
+    for (int k = 0, at = slot; k < n; ++k, at = at + 1 == places ? 0 : at + 1) wait(at, parity(at));
+}
 
 }  // namespace ggq

@@ -90,8 +90,8 @@ struct AttnSmem {
     static constexpr int oStat = oQ + D / 16 * 32 * 16;   // m, l [warps][8]
     static constexpr int oScan = (oStat + 2 * kAttnWarps * 8 * 4 + 7) / 8 * 8;
     static constexpr int oBar = (oScan + (128 + 4) * 8 + 15) / 16 * 16;
-    static constexpr int oTurns = oBar + kAttnWarps * kStages * 8 + 16;
-    static constexpr int kTotal = oTurns + kAttnWarps * kStages * 4;
+    static constexpr int oLast = oBar + kAttnWarps * kStages * 8 + 16;
+    static constexpr int kTotal = oLast + kAttnWarps * 4;
     // CTAs an SM: 12 warps leave 168 registers a thread (64-channel heads), 8 warps 255
     static constexpr int kCtas = D == 64 && 3 * (kTotal + 1024) <= 228 * 1024 ? 3 : 2 * (kTotal + 1024) <= 228 * 1024 ? 2 : 1;
 };
@@ -848,12 +848,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     uint64_t* const s_full = reinterpret_cast<uint64_t*>(smem + SM::oBar);
     volatile int* const s_abort = reinterpret_cast<volatile int*>(s_full + kAttnWarps * S);
     volatile int* const s_last = s_abort + 1;
-    const AttnRing ring{reinterpret_cast<int*>(smem + SM::oTurns)};
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int* const s_copy = reinterpret_cast<int*>(smem + SM::oLast) + warp;  // this warp's last copy
 
     pdl_launch_dependents();
     if (tid == 0) {
-        for (int i = 0; i < kAttnWarps * S; ++i) mbar_init(s_full + i, 1), ring.clear(i);
+        for (int i = 0; i < kAttnWarps * S; ++i) mbar_init(s_full + i, 1);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -928,11 +928,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
         }
         fpage = ftable[q];
     };
-    const auto fetch = [&](int at, uint32_t parity) {
+    const auto fetch = [&](int place, uint32_t parity) {
         if (fu >= fend) return;
+        const int at = warp * S + place;
         const int n = min(UNIT, fghi - fglo - UNIT * fu);  // groups of the unit
         const bool joined = __shfl_sync(0xffffffffu, fplace, 0) + n <= gpp;  // of one page: one copy
-        if (lane == 0) mbar_arrive_expect_tx(s_full + at, n * (SM::kStage / UNIT)), ring.issue(at, parity);
+        if (lane == 0) mbar_arrive_expect_tx(s_full + at, n * (SM::kStage / UNIT));
         __syncwarp();
         if (lane < (joined ? 1 : n)) {
             const int copies = joined ? n : 1;
@@ -943,12 +944,16 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
             bulk_g2s(dst + UNIT * SM::kKB + lane * SM::kVB, p.v + blob * SM::kVB, copies * SM::kVB, s_full + at, policy);
         }
         fu += kAttnWarps;
-        if (fu >= fend) enter();
+        if (fu >= fend) {
+            enter();
+            if (fend == 0) *s_copy = attn_last_copy(place, parity);
+        }
         seek();
     };
     enter();
+    *s_copy = fend == 0 ? kNoCopies : kMoreCopies;
     seek();
-    for (int i = 0; i < S; ++i) fetch(warp * S + i, 0u);
+    for (int i = 0; i < S; ++i) fetch(i, 0u);
 
     // ---- segments
     const int g8 = lane >> 2, t4 = lane & 3;
@@ -993,7 +998,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
 
             rows.unit(p, s_q, kb, vb, g, lane);
             __syncwarp();
-            fetch(at, phase ^ 1u);
+            fetch(slot, phase ^ 1u);
             if (++slot == S) slot = 0, phase ^= 1u;
         }
         // ---- the segment's result: the four warps' parts, 8 rows at a time
@@ -1052,7 +1057,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnSmem<K4, V4, D, MODE>::kCtas
     }
     if (bad_page) set_error(p.err, DEV_ERR_BAD_PLACE);
     // a wait gave up: let the copies in flight land before the CTA ends
-    if (*s_abort && lane == 0) ring.drain(warp * S, S, [&](int at, uint32_t parity) { mbar_wait(s_full + at, parity); });
+    if (*s_abort) attn_drain(*s_copy, S, slot, phase, [&](int at, uint32_t parity) { mbar_wait(s_full + warp * S + at, parity); });
     __syncthreads();
     settle();
 }

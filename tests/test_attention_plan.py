@@ -130,33 +130,30 @@ int main() {
     std::mt19937 rng(3);
     long waits = 0, violations = 0;
     for (int round = 0; round < 20000; ++round) {
-        const int S = 2 + rng() % 5, units = rng() % 20, from = S * (rng() % 4), leave = rng() % (units + 1);
-        int turns[4 * 6];
-        Barrier bars[4 * 6];
-        const AttnRing ring{turns};
-        for (int i = 0; i < 4 * S; ++i) ring.clear(i);
-        int fetched = 0;
+        const int S = 2 + rng() % 5, units = rng() % 20, leave = rng() % (units + 1);
+        Barrier bars[6];
+        int fetched = 0, last = units ? kMoreCopies : kNoCopies;
         const auto fetch = [&](int at, uint32_t parity) {  // as the kernel's: one unit into a place whose last copy is over
             if (fetched >= units) return;
             ++fetched;
             if (bars[at].issued != bars[at].done) ++violations;
             ++bars[at].issued;
-            ring.issue(at, parity);
+            if (fetched == units) last = attn_last_copy(at, parity);
         };
-        for (int i = 0; i < S; ++i) fetch(from + i, 0u);
+        for (int i = 0; i < S; ++i) fetch(i, 0u);
         int slot = 0;
         uint32_t phase = 0;
         for (int u = 0; u < leave; ++u) {
-            const int at = from + slot;
+            const int at = slot;
             bars[at].done = bars[at].issued;  // the copy lands
             if (!bars[at].test(phase)) ++violations;
             fetch(at, phase ^ 1u);
             if (++slot == S) slot = 0, phase ^= 1u;
         }
-        for (int i = 0; i < S; ++i)  // some of the others have landed, some are on their way
-            if (rng() % 2) bars[from + i].done = bars[from + i].issued;
-        ring.drain(from, S, [&](int at, uint32_t parity) {
-            if (at < from || at >= from + S || bars[at].issued == 0) ++violations;
+        for (Barrier& b : bars)  // some of the others have landed, some are on their way
+            if (rng() % 2) b.done = b.issued;
+        attn_drain(last, S, slot, phase, [&](int at, uint32_t parity) {
+            if (at < 0 || at >= S || bars[at].issued == 0) ++violations;
             const bool pending = bars[at].issued != bars[at].done;
             if (bars[at].test(parity) == pending) ++violations;  // a copy on its way is waited for, no other one
             bars[at].done = bars[at].issued;
