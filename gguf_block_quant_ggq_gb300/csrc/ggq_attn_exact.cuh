@@ -17,6 +17,10 @@ namespace ggq {
 template <bool Q4>
 __host__ __device__ constexpr uint32_t attn_half_limit() { return Q4 ? 0x6FFFu : 0x5FFFu; }
 
+// Whether scales may be past a limit, or not finite, given the bits of all of them OR'ed
+// together: 512 and above have bits 13 and 14.  May be true of harmless ones (2 beside 1).
+__device__ __forceinline__ bool attn_maybe_wide(uint32_t any) { return (any & (any << 1) & 0x40004000u) != 0u; }
+
 // The blob of a key's group.
 template <bool Q4, int D>
 __device__ __forceinline__ const uint8_t* exact_blob(const AttnParams& p, const uint8_t* pool, int b, int hk, int key) {

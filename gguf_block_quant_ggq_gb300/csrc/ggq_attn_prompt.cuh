@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
     volatile int* const abort = reinterpret_cast<volatile int*>(tslot + 1);
     int* const s_bad = reinterpret_cast<int*>(tslot + 2);  // [NB][2] first and last key whose value scale is not finite
     int* const s_wide = s_bad + 2 * NB;                    // first and last key that fp16 tiles cannot hold
+    int* const s_odd = s_wide + 2;                         // 1: there is one of either kind
 
     pdl_launch_dependents();
     pdl_wait();
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             mbar_init(pdone + i, 1);
             mbar_init(done + i, 1);
         }
-        *abort = 0;
+        *abort = *s_odd = 0;
         for (int i = 0; i <= NB; ++i) s_bad[2 * i] = 0x7fffffff, s_bad[2 * i + 1] = -1;  // and s_wide
         fence_barrier_init();
     }
@@ -507,12 +508,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             // ---- keys: lane (g, t) writes 16 channels of a 64-channel atom as two chunks of its token's row
             if (j >= 2 && !wait(kempty + buf, ((j >> 1) - 1) & 1)) break;
             uint8_t* const kt = smem + SH::oK + buf * SH::kK + (k_group * 16 + 8 * k_part + g8) * 128;
-            uint32_t most = 0u;
+            uint32_t any = 0u;
 #pragma unroll
             for (int o = 0; o < KO; ++o)
 #pragma unroll
-                for (int q = 0; q < NB / 2; ++q) most = __vmaxu2(most, ks[o][q] & 0x7FFF7FFFu);
-            if ((most & 0xFFFFu) > attn_half_limit<K4>() || (most >> 16) > attn_half_limit<K4>()) {
+                for (int q = 0; q < NB / 2; ++q) any |= ks[o][q];
+            if (attn_maybe_wide(any)) {
                 // scales whose products leave fp16: 0 here, and the rows that see them are told
 #pragma unroll
                 for (int o = 0; o < KO; ++o)
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                     for (int q = 0; q < NB / 2; ++q) {
                         const int key = 16 * (glo + j * KG + k_group) + 8 * (k_part + o) + g8;
                         const bool lo = attn_wide<K4>(ks[o][q]), hi = attn_wide<K4>(ks[o][q] >> 16);
-                        if ((lo || hi) && key < len) atomicMin(s_wide, key), atomicMax(s_wide + 1, key);
+                        if ((lo || hi) && key < len) atomicMin(s_wide, key), atomicMax(s_wide + 1, key), *s_odd = 1;
                         ks[o][q] = (lo ? 0u : ks[o][q] & 0xFFFFu) | (hi ? 0u : ks[o][q] & 0xFFFF0000u);
                     }
             }
@@ -551,16 +552,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
             // ---- values: whatever lies past the sequence's end counts as 0
             if (j >= 2 && !wait(vempty + buf, ((j >> 1) - 1) & 1)) break;
             const int key0 = 16 * (glo + j * KG + 2 * pair);
-            uint32_t odd = 0u;
+            any = 0u;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     if (key0 + 16 * c + 8 * (r >> 1) + 2 * t4 + (r & 1) >= len) vsc[c][r] = 0u;
-                    odd = __vmaxu2(odd, vsc[c][r] & 0x7FFF7FFFu);
+                    any |= vsc[c][r];
                 }
-            constexpr uint32_t kLimit = BF ? 0x7BFFu : attn_half_limit<V4>();
-            if ((odd & 0xFFFFu) > kLimit || (odd >> 16) > kLimit) {
+            if (attn_maybe_wide(any)) {
                 // scales that are not finite, or (fp16 rows) whose products are not: 0 here, and the rows that
                 // see them are told
                 int* const bad = s_bad + 4 * (b0 >> 1);
@@ -578,6 +578,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
                             if (wide_lo || wide_hi) atomicMin(s_wide, key), atomicMax(s_wide + 1, key);
                             lo |= wide_lo, hi |= wide_hi;
                         }
+                        if (lo || hi) *s_odd = 1;
                         vsc[c][r] = (lo ? 0u : u & 0xFFFFu) | (hi ? 0u : u & 0xFFFF0000u);
                     }
             }
@@ -727,11 +728,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         tc_fence_after();
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         const int64_t at = (first + i_row) * p.out_token + h * p.out_head;
+        const bool odd = *s_odd != 0;
         bool spoilt = false;  // an infinite or NaN value of the block among those that the row sees
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
             float o[16];
-            if ((c & 1) == 0) {
+            if (odd && (c & 1) == 0) {
                 spoilt = prompt_spoilt<V4, D>(p, s_bad, b, hk, c >> 1, first_key, pos);
                 __syncwarp();
             }
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) k_attn_prompt(const __grid_
         }
         // ---- rows that may see keys or values which the tiles left out
         __syncwarp();  // their outputs, written above by their own lanes, are written again by the warp
-        uint32_t again = __ballot_sync(0xffffffffu, there && s_wide[0] <= pos && s_wide[1] >= first_key && s_wide[1] >= 0);
+        uint32_t again = odd ? __ballot_sync(0xffffffffu, there && s_wide[0] <= pos && s_wide[1] >= first_key && s_wide[1] >= 0) : 0u;
         for (; again; again &= again - 1u) {
             const int from_lane = __ffs(again) - 1;
             attn_exact_row<K4, V4, D, std::conditional_t<BF, __nv_bfloat16, __half>, !BF>(
