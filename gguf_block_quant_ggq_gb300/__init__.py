@@ -231,6 +231,14 @@ class Context:
             stream = self._torch.cuda.current_stream(self.device)
         return stream.cuda_stream
 
+    def _empty(self, shape, dtype, stream):
+        """A new tensor on the context's device, of the memory of the stream that will write it: a block freed on
+        another stream may still be in use there."""
+        if stream is None:
+            return self._torch.empty(shape, dtype=dtype, device=self._dev)
+        with self._torch.cuda.stream(stream):
+            return self._torch.empty(shape, dtype=dtype, device=self._dev)
+
     def _vec(self, t, dtype):
         """Address of a contiguous tensor of `dtype` on the context's device (None passes NULL)."""
         if t is None:
@@ -288,14 +296,14 @@ class Context:
     def quantize_act(self, act: str, x, out=None, stream=None):
         T, K = x.shape
         if out is None:
-            out = self._torch.empty((T, row_bytes(act, K)), dtype=self._torch.uint8, device=x.device)
+            out = self._empty((T, row_bytes(act, K)), self._torch.uint8, stream)
         self._check(load().ggq_quantize_act(self.handle, TYPE[act], _ptr(x, "float32"), T, K, _ptr(out, "uint8"),
                                             self._stream(stream)))
         return out
 
     def dequant(self, fmt: str, blocks, rows: int, K: int, out=None, stream=None):
         if out is None:
-            out = self._torch.empty((rows, K), dtype=self._torch.float32, device=blocks.device)
+            out = self._empty((rows, K), self._torch.float32, stream)
         self._check(load().ggq_dequant(self.handle, TYPE[fmt], _ptr(blocks), rows, K, _ptr(out, "float32"),
                                        self._stream(stream)))
         return out
@@ -303,7 +311,7 @@ class Context:
     def mul_mat_vec(self, fmt: str, W, N: int, K: int, X, Y=None, stream=None, reserve=True):
         T = X.shape[0]
         if Y is None:
-            Y = self._torch.empty((T, N), dtype=self._torch.float32, device=X.device)
+            Y = self._empty((T, N), self._torch.float32, stream)
         if reserve:
             self.reserve(max_tokens=T, max_k=K, stream=stream)
         self._check(load().ggq_mul_mat_vec(self.handle, TYPE[fmt], _ptr(W), N, K, _ptr(X, "float32"), T,
@@ -312,28 +320,28 @@ class Context:
 
     def mul_mat_vec_q(self, fmt: str, W, N: int, K: int, Xq, T: int, Y=None, stream=None):
         if Y is None:
-            Y = self._torch.empty((T, N), dtype=self._torch.float32, device=Xq.device)
+            Y = self._empty((T, N), self._torch.float32, stream)
         self._check(load().ggq_mul_mat_vec_q(self.handle, TYPE[fmt], _ptr(W), N, K, _ptr(Xq), T, _ptr(Y, "float32"),
                                              self._stream(stream)))
         return Y
 
     def mul_mat_vec_qa(self, fmt: str, act: str, W, N: int, K: int, Xq, T: int, Y=None, stream=None):
         if Y is None:
-            Y = self._torch.empty((T, N), dtype=self._torch.float32, device=Xq.device)
+            Y = self._empty((T, N), self._torch.float32, stream)
         self._check(load().ggq_mul_mat_vec_qa(self.handle, TYPE[fmt], TYPE[act], _ptr(W), N, K, _ptr(Xq), T,
                                               _ptr(Y, "float32"), self._stream(stream)))
         return Y
 
     def block_dots_qa(self, fmt: str, act: str, W, N: int, K: int, Xq, T: int, stream=None):
         nc = K // BLOCK_ELEMS[fmt] * (2 if fmt in ("Q4_K", "Q5_K", "Q2_K") else 1)
-        out = self._torch.empty((T, N, nc), dtype=self._torch.int32, device=Xq.device)
+        out = self._empty((T, N, nc), self._torch.int32, stream)
         self._check(load().ggq_block_dots_qa(self.handle, TYPE[fmt], TYPE[act], _ptr(W), N, K, _ptr(Xq), T,
                                              _ptr(out), self._stream(stream)))
         return out
 
     def block_dots(self, fmt: str, W, N: int, K: int, Xq, T: int, stream=None):
         nc = K // BLOCK_ELEMS[fmt] * (2 if fmt in ("Q4_K", "Q5_K", "Q2_K") else 1)
-        out = self._torch.empty((T, N, nc), dtype=self._torch.int32, device=Xq.device)
+        out = self._empty((T, N, nc), self._torch.int32, stream)
         self._check(load().ggq_block_dots(self.handle, TYPE[fmt], _ptr(W), N, K, _ptr(Xq), T, _ptr(out),
                                           self._stream(stream)))
         return out
@@ -364,9 +372,9 @@ class Context:
         if dtype is None:
             dtype = k.dtype if k is not None else v.dtype if v is not None else self._f32
         if k is None:
-            k = self._torch.empty((n, heads, dim), dtype=dtype, device=self._dev)
+            k = self._empty((n, heads, dim), dtype, stream)
         if v is None:
-            v = self._torch.empty((n, heads, dim), dtype=dtype, device=self._dev)
+            v = self._empty((n, heads, dim), dtype, stream)
         kp, code, kt, kh = self._rows(k, heads, dim)
         vp, vcode, vt, vh = self._rows(v, heads, dim)
         if code != vcode or k.shape[0] != n or v.shape[0] != n:
@@ -387,7 +395,7 @@ class Context:
             raise ValueError(f"expected a [tokens, heads, {cache.head_dim}] tensor, got {tuple(q.shape)}")
         n, heads, dim = q.shape
         if out is None:
-            out = self._torch.empty((n, heads, dim), dtype=q.dtype, device=self._dev)
+            out = self._empty((n, heads, dim), q.dtype, stream)
         qp, code, qt, qh = self._rows(q, heads, cache.head_dim)
         op, ocode, ot, oh = self._rows(out, heads, cache.head_dim)
         seqs = lens.numel()
@@ -423,11 +431,11 @@ class Context:
         if bias is not None and bias.numel() != E:
             raise ValueError(f"expected a bias of {E} experts, got {bias.numel()}")
         if ids is None:
-            ids = self._torch.empty((T, max(top_k, 0)), dtype=self._i32, device=self._dev)
+            ids = self._empty((T, max(top_k, 0)), self._i32, stream)
         elif tuple(ids.shape) != (T, top_k):
             raise ValueError(f"expected a [{T}, {top_k}] output, got {tuple(ids.shape)}")
         if weights is None:
-            weights = self._torch.empty((T, max(top_k, 0)), dtype=self._f32, device=self._dev)
+            weights = self._empty((T, max(top_k, 0)), self._f32, stream)
         elif tuple(weights.shape) != (T, top_k):
             raise ValueError(f"expected a [{T}, {top_k}] output, got {tuple(weights.shape)}")
         _ROUTER.pack_into(self._router_args, 0, SCORING[scoring], n_groups, top_groups, group_best, top_k,
@@ -445,7 +453,7 @@ class Context:
                     Y=None, dump: dict | None = None, stream=None, reserve=True):
         T = X.shape[0]
         if Y is None:
-            Y = self._torch.empty((T, H), dtype=self._torch.float32, device=X.device)
+            Y = self._empty((T, H), self._torch.float32, stream)
         if reserve:
             self.reserve(max_tokens=T, n_experts=E, hidden=H, inter=I, top_k=top_k, stream=stream)
         d = None
@@ -467,7 +475,7 @@ def _moe_q(ctx, weights, E, H, I, top_k, Xq, logits, Y=None, dump=None, stream=N
     """ggq_moe_experts_q: the layer on pre-quantized Q8_K activations Xq [T][H/256*292] (uint8)."""
     T = Xq.shape[0]
     if Y is None:
-        Y = ctx._torch.empty((T, H), dtype=ctx._torch.float32, device=Xq.device)
+        Y = ctx._empty((T, H), ctx._torch.float32, stream)
     if reserve:
         ctx.reserve(max_tokens=T, n_experts=E, hidden=H, inter=I, top_k=top_k, stream=stream)
     d = ggq_moe_dump(**{k: _ptr(v) for k, v in dump.items()}) if dump is not None else None

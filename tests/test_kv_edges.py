@@ -57,3 +57,28 @@ def test_one_given_buffer_sets_the_type_of_both(ctx):  # noqa: F811
         assert got["kv".index(name)] is given
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     ctx.sync_status()
+
+
+def test_outputs_are_of_the_given_streams_memory(ctx):  # noqa: F811
+    """What a call makes for itself comes from the memory of the stream that writes it: the block goes back to
+    that stream when the output is dropped, and to no other one."""
+    c = Case(ctx, [21, 40], [1, 1], 2, 2, 64)
+    x = torch.zeros((3, 70000), device="cuda")
+    calls = {
+        "attention": lambda s: ctx.attention(c.cache, c.q, c.dlens, c.table, stream=s),
+        "kv_load": lambda s: ctx.kv_load(c.cache, c.slots, stream=s)[1],
+        "moe_route": lambda s: ctx.moe_route(x[:, :64].contiguous(), 2, stream=s)[0],
+        "quantize_act": lambda s: ctx.quantize_act("Q8_0", x[:, :256].contiguous(), stream=s),
+    }
+    s = torch.cuda.Stream()
+    for name, call in calls.items():
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        out = call(s)
+        torch.cuda.synchronize()
+        at, size = out.untyped_storage().data_ptr(), out.untyped_storage().nbytes()
+        del out
+        with torch.cuda.stream(s):
+            blocks = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert at in [b.data_ptr() for b in blocks], name
+    ctx.sync_status()
