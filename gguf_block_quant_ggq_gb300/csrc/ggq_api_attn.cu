@@ -40,8 +40,12 @@ ggq_status cache_checks(ggq_ctx* c, const ggq_kv_cache* kv, const char* op) {
 // A page's 16-token groups as a multiplier for division (exact or one too large).
 uint32_t page_magic(int page_size) { return static_cast<uint32_t>((1ull << 32) / (page_size / 16) + 1); }
 
-// Partial results of items that two or more CTAs share, for the widest heads.
-size_t attn_scratch() { return align_up(2ull * kAttnMaxCtas * attn_part_floats(256) * sizeof(float)); }
+// Partial results of items that two or more CTAs share: two a CTA, for the widest heads
+// (whose CTAs an SM and those of narrower ones the streaming kernel asserts to fit).
+size_t attn_scratch(const ggq_ctx* c) {
+    const size_t ctas = std::min(kAttnMaxCtas, kAttnWideCtas * c->nsm);
+    return align_up(2 * ctas * attn_part_floats(256) * sizeof(float));
+}
 
 // Rows of four elements at a time: the pointer and the strides of axes of more than one element are multiples of 4.
 bool rows4(const void* p, int64_t tokens, int64_t token, int heads, int64_t head, int dtype) {
@@ -172,7 +176,7 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
     // beyond 2^+-100 the quotients by the cap leave fp32, and a larger (smaller) cap changes no result
     p.cap = a->cap > 0.0f ? std::min(std::max(a->cap, 0x1p-100f), 0x1p100f) : 0.0f;
     p.err = &c->ctrl->err;
-    s = need_scratch(c, attn_scratch());
+    s = need_scratch(c, attn_scratch(c));
     if (s != GGQ_OK) return s;
     p.min_share = 4;  // one sequence of 777 tokens, 8 kv heads: 11.8 us; 13.6 at 2, 12.6 at 8, 15.1 at 16
     p.parts = reinterpret_cast<float*>(c->pool);
@@ -184,7 +188,7 @@ ggq_status ggq_attention(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_attn* a, 
 ggq_status ggq_reserve_attention(ggq_ctx* c, void* stream) {
     DeviceScope scope;
     ggq_status s = check_ctx(c, scope);
-    return s == GGQ_OK ? grow_pool(c, attn_scratch(), stream) : s;
+    return s == GGQ_OK ? grow_pool(c, attn_scratch(c), stream) : s;
 }
 
 ggq_status ggq_moe_route(ggq_ctx* c, const ggq_router* r, int dtype, const void* logits, int64_t T, int64_t E,

@@ -43,8 +43,10 @@ constexpr int64_t kAttnMaxRows = 1 << 24, kAttnMaxLen = (1ll << 31) - (1 << 25);
 // calls take the streaming kernel of fp32 rows, which has tanhf, at about its times for fp32.
 constexpr float kWideCap = 1024.0f;
 
-// A partial result: reference maxima [16], sums [16], values [16][D].
+// A partial result: reference maxima [16], sums [16], values [16][D]; CTAs an SM at most for
+// heads of 256 channels.
 __host__ __device__ constexpr int attn_part_floats(int D) { return 32 + 16 * D; }
+constexpr int kAttnWideCtas = 2;
 
 cudaError_t launch_attention(const AttnParams& p, int nsm, cudaStream_t s);
 cudaError_t launch_attn_stream_64(const AttnParams& p, int nsm, cudaStream_t s);

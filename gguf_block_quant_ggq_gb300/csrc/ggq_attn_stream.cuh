@@ -1076,6 +1076,7 @@ cudaError_t launch_attn_stream(const AttnParams& p, int nsm, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_release);
     }
+    static_assert(SM::kCtas * attn_part_floats(D) <= kAttnWideCtas * attn_part_floats(256), "scratch of the partial results");
     const int64_t tiles = (static_cast<int64_t>(p.max_q) * p.G + SM::kRows - 1) / SM::kRows;
     const int64_t units = p.n_seqs * p.Hkv * tiles * ((static_cast<int64_t>(p.max_len) + 16 * SM::kUnit - 1) / (16 * SM::kUnit) + 1 + kItemCost);
     int64_t grid = (units + p.min_share - 1) / p.min_share;

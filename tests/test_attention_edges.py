@@ -211,3 +211,16 @@ def test_caps_of_any_size(ctx, dtype, D, slopes, cap):  # noqa: F811
             out = c.call(**opts)
             ctx.sync_status()
             check(c, out, **opts)
+
+
+def test_scratch_is_what_a_call_can_use():
+    """Two partial results of 16 rows of 256 channels for each of two CTAs an SM, no more."""
+    own = ggq.Context(0)
+    try:
+        c = Case(own, [5000], [1], 2, 1, 256)
+        c.call()
+        own.sync_status()
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        assert own.scratch_bytes() <= 2 * 2 * sms * (16 * 256 + 32) * 4 + 256
+    finally:
+        own.close()
