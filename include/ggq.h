@@ -40,7 +40,9 @@
  *   - Errors are returned as ggq_status; no exception crosses the ABI.  The
  *     message of the last error is ggq_last_error(ctx).  A call that returns
  *     an error has enqueued nothing.
- *   - Calls on one context are not thread-safe with each other.
+ *   - Calls on one context are not thread-safe with each other, and share its
+ *     scratch and counters: their work must not overlap on the GPU.  Order them on
+ *     one stream (or streams by events), or give each stream a context of its own.
  *   - A call that takes a context runs on the context's device and leaves the
  *     calling thread's current device as it found it.
  */
