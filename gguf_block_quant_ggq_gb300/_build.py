@@ -92,15 +92,23 @@ def ptxas_summary(report: str | None = None) -> str:
             rows.append(cur)
             cur = None
     def pretty(mangled):
-        # _ZN3ggq<len><name>I<template args>E... -> name<args> (Li5E -> 5, Lb1E -> true)
+        # _ZN3ggq<len><name>I<template args>E... -> name<args> (Li5E -> 5, Lb1E -> true, f -> float, 6__half -> __half);
+        # a file's unnamed namespace between the two is left out
         m = re.match(r"_ZN3ggq(\d+)", mangled)
         if not m:
             return mangled
-        n = int(m.group(1))
-        start = m.end()
-        name = mangled[start:start + n]
-        args = re.findall(r"L([ib])(\d+)E", mangled[start + n:])
-        vals = [("true" if v == "1" else "false") if t == "b" else v for t, v in args]
+        n, start = int(m.group(1)), m.end()
+        if mangled[start:start + n].startswith("_GLOBAL__N_"):
+            m = re.compile(r"\d+").match(mangled, start + n)
+            n, start = int(m.group(0)), m.end()
+        name, rest = mangled[start:start + n], mangled[start + n:]
+        if not rest.startswith("I"):
+            return name
+        args = re.match(r"I((?:L[ib]\d+E|f|6__half|13__nv_bfloat16)*)E", rest)
+        vals = []
+        for t, v, word in re.findall(r"L([ib])(\d+)E|(f|6__half|13__nv_bfloat16)", args.group(1)) if args else []:
+            vals.append({"f": "float", "6__half": "__half", "13__nv_bfloat16": "__nv_bfloat16"}[word] if word
+                        else ("true" if v == "1" else "false") if t == "b" else v)
         return f"{name}<{', '.join(vals)}>" if vals else name
     out = ["| kernel | registers | stack (B) | spill stores (B) | spill loads (B) |", "|---|---|---|---|---|"]
     for r in sorted(rows, key=lambda r: pretty(r["name"])):
@@ -122,7 +130,7 @@ if __name__ == "__main__":
                     "k_gmm<kind, format, dump>, k_gmmtc<format, dump>, k_direct<kind, format, "
                     "tokens, dump>, k_attn_stream<K is 4-bit, V is 4-bit, channels, rows (0 8 of fp32, 1 8 and 2 16 of 16 "
                     "bits)>, k_attn_prompt<K, V, channels, bf16>, k_attn_promptf<K, V, channels>, k_attn_rows<K, V, "
-                    "channels>, k_kv<store, channels> and k_route<keys a lane> (one row an element type); "
+                    "channels>, k_kv<store, channels, element> and k_route<keys a lane, element>; "
                     "k_attn_prompt and k_attn_promptf launch with 96 and 72 registers and split them by warp role; formats 0 Q4_0, 1 Q8_0, 2 Q4_K, 3 Q5_K, 4 Q6_K, 5 MXFP4, 6 Q2_K, 7 Q3_K.\n\n")
             f.write(ptxas_summary())
     else:

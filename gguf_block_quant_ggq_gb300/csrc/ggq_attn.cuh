@@ -40,7 +40,9 @@ constexpr int64_t kAttnMaxRows = 1 << 24, kAttnMaxLen = (1ll << 31) - (1 << 25);
 
 // The kernels of 16-bit rows form cap * tanh(z) as cap - 2 cap / (1 + exp(2 z)), whose error is
 // a few 2^-23 cap.  Beyond this cap that would show beside the scores' own roundings: such
-// calls take the streaming kernel of fp32 rows, which has tanhf, at about its times for fp32.
+// calls take the streaming kernel of fp32 rows, which has tanhf, at its times for fp32 (32
+// heads on 8 of 128 channels, bf16, caps 50 / 2000: one token of 64 sequences of 4096 119 /
+// 143 us, a prompt of 4096 274 / 4160 us).
 constexpr float kWideCap = 1024.0f;
 
 // A partial result: reference maxima [16], sums [16], values [16][D]; CTAs an SM at most for

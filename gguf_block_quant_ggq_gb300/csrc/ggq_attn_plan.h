@@ -14,7 +14,8 @@ constexpr int kAttnMaxCtas = 1024;
 
 // What an item counts in the shares beside its units, measured on 64 ragged sequences
 // of up to 4096 tokens (units of 32 tokens, 128 channels): 82 us at 0, 68 at 6, 63.6 at
-// 12, 65 at 20.
+// 12, 65 at 20.  Other units (16 tokens of 256 channels, 64 of 4-bit 64 channels) use the
+// same count, not measured by itself.
 constexpr int kItemCost = 12;
 
 // Sixteen neighbouring pieces are joined by the last of them, then these results by

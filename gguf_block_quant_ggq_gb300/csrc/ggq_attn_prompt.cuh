@@ -4,7 +4,7 @@
 // Mathematics: S = Q K^T and O = P V per kv head, the rows being the head
 // group's query heads of consecutive tokens, with the softmax's running maximum
 // and sum.  4 D operations per (row, key); the packed cache is a small part.  Measured:
-// the last 4096 of 8192 causal bf16 rows, 32 heads on 8 of 128 channels: 431 us, 956
+// the last 4096 of 8192 causal bf16 rows, 32 heads on 8 of 128 channels: 427 us, 966
 // TFLOP/s, half the rate of a plain 16-bit product; the tensor pipe is busy 39% of the
 // time, the issue slots 65%: bound by the instructions of the softmax and of unpacking
 // the blobs (done once for 256 rows) and the waits between them.

@@ -11,10 +11,10 @@
 // in registers, in fp32 with rounding to nearest.
 //
 // Measured (28 heads on 4 of 128 channels, distance bias, 5 ragged prompts of up to 1000
-// rows): 175 us, 104 TFLOP/s of the formula's operations (on mma.sync with the scales in
-// the accumulators: 321 us); 4096 causal rows of 32 heads on 8: 737 us (1716).  Bound by
-// its small MMAs: a step of 32 keys takes 128 rows 1.5 us for 40 MMAs of 32 columns, some
-// 70 cycles each whatever their width.
+// rows): 177 us, 103 TFLOP/s of the formula's operations (on mma.sync with the scales in
+// the accumulators: 321 us); 4096 causal rows of 32 heads on 8: 744 us (1716).  A step of
+// 32 keys takes 128 rows 1.5 us for 40 MMAs of 32 columns, some 70 cycles each whatever
+// their width; issue slots 64% used, tensor pipe 11%.
 //
 // A CTA takes 128 rows of one kv head of one sequence.  Roles:
 //   * warps 0-15: four threads a row, each a quarter of a step's keys and of the output's
@@ -32,9 +32,9 @@
 
 namespace ggq {
 
-// Four threads a row: 16 softmax warps, four a scheduler (5 ragged prompts of up to 1000
-// rows with a distance bias: 175 us; two threads a row with 160 registers each: 191.  4096
-// causal rows without one: 737 and 727).
+// Four threads a row: 16 softmax warps, four a scheduler (measured together, 5 ragged prompts
+// of up to 1000 rows with a distance bias: 175 us; two threads a row with 160 registers each:
+// 191.  4096 causal rows without one: 737 and 727).
 constexpr int kPfParts = 4, kPfSoftmaxWarps = 4 * kPfParts, kPfFirstMma = kPfSoftmaxWarps + kDecodeWarps;
 constexpr int kPfThreads = (kPfFirstMma + kMmaWarps) * 32;
 constexpr int kPfLaunchRegs = 72, kPfSoftmaxRegs = 88, kPfDecodeRegs = 56, kPfMmaRegs = 40;

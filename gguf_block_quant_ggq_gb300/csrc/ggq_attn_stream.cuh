@@ -35,10 +35,12 @@
 //
 // Measured (32 heads on 8 of 128 channels, Q8_0): one token of 4 sequences of 131072,
 // fp32: 204 us, 5.6 TB/s, 83% of the copy's rate; 64 ragged sequences of up to 4096,
-// bf16: 64 us, 4.9 TB/s (shares end together, but an item's start and join cost what 12
-// units do); one of 777, fp32: 11.6 us, all latency.  64 heads on 8 of 64 channels, Q4_0,
-// 33 of up to 16384, f16: 66 us, 2.6 TB/s, bound by instructions (half the bytes a
-// value, the same unpacking), as are 5 rows of 16 heads on 8 of 256 channels (86 us).
+// bf16: 63 us, 5.0 TB/s (shares end together, but an item's start and join cost what 12
+// units do); one of 777, fp32: 11.7 us, all latency.  64 heads on 8 of 64 channels, Q4_0,
+// 33 of up to 16384, f16: 66 us, 2.6 TB/s, bound by each warp's chain of product, maximum,
+// exponential and product at 12 warps an SM (issue slots 50% used: half the bytes a value,
+// the same unpacking); 5 rows of 16 heads on 8 of 256 channels: 86 us, the same at 8 warps
+// an SM and with spilled totals (36%).
 #pragma once
 #include <atomic>
 

@@ -441,8 +441,12 @@ ggq_status ggq_kv_load(ggq_ctx* ctx, const ggq_kv_cache* cache, int dtype, const
  * window).  For query head h (kv head h / (n_heads / n_kv_heads)):
  *   s_j = scale * q . k_j;  cap > 0: s_j = cap * tanh(s_j / cap);
  *   s_j += slope_h * (j - p);  out = sum_j softmax(s)_j v_j.
- * Scores, statistics and sums are fp32.  A row that sees nothing (p < 0) is
- * zeros; whatever unseen places hold never reaches an output.  Rows outside
+ * Scores, statistics and sums are fp32.  fp32 rows keep 22 bits of every operand.  Rows of
+ * 16 bits: calls of many rows, by a rule of cost on the call's sizes, round K to fp16 and V
+ * and the probabilities to the rows' type (fp16 2^-11 of each at most, bf16 2^-8), others
+ * the probabilities to fp16 only; so a row's last bits depend on what it is called with.
+ * A row that sees nothing (p < 0) is zeros; whatever unseen places hold never reaches an
+ * output.  Rows outside
  * q_start's ranges are not written.  A page id outside the cache counts as page 0,
  * lengths above max_len and ranges above max_q are cut; each is reported by
  * ggq_sync_status.  Scratch: ggq_reserve_attention. */
