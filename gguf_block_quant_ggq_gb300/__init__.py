@@ -21,6 +21,8 @@ TYPE = {"Q4_0": 2, "Q8_0": 8, "Q8_1": 9, "Q2_K": 10, "Q3_K": 11, "Q4_K": 12, "Q5
 OP = {"quantize_act": 0, "dequant": 1, "mul_mat_vec": 2, "moe": 3, "kv_cache": 4}
 DTYPE = {"float32": 0, "float16": 1, "bfloat16": 30}  # ggq_dtype of activations
 SCORING = {"softmax": 0, "sigmoid": 1}
+GATE_ACT = {"none": 0, "sigmoid": 1}
+ROTARY_LAYOUT = {"half": 0, "pairs": 1}
 STATUS = {0: "GGQ_OK", 1: "GGQ_ERR_INVALID_ARG", 2: "GGQ_ERR_SHAPE", 3: "GGQ_ERR_UNSUPPORTED", 4: "GGQ_ERR_ARCH",
           5: "GGQ_ERR_CUDA", 6: "GGQ_ERR_CAPACITY", 7: "GGQ_ERR_CAPTURE_ALLOC", 8: "GGQ_ERR_DEVICE"}
 BLOCK_ELEMS = {"Q4_0": 32, "Q8_0": 32, "MXFP4": 32, "Q8_1": 32, "Q4_K": 256, "Q5_K": 256, "Q6_K": 256, "Q8_K": 256,
@@ -57,6 +59,13 @@ SIGNATURES = {
     "ggq_attention": (_I32, [_P, _P, _P, _P]),
     "ggq_reserve_attention": (_I32, [_P, _P]),
     "ggq_moe_route": (_I32, [_P, _P, _I32, _P, _I64, _I64, _P, _P, _P]),
+    "ggq_norm": (_I32, [_P, _P, _P]),
+    "ggq_rotary_table": (_I32, [_P, _P, _I64, _I64, _P, _P]),
+    "ggq_rotate": (_I32, [_P, _P, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P]),
+    "ggq_kv_append": (_I32, [_P, _P, _P, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P,
+                             _I64, _P]),
+    "ggq_adapt": (_I32, [_P, _P, _P, _P]),
+    "ggq_logprobs": (_I32, [_P, _P, _P]),
     "ggq_block_dots_qa": (_I32, [_P, _I32, _I32, _P, _I64, _I64, _P, _I64, _P, _P]),
 }
 
@@ -96,10 +105,56 @@ class ggq_router(ctypes.Structure):
                                               "normalize")] + [("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
 
 
-# ggq_attn and ggq_router as packed fields: filled in place for every call
+class ggq_norm_args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("gate_act", ctypes.c_int32), ("T", ctypes.c_int64), ("H", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_token", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("residual_token", ctypes.c_int64), ("gate", ctypes.c_void_p), ("gate_token", ctypes.c_int64),
+                ("gate_channel", ctypes.c_int64), ("total", ctypes.c_void_p), ("total_token", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_token", ctypes.c_int64), ("packed", ctypes.c_void_p),
+                ("packed_type", ctypes.c_int32), ("norms", ctypes.c_int32), ("after", ctypes.c_void_p),
+                ("before", ctypes.c_void_p), ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
+class ggq_rotary(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_positions", ctypes.c_int64), ("turn", ctypes.c_int32),
+                ("first", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
+class ggq_rotary_spec(ctypes.Structure):
+    _fields_ = [("turn", ctypes.c_int32), ("base", ctypes.c_double), ("factors", ctypes.c_void_p), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_int64), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class ggq_adapters(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("max_rank", ctypes.c_int32), ("n", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("N", ctypes.c_int64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("ranks", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
+class ggq_adapt_args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("T", ctypes.c_int64), ("n_seqs", ctypes.c_int64), ("x", ctypes.c_void_p),
+                ("x_token", ctypes.c_int64), ("y", ctypes.c_void_p), ("y_token", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_token", ctypes.c_int64), ("ids", ctypes.c_void_p), ("q_start", ctypes.c_void_p)]
+
+
+class ggq_logprobs_args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("top_k", ctypes.c_int32), ("T", ctypes.c_int64), ("V", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("row", ctypes.c_int64), ("tokens", ctypes.c_void_p), ("given", ctypes.c_int64),
+                ("logprobs", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("top", ctypes.c_void_p),
+                ("scale", ctypes.c_float)]
+
+
+# the calls' argument structures as packed fields: filled in place for every call
 _ATTN = struct.Struct("@iiqqPqqPqqPqPPqqffqP")
 _ROUTER = struct.Struct("@iiiiiifP")
+_NORM = struct.Struct("@iiqqPqPqPqqPqPqPiiPPfff4x")
+_ROTARY = struct.Struct("@Pqiii4x")
+_ADAPT = struct.Struct("@iqqPqPqPqPP")
+_LOGPROBS = struct.Struct("@iiqqPqPqPPPPf4x")
 assert _ATTN.size == ctypes.sizeof(ggq_attn) and _ROUTER.size == ctypes.sizeof(ggq_router)
+assert _NORM.size == ctypes.sizeof(ggq_norm_args) and _ROTARY.size == ctypes.sizeof(ggq_rotary)
+assert _ADAPT.size == ctypes.sizeof(ggq_adapt_args) and _LOGPROBS.size == ctypes.sizeof(ggq_logprobs_args)
 
 
 class GGQError(RuntimeError):
@@ -190,6 +245,38 @@ class KVCache:
         self.ref = ctypes.addressof(self.struct)
 
 
+class Adapters:
+    """Low-rank adapters of one projection: a [n][rank][K] and b [n][N][rank] of one 16-bit type on the context's
+    device, ranks int32 [n] (default: all), scales float32 [n] (default: 1).  Ranks that are no multiple of 8 are
+    laid out anew with the next one, once; else the tensors are used as they are."""
+
+    def __init__(self, ctx, a, b, ranks=None, scales=None):
+        torch = ctx._torch
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] or a.dtype is not b.dtype:
+            raise ValueError(f"expected banks [n, rank, K] and [n, N, rank] of one type, got {tuple(a.shape)} {a.dtype} and "
+                             f"{tuple(b.shape)} {b.dtype}")
+        if a.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"expected float16 or bfloat16 adapters, got {a.dtype}")
+        n, rank, K = a.shape
+        for t in (a, b):
+            ctx._vec(t, t.dtype)
+        if rank % 8:
+            wide = (rank + 7) // 8 * 8
+            na, nb = a.new_zeros((n, wide, K)), b.new_zeros((n, b.shape[1], wide))
+            na[:, :rank], nb[:, :, :rank] = a, b
+            a, b = na, nb
+            if ranks is None:
+                ranks = torch.full((n,), rank, dtype=torch.int32, device=a.device)
+        for t, name in ((ranks, "ranks"), (scales, "scales")):
+            if t is not None and t.numel() != n:
+                raise ValueError(f"expected {n} {name}, got {t.numel()}")
+        self.a, self.b, self.ranks, self.scales = a, b, ranks, scales
+        self.K, self.N, self.device = K, b.shape[1], ctx.device
+        self.struct = ggq_adapters(ctx._codes[a.dtype], a.shape[1], n, K, self.N, a.data_ptr(), b.data_ptr(),
+                                   ctx._vec(ranks, ctx._i32), ctx._vec(scales, ctx._f32))
+        self.ref = ctypes.addressof(self.struct)
+
+
 class Context:
     """A libggq context on one CUDA device; methods take torch CUDA tensors and
     enqueue on torch's current stream (or the given one)."""
@@ -207,6 +294,8 @@ class Context:
         self._router_args = ctypes.create_string_buffer(_ROUTER.size)
         self._attn_at, self._router_at = ctypes.addressof(self._attn_args), ctypes.addressof(self._router_args)
         self._attn_ready = False
+        self._step_args = ctypes.create_string_buffer(max(_NORM.size, _ROTARY.size, _ADAPT.size, _LOGPROBS.size))
+        self._step_at = ctypes.addressof(self._step_args)
         h = ctypes.c_void_p()
         st = load().ggq_create(ctypes.byref(h), device)
         if st != 0:
@@ -263,6 +352,23 @@ class Context:
         if one != 1:
             raise ValueError("the channels of a head have to be dense")
         return t.data_ptr(), code, token, head
+
+    def _mat(self, t, rows, cols, dtype):
+        """(address, row stride) of a [rows][cols] tensor of `dtype` on the context's device whose rows are dense."""
+        if t.dtype is not dtype or t.get_device() != self.device:
+            raise ValueError(f"expected a {dtype} tensor on cuda:{self.device}, got {t.dtype} on {t.device}")
+        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+            raise ValueError(f"expected a [{rows}, {cols}] tensor, got {tuple(t.shape)}")
+        row, one = t.stride()
+        if one != 1 and cols > 1:
+            raise ValueError("the channels of a row have to be dense")
+        return t.data_ptr(), row
+
+    def _code(self, dtype):
+        code = self._codes.get(dtype)
+        if code is None:
+            raise ValueError(f"expected a float32, float16 or bfloat16 tensor, got {dtype}")
+        return code
 
     def _own(self, cache):
         if cache.device != self.device:
@@ -445,6 +551,213 @@ class Context:
         if st:
             self._check(st)
         return ids, weights
+
+    def norm(self, x, before=None, after=None, gate=None, gate_act: str = "none", scale: float = 1.0, residual=None,
+             eps: float = 1e-6, offset: float = 0.0, act: str | None = None, out=None, total=None, packed=None, stream=None):
+        """(out, total): total = residual + scale * act(gate) * norm(x; after), out = norm(total; before), of x [tokens][H].
+
+        before, after: float32 weights [H] (offset is added to them), True for a norm without weights, None for
+        no norm.  gate: of x's type, [tokens][H], [H], or [tokens][1].  total is made where there is a residual, or
+        nothing else to return; given buffers are always written.  act: out is packed Q8_K, Q8_1 or Q8_0 rows
+        (uint8, into `packed` where given) that the products take; a given `out` then gets the float rows too."""
+        if x.dim() != 2:
+            raise ValueError(f"expected a [tokens, channels] tensor, got {tuple(x.shape)}")
+        n, H = x.shape
+        dtype = x.dtype
+        code = self._code(dtype)
+        norms = (after is not None) + 2 * (before is not None)
+        if before is None and (out is not None or act is not None):
+            raise ValueError("out and packed rows are the norm of the total: `before` is needed")
+        if before is not None and out is None and act is None:
+            out = self._empty((n, H), dtype, stream)
+        if total is None and (residual is not None or before is None):
+            total = self._empty((n, H), dtype, stream)
+        pp = 0
+        if act is not None:
+            width = row_bytes(act, H)
+            if packed is None:
+                packed = self._empty((n, width), self._torch.uint8, stream)
+            elif tuple(packed.shape) != (n, width):
+                raise ValueError(f"expected a [{n}, {width}] output, got {tuple(packed.shape)}")
+            pp = self._vec(packed, self._torch.uint8)
+        xp, xt = self._mat(x, n, H, dtype)
+        rp, rt = self._mat(residual, n, H, dtype) if residual is not None else (0, 0)
+        tp, tt = self._mat(total, n, H, dtype) if total is not None else (0, 0)
+        op, ot = self._mat(out, n, H, dtype) if out is not None else (0, 0)
+        gp = gt = gc = 0
+        if gate is not None:
+            if gate.dim() == 1 and gate.shape[0] == H:
+                gp, gc = self._vec(gate, dtype), 1
+            elif gate.dim() == 2 and gate.shape[1] == 1 and H != 1:
+                gp, gt = self._mat(gate, n, 1, dtype)
+            else:
+                gp, gt = self._mat(gate, n, H, dtype)
+                gc = 1
+        ap = bp = 0
+        if after is not None and after is not True:
+            ap = self._weights(after, H)
+        if before is not None and before is not True:
+            bp = self._weights(before, H)
+        _NORM.pack_into(self._step_args, 0, code, GATE_ACT[gate_act], n, H, xp, xt, rp, rt, gp, gt, gc, tp, tt, op, ot, pp,
+                        TYPE[act] if act else 0, norms, ap, bp, scale, eps, offset)
+        st = _lib.ggq_norm(self.handle, self._step_at, self._stream(stream))
+        if st:
+            self._check(st)
+        return (packed if act is not None else out), total
+
+    def _weights(self, w, n):
+        if w.numel() != n:
+            raise ValueError(f"expected {n} weights, got {w.numel()}")
+        return self._vec(w, self._f32)
+
+    def rotary_table(self, n: int, turn: int, base: float = 10000.0, factor: float = 1.0, factors=None, original_len: int = 0,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0, magnitude: float = 1.0, first: int = 0, out=None,
+                     stream=None):
+        """float32 [n][turn / 2][2]: cosine and sine of positions first .. first + n - 1.  factors: the frequencies'
+        divisors (a sequence of numbers, or a CPU tensor), e.g. a model file's rope_freqs; factor and original_len slow
+        positions down for long contexts (see ggq_rotary_table)."""
+        if out is None:
+            out = self._empty((n, turn // 2, 2), self._f32, stream)
+        elif tuple(out.shape) != (n, turn // 2, 2):
+            raise ValueError(f"expected a [{n}, {turn // 2}, 2] output, got {tuple(out.shape)}")
+        host = None
+        if factors is not None:
+            host = (ctypes.c_float * len(factors))(*[float(f) for f in factors])
+            if 2 * len(host) != turn:
+                raise ValueError(f"expected {turn // 2} factors, got {len(host)}")
+        spec = ggq_rotary_spec(turn, base, ctypes.cast(host, ctypes.c_void_p) if host is not None else None, factor,
+                               original_len, beta_fast, beta_slow, magnitude)
+        self._check(load().ggq_rotary_table(self.handle, ctypes.byref(spec), first, n, self._vec(out, self._f32),
+                                            self._stream(stream)))
+        return out
+
+    def _rotary(self, table, positions, n, layout, first):
+        """Fills the rotation's arguments; the address of the positions."""
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError(f"expected a [positions, turn / 2, 2] table, got {tuple(table.shape)}")
+        if positions.numel() != n:
+            raise ValueError(f"expected {n} positions, got {positions.numel()}")
+        _ROTARY.pack_into(self._step_args, 0, self._vec(table, self._f32), table.shape[0], 2 * table.shape[1], first,
+                          ROTARY_LAYOUT[layout])
+        return self._vec(positions, self._i32)
+
+    def rotate(self, x, table, positions, layout: str = "half", first: int = 0, out=None, stream=None):
+        """x [tokens][heads][D] with the channels from `first` on turned by the table's rows at positions (int32
+        [tokens]); out may be x."""
+        if x.dim() != 3:
+            raise ValueError(f"expected a [tokens, heads, channels] tensor, got {tuple(x.shape)}")
+        n, heads, dim = x.shape
+        if out is None:
+            out = self._empty((n, heads, dim), x.dtype, stream)
+        xp, code, xt, xh = self._rows(x, heads, dim)
+        op, ocode, ot, oh = self._rows(out, heads, dim)
+        if ocode != code or out.shape[0] != n:
+            raise ValueError("out has to have x's type and tokens")
+        pos = self._rotary(table, positions, n, layout, first)
+        st = _lib.ggq_rotate(self.handle, self._step_at, code, heads, dim, xp, xt, xh, op, ot, oh, pos, n, self._stream(stream))
+        if st:
+            self._check(st)
+        return out
+
+    def kv_append(self, cache: KVCache, k, v, slots, table, positions, layout: str = "half", first: int = 0, q=None, q_out=None,
+                  stream=None):
+        """kv_store of k turned by positions, and of v; q [tokens][heads][D], where given, is turned into q_out (which
+        may be q) and returned."""
+        self._own(cache)
+        n, dim = slots.numel(), cache.head_dim
+        kp, code, kt, kh = self._rows(k, cache.n_kv_heads, dim)
+        vp, vcode, vt, vh = self._rows(v, cache.n_kv_heads, dim)
+        if code != vcode or k.shape[0] != n or v.shape[0] != n:
+            raise ValueError("k, v and slots have to agree in type and tokens")
+        heads = qp = qt = qh = op = ot = oh = 0
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError(f"expected a [tokens, heads, {dim}] tensor, got {tuple(q.shape)}")
+            heads = q.shape[1]
+            if q_out is None:
+                q_out = self._empty((n, heads, dim), q.dtype, stream)
+            qp, qcode, qt, qh = self._rows(q, heads, dim)
+            op, ocode, ot, oh = self._rows(q_out, heads, dim)
+            if qcode != code or ocode != code or q.shape[0] != n or q_out.shape[0] != n:
+                raise ValueError("q and q_out have to agree with k in type and tokens")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        pos = self._rotary(table, positions, n, layout, first)
+        st = _lib.ggq_kv_append(self.handle, cache.ref, self._step_at, code, heads, qp, qt, qh, op, ot, oh, kp, kt, kh, vp, vt,
+                                vh, self._vec(slots, self._i64), pos, n, self._stream(stream))
+        if st:
+            self._check(st)
+        return q_out
+
+    def adapters(self, a, b, ranks=None, scales=None) -> Adapters:
+        """Low-rank adapters of one projection (see Adapters)."""
+        return Adapters(self, a, b, ranks, scales)
+
+    def adapt(self, adapters: Adapters, x, y, ids, q_start=None, out=None, stream=None):
+        """y + scale * B (A x) with each sequence's adapter: x [tokens][K], y [tokens][N] (the projection's output), ids
+        int32 [sequences] (negative: none), q_start int32 [sequences + 1] unless every sequence has one token; out may
+        be y."""
+        self._own(adapters)
+        n, seqs = x.shape[0], ids.numel()
+        dtype = x.dtype
+        code = self._code(dtype)
+        if out is None:
+            out = self._empty((n, adapters.N), dtype, stream)
+        if q_start is None and n != seqs:
+            raise ValueError(f"{n} rows for {seqs} sequences: q_start is needed")
+        if q_start is not None and q_start.numel() != seqs + 1:
+            raise ValueError(f"{seqs} sequences need {seqs + 1} row starts")
+        xp, xt = self._mat(x, n, adapters.K, dtype)
+        yp, yt = self._mat(y, n, adapters.N, dtype)
+        op, ot = self._mat(out, n, adapters.N, dtype)
+        _ADAPT.pack_into(self._step_args, 0, code, n, seqs, xp, xt, yp, yt, op, ot, self._vec(ids, self._i32),
+                         self._vec(q_start, self._i32))
+        st = _lib.ggq_adapt(self.handle, adapters.ref, self._step_at, self._stream(stream))
+        if st:
+            self._check(st)
+        return out
+
+    def logprobs(self, logits, tokens=None, top_k: int = 0, scale: float = 1.0, logprobs=None, entropy=None, ids=None, top=None,
+                 stream=None):
+        """(logprobs [tokens][given] of the given ids, entropy [tokens], ids [tokens][top_k], top [tokens][top_k]) of
+        softmax(scale * logits), logits [tokens][V]; tokens int32 [tokens][given] or [tokens].  What is not asked for
+        is None."""
+        if logits.dim() != 2:
+            raise ValueError(f"expected [tokens, vocabulary] logits, got {tuple(logits.shape)}")
+        n, V = logits.shape
+        code = self._code(logits.dtype)
+        given = 0
+        if tokens is not None:
+            if tokens.dim() not in (1, 2) or tokens.shape[0] != n:
+                raise ValueError(f"expected [{n}, given] tokens, got {tuple(tokens.shape)}")
+            given = 1 if tokens.dim() == 1 else tokens.shape[1]
+            if logprobs is None:
+                logprobs = self._empty(tuple(tokens.shape), self._f32, stream)
+            elif logprobs.numel() != n * given:
+                raise ValueError(f"expected {n * given} log probabilities, got {logprobs.numel()}")
+        elif logprobs is not None:
+            raise ValueError("log probabilities of which tokens?")
+        if entropy is None:
+            entropy = self._empty((n,), self._f32, stream)
+        elif entropy.numel() != n:
+            raise ValueError(f"expected {n} entropies, got {entropy.numel()}")
+        if top_k:
+            if ids is None:
+                ids = self._empty((n, top_k), self._i32, stream)
+            if top is None:
+                top = self._empty((n, top_k), self._f32, stream)
+            if ids.numel() != n * top_k or top.numel() != n * top_k:
+                raise ValueError(f"expected [{n}, {top_k}] alternatives, got {tuple(ids.shape)} and {tuple(top.shape)}")
+        elif ids is not None or top is not None:
+            raise ValueError("alternatives without top_k")
+        lp, row = self._mat(logits, n, V, logits.dtype)
+        _LOGPROBS.pack_into(self._step_args, 0, code, top_k, n, V, lp, row, self._vec(tokens, self._i32), given,
+                            self._vec(logprobs, self._f32), self._vec(entropy, self._f32), self._vec(ids, self._i32),
+                            self._vec(top, self._f32), scale)
+        st = _lib.ggq_logprobs(self.handle, self._step_at, self._stream(stream))
+        if st:
+            self._check(st)
+        return logprobs, entropy, ids, top
 
     def moe_weights(self, gate_fmt, gate, up_fmt, up, down_fmt, down):
         return ggq_moe_weights(TYPE[gate_fmt], TYPE[up_fmt], TYPE[down_fmt], _ptr(gate), _ptr(up), _ptr(down))

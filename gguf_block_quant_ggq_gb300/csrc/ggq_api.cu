@@ -1135,7 +1135,10 @@ ggq_status ggq_sync_status(ggq_ctx* c, void* stream) {
                     : word == DEV_ERR_BAD_IDS ? "a routed expert id out of range"
                     : word == DEV_ERR_BAD_PLACE
                         ? "a slot, page id, length or row range outside the key/value cache or its bounds"
-                                              : "unknown device error");
+                    : word == DEV_ERR_BAD_POSITION ? "a position outside the rotary table"
+                    : word == DEV_ERR_BAD_ADAPTER  ? "an adapter id or row range outside its bounds"
+                    : word == DEV_ERR_BAD_TOKEN    ? "a token id outside the vocabulary"
+                                                   : "unknown device error");
     }
     return GGQ_OK;
 }

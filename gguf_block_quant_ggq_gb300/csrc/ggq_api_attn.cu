@@ -9,15 +9,12 @@
 #include "ggq_attn.cuh"
 #include "ggq_ctx.h"
 #include "ggq_kv.cuh"
+#include "ggq_rope.cuh"
 #include "ggq_route.cuh"
 
 using namespace ggq;
 
 namespace {
-
-// 0 f32, 1 f16, 2 bf16, -1 otherwise
-int dtype_of(int t) { return t == GGQ_F32 ? 0 : t == GGQ_F16 ? 1 : t == GGQ_BF16 ? 2 : -1; }
-int64_t dtype_bytes(int d) { return d == 0 ? 4 : 2; }
 
 bool kv_type_ok(int t) { return t == GGQ_TYPE_Q8_0 || t == GGQ_TYPE_Q4_0; }
 
@@ -47,12 +44,6 @@ size_t attn_scratch(const ggq_ctx* c) {
     return align_up(2 * ctas * attn_part_floats(256) * sizeof(float));
 }
 
-// Rows of four elements at a time: the pointer and the strides of axes of more than one element are multiples of 4.
-bool rows4(const void* p, int64_t tokens, int64_t token, int heads, int64_t head, int dtype) {
-    return (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(4 * dtype_bytes(dtype))) == 0 &&
-           (tokens < 2 || token % 4 == 0) && (heads < 2 || head % 4 == 0);
-}
-
 ggq_status kv_params(ggq_ctx* c, const ggq_kv_cache* kv, int dtype, const void* k, int64_t k_token, int64_t k_head,
                      const void* v, int64_t v_token, int64_t v_head, const int64_t* slots, int64_t T, const char* op,
                      KvParams* p, int* dt) {
@@ -71,6 +62,45 @@ ggq_status kv_params(ggq_ctx* c, const ggq_kv_cache* kv, int dtype, const void* 
                   {static_cast<uint8_t*>(kv->v), kv->v_type == GGQ_TYPE_Q4_0},
                   kv->n_kv_heads, kv->head_dim, kv->page_size, page_magic(kv->page_size), 1, kv->n_pages * kv->page_size,
                   slots, T, k, v, k_token, k_head, v_token, v_head, &c->ctrl->err};
+    return GGQ_OK;
+}
+
+// The rotation of heads of D channels; positions are the caller's to set.
+ggq_status rotary_params(ggq_ctx* c, const ggq_rotary* r, int D, const int32_t* positions, const char* op, Rotary* out) {
+    if (!r) return fail(c, GGQ_ERR_INVALID_ARG, "%s: null rotary", op);
+    if (r->layout != GGQ_ROTARY_HALF && r->layout != GGQ_ROTARY_PAIRS)
+        return fail(c, GGQ_ERR_UNSUPPORTED, "%s: rotary layout %d; supported: halves, pairs", op, r->layout);
+    if (D < 1 || D > kRotaryMaxDim || r->turn < 2 || r->turn % 2 || r->first < 0 || r->turn > D || r->first > D - r->turn ||
+        r->n_positions < 1)
+        return fail(c, GGQ_ERR_SHAPE, "%s: %d channels from %d on turned in heads of %d (at most %d), %lld positions", op, r->turn,
+                    r->first, D, kRotaryMaxDim, static_cast<long long>(r->n_positions));
+    if (!r->table || !positions) return fail(c, GGQ_ERR_INVALID_ARG, "%s: null table or positions", op);
+    if (!multiple_of(r->table, 8) || !multiple_of(positions, 4))
+        return fail(c, GGQ_ERR_INVALID_ARG, "%s: the table must be 8-byte and positions 4-byte aligned", op);
+    *out = Rotary{reinterpret_cast<const float2*>(r->table), r->n_positions, positions, r->turn / 2, r->first,
+                  r->layout == GGQ_ROTARY_PAIRS, 0};
+    return GGQ_OK;
+}
+
+ggq_status rotate_params(ggq_ctx* c, int dtype, int n_heads, int D, const void* x, int64_t x_token, int64_t x_head, void* out,
+                         int64_t out_token, int64_t out_head, int64_t T, const char* op, RotateParams* p) {
+    if (n_heads < 0 || n_heads > 16384) return fail(c, GGQ_ERR_SHAPE, "%s: %d heads", op, n_heads);
+    if (n_heads > 0 && (!x || !out)) return fail(c, GGQ_ERR_INVALID_ARG, "%s: null pointer", op);
+    if (!multiple_of(x, dtype_bytes(dtype)) || !multiple_of(out, dtype_bytes(dtype)))
+        return fail(c, GGQ_ERR_INVALID_ARG, "%s: misaligned heads", op);
+    p->x = x;
+    p->out = out;
+    p->x_token = x_token;
+    p->x_head = x_head;
+    p->out_token = out_token;
+    p->out_head = out_head;
+    p->T = T;
+    p->H = n_heads;
+    p->D = D;
+    p->in_place = x == out;
+    p->err = &c->ctrl->err;
+    if (p->in_place && ((T > 1 && x_token != out_token) || (n_heads > 1 && x_head != out_head)))
+        return fail(c, GGQ_ERR_INVALID_ARG, "%s: heads turned in place have one stride", op);
     return GGQ_OK;
 }
 
@@ -96,6 +126,45 @@ ggq_status ggq_kv_store(ggq_ctx* c, const ggq_kv_cache* kv, int dtype, const voi
     if (s != GGQ_OK) return s;
     const cudaError_t e = launch_kv_store(p, dt, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GGQ_OK : cuda_fail(c, e, "kv_store launch");
+}
+
+ggq_status ggq_rotate(ggq_ctx* c, const ggq_rotary* r, int dtype, int n_heads, int D, const void* x, int64_t x_token,
+                      int64_t x_head, void* out, int64_t out_token, int64_t out_head, const int32_t* positions, int64_t T,
+                      void* stream) {
+    DeviceScope scope;
+    ggq_status s = check_ctx(c, scope);
+    if (s != GGQ_OK) return s;
+    const int dt = dtype_of(dtype);
+    if (dt < 0) return fail(c, GGQ_ERR_UNSUPPORTED, "rotate: element type %d; supported: F32, F16, BF16", dtype);
+    if (T < 0 || T > INT32_MAX) return fail(c, GGQ_ERR_SHAPE, "rotate: T=%lld", static_cast<long long>(T));
+    if (T == 0 || n_heads == 0) return GGQ_OK;
+    RotateParams p{};
+    s = rotary_params(c, r, D, positions, "rotate", &p.r);
+    if (s == GGQ_OK) s = rotate_params(c, dt, n_heads, D, x, x_token, x_head, out, out_token, out_head, T, "rotate", &p);
+    if (s != GGQ_OK) return s;
+    const cudaError_t e = launch_rotate(p, dt, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GGQ_OK : cuda_fail(c, e, "rotate launch");
+}
+
+ggq_status ggq_kv_append(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_rotary* r, int dtype, int n_heads, const void* q,
+                         int64_t q_token, int64_t q_head, void* q_out, int64_t q_out_token, int64_t q_out_head, const void* k,
+                         int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head, const int64_t* slots,
+                         const int32_t* positions, int64_t T, void* stream) {
+    DeviceScope scope;
+    ggq_status s = check_ctx(c, scope);
+    if (s != GGQ_OK) return s;
+    KvParams p{};
+    int dt = -1;
+    s = kv_params(c, kv, dtype, k, k_token, k_head, v, v_token, v_head, slots, T, "kv_append", &p, &dt);
+    if (s != GGQ_OK || T == 0) return s;
+    RotateParams rot{};
+    s = rotary_params(c, r, kv->head_dim, positions, "kv_append", &rot.r);
+    if (s == GGQ_OK)
+        s = rotate_params(c, dt, n_heads, kv->head_dim, q, q_token, q_head, q_out, q_out_token, q_out_head, T, "kv_append", &rot);
+    if (s != GGQ_OK) return s;
+    rot.slots = slots;
+    const cudaError_t e = launch_kv_append(p, rot, dt, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GGQ_OK : cuda_fail(c, e, "kv_append launch");
 }
 
 ggq_status ggq_kv_load(ggq_ctx* c, const ggq_kv_cache* kv, int dtype, const int64_t* slots, int64_t T, void* k,

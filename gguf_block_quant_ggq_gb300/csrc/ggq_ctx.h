@@ -45,6 +45,16 @@ namespace ggq {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Element types of activations: 0 f32, 1 f16, 2 bf16, -1 otherwise
+inline int dtype_of(int t) { return t == GGQ_F32 ? 0 : t == GGQ_F16 ? 1 : t == GGQ_BF16 ? 2 : -1; }
+inline int64_t dtype_bytes(int d) { return d == 0 ? 4 : 2; }
+inline bool multiple_of(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
+
+// Rows of four elements at a time: the pointer and the strides of axes of more than one element are multiples of 4.
+inline bool rows4(const void* p, int64_t tokens, int64_t token, int heads, int64_t head, int dtype) {
+    return multiple_of(p, 4 * dtype_bytes(dtype)) && (tokens < 2 || token % 4 == 0) && (heads < 2 || head % 4 == 0);
+}
+
 inline ggq_status fail(ggq_ctx* c, ggq_status s, const char* fmt, ...) {
     char buf[512];
     va_list ap;

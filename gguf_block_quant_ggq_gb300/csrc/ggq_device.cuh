@@ -33,8 +33,18 @@ __host__ __device__ constexpr int fmt_coefs(int f) { return (f == F_Q4_K || f ==
 __host__ __device__ constexpr bool fmt_q81(int f) { return f == F_Q4_0; }
 
 // Device error word values (a bounded wait ran out; a routed expert id out of range;
-// a slot, page, length or row range outside the key/value cache or its bounds).
-enum : int { DEV_OK = 0, DEV_ERR_TIMEOUT = 1, DEV_ERR_BAD_IDS = 2, DEV_ERR_BAD_PLACE = 3 };
+// a slot, page, length or row range outside the key/value cache or its bounds; a position
+// outside the rotary table; an adapter or row range outside its bounds; a token id outside
+// the vocabulary).
+enum : int {
+    DEV_OK = 0,
+    DEV_ERR_TIMEOUT = 1,
+    DEV_ERR_BAD_IDS = 2,
+    DEV_ERR_BAD_PLACE = 3,
+    DEV_ERR_BAD_POSITION = 4,
+    DEV_ERR_BAD_ADAPTER = 5,
+    DEV_ERR_BAD_TOKEN = 6
+};
 
 // ---------------------------------------------------------------- PTX
 

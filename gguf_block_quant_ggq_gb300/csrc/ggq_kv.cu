@@ -14,9 +14,12 @@
 // 128 channels by instructions (bf16 to Q8_0 and Q4_0: 33 us, issue slots 65% used, where
 // its 94 MB take 14; back to fp32: 30 us, its 161 MB 24), at a decode step's by latency (5
 // us for both).
+#include <algorithm>
+
 #include "ggq_device.cuh"
 #include "ggq_internal.h"
 #include "ggq_kv.cuh"
+#include "ggq_rope.cuh"
 
 namespace ggq {
 
@@ -151,6 +154,11 @@ struct Window {
     int single[kKvRows], zero[kKvRows];
 };
 
+// Table entries of the positions of rows row0 .. row0 + 31 (keys that are turned on the way).
+struct WindowTurns {
+    const float2* entry[2 * kKvRows];
+};
+
 // Blob of a slot: division by the groups of a page as a multiplication that is at most one too large.
 __device__ __forceinline__ int64_t blob_of(const KvParams& p, int64_t slot, int h) {
     const int g = static_cast<int>(slot >> 4), gpp = p.page >> 4;
@@ -163,14 +171,19 @@ __device__ __forceinline__ int64_t blob_of(const KvParams& p, int64_t slot, int 
     return (static_cast<int64_t>(pg) * p.H + h) * gpp + place;
 }
 
-template <bool STORE, bool Q4, bool V, int D, typename T>
-__device__ __forceinline__ void kv_rows(const KvParams& p, const Window& w, int64_t row0, T* rows, int64_t head, int64_t st,
+// turns: null, or of keys that are turned before they are quantized
+template <bool STORE, bool Q4, bool V, int D, bool TURN = false, typename T>
+__device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, const WindowTurns* turns, const Window& w, int64_t row0, T* rows, int64_t head, int64_t st,
                                         uint8_t* pool, int h0, int h1, uint8_t* image) {
     // threads a row (eight channels each; four to read back) and rows at once
     constexpr int kChannels = STORE ? 8 : 4, kPer = D / kChannels, kAtOnce = kKvThreads / kPer, kPasses = kKvRows / kAtOnce;
     constexpr int kBlob = kv_blob_bytes(Q4, D), kLines = kBlob / 16, kQuants = kv_quant_bytes(Q4, D) / 16;
     const int tid = threadIdx.x, r_at = tid / kPer, c = kChannels * (tid % kPer);
-    const auto load8 = [&](const T* src, float (&x)[8]) {
+    const auto load8 = [&](const T* src, int row, float (&x)[8]) {  // row: from row0
+        if constexpr (TURN) {
+            turned8(*turn, src - c, c, turns->entry[row], x);
+            return;
+        }
         const float4 a = ld4(src), b = ld4(src + 4);
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     };
@@ -185,7 +198,7 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Window& w, int6
             if constexpr (STORE) {
                 float x[kPasses][8];
 #pragma unroll
-                for (int k = 0; k < kPasses; ++k) load8(first + k * kAtOnce * st, x[k]);
+                for (int k = 0; k < kPasses; ++k) load8(first + k * kAtOnce * st, w.start + r_at + k * kAtOnce, x[k]);
                 if (h > h0) __syncthreads();  // the blob before this one has left
 #pragma unroll
                 for (int k = 0; k < kPasses; ++k) {
@@ -214,7 +227,7 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Window& w, int6
             if constexpr (STORE) {
                 float x[8];
                 uint32_t q[8];
-                load8(at, x);
+                load8(at, row, x);
                 const float d = quantize8<Q4>(x, q);
                 put8<false, Q4, V, D>(blob, static_cast<int>(slot & 15), c, q, d, there);
             } else if (there) {
@@ -227,17 +240,13 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Window& w, int6
     }
 }
 
-// Grid: (windows of 16 rows, 2 * parts of the heads); the first half of the parts: keys.
-template <bool STORE, int D, typename T>
-__global__ void __launch_bounds__(kKvThreads) k_kv(const __grid_constant__ KvParams p) {
-    pdl_launch_dependents();
-    pdl_wait();
-    __shared__ __align__(16) uint8_t image[D / 32 * 592 + D];
-    __shared__ Window w;
+// The rows of a window: the slots around it, the group that begins in it, single rows and those without a place.
+// False: no row.
+__device__ __forceinline__ bool kv_window(const KvParams& p, Window& w, int64_t& row0) {
     const int tid = threadIdx.x;
     const int64_t s0 = p.slots[0];
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kKvRows - (s0 > 0 ? s0 & 15 : 0);
-    if (row0 >= p.n) return;
+    row0 = static_cast<int64_t>(blockIdx.x) * kKvRows - (s0 > 0 ? s0 & 15 : 0);
+    if (row0 >= p.n) return false;
     if (tid < 3 * kKvRows) {
         const int64_t r = row0 - (kKvRows - 1) + tid;
         w.slot[tid] = r >= 0 && r < p.n ? p.slots[r] : -1;
@@ -276,24 +285,86 @@ __global__ void __launch_bounds__(kKvThreads) k_kv(const __grid_constant__ KvPar
         }
     }
     __syncthreads();
+    return true;
+}
+
+// Grid: (windows of 16 rows, 2 * parts of the heads); the first half of the parts: keys.
+template <bool STORE, int D, typename T>
+__global__ void __launch_bounds__(kKvThreads) k_kv(const __grid_constant__ KvParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ __align__(16) uint8_t image[D / 32 * 592 + D];
+    __shared__ Window w;
+    int64_t row0;
+    if (!kv_window(p, w, row0)) return;
     const int parts = static_cast<int>(gridDim.y) >> 1;
     const bool is_v = static_cast<int>(blockIdx.y) >= parts;
     const int part = static_cast<int>(blockIdx.y) - (is_v ? parts : 0);
     const int h0 = part * p.heads_at_once, h1 = min(p.H, h0 + p.heads_at_once);
     T* const rows = static_cast<T*>(const_cast<void*>(is_v ? p.vs : p.ks));
     if (is_v) {
-        if (p.v.q4) kv_rows<STORE, true, true, D, T>(p, w, row0, rows, p.v_head, p.v_token, p.v.p, h0, h1, image);
-        else kv_rows<STORE, false, true, D, T>(p, w, row0, rows, p.v_head, p.v_token, p.v.p, h0, h1, image);
+        if (p.v.q4) kv_rows<STORE, true, true, D>(p, nullptr, nullptr, w, row0, rows, p.v_head, p.v_token, p.v.p, h0, h1, image);
+        else kv_rows<STORE, false, true, D>(p, nullptr, nullptr, w, row0, rows, p.v_head, p.v_token, p.v.p, h0, h1, image);
     } else {
-        if (p.k.q4) kv_rows<STORE, true, false, D, T>(p, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image);
-        else kv_rows<STORE, false, false, D, T>(p, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image);
+        if (p.k.q4) kv_rows<STORE, true, false, D>(p, nullptr, nullptr, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image);
+        else kv_rows<STORE, false, false, D>(p, nullptr, nullptr, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image);
     }
 }
 
+struct AppendParams {
+    KvParams kv;
+    RotateParams q;  // of the keys too: the rotation; no heads: no queries
+    int kv_parts;
+};
+
+// The same with the keys turned before they are quantized, and the queries turned in further parts of the grid
+// (y: parts of the keys' heads, of the values', of the queries').
+template <int D, int QV, typename T>
+__global__ void __launch_bounds__(kKvThreads) k_kv_append(const __grid_constant__ AppendParams a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ __align__(16) uint8_t image[D / 32 * 592 + D];
+    __shared__ Window w;
+    __shared__ WindowTurns turns;
+    const KvParams& p = a.kv;
+    const int part = static_cast<int>(blockIdx.y);
+    if (part >= 2 * a.kv_parts) {
+        const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kKvRows;
+        const int h0 = (part - 2 * a.kv_parts) * a.q.heads_at_once;
+        rotate_tile<QV, T>(a.q, r0, min(p.n, r0 + kKvRows), h0, min(a.q.H, h0 + a.q.heads_at_once));
+        return;
+    }
+    int64_t row0;
+    if (!kv_window(p, w, row0)) return;
+    const bool is_v = part >= a.kv_parts;
+    const int h0 = (part - (is_v ? a.kv_parts : 0)) * p.heads_at_once, h1 = min(p.H, h0 + p.heads_at_once);
+    if (is_v) {
+        T* const rows = static_cast<T*>(const_cast<void*>(p.vs));
+        if (p.v.q4) kv_rows<true, true, true, D>(p, nullptr, nullptr, w, row0, rows, p.v_head, p.v_token, p.v.p, h0, h1, image);
+        else kv_rows<true, false, true, D>(p, nullptr, nullptr, w, row0, rows, p.v_head, p.v_token, p.v.p, h0, h1, image);
+        return;
+    }
+    if (threadIdx.x < 2 * kKvRows) {
+        const int64_t row = row0 + threadIdx.x;
+        const float2* entry = nullptr;
+        if (row >= 0 && row < p.n) {
+            entry = rotary_row(a.q.r, row);
+            if (!entry && p.slots[row] >= 0) set_error(p.err, DEV_ERR_BAD_POSITION);
+        }
+        turns.entry[threadIdx.x] = entry;
+    }
+    __syncthreads();
+    T* const rows = static_cast<T*>(const_cast<void*>(p.ks));
+    if (p.k.q4) kv_rows<true, true, false, D, true>(p, &a.q.r, &turns, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image);
+    else kv_rows<true, false, false, D, true>(p, &a.q.r, &turns, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image);
+}
+
+// the first window may begin up to 15 rows before the first row
+int64_t kv_windows(const KvParams& p) { return (p.n + 2 * kKvRows - 2) / kKvRows; }
+
 template <bool STORE, int D>
 cudaError_t launch_kv_dim(KvParams p, int dtype, cudaStream_t s) {
-    // the first window may begin up to 15 rows before the first row
-    const int64_t windows = (p.n + 2 * kKvRows - 2) / kKvRows;
+    const int64_t windows = kv_windows(p);
     // One head a CTA while the CTAs are few, four once there are plenty (store and load
     // of 8 heads of 128 channels, us, one / four: 64 tokens 5.0 / 8.8, 1024 7.8 / 13.5,
     // 4096 18.6 / 19.5, 16384 70 / 60).
@@ -313,9 +384,42 @@ cudaError_t launch_kv(const KvParams& p, int dtype, cudaStream_t s) {
     return launch_kv_dim<STORE, 256>(p, dtype, s);
 }
 
+template <int D, typename T>
+cudaError_t launch_append_type(AppendParams a, int v, cudaStream_t s) {
+    const int64_t windows = kv_windows(a.kv);
+    a.kv.heads_at_once = windows * 2 * a.kv.H < 8192 ? 1 : 4;
+    a.kv_parts = (a.kv.H + a.kv.heads_at_once - 1) / a.kv.heads_at_once;
+    a.q.units = a.q.r.half / v + ((D - 2 * a.q.r.half) / v + 1) / 2;
+    a.q.heads_at_once = std::max(1, std::min(a.q.H, windows < 64 ? 1 : 8));
+    const int q_parts = (a.q.H + a.q.heads_at_once - 1) / a.q.heads_at_once;
+    const dim3 grid(static_cast<unsigned>(windows), static_cast<unsigned>(2 * a.kv_parts + q_parts));
+    if (v == 8) {
+        if constexpr (sizeof(T) == 2) return launch_pdl(k_kv_append<D, 8, T>, grid, dim3(kKvThreads), 0, s, a);
+    }
+    if (v == 4) return launch_pdl(k_kv_append<D, 4, T>, grid, dim3(kKvThreads), 0, s, a);
+    return launch_pdl(k_kv_append<D, 1, T>, grid, dim3(kKvThreads), 0, s, a);
+}
+
+template <int D>
+cudaError_t launch_append_dim(const AppendParams& a, int dtype, int v, cudaStream_t s) {
+    if (dtype == 0) return launch_append_type<D, float>(a, v, s);
+    if (dtype == 1) return launch_append_type<D, __half>(a, v, s);
+    return launch_append_type<D, __nv_bfloat16>(a, v, s);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_store(const KvParams& p, int dtype, cudaStream_t s) { return launch_kv<true>(p, dtype, s); }
 cudaError_t launch_kv_load(const KvParams& p, int dtype, cudaStream_t s) { return launch_kv<false>(p, dtype, s); }
+
+cudaError_t launch_kv_append(const KvParams& kv, const RotateParams& q, int dtype, cudaStream_t s) {
+    if (kv.n == 0) return cudaSuccess;
+    AppendParams a{kv, q, 0};
+    a.q.r.whole = q.r.half % 8 == 0 && q.r.first % 8 == 0 && aligned_to(q.r.table, 16);
+    const int v = q.H ? rotate_vector(q, dtype) : dtype == 0 ? 4 : 8;
+    if (kv.D == 64) return launch_append_dim<64>(a, dtype, v, s);
+    if (kv.D == 128) return launch_append_dim<128>(a, dtype, v, s);
+    return launch_append_dim<256>(a, dtype, v, s);
+}
 
 }  // namespace ggq

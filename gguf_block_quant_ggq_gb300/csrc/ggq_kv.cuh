@@ -16,6 +16,8 @@ namespace ggq {
 
 constexpr int kBlobTokens = 16;
 
+inline bool aligned_to(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 __host__ __device__ constexpr int kv_quant_bytes(bool q4, int D) { return q4 ? 8 * D : 16 * D; }
 __host__ __device__ constexpr int kv_blob_bytes(bool q4, int D) { return kv_quant_bytes(q4, D) + D; }
 

@@ -1,0 +1,290 @@
+// ggq_norm.cu -- the norms before and after a block with its gate, scale and residual.
+//
+// Mathematics: t = residual + scale * act(gate) * N(x; after), out = N(t; before), with
+// N(v; w) = v / sqrt(mean v^2 + eps) * (w + offset); either norm, the gate and the residual
+// may be missing.  Statistics and everything between input and output are fp32; t is rounded
+// to the rows' type when it is stored, the second norm takes it unrounded.
+//
+// Each value is read once and stays in registers between the two sums, so the bound is memory
+// at many rows and the chain launch - load - sum - sum - store at few.  A row of up to 256
+// channels is one warp's, wider ones a CTA's with eight channels a thread: the widest loads
+// there are for 16-bit rows, and the eight that a packed block of 32 or 256 channels gives a
+// lane, so that the packed forms are quantized from registers.
+#include <algorithm>
+
+#include "ggq_device.cuh"
+#include "ggq_internal.h"
+#include "ggq_kv.cuh"
+#include "ggq_norm.cuh"
+
+namespace ggq {
+
+namespace {
+
+__device__ __forceinline__ void ld8(const float* p, float (&x)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void ld8(const __half* p, float (&x)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void ld8(const __nv_bfloat16* p, float (&x)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void st8(float* p, const float (&x)[8]) {
+    st4(p, make_float4(x[0], x[1], x[2], x[3]));
+    st4(p + 4, make_float4(x[4], x[5], x[6], x[7]));
+}
+template <typename T2, typename F>
+__device__ __forceinline__ void st8_pairs(void* p, const float (&x)[8], F pack) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const T2 h = pack(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void st8(__half* p, const float (&x)[8]) {
+    st8_pairs<__half2>(p, x, [](float a, float b) { return __floats2half2_rn(a, b); });
+}
+__device__ __forceinline__ void st8(__nv_bfloat16* p, const float (&x)[8]) {
+    st8_pairs<__nv_bfloat162>(p, x, [](float a, float b) { return __floats2bfloat162_rn(a, b); });
+}
+
+// Eight channels as they come from memory: asked for a row ahead
+template <typename T>
+struct Raw {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void to(float (&x)[8]) const { ld8(reinterpret_cast<const T*>(u), x); }
+};
+
+// Eight consecutive channels of a row as four of a block of 32 (the quantizers of ggq_quantize_act).
+// All lanes take part; `there`: this one writes.
+template <bool SUMS>
+__device__ __forceinline__ void quant32_regs(const float (&x)[8], uint8_t* block, bool there) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    float id;
+    const float d = quant_scale(m, &id);
+    int q[8], s = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += q[i] = quant_one(x[i], id);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (!there) return;
+    const int at = 8 * (threadIdx.x & 3);
+    uint16_t* const to = reinterpret_cast<uint16_t*>(block + (SUMS ? 4 : 2) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = static_cast<uint16_t>((q[2 * i] & 0xFF) | (q[2 * i + 1] & 0xFF) << 8);
+    if (at == 0) {
+        reinterpret_cast<__half*>(block)[0] = __float2half_rn(d);
+        if (SUMS) reinterpret_cast<__half*>(block)[1] = __float2half_rn(__fmul_rn(d, static_cast<float>(s)));
+    }
+}
+
+// The sum of v over the row's threads.  `part`: a slot for each warp, not in use by another sum.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if constexpr (!WARP) {
+        const int warps = static_cast<int>(blockDim.x) >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    }
+    return v;
+}
+
+// NU: groups of eight channels a thread holds.  THREADS: at most so many a CTA; a row is a CTA's, with 128 a
+// warp's.  VEC: rows of whole aligned groups; otherwise a thread's channels lie a row's threads apart and are
+// loaded one by one.  Rows of up to 4096 channels (EARLY): a CTA keeps the weights in registers, goes through
+// rows and asks for the next one before it sums; wider ones have no registers for it, and enough threads to
+// hide the waits.
+template <typename T, int NU, int THREADS, bool VEC, bool EARLY = (THREADS <= 512)>
+__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1024 / THREADS) k_norm(const __grid_constant__ NormParams p) {
+    static_assert(!EARLY || NU == 1, "rows a thread keeps whole");
+    constexpr bool WARP = THREADS == 128;
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ float part[4][32];
+    const int threads = WARP ? 32 : static_cast<int>(blockDim.x), at = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x;
+    int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP && t >= p.T) return;
+    const auto first = [&](int u) { return VEC ? (u * threads + at) * 8 : u * 8 * threads + at; };
+    const auto channel = [&](int u, int i) { return first(u) + (VEC ? i : i * threads); };
+    // channels behind the row's end are zeros
+    const auto load = [&](const auto* row, int u, float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+        if constexpr (VEC) {
+            if (first(u) < p.H) ld8(row + first(u), x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (channel(u, i) < p.H) x[i] = ld1(row + channel(u, i));
+        }
+    };
+    const auto weight = [&](const float* w, int u, float (&x)[8]) {  // w + offset
+        load(w, u, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], p.offset);
+    };
+    const auto store = [&](T* row, int u, const float (&x)[8]) {
+        if constexpr (VEC) {
+            if (first(u) < p.H) st8(row + first(u), x);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (channel(u, i) < p.H) st1(row + channel(u, i), x[i]);
+        }
+    };
+    const T* const xs = static_cast<const T*>(p.x);
+    const T* const rs = static_cast<const T*>(p.residual);
+    const T* const gs = static_cast<const T*>(p.gate);
+    const bool gates = p.gate && p.gate_channel;
+    constexpr bool AHEAD = EARLY && VEC;
+    Raw<T> next_x{}, next_r{}, next_g{};
+    const auto ask = [&](int64_t row) {
+        if (first(0) >= p.H) return;
+        next_x.load(xs + row * p.x_token + first(0));
+        if (p.residual) next_r.load(rs + row * p.residual_token + first(0));
+        if (gates) next_g.load(gs + row * p.gate_token + first(0));
+    };
+    const auto act = [&](float x) { return p.sigmoid ? __frcp_rn(1.0f + expf(-x)) : x; };
+    float wa[8], wb[8];
+    if constexpr (AHEAD) ask(t);
+    if constexpr (EARLY) {
+        if (p.after_w) weight(p.after_w, 0, wa);
+        if (p.before_w) weight(p.before_w, 0, wb);
+    }
+    for (int turn = 0; t < p.T; t += step, turn ^= 2) {
+        float v[NU][8], r[8], g[8];
+        if constexpr (AHEAD) {
+            next_x.to(v[0]);
+            next_r.to(r);
+            next_g.to(g);
+        } else {
+#pragma unroll
+            for (int u = 0; u < NU; ++u) load(xs + t * p.x_token, u, v[u]);
+        }
+        float g1 = p.gate && !p.gate_channel ? ld1(gs + t * p.gate_token) : 1.0f;
+        if constexpr (AHEAD)
+            if (t + step < p.T) ask(t + step);
+        const auto inverse = [&](float* parts) {
+            float s = 0.0f;
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(v[u][i], v[u][i], s);
+            return rsqrtf(fmaf(row_sum<WARP>(s, parts), p.inv_width, p.eps));
+        };
+        const float inv_after = p.after ? inverse(part[turn]) : 1.0f;
+        if (p.gate && !p.gate_channel) g1 = act(g1);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            if constexpr (!AHEAD) {
+                if (p.residual) load(rs + t * p.residual_token, u, r);
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+                if (gates) load(gs + t * p.gate_token, u, g);
+            }
+            if constexpr (!EARLY)
+                if (p.after_w) weight(p.after_w, u, wa);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float y = v[u][i];
+                if (p.after) y *= inv_after;
+                if (p.after_w) y *= wa[i];
+                y *= gates ? act(g[i]) : g1;
+                v[u][i] = fmaf(y, p.scale, r[i]);
+            }
+            if (p.total) store(static_cast<T*>(p.total) + t * p.total_token, u, v[u]);
+        }
+        if (!p.before) continue;
+        const float inv = inverse(part[turn + 1]);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            if constexpr (!EARLY)
+                if (p.before_w) weight(p.before_w, u, wb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[u][i] *= inv;
+                if (p.before_w) v[u][i] *= wb[i];
+            }
+            if (p.out) store(static_cast<T*>(p.out) + t * p.out_token, u, v[u]);
+            if constexpr (VEC) {
+                if (p.packed) {
+                    const int c = first(u);
+                    const int64_t row = t * p.H;
+                    if (p.form == NORM_Q8_K) {  // whole warps: the width is a multiple of 256
+                        if (c < p.H) warp_quant_q8k_regs(v[u], p.packed + ((row + c) >> 8) * 292, threadIdx.x & 31);
+                    } else if (p.form == NORM_Q8_1) {
+                        quant32_regs<true>(v[u], p.packed + ((row + c) >> 5) * 36, c < p.H);
+                    } else {
+                        quant32_regs<false>(v[u], p.packed + ((row + c) >> 5) * 34, c < p.H);
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <typename T, bool VEC>
+cudaError_t launch(const NormParams& p, cudaStream_t s) {
+    // as many CTAs as the SMs hold at once go through the rows
+    const auto grid = [&](int64_t ctas, int threads) { return dim3(static_cast<unsigned>(std::min<int64_t>(ctas, 152 * (1024 / threads)))); };
+    if (p.H <= 256) return launch_pdl(k_norm<T, 1, 128, VEC>, grid((p.T + 3) / 4, 128), dim3(128), 0, s, p);
+    const auto threads = [&](int units) { return (p.H + 256 * units - 1) / (256 * units) * 32; };
+    if (p.H <= 4096) return launch_pdl(k_norm<T, 1, 512, VEC>, grid(p.T, threads(1)), dim3(threads(1)), 0, s, p);
+    const dim3 rows(static_cast<unsigned>(p.T));
+    if (p.H <= 8192) return launch_pdl(k_norm<T, 1, 1024, VEC>, rows, dim3(threads(1)), 0, s, p);
+    if (p.H <= 16384) return launch_pdl(k_norm<T, 2, 1024, VEC>, rows, dim3(threads(2)), 0, s, p);
+    return launch_pdl(k_norm<T, 4, 1024, VEC>, rows, dim3(threads(4)), 0, s, p);
+}
+
+template <typename T>
+cudaError_t launch_type(const NormParams& p, bool whole, cudaStream_t s) {
+    return whole ? launch<T, true>(p, s) : launch<T, false>(p, s);
+}
+
+}  // namespace
+
+bool norm_whole(const NormParams& p, int dtype) {
+    const int size = dtype == 0 ? 4 : 2;
+    const auto whole = [&](const void* at, int64_t stride) { return aligned_to(at, 16) && (!at || p.T < 2 || stride * size % 16 == 0); };
+    return p.H % 8 == 0 && whole(p.x, p.x_token) && whole(p.residual, p.residual_token) &&
+           (!p.gate || !p.gate_channel || whole(p.gate, p.gate_token)) && whole(p.total, p.total_token) && whole(p.out, p.out_token) &&
+           aligned_to(p.after_w, 16) && aligned_to(p.before_w, 16);
+}
+
+cudaError_t launch_norm(const NormParams& p, int dtype, cudaStream_t s) {
+    if (p.T == 0) return cudaSuccess;
+    const bool whole = norm_whole(p, dtype);
+    if (dtype == 0) return launch_type<float>(p, whole, s);
+    if (dtype == 1) return launch_type<__half>(p, whole, s);
+    return launch_type<__nv_bfloat16>(p, whole, s);
+}
+
+}  // namespace ggq

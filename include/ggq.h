@@ -91,8 +91,8 @@ typedef enum ggq_op {
     GGQ_OP_KV_CACHE = 4      /* ggq_kv_store / ggq_kv_load / ggq_attention: w = K format, act = V format */
 } ggq_op;
 
-/* Element types of activations in ggq_kv_store, ggq_kv_load, ggq_attention and
- * ggq_moe_route (the GGUF type ids of the unquantized types). */
+/* Element types of activations in ggq_kv_store, ggq_kv_load, ggq_attention, ggq_moe_route and the
+ * calls behind them (the GGUF type ids of the unquantized types). */
 typedef enum ggq_dtype { GGQ_F32 = 0, GGQ_F16 = 1, GGQ_BF16 = 30 } ggq_dtype;
 
 typedef struct ggq_ctx ggq_ctx;
@@ -201,6 +201,92 @@ typedef struct ggq_router {
     float scale;        /* then multiplied by this                               */
     const float* bias;  /* [E] added to the score for the choice only, or NULL   */
 } ggq_router;
+
+/* Arguments of ggq_norm (device pointers; strides in elements, channels dense). */
+typedef enum ggq_gate_act { GGQ_GATE_LINEAR = 0, GGQ_GATE_SIGMOID = 1 } ggq_gate_act;
+typedef struct ggq_norm_args {
+    int32_t dtype;          /* ggq_dtype of x, residual, gate, total and out             */
+    int32_t gate_act;       /* ggq_gate_act                                              */
+    int64_t T, H;           /* tokens and channels, H <= 32768                           */
+    const void* x;          /* [T][H] the block's output                                 */
+    int64_t x_token;
+    const void* residual;   /* [T][H] or NULL                                            */
+    int64_t residual_token;
+    const void* gate;       /* [T][H], one row for all tokens (gate_token = 0) or one value a token (gate_channel = 0); or NULL */
+    int64_t gate_token, gate_channel;
+    void* total;            /* [T][H] or NULL; may be x or residual, with its stride     */
+    int64_t total_token;
+    void* out;              /* [T][H] or NULL; may be x or residual, with its stride     */
+    int64_t out_token;
+    void* packed;           /* [T][H / blk] blocks of packed_type, or NULL               */
+    int32_t packed_type;    /* GGQ_TYPE_Q8_K, Q8_1 or Q8_0 (ignored without packed)      */
+    int32_t norms;          /* 1: the norm of x, 2: the norm of the total, 3: both       */
+    const float* after;     /* [H] weights of the norm of x, or NULL: ones               */
+    const float* before;    /* [H] weights of the norm of the total, or NULL: ones       */
+    float scale, eps, offset;
+} ggq_norm_args;
+
+/* Which channels of a head a rotation turns, and by what (see ggq_rotate). */
+typedef enum ggq_rotary_layout { GGQ_ROTARY_HALF = 0, GGQ_ROTARY_PAIRS = 1 } ggq_rotary_layout;
+typedef struct ggq_rotary {
+    const float* table;     /* [n_positions][turn / 2][2] cosine and sine (ggq_rotary_table), 8-byte aligned */
+    int64_t n_positions;
+    int32_t turn;           /* turned channels of a head, even, at most 1024             */
+    int32_t first;          /* the first of them                                         */
+    int32_t layout;         /* ggq_rotary_layout                                         */
+} ggq_rotary;
+
+/* The angles of ggq_rotary_table (host memory). */
+typedef struct ggq_rotary_spec {
+    int32_t turn;           /* as in ggq_rotary                                          */
+    double base;            /* frequency of pair j: base^(-2 j / turn)                   */
+    const float* factors;   /* [turn / 2], HOST memory: frequency j is divided by factors[j]; or NULL */
+    double factor;          /* slows positions down: 1 none                              */
+    int64_t original_len;   /* > 0: factor applies by channel (see ggq_rotary_table); 0: to all */
+    double beta_fast, beta_slow;
+    double magnitude;       /* of cosine and sine                                        */
+} ggq_rotary_spec;
+
+/* Adapters of one projection (device pointers): adapter i is B_i A_i, of rank ranks[i]. */
+typedef struct ggq_adapters {
+    int32_t dtype;          /* GGQ_F16 or GGQ_BF16: type of a and b                      */
+    int32_t max_rank;       /* R, a multiple of 8, at most 256                           */
+    int64_t n, K, N;        /* adapters, inputs (a multiple of 8), outputs               */
+    const void* a;          /* [n][R][K], 16-byte aligned                                */
+    const void* b;          /* [n][N][R], 16-byte aligned                                */
+    const int32_t* ranks;   /* [n] or NULL: R.  What stands behind a rank is not used    */
+    const float* scales;    /* [n] or NULL: 1                                            */
+} ggq_adapters;
+
+/* Arguments of ggq_adapt (device pointers; strides in elements, channels dense). */
+typedef struct ggq_adapt_args {
+    int32_t dtype;          /* ggq_dtype of x, y and out                                 */
+    int64_t T, n_seqs;
+    const void* x;          /* [T][K]                                                    */
+    int64_t x_token;
+    const void* y;          /* [T][N] the projection's output                            */
+    int64_t y_token;
+    void* out;              /* [T][N]; may be y, with its stride                         */
+    int64_t out_token;
+    const int32_t* ids;     /* [n_seqs] adapter of each sequence, negative: none         */
+    const int32_t* q_start; /* [n_seqs + 1] first row of each sequence; NULL: row b is sequence b's */
+} ggq_adapt_args;
+
+/* Arguments of ggq_logprobs (device pointers). */
+typedef struct ggq_logprobs_args {
+    int32_t dtype;          /* ggq_dtype of the logits                                   */
+    int32_t top_k;          /* alternatives a token, 0..32, at most V                    */
+    int64_t T, V;           /* tokens, vocabulary (at most 2^30)                         */
+    const void* logits;     /* [T][V]                                                    */
+    int64_t row;            /* stride of the logits' rows in elements                    */
+    const int32_t* tokens;  /* [T][given] token ids, or NULL (given = 0)                 */
+    int64_t given;
+    float* logprobs;        /* [T][given]                                                */
+    float* entropy;         /* [T] or NULL                                               */
+    int32_t* ids;           /* [T][top_k]                                                */
+    float* top;             /* [T][top_k]                                                */
+    float scale;            /* of the logits (1 / temperature), > 0                      */
+} ggq_logprobs_args;
 
 /* Create a context on `device` (a CUDA ordinal).  Refuses any device that is
  * not compute capability 10.3 with GGQ_ERR_ARCH: the kernels are built for
@@ -474,6 +560,71 @@ ggq_status ggq_moe_route(ggq_ctx* ctx, const ggq_router* router, int dtype, cons
  * page, length or row range was out of bounds; the word is cleared in the stream's
  * order), or GGQ_ERR_CUDA.  No other stream is waited for. */
 ggq_status ggq_sync_status(ggq_ctx* ctx, void* stream);
+
+/* The norms before and after a block, with its gate, scale and residual:
+ *   u = norms & 1 ? x * r(x) * (after + offset) : x
+ *   total = residual + scale * act(gate) * u        (each part that is missing left out)
+ *   out = total * r(total) * (before + offset)      (norms & 2)
+ * with r(v) = 1 / sqrt(mean(v^2) + eps) over the token's channels and act the identity or the
+ * sigmoid.  Everything in between is fp32 (a sum of squares that leaves fp32, at magnitudes
+ * about 2^63, gives zeros); total is rounded where it is stored, its norm takes it unrounded.
+ * `total` without norms & 2 and `out` or `packed` with it are what a call needs at least.
+ * packed: the same rows as out, before their rounding to dtype, as blocks that
+ * ggq_mul_mat_vec_q, _qa and ggq_moe_experts_q take, byte for byte what ggq_quantize_act makes
+ * of fp32 rows; H a multiple of the block, and rows, weights and outputs that start at 16 bytes
+ * (block rows at 4, Q8_0 at 2).  Needs no scratch. */
+ggq_status ggq_norm(ggq_ctx* ctx, const ggq_norm_args* args, void* stream);
+
+/* Cosines and sines of positions first .. first + n - 1 (0 <= first, first + n <= 2^31):
+ * table[i][j] = magnitude * (cos, sin)((first + i) * f_j), f_j = base^(-2 j / turn) / factors[j].
+ * factor > 1 reaches positions beyond the trained ones: with original_len = 0 every f_j is
+ * divided by it; with original_len = L those of channels that turn fewer than beta_slow times
+ * within L positions are, those that turn more than beta_fast times are not, and in between the
+ * two are mixed by the channel's place (YaRN: Peng et al. 2023, section 3.2; its magnitude
+ * 0.1 ln(factor) + 1 is the caller's to give).  Angles are off by 2^-27 of a turn up to position 2^26
+ * (beyond it by the frequencies' own rounding to fp64).
+ * spec and its factors are host memory, read before the call returns.  Needs no scratch. */
+ggq_status ggq_rotary_table(ggq_ctx* ctx, const ggq_rotary_spec* spec, int64_t first, int64_t n, float* table, void* stream);
+
+/* Rotate heads by their tokens' positions [T]: x [T][n_heads][D] of dtype (strides in elements, D
+ * dense, D <= 1024) to out.  Of a head's channels the `turn` from `first` on are turned in pairs,
+ * j and j + turn / 2 of them (HALF) or 2 j and 2 j + 1 (PAIRS): (a, b) -> (a c - b s, a s + b c)
+ * with (c, s) = table[position][j], in fp32, each product and the sum rounded; the others are
+ * copied.  out may be x with its strides, and must not overlap it otherwise.  A position outside
+ * the table turns nothing and is reported by ggq_sync_status.  Needs no scratch. */
+ggq_status ggq_rotate(ggq_ctx* ctx, const ggq_rotary* rotary, int dtype, int n_heads, int D, const void* x,
+                      int64_t x_token, int64_t x_head, void* out, int64_t out_token, int64_t out_head,
+                      const int32_t* positions, int64_t T, void* stream);
+
+/* ggq_kv_store with the rotation on the way: keys are turned as ggq_rotate turns them and
+ * quantized unrounded (fp32), values are stored as they are, and the n_heads query heads q are
+ * turned into q_out (which may be q; n_heads = 0: none).  The rotation's head is the cache's.
+ * Rows of every token whose slot is negative (padding) are not stored; their queries are turned,
+ * and their positions are not reported.  Other arguments, checks and reports as in ggq_kv_store
+ * and ggq_rotate. */
+ggq_status ggq_kv_append(ggq_ctx* ctx, const ggq_kv_cache* cache, const ggq_rotary* rotary, int dtype, int n_heads,
+                         const void* q, int64_t q_token, int64_t q_head, void* q_out, int64_t q_out_token,
+                         int64_t q_out_head, const void* k, int64_t k_token, int64_t k_head, const void* v,
+                         int64_t v_token, int64_t v_head, const int64_t* slots, const int32_t* positions, int64_t T,
+                         void* stream);
+
+/* Low-rank adapters beside a projection: out[t] = y[t] + scales[a] * B_a (A_a x[t]) for the rows t
+ * of every sequence whose adapter is a; rows of sequences without one are copied (not touched where
+ * out is y), rows of no sequence are not written.  Products and sums are fp32 whatever the types:
+ * 16-bit rows and banks enter exactly, fp32 rows of sequences of more than eight rows with 22 bits
+ * or more.  x rows start at multiples of 4 elements (pointer and stride).  An adapter id outside 0 ..
+ * n - 1 counts as none, row ranges outside 0 .. T are cut; both are reported by ggq_sync_status.  No
+ * row may be of two sequences.  Needs no scratch. */
+ggq_status ggq_adapt(ggq_ctx* ctx, const ggq_adapters* adapters, const ggq_adapt_args* args, void* stream);
+
+/* Log probabilities of rows of logits, p = softmax(scale * logits):
+ *   logprobs[t][i] = log p(tokens[t][i]), entropy[t] = -sum p log p (nats), and the top_k largest
+ *   logits' ids, best first (ties to the lower id), with their log probabilities.
+ * Statistics are fp32.  A NaN logit counts as -inf; a row of -inf alone has log probabilities of
+ * -inf and entropy 0, one that holds +inf NaN for both (its ids are in order).  A negative token
+ * (padding) gets 0, one outside the vocabulary too and is reported by ggq_sync_status.  Needs no
+ * scratch. */
+ggq_status ggq_logprobs(ggq_ctx* ctx, const ggq_logprobs_args* args, void* stream);
 
 #ifdef __cplusplus
 }
