@@ -17,10 +17,11 @@
 // values as its elements of four k = 8 steps; the order of the outputs is free too: a lane's columns of four
 // 8-column tiles are eight neighbouring outputs, so y moves in whole vectors.
 //
-// 16-bit rows with banks of the same type: their own m16n8k16 instruction, operands exact.  Others: m16n8k8 of
-// tf32, in which either 16-bit type is exact and an fp32 value is two terms of 11 bits (off by 2^-22).  A x as an
-// operand of the second product is two terms, of 11 bits, or of 8 for bf16 rows and banks (off by 2^-17, a
-// hundredth of the output's rounding).
+// Operands of the matrix instruction (m16n8k16) are bf16 terms: an fp32 value is three of 8 bits each, an f16 value
+// two, exactly, and products of terms that lie below the last bit of the whole are left out.  f16 rows with f16 banks
+// enter as they are.  A x, fp32, is an operand of three terms for fp32 rows and of two for 16-bit ones (off by 2^-17,
+// a hundredth of the output's rounding).  (tf32 instructions, of which an fp32 value takes two, run at a third of the
+// rate a product on this part.)
 #include <algorithm>
 
 #include "ggq_adapt.cuh"
@@ -85,6 +86,7 @@ __device__ __forceinline__ void find_group(const AdaptParams& p, Group<ROWS>& sh
     if (tid == 0) sh.rows = 0;
     if (!p.q_start) {
         const int id = p.ids[c];
+        int next = tid < p.seqs ? p.ids[tid] : -1;
         if (tid == 0) sh.adapter = adapter_of(p, c);
         __syncthreads();
         if (sh.adapter < 0) {
@@ -97,7 +99,8 @@ __device__ __forceinline__ void find_group(const AdaptParams& p, Group<ROWS>& sh
         int first = -1;  // this row's place among them
         for (int64_t j0 = 0; j0 < p.seqs; j0 += kThreads) {
             const int64_t j = j0 + tid;
-            const bool mine = j < p.seqs && p.ids[j] == id;
+            const bool mine = next == id;
+            next = j + kThreads < p.seqs ? p.ids[j + kThreads] : -1;
             int total;
             const int at = static_cast<int>(seen) + block_scan<WARPS>(mine, sh.count, total);
             if (first < 0 && c < j0 + kThreads) {
@@ -159,9 +162,11 @@ __device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) 
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Waits until at most n groups of copies (0 .. 2) are under way.
+__device__ __forceinline__ void copies_wait(int n) {
+    if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 2;" ::: "memory");
 }
 
 template <bool BF16>
@@ -175,44 +180,31 @@ __device__ __forceinline__ void mma_k16(float (&d)[4], const uint32_t (&a)[4], u
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// x as two tf32 terms; infinities and NaN stay in the first
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-    const bool fine = fabsf(x) < INFINITY;
-    hi = fine ? __float_as_uint(x) & 0xffffe000u : __float_as_uint(x + x) & 0xffffe000u;
-    lo = fine ? __float_as_uint(__fsub_rn(x, __uint_as_float(hi))) & 0xffffe000u : 0u;
-}
-// a pair as two bf16 terms
-__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    const float ra = fabsf(a) < INFINITY ? a - __bfloat162float(h.x) : 0.0f, rb = fabsf(b) < INFINITY ? b - __bfloat162float(h.y) : 0.0f;
-    const __nv_bfloat162 l = __floats2bfloat162_rn(ra, rb);
-    hi = *reinterpret_cast<const uint32_t*>(&h);
-    lo = *reinterpret_cast<const uint32_t*>(&l);
-}
-
-// A word of two 16-bit values (f16, or bf16) as tf32.
-template <bool F16>
-__device__ __forceinline__ void pair_tf32(uint32_t w, uint32_t& a, uint32_t& b) {
-    if constexpr (F16) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        a = __float_as_uint(v.x), b = __float_as_uint(v.y);
-    } else {
-        a = w << 16, b = w & 0xFFFF0000u;
+// A pair of values as N pairs of bf16 terms.  What is not finite gives NaN.
+template <int N>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&t)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        t[i] = *reinterpret_cast<const uint32_t*>(&h);
+        a = __fsub_rn(a, __uint_as_float(t[i] << 16)), b = __fsub_rn(b, __uint_as_float(t[i] & 0xFFFF0000u));
     }
 }
-// Eight values of a bank row (1 f16, 2 bf16).
-__device__ __forceinline__ void bank_tf32(uint4 u, int bank, uint32_t (&f)[8]) {
+// Eight 16-bit values as N terms: bf16 ones as they are, f16 ones (F16) as two.
+template <bool F16, int N>
+__device__ __forceinline__ void terms_of(uint4 u, uint32_t (&f)[N][4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (bank == 1) pair_tf32<true>(w[i], f[2 * i], f[2 * i + 1]);
-        else pair_tf32<false>(w[i], f[2 * i], f[2 * i + 1]);
+        if constexpr (F16 && N > 1) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            uint32_t t[N];
+            split(v.x, v.y, t);
+#pragma unroll
+            for (int k = 0; k < N; ++k) f[k][i] = t[k];
+        } else {
+            f[0][i] = w[i];
+        }
     }
 }
 
@@ -235,33 +227,43 @@ __host__ __device__ constexpr int up32(int r) { return (r + 31) / 32 * 32; }
 
 // Of WARPS warps, 16 MT rows and banks of R ranks:
 //   sums [rows][up32(R) + 4]: this CTA's A x, which the others read;
-//   t    [rows / 16][up32(R) / 8][32 lanes][4]: the whole A x in the order of the matrix instruction's operand;
-//   part: sums of half of the parts of a block; ring: the blocks' copies, of the first product over part too.
+//   t    the whole A x as the matrix instruction's operand: [rows / 16][steps of 16][term][32 lanes][4 words],
+//        and before it the sums of half of the parts of a block;
+//   ring: the blocks' copies; those of the first product over t too.
 template <typename T, int WARPS, int MT>
 struct Plan {
-    int sums, t, part, stage1, stage2;
+    int sums, t, stage1, stage2, stages1, stages2;
+    static constexpr int kTerms = sizeof(T) == 4 ? 3 : 2;  // of A x
     static constexpr int kParts = WARPS / MT, kBlock = 32 * kParts, kRows = 16 * MT;
-    __host__ __device__ constexpr explicit Plan(int R) : sums(0), t(0), part(0), stage1(0), stage2(0) {
+    __host__ __device__ constexpr explicit Plan(int R, bool alone = false) : sums(0), t(0), stage1(0), stage2(0), stages1(0), stages2(0) {
         sums = kRows * (up32(R) + 4) * 4;
-        t = kRows * up32(R) * 4;
-        part = kParts / 2 * sums;
-        stage1 = kRows * row_pitch<T>(kBlock) + R * bank_pitch(2 * kBlock);
+        t = kRows * up32(R) * 2 * kTerms;
+        if (t < kParts / 2 * sums) t = kParts / 2 * sums;
+        stage1 = kRows * row_pitch<T>(kBlock) + up32(R) * bank_pitch(2 * kBlock);
         stage2 = kRows * row_pitch<T>(kBlock) + kBlock * bank_pitch(2 * R);
+        // two to four blocks at once, of two CTAs an SM if they fit (and there are so many: not `alone`)
+        const int half = kSmemLimit / 2 - 2048;
+        const int room = bytes(2, 2) <= half && !alone ? half : kSmemLimit - 2048;
+        for (stages1 = 2; stages1 < 4 && bytes(stages1 + 1, 2) <= room;) ++stages1;
+        for (stages2 = 2; stages2 < 4 && bytes(2, stages2 + 1) <= room;) ++stages2;
     }
-    __host__ __device__ constexpr int bytes(int stages) const {
-        const int one = stages * stage1, two = part + stages * stage2;
-        return sums + t + (one > two ? one : two);
+    __host__ __device__ constexpr int bytes(int s1, int s2) const {
+        const int one = s1 * stage1, two = t + s2 * stage2;
+        return sums + (one > two ? one : two);
     }
+    __host__ __device__ constexpr int bytes() const { return bytes(stages1, stages2); }
 };
 
 // ---------------------------------------------------------------- kernel
 
-// NATIVE: rows and banks of one 16-bit type.  NT: 8-column tiles of the rank.  MT: tiles of 16 rows.
-template <typename T, bool NATIVE, int NT, int WARPS, int MT>
+// BF: banks of bf16, else f16.  NT: 8-column tiles of the rank.  MT: tiles of 16 rows.
+template <typename T, bool BF, int NT, int WARPS, int MT>
 __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : 2) k_adapt(const __grid_constant__ AdaptParams p) {
-    constexpr bool PAIRS = NATIVE && __is_same(T, __nv_bfloat16);
     using P = Plan<T, WARPS, MT>;
-    constexpr int kStages = MT == 1 ? 2 : 3, kThreads = 32 * WARPS, kParts = P::kParts, kHalf = kParts / 2;
+    // terms: of x and A's bank, of A x and B's bank
+    constexpr bool F16 = __is_same(T, __half) && !BF;
+    constexpr int kX = sizeof(T) == 4 ? 3 : __is_same(T, __half) && BF ? 2 : 1, kA = BF || F16 ? 1 : 2, kT = P::kTerms, kB = BF ? 1 : 2;
+    constexpr int kThreads = 32 * WARPS, kParts = P::kParts, kHalf = kParts / 2;
     constexpr int kBlock = P::kBlock, kRows = P::kRows, kPitch = row_pitch<T>(kBlock), kBankPitch = bank_pitch(2 * kBlock);
     pdl_launch_dependents();
     pdl_wait();
@@ -288,55 +290,46 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : 2) k_adapt(const __gr
     const P plan(p.R);
     const int wide = up32(p.R), pitch = wide + 4;  // floats of a row of the sums
     float* const sums = reinterpret_cast<float*>(smem);
-    float* const t_frag = reinterpret_cast<float*>(smem + plan.sums);
-    uint8_t* const ring1 = smem + plan.sums + plan.t;
-    float* const parts_sums = reinterpret_cast<float*>(ring1);
-    uint8_t* const ring2 = ring1 + plan.part;
-    const int b_pitch = bank_pitch(2 * p.R);
+    uint32_t* const t_words = reinterpret_cast<uint32_t*>(smem + plan.sums);
+    float* const parts_sums = reinterpret_cast<float*>(smem + plan.sums);
+    uint8_t* const ring1 = smem + plan.sums;
+    uint8_t* const ring2 = ring1 + plan.t;
+    const int b_pitch = bank_pitch(2 * p.R), stages1 = p.stages1, stages2 = p.stages2;
 
-    // rows' values [c0, c1) of a block that starts at column c: copies of 16 bytes, or of four 16-bit values
-    const auto copy_rows = [&](const void* base, int64_t stride, bool wide16, int64_t c, int64_t c1, uint32_t to) {
+    // A thread's share of the copies of a block of rows: the same places of every block.  16 bytes, or four 16-bit values.
+    struct Share {
+        const T* at[4];  // null: no row
+        int column, per, step;
+        uint32_t to;
+    };
+    const auto share_of = [&](const void* base, int64_t stride, bool wide16, int64_t c0) {
         constexpr int kLog = kBlock == 64 ? 6 : kBlock == 128 ? 7 : 8;
-        const int log_per = wide16 && sizeof(T) == 2 ? 3 : 2, per = 1 << log_per, log_chunks = kLog - log_per;
-        for (int i = tid; i < kRows << log_chunks; i += kThreads) {
-            const int r = i >> log_chunks, e = (i & ((1 << log_chunks) - 1)) << log_per;
-            const int have = r < rows ? static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(per), c1 - c - e))) : 0;
-            const T* const src = have ? static_cast<const T*>(base) + sh.row[r] * stride + c + e : static_cast<const T*>(base);
-            const uint32_t dst = to + r * kPitch + e * static_cast<int>(sizeof(T));
-            if (per * sizeof(T) == 16) copy16(dst, src, have * static_cast<int>(sizeof(T)));
+        const int log_per = wide16 && sizeof(T) == 2 ? 3 : 2, log_chunks = kLog - log_per, r0 = tid >> log_chunks;
+        Share h;
+        h.per = 1 << log_per, h.step = kThreads >> log_chunks, h.column = (tid & ((1 << log_chunks) - 1)) << log_per;
+        h.to = r0 * kPitch + h.column * static_cast<int>(sizeof(T));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + i * h.step;
+            h.at[i] = r < rows ? static_cast<const T*>(base) + sh.row[r] * stride + c0 + h.column : nullptr;
+        }
+        return h;
+    };
+    // its copies of the block of columns b kBlock .. of `count` columns
+    const auto copy_rows = [&](const Share& h, int b, int count, uint32_t to) {
+        const int have = max(0, min(h.per, count - b * kBlock - h.column));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i * h.step >= kRows) break;
+            if (!h.at[i]) continue;  // (what stands in the place of a row that is not there stays in that row)
+            const void* const src = have ? static_cast<const void*>(h.at[i] + b * kBlock) : p.x;
+            const uint32_t dst = to + h.to + i * h.step * kPitch;
+            if (sizeof(T) == 4 || h.per == 8) copy16(dst, src, have * static_cast<int>(sizeof(T)));
             else copy8(dst, src, have * static_cast<int>(sizeof(T)));
         }
     };
-    const int blocks1 = (k1 - k0 + kBlock - 1) / kBlock, blocks2 = static_cast<int>((n1 - n0 + kBlock - 1) / kBlock);
-    const auto load1 = [&](int b) {
-        if (b < blocks1) {
-            const uint32_t to = smem_addr(ring1 + (b % kStages) * plan.stage1), bank = to + kRows * kPitch;
-            const int c = k0 + b * kBlock;
-            copy_rows(p.x, p.x_token, p.x_whole, c, k1, to);
-            constexpr int kChunks = kBlock / 8;
-            for (int i = tid; i < (rank + 7) / 8 * 8 * kChunks; i += kThreads) {
-                const int r = i / kChunks, k = c + i % kChunks * 8;
-                const bool there = r < rank && k < k1;
-                copy16(bank + r * kBankPitch + i % kChunks * 16, there ? bank_a + static_cast<int64_t>(r) * p.K + k : bank_a, there ? 16 : 0);
-            }
-        }
-        copies_end();
-    };
-    const auto load2 = [&](int b) {
-        if (b < blocks2) {
-            const uint32_t to = smem_addr(ring2 + (b % kStages) * plan.stage2), bank = to + kRows * kPitch;
-            const int64_t c = n0 + static_cast<int64_t>(b) * kBlock;
-            if (p.y_whole) copy_rows(p.y, p.y_token, p.y_whole == 2, c, n1, to);
-            const int chunks = (rank + 7) / 8, log_chunks = 32 - __clz(chunks - 1);  // (of a power of two)
-            for (int i = tid; i < kBlock << log_chunks; i += kThreads) {
-                const int r = i >> log_chunks, o = i & ((1 << log_chunks) - 1);
-                if (o >= chunks) continue;
-                const bool there = c + r < n1;
-                copy16(bank + r * b_pitch + 16 * o, there ? bank_b + (c + r) * p.R + 8 * o : bank_b, there ? 16 : 0);
-            }
-        }
-        copies_end();
-    };
+    const int inputs = k1 - k0, outputs = static_cast<int>(n1 - n0);
+    const int blocks1 = (inputs + kBlock - 1) / kBlock, blocks2 = (outputs + kBlock - 1) / kBlock;
 
     const int m = warp % MT, sub = warp / MT, r_lo = 16 * m + g, r_hi = r_lo + 8;  // this warp's rows and part of a block
     const bool busy = 16 * m < rows;
@@ -344,62 +337,101 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : 2) k_adapt(const __gr
     // A x of this CTA's inputs
     float acc[NT][4] = {};
     const int nt = (rank + 7) / 8;
-#pragma unroll
-    for (int b = 0; b < kStages - 1; ++b) load1(b);
-    for (int b = 0; b < blocks1; ++b) {
-        copies_wait<kStages - 2>();
-        __syncthreads();
-        load1(b + kStages - 1);
-        if (!busy) continue;
-        const uint8_t* const stage = ring1 + (b % kStages) * plan.stage1;
-        const uint8_t* const bank = stage + kRows * kPitch + g * kBankPitch + 64 * sub + 16 * tq;
-        const T* const x_lo = reinterpret_cast<const T*>(stage + r_lo * kPitch) + 32 * sub + 8 * tq;
-        const T* const x_hi = reinterpret_cast<const T*>(stage + r_hi * kPitch) + 32 * sub + 8 * tq;
-        if constexpr (NATIVE) {
-            const uint4 lo = *reinterpret_cast<const uint4*>(x_lo), hi = *reinterpret_cast<const uint4*>(x_hi);
-            const uint32_t f[2][4] = {{lo.x, hi.x, lo.y, hi.y}, {lo.z, hi.z, lo.w, hi.w}};
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if (j >= nt) break;
-                const uint4 u = *reinterpret_cast<const uint4*>(bank + 8 * j * kBankPitch);
-                mma_k16<PAIRS>(acc[j], f[0], u.x, u.y);
-                mma_k16<PAIRS>(acc[j], f[1], u.z, u.w);
+    {
+        const Share h = share_of(p.x, p.x_token, p.x_whole, k0);
+        constexpr int kChunks = kBlock / 8, kStep = kThreads / kChunks;
+        const int row = tid / kChunks, column = tid % kChunks * 8;
+        const uint16_t* const mine = bank_a + static_cast<int64_t>(row) * p.K + k0 + column;
+        const auto load = [&](int b, int slot) {
+            if (b < blocks1) {
+                const uint32_t to = smem_addr(ring1 + slot * plan.stage1);
+                copy_rows(h, b, inputs, to);
+                const bool in = b * kBlock + column < inputs;
+                const uint16_t* src = mine + b * kBlock;
+                uint32_t dst = to + kRows * kPitch + row * kBankPitch + 2 * column;
+                for (int r = row; r < rank; r += kStep, src += static_cast<int64_t>(kStep) * p.K, dst += kStep * kBankPitch)
+                    copy16(dst, in ? src : bank_a, in ? 16 : 0);
             }
-        } else {
-            constexpr int kTerms = sizeof(T) == 4 ? 2 : 1;
-            uint32_t f[kTerms][4][4];  // [term][step][register]
+            copies_end();
+        };
+        for (int b = 0; b < stages1 - 1; ++b) load(b, b);
+        for (int b = 0, slot = 0, next = stages1 - 1; b < blocks1; ++b) {
+            copies_wait(stages1 - 2);
+            __syncthreads();
+            load(b + stages1 - 1, next);
+            const uint8_t* const stage = ring1 + slot * plan.stage1;
+            slot = slot + 1 == stages1 ? 0 : slot + 1, next = next + 1 == stages1 ? 0 : next + 1;
+            if (!busy) continue;
+            const uint8_t* const bank = stage + kRows * kPitch + g * kBankPitch + 64 * sub + 16 * tq;
+            const T* const x_lo = reinterpret_cast<const T*>(stage + r_lo * kPitch) + 32 * sub + 8 * tq;
+            const T* const x_hi = reinterpret_cast<const T*>(stage + r_hi * kPitch) + 32 * sub + 8 * tq;
+            uint32_t f[kX][2][4];  // [term][step][register]
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
+                uint32_t v[kX][4];
                 if constexpr (sizeof(T) == 4) {
-                    float v[8];
                     const float4 a = ld4(r ? x_hi : x_lo), c = ld4((r ? x_hi : x_lo) + 4);
-                    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
+                    const float e[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) split_tf32(v[e], f[0][e >> 1][r + 2 * (e & 1)], f[1][e >> 1][r + 2 * (e & 1)]);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t t[kX];
+                        split(e[2 * i], e[2 * i + 1], t);
+#pragma unroll
+                        for (int k = 0; k < kX; ++k) v[k][i] = t[k];
+                    }
                 } else {
-                    const uint4 u = *reinterpret_cast<const uint4*>(r ? x_hi : x_lo);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) pair_tf32<__is_same(T, __half)>(w[q], f[0][q][r], f[0][q][r + 2]);
+                    terms_of<__is_same(T, __half) && !F16>(*reinterpret_cast<const uint4*>(r ? x_hi : x_lo), v);
                 }
+#pragma unroll
+                for (int k = 0; k < kX; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[k][i >> 1][r + 2 * (i & 1)] = v[k][i];
             }
+            // four tiles at once: four chains of dependent instructions (columns behind the rank are not looked at)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                if (j >= nt) break;
-                uint32_t u[8];
-                bank_tf32(*reinterpret_cast<const uint4*>(bank + 8 * j * kBankPitch), p.bank, u);
+            for (int j0 = 0; j0 < NT; j0 += 4) {
+                if (j0 >= nt) break;
+                uint32_t u[4][kA][4];
 #pragma unroll
-                for (int term = 0; term < kTerms; ++term)
+                for (int j = 0; j < 4; ++j) terms_of<!BF && !F16>(*reinterpret_cast<const uint4*>(bank + 8 * (j0 + j) * kBankPitch), u[j]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) mma_tf32(acc[j], f[term][q], u[2 * q], u[2 * q + 1]);
+                for (int i = 0; i < kX; ++i)
+#pragma unroll
+                    for (int k = 0; k < kA; ++k) {
+                        if (i + k >= (kX > kA ? kX : kA)) continue;  // below the last bit
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) mma_k16<!F16>(acc[j0 + j], f[i][q], u[j][k][2 * q], u[j][k][2 * q + 1]);
+                    }
             }
         }
     }
-    copies_wait<0>();
+    copies_wait(0);
     __syncthreads();
+
     // the second product's first blocks come while the sums are joined
-#pragma unroll
-    for (int b = 0; b < kStages - 1; ++b) load2(b);
+    const Share h = share_of(p.y, p.y_token, p.y_whole == 2, n0);
+    const int chunks = nt, log_chunks = 32 - __clz(chunks - 1), b_row = tid >> log_chunks, b_chunk = tid & ((1 << log_chunks) - 1);
+    const uint16_t* const b_mine = bank_b + (n0 + b_row) * p.R + 8 * b_chunk;
+    const auto load2 = [&](int b, int slot) {
+        if (b < blocks2) {
+            const uint32_t to = smem_addr(ring2 + slot * plan.stage2);
+            if (p.y_whole) copy_rows(h, b, outputs, to);
+            if (b_chunk < chunks) {
+                const int step = kThreads >> log_chunks, left = outputs - b * kBlock;
+                const uint16_t* src = b_mine + static_cast<int64_t>(b * kBlock) * p.R;
+                uint32_t dst = to + kRows * kPitch + b_row * b_pitch + 16 * b_chunk;
+                for (int r = b_row; r < kBlock; r += step, src += step * p.R, dst += step * b_pitch) copy16(dst, r < left ? src : bank_b, r < left ? 16 : 0);
+            }
+        }
+        copies_end();
+    };
+    for (int b = 0; b < stages2 - 1; ++b) load2(b, b);
+    // zeros in the places behind the rank, up to 32
+    for (int i = tid; i < stages2 * kBlock; i += kThreads)
+        for (int o = nt; o < (rank + 31) / 32 * 4; ++o)
+            *reinterpret_cast<uint4*>(ring2 + i / kBlock * plan.stage2 + kRows * kPitch + i % kBlock * b_pitch + 16 * o) = make_uint4(0, 0, 0, 0);
     {
         const auto put = [&](float* to, bool add) {
 #pragma unroll
@@ -432,12 +464,14 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : 2) k_adapt(const __gr
     cluster_arrive();
     cluster_wait();
     // the sums of all CTAs, scaled, as the second product's operand
-    for (int i = tid; i < kRows * (wide / 8); i += kThreads) {
-        const int r = i / (wide / 8), o = i - r * (wide / 8);  // eight ranks of a row
+    const int eights = wide / 8;
+    for (int i = tid; i < kRows * eights * 4; i += kThreads) {
+        // eight ranks of a row; four lanes add up a quarter of the CTAs each
+        const int r = (i >> 2) / eights, o = (i >> 2) - r * eights, quarter = i & 3;
         float t[8] = {};
         if (8 * o < rank && r < rows) {
 #pragma unroll 4
-            for (int c = 0; c < parts; ++c) {
+            for (int c = quarter * parts / 4; c < (quarter + 1) * parts / 4; ++c) {
                 const uint32_t at = cluster_addr(sums + r * pitch + 8 * o, c);
                 float v[8];
 #pragma unroll
@@ -449,127 +483,136 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : 2) k_adapt(const __gr
                 for (int e = 0; e < 8; ++e) t[e] += v[e];
             }
         }
-        // element e of the eight is lane 4 (r % 8) + o % 4's, register (r / 8) % 2 + 2 (e % 2) of step e / 2
-        float* const to = t_frag + (((r >> 4) * (wide / 8) + (o >> 2) * 4) * 32 + (r & 7) * 4 + (o & 3)) * 4 + ((r >> 3) & 1);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) to[(e >> 1) * 128 + 2 * (e & 1)] = 8 * o + e < rank ? t[e] * scale : 0.0f;
+        for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] += __shfl_xor_sync(kFull, t[e], d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = 8 * o + e < rank ? t[e] * scale : 0.0f;
+        // lane 4 (r % 8) + o % 4 of the steps of these 32 ranks; register (r / 8) % 2 and that + 2
+        const int lane4 = ((r & 7) * 4 + (o & 3)) * 4 + ((r >> 3) & 1);
+        // (a step: four neighbours as two pairs)
+        uint32_t* const to = t_words + ((r >> 4) * (wide / 16) + (o >> 2) * 2) * kT * 128 + lane4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q != quarter) continue;
+            uint32_t v[kT];
+            split(t[2 * q], t[2 * q + 1], v);
+#pragma unroll
+            for (int k = 0; k < kT; ++k) to[((q >> 1) * kT + k) * 128 + 2 * (q & 1)] = v[k];
+        }
     }
     cluster_arrive();  // nobody leaves before its sums are read
 
     // out = y + (A x) B^T
-    const float4* const t_mine = reinterpret_cast<const float4*>(t_frag) + m * (wide / 8) * 32 + lane;
-    for (int b = 0; b < blocks2; ++b) {
-        copies_wait<kStages - 2>();
+    const uint4* const t_mine = reinterpret_cast<const uint4*>(t_words) + m * (wide / 16) * kT * 32 + lane;
+    T* const out_lo = out + (r_lo < rows ? sh.row[r_lo] * p.out_token : 0) + n0 + 32 * sub + 8 * tq;
+    T* const out_hi = out + (r_hi < rows ? sh.row[r_hi] * p.out_token : 0) + n0 + 32 * sub + 8 * tq;
+    for (int b = 0, slot = 0, next = stages2 - 1; b < blocks2; ++b) {
+        copies_wait(stages2 - 2);
         __syncthreads();
-        load2(b + kStages - 1);
+        load2(b + stages2 - 1, next);
+        const uint8_t* const stage = ring2 + slot * plan.stage2;
+        slot = slot + 1 == stages2 ? 0 : slot + 1, next = next + 1 == stages2 ? 0 : next + 1;
         if (!busy) continue;
-        const uint8_t* const stage = ring2 + (b % kStages) * plan.stage2;
         const uint8_t* const bank = stage + kRows * kPitch + (32 * sub + 8 * (g >> 1) + (g & 1)) * b_pitch + 16 * tq;
-        const int64_t n = n0 + static_cast<int64_t>(b) * kBlock + 32 * sub + 8 * tq;  // this lane's eight outputs
+        const int n = b * kBlock + 32 * sub + 8 * tq;  // this lane's eight outputs, from n0
         float o[4][4] = {};
         for (int s0 = 0; 32 * s0 < rank; ++s0) {
-            const int have = rank - 32 * s0 - 8 * tq;
             uint4 u[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                u[j] = have > 0 ? first_of(*reinterpret_cast<const uint4*>(bank + 2 * j * b_pitch + 64 * s0), have) : make_uint4(0, 0, 0, 0);
-            if constexpr (PAIRS) {
+            for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const uint4*>(bank + 2 * j * b_pitch + 64 * s0);
+            if (rank & 7) {
+                const int have = max(0, rank - 32 * s0 - 8 * tq);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float4 a = t_mine[(4 * s0 + 2 * q) * 32], c = t_mine[(4 * s0 + 2 * q + 1) * 32];
-                    uint32_t f[2][4];
-                    split_bf16(a.x, a.z, f[0][0], f[1][0]);
-                    split_bf16(a.y, a.w, f[0][1], f[1][1]);
-                    split_bf16(c.x, c.z, f[0][2], f[1][2]);
-                    split_bf16(c.y, c.w, f[0][3], f[1][3]);
-#pragma unroll
-                    for (int term = 0; term < 2; ++term)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) mma_k16<true>(o[j], f[term], q ? u[j].z : u[j].x, q ? u[j].w : u[j].y);
-                }
-            } else {
-                uint32_t w[4][8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) bank_tf32(u[j], p.bank, w[j]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 a = t_mine[(4 * s0 + q) * 32];
-                    uint32_t f[2][4];
-                    split_tf32(a.x, f[0][0], f[1][0]);
-                    split_tf32(a.y, f[0][1], f[1][1]);
-                    split_tf32(a.z, f[0][2], f[1][2]);
-                    split_tf32(a.w, f[0][3], f[1][3]);
-#pragma unroll
-                    for (int term = 0; term < 2; ++term)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) mma_tf32(o[j], f[term], w[j][2 * q], w[j][2 * q + 1]);
-                }
+                for (int j = 0; j < 4; ++j) u[j] = first_of(u[j], have);
             }
+            uint32_t w[4][kB][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) terms_of<!BF>(u[j], w[j]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < kT; ++i) {
+                    const uint4 f4 = t_mine[((2 * s0 + q) * kT + i) * 32];
+                    const uint32_t f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                    for (int k = 0; k < kB; ++k) {
+                        if (i + k >= kT) continue;  // below the last bit
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma_k16<true>(o[j], f, w[j][k][2 * q], w[j][k][2 * q + 1]);
+                    }
+                }
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int at = r ? r_hi : r_lo;
-            if (at >= rows || n >= n1) continue;
-            T* const to = out + sh.row[at] * p.out_token + n;
+            if (at >= rows || n >= outputs) continue;
+            T* const to = (r ? out_hi : out_lo) + b * kBlock;
             float v[8];
             if (p.y_whole) {
                 const T* const from = reinterpret_cast<const T*>(stage + at * kPitch) + 32 * sub + 8 * tq;
                 const float4 a = ld4(from), c = ld4(from + 4);
                 v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
             } else {
-                const T* const from = y + sh.row[at] * p.y_token + n;
+                const T* const from = y + sh.row[at] * p.y_token + n0 + n;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = n + e < n1 ? ld1(from + e) : 0.0f;
+                for (int e = 0; e < 8; ++e) v[e] = n + e < outputs ? ld1(from + e) : 0.0f;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) v[2 * j + e] += o[j][2 * r + e];
-            if (p.out_whole && n + 8 <= n1) {
+            if (p.out_whole && n + 8 <= outputs) {
                 st4(to, make_float4(v[0], v[1], v[2], v[3]));
                 st4(to + 4, make_float4(v[4], v[5], v[6], v[7]));
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (n + e < n1) st1(to + e, v[e]);
+                    if (n + e < outputs) st1(to + e, v[e]);
             }
         }
     }
     cluster_wait();
 }
 
-template <typename T, bool NATIVE, int NT, int WARPS, int MT>
-cudaError_t launch(const AdaptParams& p, int64_t groups, int parts, cudaStream_t s) {
+template <typename T, bool BF, int NT, int WARPS, int MT>
+cudaError_t launch(AdaptParams p, int64_t groups, int parts, cudaStream_t s) {
     using P = Plan<T, WARPS, MT>;
-    constexpr int kStages = MT == 1 ? 2 : 3, kMost = P(8 * NT).bytes(kStages);
-    static_assert(kMost + 768 <= kSmemLimit, "ring, operand and sums of the largest rank in a CTA's shared memory");
+    static_assert(P(8 * NT).bytes() + 1024 <= kSmemLimit, "ring, operand and sums of the largest rank in a CTA's shared memory");
+    const P plan(p.R, groups * parts <= 152);
+    p.stages1 = plan.stages1, p.stages2 = plan.stages2;
     static thread_local bool done[kMaxDevices] = {};
-    const auto kernel = k_adapt<T, NATIVE, NT, WARPS, MT>;
+    const auto kernel = k_adapt<T, BF, NT, WARPS, MT>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev >= kMaxDevices || !done[dev])) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 1024);
         if (e == cudaSuccess && dev < kMaxDevices) done[dev] = true;
     }
     if (e != cudaSuccess) return e;
-    return launch_cluster(kernel, dim3(static_cast<unsigned>(groups * parts)), dim3(32 * WARPS), P(p.R).bytes(kStages), parts, s, p);
+    return launch_cluster(kernel, dim3(static_cast<unsigned>(groups * parts)), dim3(32 * WARPS), plan.bytes(), parts, s, p);
 }
 
-template <typename T, bool NATIVE>
+template <typename T, bool BF>
 cudaError_t launch_type(const AdaptParams& p, cudaStream_t s) {
     const int64_t rows = p.q_start && p.T > 8 * p.seqs && p.R <= 128 ? 64 : 16;
     const int64_t groups = p.q_start ? p.T / rows + std::min(p.seqs, p.T) : p.seqs;
     if (rows == 64) {  // more than eight rows a sequence
-        const int parts = groups <= 38 ? 8 : 4;
-        if (p.R <= 64) return launch<T, NATIVE, 8, 8, 4>(p, groups, parts, s);
-        return launch<T, NATIVE, 16, 8, 4>(p, groups, parts, s);
+        // CTAs a tile: so many that two an SM are in flight at once (five prompts of 150 to 1000 rows, 47 tiles: 52.8 us
+        // with 4, 46.1 with 5, 63.8 with 6, whose clusters no longer fit all at once)
+        const int parts = std::max<int>(4, std::min<int>(8, 250 / groups));
+        if (p.R <= 64) return launch<T, BF, 8, 8, 4>(p, groups, parts, s);
+        return launch<T, BF, 16, 8, 4>(p, groups, parts, s);
     }
-    const int parts = groups <= 18 ? 16 : groups <= 304 ? 8 : 4;
-    if (p.R <= 64) return launch<T, NATIVE, 8, 8, 1>(p, groups, parts, s);
+    // 16 CTAs a group while they are few (one row, 4096 to 14336, rank 16: 9.7 us with 16, 14.9 with 8), 4 of many (32 rows of
+    // 32 adapters of rank 64: 16.1 us with 4, 20.3 with 8; 256 of 32: 32.7 and 41.3)
+    const int parts = groups <= 16 ? 16 : groups <= 24 ? 8 : 4;
+    if (p.R <= 64) return launch<T, BF, 8, 8, 1>(p, groups, parts, s);
     // (wide blocks of high ranks do not fit a CTA)
-    if (p.R <= 128) return launch<T, NATIVE, 16, 4, 1>(p, groups, parts, s);
-    return launch<T, NATIVE, 32, 4, 1>(p, groups, parts, s);
+    if (p.R <= 128) return launch<T, BF, 16, 4, 1>(p, groups, parts, s);
+    return launch<T, BF, 32, 4, 1>(p, groups, parts, s);
 }
 
 }  // namespace
@@ -585,9 +628,10 @@ cudaError_t launch_adapt(const AdaptParams& given, int dtype, cudaStream_t s) {
     p.x_whole = whole(p.x, p.x_token, 16);
     p.y_whole = whole(p.y, p.y_token, 16) ? 2 : whole(p.y, p.y_token, 4 * size) ? 1 : 0;
     p.out_whole = whole(p.out, p.out_token, 4 * size);
-    if (dtype == 0) return launch_type<float, false>(p, s);
-    if (dtype == 1) return p.bank == 1 ? launch_type<__half, true>(p, s) : launch_type<__half, false>(p, s);
-    return p.bank == 2 ? launch_type<__nv_bfloat16, true>(p, s) : launch_type<__nv_bfloat16, false>(p, s);
+    const bool bf = p.bank == 2;
+    if (dtype == 0) return bf ? launch_type<float, true>(p, s) : launch_type<float, false>(p, s);
+    if (dtype == 1) return bf ? launch_type<__half, true>(p, s) : launch_type<__half, false>(p, s);
+    return bf ? launch_type<__nv_bfloat16, true>(p, s) : launch_type<__nv_bfloat16, false>(p, s);
 }
 
 }  // namespace ggq

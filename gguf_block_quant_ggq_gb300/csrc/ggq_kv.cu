@@ -173,15 +173,22 @@ __device__ __forceinline__ int64_t blob_of(const KvParams& p, int64_t slot, int 
 
 // turns: null, or of keys that are turned before they are quantized
 template <bool STORE, bool Q4, bool V, int D, bool TURN = false, typename T>
-__device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, const WindowTurns* turns, const Window& w, int64_t row0, T* rows, int64_t head, int64_t st,
-                                        uint8_t* pool, int h0, int h1, uint8_t* image) {
+__device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, const WindowTurns* turns, const Window& w,
+                                        int64_t row0, T* rows, int64_t head, int64_t st, uint8_t* pool, int h0, int h1, uint8_t* image) {
     // threads a row (eight channels each; four to read back) and rows at once
     constexpr int kChannels = STORE ? 8 : 4, kPer = D / kChannels, kAtOnce = kKvThreads / kPer, kPasses = kKvRows / kAtOnce;
     constexpr int kBlob = kv_blob_bytes(Q4, D), kLines = kBlob / 16, kQuants = kv_quant_bytes(Q4, D) / 16;
     const int tid = threadIdx.x, r_at = tid / kPer, c = kChannels * (tid % kPer);
-    const auto load8 = [&](const T* src, int row, float (&x)[8]) {  // row: from row0
+    // a thread's table entries are those of all heads
+    Turn8 known[TURN ? kPasses : 1];
+    if constexpr (TURN) {
+        if (w.start >= 0 && turn->whole)
+#pragma unroll
+            for (int k = 0; k < kPasses; ++k) known[k] = turn8_of(*turn, c, turns->entry[w.start + r_at + k * kAtOnce]);
+    }
+    const auto load8 = [&](const T* src, int row, const Turn8* entries, float (&x)[8]) {  // row: from row0
         if constexpr (TURN) {
-            turned8(*turn, src - c, c, turns->entry[row], x);
+            turned8(*turn, src - c, c, turns->entry[row], entries, x);
             return;
         }
         const float4 a = ld4(src), b = ld4(src + 4);
@@ -198,7 +205,7 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, c
             if constexpr (STORE) {
                 float x[kPasses][8];
 #pragma unroll
-                for (int k = 0; k < kPasses; ++k) load8(first + k * kAtOnce * st, w.start + r_at + k * kAtOnce, x[k]);
+                for (int k = 0; k < kPasses; ++k) load8(first + k * kAtOnce * st, w.start + r_at + k * kAtOnce, turn && turn->whole ? &known[k] : nullptr, x[k]);
                 if (h > h0) __syncthreads();  // the blob before this one has left
 #pragma unroll
                 for (int k = 0; k < kPasses; ++k) {
@@ -227,7 +234,7 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, c
             if constexpr (STORE) {
                 float x[8];
                 uint32_t q[8];
-                load8(at, row, x);
+                load8(at, row, nullptr, x);
                 const float d = quantize8<Q4>(x, q);
                 put8<false, Q4, V, D>(blob, static_cast<int>(slot & 15), c, q, d, there);
             } else if (there) {
@@ -242,10 +249,10 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, c
 
 // The rows of a window: the slots around it, the group that begins in it, single rows and those without a place.
 // False: no row.
-__device__ __forceinline__ bool kv_window(const KvParams& p, Window& w, int64_t& row0) {
+__device__ __forceinline__ bool kv_window(const KvParams& p, Window& w, unsigned window, int64_t& row0) {
     const int tid = threadIdx.x;
     const int64_t s0 = p.slots[0];
-    row0 = static_cast<int64_t>(blockIdx.x) * kKvRows - (s0 > 0 ? s0 & 15 : 0);
+    row0 = static_cast<int64_t>(window) * kKvRows - (s0 > 0 ? s0 & 15 : 0);
     if (row0 >= p.n) return false;
     if (tid < 3 * kKvRows) {
         const int64_t r = row0 - (kKvRows - 1) + tid;
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv(const __grid_constant__ KvPar
     __shared__ __align__(16) uint8_t image[D / 32 * 592 + D];
     __shared__ Window w;
     int64_t row0;
-    if (!kv_window(p, w, row0)) return;
+    if (!kv_window(p, w, blockIdx.x, row0)) return;
     const int parts = static_cast<int>(gridDim.y) >> 1;
     const bool is_v = static_cast<int>(blockIdx.y) >= parts;
     const int part = static_cast<int>(blockIdx.y) - (is_v ? parts : 0);
@@ -314,11 +321,13 @@ __global__ void __launch_bounds__(kKvThreads) k_kv(const __grid_constant__ KvPar
 struct AppendParams {
     KvParams kv;
     RotateParams q;  // of the keys too: the rotation; no heads: no queries
-    int kv_parts;
+    int kv_parts;    // of the keys' heads, and of the values'
+    unsigned parts;  // of a window
 };
 
-// The same with the keys turned before they are quantized, and the queries turned in further parts of the grid
-// (y: parts of the keys' heads, of the values', of the queries').
+// The same with the keys turned before they are quantized, and the queries turned in further parts.  Grid: windows, in
+// each the parts of the keys' heads, of the values' and of the queries', so that the quantizers, which are bound by
+// instructions, run beside the queries, which are bound by memory.
 template <int D, int QV, typename T>
 __global__ void __launch_bounds__(kKvThreads) k_kv_append(const __grid_constant__ AppendParams a) {
     pdl_launch_dependents();
@@ -327,15 +336,16 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_append(const __grid_constant_
     __shared__ Window w;
     __shared__ WindowTurns turns;
     const KvParams& p = a.kv;
-    const int part = static_cast<int>(blockIdx.y);
+    const unsigned window = blockIdx.x / a.parts;
+    const int part = static_cast<int>(blockIdx.x - window * a.parts);
     if (part >= 2 * a.kv_parts) {
-        const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kKvRows;
+        const int64_t r0 = static_cast<int64_t>(window) * kKvRows;
         const int h0 = (part - 2 * a.kv_parts) * a.q.heads_at_once;
         rotate_tile<QV, T>(a.q, r0, min(p.n, r0 + kKvRows), h0, min(a.q.H, h0 + a.q.heads_at_once));
         return;
     }
     int64_t row0;
-    if (!kv_window(p, w, row0)) return;
+    if (!kv_window(p, w, window, row0)) return;
     const bool is_v = part >= a.kv_parts;
     const int h0 = (part - (is_v ? a.kv_parts : 0)) * p.heads_at_once, h1 = min(p.H, h0 + p.heads_at_once);
     if (is_v) {
@@ -392,7 +402,9 @@ cudaError_t launch_append_type(AppendParams a, int v, cudaStream_t s) {
     a.q.units = a.q.r.half / v + ((D - 2 * a.q.r.half) / v + 1) / 2;
     a.q.heads_at_once = std::max(1, std::min(a.q.H, windows < 64 ? 1 : 8));
     const int q_parts = (a.q.H + a.q.heads_at_once - 1) / a.q.heads_at_once;
-    const dim3 grid(static_cast<unsigned>(windows), static_cast<unsigned>(2 * a.kv_parts + q_parts));
+    a.parts = static_cast<unsigned>(2 * a.kv_parts + q_parts);
+    if (windows * a.parts > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(windows * a.parts));
     if (v == 8) {
         if constexpr (sizeof(T) == 2) return launch_pdl(k_kv_append<D, 8, T>, grid, dim3(kKvThreads), 0, s, a);
     }
@@ -414,7 +426,7 @@ cudaError_t launch_kv_load(const KvParams& p, int dtype, cudaStream_t s) { retur
 
 cudaError_t launch_kv_append(const KvParams& kv, const RotateParams& q, int dtype, cudaStream_t s) {
     if (kv.n == 0) return cudaSuccess;
-    AppendParams a{kv, q, 0};
+    AppendParams a{kv, q, 0, 0};
     a.q.r.whole = q.r.half % 8 == 0 && q.r.first % 8 == 0 && aligned_to(q.r.table, 16);
     const int v = q.H ? rotate_vector(q, dtype) : dtype == 0 ? 4 : 8;
     if (kv.D == 64) return launch_append_dim<64>(a, dtype, v, s);

@@ -30,8 +30,7 @@ namespace ggq {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kRowThreads = 512, kWarps = kRowThreads / 32;
-constexpr int kGroups = kRowThreads / 8;
+constexpr int kMaxWarps = 16;
 constexpr int kPool = 512;
 constexpr int kNone = INT32_MAX;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -89,16 +88,16 @@ __device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, f
 __device__ __forceinline__ bool before(float x, int i, float y, int j) { return x > y || (x == y && i < j); }
 
 struct Shared {
-    Sums sums[kWarps];
-    float group[kGroups];
+    Sums sums[kMaxWarps];
+    float group[4 * kMaxWarps];
     float bound;
     int count;
     float pool_x[kPool];
     int pool_id[kPool];
     float best_x[kLogprobsMaxTop];
     int best_id[kLogprobsMaxTop];
-    float pick_x[kWarps];
-    int pick_id[kWarps];
+    float pick_x[kMaxWarps];
+    int pick_id[kMaxWarps];
     // of the cluster's CTAs, in the first one
     Sums part[16];
     float part_x[16 * kLogprobsMaxTop];
@@ -106,6 +105,7 @@ struct Shared {
 };
 
 // The entries of (x, id)[n] that come first, in order, to best (n >= top, or kNone entries fill up).
+template <int kRowThreads>
 __device__ __forceinline__ void rank_entries(const float* x, const int* id, int n, int top, float* best_x, int* best_id) {
     for (int i = threadIdx.x; i < n; i += kRowThreads) {
         const float mx = x[i];
@@ -177,12 +177,13 @@ struct Vec {
 };
 
 // TOP: whether alternatives are asked for
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kRowThreads, 2) k_logprobs(const __grid_constant__ LogprobsParams p) {
+template <typename T, bool TOP, int kRowThreads>
+__global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(const __grid_constant__ LogprobsParams p) {
     pdl_launch_dependents();
     pdl_wait();
     using V = Vec<T>;
-    constexpr int kN = V::kN, kLoads = 4;
+    constexpr int kN = V::kN, kLoads = 4, kWarps = kRowThreads / 32, kGroups = kRowThreads / 8;
+    static_assert(kGroups >= kLogprobsMaxTop && 2 * 16 <= kRowThreads, "the bound and the row's ends");
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(cluster_rank()), parts = static_cast<int>(cluster_size());
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_logprobs(const __grid_consta
         __syncthreads();
         const int n = sh.count;
         if (n <= kPool) {
-            rank_entries(sh.pool_x, sh.pool_id, n, p.top, sh.best_x, sh.best_id);
+            rank_entries<kRowThreads>(sh.pool_x, sh.pool_id, n, p.top, sh.best_x, sh.best_id);
             __syncthreads();
         } else {
             // place by place: the first value behind the last one taken
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_logprobs(const __grid_consta
         if (rank != 0) return;
         if (warp == 0) v = warp_join(lane < parts ? sh.part[lane] : no_sums(), c);
         if constexpr (TOP) {
-            rank_entries(sh.part_x, sh.part_id, parts * p.top, p.top, sh.best_x, sh.best_id);
+            rank_entries<kRowThreads>(sh.part_x, sh.part_id, parts * p.top, p.top, sh.best_x, sh.best_id);
             __syncthreads();
         }
     }
@@ -381,20 +382,23 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_logprobs(const __grid_consta
 
 template <typename T, bool TOP>
 cudaError_t launch(const LogprobsParams& p, cudaStream_t s) {
+    constexpr int kRowThreads = 512;
     // CTAs a row: as many as the SMs take at once, with at least two loads a thread
     int parts = 1;
     while (parts < 16 && p.T * parts * 2 <= 304 && p.V / (2 * parts) >= kRowThreads * 2 * Vec<T>::kN) parts *= 2;
+    // many rows: smaller CTAs, so that an SM sums some while it ranks others
+    if (parts == 1 && p.T >= 608) return launch_cluster(k_logprobs<T, TOP, 256>, dim3(static_cast<unsigned>(p.T)), dim3(256), 0, 1, s, p);
     if (parts > 8) {
         static thread_local bool wide[kMaxDevices] = {};
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess && (dev >= kMaxDevices || !wide[dev])) {
-            e = cudaFuncSetAttribute(k_logprobs<T, TOP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            e = cudaFuncSetAttribute(k_logprobs<T, TOP, kRowThreads>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e == cudaSuccess && dev < kMaxDevices) wide[dev] = true;
         }
         if (e != cudaSuccess) return e;
     }
-    return launch_cluster(k_logprobs<T, TOP>, dim3(static_cast<unsigned>(p.T * parts)), dim3(kRowThreads), 0, parts, s, p);
+    return launch_cluster(k_logprobs<T, TOP, kRowThreads>, dim3(static_cast<unsigned>(p.T * parts)), dim3(kRowThreads), 0, parts, s, p);
 }
 
 template <typename T>

@@ -191,9 +191,24 @@ __device__ __forceinline__ void rotate_tile(const RotateParams& p, int64_t r0, i
     }
 }
 
-// Channels c .. c + 7 of the head that starts at `head`, turned.  entry: the row's table entries, null: as they are.
+// Table entries of channels c .. c + 7 (of a rotation of whole eights): four pairs (PAIRS), or eight.
+struct Turn8 {
+    float4 cs[4];
+};
+__device__ __forceinline__ Turn8 turn8_of(const Rotary& r, int c, const float2* entry) {
+    Turn8 t;
+    const int at = c - r.first, j = r.pairs ? at / 2 : at < r.half ? at : at - r.half;
+    const bool turned = entry && at >= 0 && at < 2 * r.half;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        t.cs[i] = turned && (i < 2 || !r.pairs) ? reinterpret_cast<const float4*>(entry + j)[i] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    return t;
+}
+
+// Channels c .. c + 7 of the head that starts at `head`, turned.  entry: the row's table entries, null: as they are; known:
+// those of these channels, of a rotation of whole eights, or null.
 template <typename T>
-__device__ __forceinline__ void turned8(const Rotary& r, const T* head, int c, const float2* entry, float (&x)[8]) {
+__device__ __forceinline__ void turned8(const Rotary& r, const T* head, int c, const float2* entry, const Turn8* known, float (&x)[8]) {
     const auto load = [&](int at, float (&v)[8]) {
         const float4 a = ld4(head + at), b = ld4(head + at + 4);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -204,7 +219,7 @@ __device__ __forceinline__ void turned8(const Rotary& r, const T* head, int c, c
     if (r.whole && r.pairs) {
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(entry + (at + i) / 2);
+            const float4 f = known ? known->cs[i / 4] : *reinterpret_cast<const float4*>(entry + (at + i) / 2);
             const float e0 = x[i], o0 = x[i + 1], e1 = x[i + 2], o1 = x[i + 3];
             x[i] = turned_a(e0, o0, make_float2(f.x, f.y)), x[i + 1] = turned_b(e0, o0, make_float2(f.x, f.y));
             x[i + 2] = turned_a(e1, o1, make_float2(f.z, f.w)), x[i + 3] = turned_b(e1, o1, make_float2(f.z, f.w));
@@ -216,7 +231,7 @@ __device__ __forceinline__ void turned8(const Rotary& r, const T* head, int c, c
         load(low ? c + r.half : c - r.half, other);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float4 f = *reinterpret_cast<const float4*>(entry + j + i);
+            const float4 f = known ? known->cs[i / 2] : *reinterpret_cast<const float4*>(entry + j + i);
             const float2 c0 = make_float2(f.x, f.y), c1 = make_float2(f.z, f.w);
             x[i] = low ? turned_a(x[i], other[i], c0) : turned_b(other[i], x[i], c0);
             x[i + 1] = low ? turned_a(x[i + 1], other[i + 1], c1) : turned_b(other[i + 1], x[i + 1], c1);
