@@ -174,21 +174,14 @@ __device__ __forceinline__ int64_t blob_of(const KvParams& p, int64_t slot, int 
 // turns: null, or of keys that are turned before they are quantized
 template <bool STORE, bool Q4, bool V, int D, bool TURN = false, typename T>
 __device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, const WindowTurns* turns, const Window& w,
-                                        int64_t row0, T* rows, int64_t head, int64_t st, uint8_t* pool, int h0, int h1, uint8_t* image) {
+                                        int64_t row0, T* rows, int64_t head, int64_t st, uint8_t* pool, int h0, int h1, uint8_t* image, float* tile = nullptr) {
     // threads a row (eight channels each; four to read back) and rows at once
     constexpr int kChannels = STORE ? 8 : 4, kPer = D / kChannels, kAtOnce = kKvThreads / kPer, kPasses = kKvRows / kAtOnce;
     constexpr int kBlob = kv_blob_bytes(Q4, D), kLines = kBlob / 16, kQuants = kv_quant_bytes(Q4, D) / 16;
     const int tid = threadIdx.x, r_at = tid / kPer, c = kChannels * (tid % kPer);
-    // a thread's table entries are those of all heads
-    Turn8 known[TURN ? kPasses : 1];
-    if constexpr (TURN) {
-        if (w.start >= 0 && turn->whole)
-#pragma unroll
-            for (int k = 0; k < kPasses; ++k) known[k] = turn8_of(*turn, c, turns->entry[w.start + r_at + k * kAtOnce]);
-    }
-    const auto load8 = [&](const T* src, int row, const Turn8* entries, float (&x)[8]) {  // row: from row0
+    const auto load8 = [&](const T* src, int row, float (&x)[8]) {  // row: from row0
         if constexpr (TURN) {
-            turned8(*turn, src - c, c, turns->entry[row], entries, x);
+            turned8(*turn, src - c, c, turns->entry[row], x);
             return;
         }
         const float4 a = ld4(src), b = ld4(src + 4);
@@ -197,6 +190,8 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, c
     const auto line = [&](int i) {  // 16 bytes i of the blob in its image
         return reinterpret_cast<uint4*>(image + (i < kQuants ? place<true>(4 * (i >> 5), i & 31) : scales_at<true>(Q4, D) + 16 * (i - kQuants)));
     };
+    constexpr int kUnits = D / 64;  // of eight channels that a thread turns: 16 rows of D / 8
+    Turn4 mine4[kUnits];
     for (int h = h0; h < h1; ++h) {
         T* const mine = rows + h * head + c;
         if (w.start >= 0) {
@@ -204,8 +199,41 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, c
             T* const first = mine + (row0 + w.start + r_at) * st;
             if constexpr (STORE) {
                 float x[kPasses][8];
+                bool done = false;
+                if constexpr (TURN) {
+                    if (turn->whole) {
+                        // a thread turns the same places of every head, four pairs at a time, into a tile of the group's rows
+                        if (h == h0)
 #pragma unroll
-                for (int k = 0; k < kPasses; ++k) load8(first + k * kAtOnce * st, w.start + r_at + k * kAtOnce, turn && turn->whole ? &known[k] : nullptr, x[k]);
+                            for (int k = 0; k < kUnits; ++k) mine4[k] = turn4_of(*turn, (tid + k * kKvThreads) % (D / 8),
+                                                                                 turns->entry[w.start + (tid + k * kKvThreads) / (D / 8)]);
+                        float4 a[kUnits], b[kUnits];
+#pragma unroll
+                        for (int k = 0; k < kUnits; ++k) {
+                            const T* const src = rows + h * head + (row0 + w.start + (tid + k * kKvThreads) / (D / 8)) * st;
+                            a[k] = ld4(src + mine4[k].ca), b[k] = ld4(src + mine4[k].cb);
+                        }
+#pragma unroll
+                        for (int k = 0; k < kUnits; ++k) {
+                            turn4(mine4[k], turn->pairs, a[k], b[k]);
+                            float* const to = tile + (tid + k * kKvThreads) / (D / 8) * (D + 4);
+                            st4(to + mine4[k].ca, a[k]);
+                            st4(to + mine4[k].cb, b[k]);
+                        }
+                        __syncthreads();
+#pragma unroll
+                        for (int k = 0; k < kPasses; ++k) {
+                            const float* const from = tile + (r_at + k * kAtOnce) * (D + 4) + c;
+                            const float4 lo = ld4(from), hi = ld4(from + 4);
+                            x[k][0] = lo.x, x[k][1] = lo.y, x[k][2] = lo.z, x[k][3] = lo.w;
+                            x[k][4] = hi.x, x[k][5] = hi.y, x[k][6] = hi.z, x[k][7] = hi.w;
+                        }
+                        done = true;
+                    }
+                }
+                if (!done)
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k) load8(first + k * kAtOnce * st, w.start + r_at + k * kAtOnce, x[k]);
                 if (h > h0) __syncthreads();  // the blob before this one has left
 #pragma unroll
                 for (int k = 0; k < kPasses; ++k) {
@@ -234,7 +262,7 @@ __device__ __forceinline__ void kv_rows(const KvParams& p, const Rotary* turn, c
             if constexpr (STORE) {
                 float x[8];
                 uint32_t q[8];
-                load8(at, row, nullptr, x);
+                load8(at, row, x);
                 const float d = quantize8<Q4>(x, q);
                 put8<false, Q4, V, D>(blob, static_cast<int>(slot & 15), c, q, d, there);
             } else if (there) {
@@ -328,13 +356,15 @@ struct AppendParams {
 // The same with the keys turned before they are quantized, and the queries turned in further parts.  Grid: windows, in
 // each the parts of the keys' heads, of the values' and of the queries', so that the quantizers, which are bound by
 // instructions, run beside the queries, which are bound by memory.
+// (six CTAs an SM: 16384 tokens with their queries 77 us, with the four that 128 registers leave 93)
 template <int D, int QV, typename T>
-__global__ void __launch_bounds__(kKvThreads) k_kv_append(const __grid_constant__ AppendParams a) {
+__global__ void __launch_bounds__(kKvThreads, D == 256 ? 4 : 6) k_kv_append(const __grid_constant__ AppendParams a) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ __align__(16) uint8_t image[D / 32 * 592 + D];
     __shared__ Window w;
     __shared__ WindowTurns turns;
+    __shared__ __align__(16) float tile[kKvRows * (D + 4)];
     const KvParams& p = a.kv;
     const unsigned window = blockIdx.x / a.parts;
     const int part = static_cast<int>(blockIdx.x - window * a.parts);
@@ -365,8 +395,8 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_append(const __grid_constant_
     }
     __syncthreads();
     T* const rows = static_cast<T*>(const_cast<void*>(p.ks));
-    if (p.k.q4) kv_rows<true, true, false, D, true>(p, &a.q.r, &turns, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image);
-    else kv_rows<true, false, false, D, true>(p, &a.q.r, &turns, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image);
+    if (p.k.q4) kv_rows<true, true, false, D, true>(p, &a.q.r, &turns, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image, tile);
+    else kv_rows<true, false, false, D, true>(p, &a.q.r, &turns, w, row0, rows, p.k_head, p.k_token, p.k.p, h0, h1, image, tile);
 }
 
 // the first window may begin up to 15 rows before the first row
@@ -427,7 +457,8 @@ cudaError_t launch_kv_load(const KvParams& p, int dtype, cudaStream_t s) { retur
 cudaError_t launch_kv_append(const KvParams& kv, const RotateParams& q, int dtype, cudaStream_t s) {
     if (kv.n == 0) return cudaSuccess;
     AppendParams a{kv, q, 0, 0};
-    a.q.r.whole = q.r.half % 8 == 0 && q.r.first % 8 == 0 && aligned_to(q.r.table, 16);
+    const int both = q.r.half | q.r.first;
+    a.q.r.whole = !aligned_to(q.r.table, 16) ? 0 : both % 8 == 0 ? 8 : both % 4 == 0 ? 4 : 0;
     const int v = q.H ? rotate_vector(q, dtype) : dtype == 0 ? 4 : 8;
     if (kv.D == 64) return launch_append_dim<64>(a, dtype, v, s);
     if (kv.D == 128) return launch_append_dim<128>(a, dtype, v, s);

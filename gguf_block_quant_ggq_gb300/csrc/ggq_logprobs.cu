@@ -9,7 +9,7 @@
 //
 // The best: in the pass nothing but the largest logit of each thread is kept.  Of 64 groups of eight
 // lanes the `top`-th largest maximum is a bound that at least `top` logits reach; threads whose maximum
-// reaches it (a handful) have their part read again, and what reaches the bound goes to a pool, whose
+// reaches it (a handful) have their part read again, by all, and what reaches the bound goes to a pool, whose
 // entries find their places by counting those before them (value, then id), so the order in which
 // they arrive does not show.  Where ties overflow the pool (a mask that leaves fewer than `top`), the
 // places are found one after another by passes over the part.
@@ -91,7 +91,8 @@ struct Shared {
     Sums sums[kMaxWarps];
     float group[4 * kMaxWarps];
     float bound;
-    int count;
+    int count, hots;
+    int16_t hot[32 * kMaxWarps];
     float pool_x[kPool];
     int pool_id[kPool];
     float best_x[kLogprobsMaxTop];
@@ -104,16 +105,47 @@ struct Shared {
     int part_id[16 * kLogprobsMaxTop];
 };
 
-// The entries of (x, id)[n] that come first, in order, to best (n >= top, or kNone entries fill up).
+// The entries of (x, id)[n] that come first, in order, to best_x, best_id (entries without an id come nowhere).  As many
+// neighbouring lanes an entry as there are threads for count those before it.
 template <int kRowThreads>
 __device__ __forceinline__ void rank_entries(const float* x, const int* id, int n, int top, float* best_x, int* best_id) {
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-        const float mx = x[i];
-        const int mi = id[i];
-        if (mi == kNone) continue;
+    int log_lanes = 5;
+    while (log_lanes > 0 && n << log_lanes > kRowThreads) --log_lanes;
+    const int lanes = 1 << log_lanes, mine = threadIdx.x & (lanes - 1), step = kRowThreads >> log_lanes;
+    for (int i0 = 0; i0 < n; i0 += step) {
+        const int i = i0 + (static_cast<int>(threadIdx.x) >> log_lanes);
+        const float mx = i < n ? x[i] : 0.0f;
+        const int mi = i < n ? id[i] : kNone;
         int at = 0;
-        for (int j = 0; j < n; ++j) at += before(x[j], id[j], mx, mi) ? 1 : 0;
-        if (at < top) best_x[at] = mx, best_id[at] = mi;
+        for (int j = mine; j < n; j += lanes) at += before(x[j], id[j], mx, mi) ? 1 : 0;
+        for (int d = 1; d < lanes; d <<= 1) at += __shfl_xor_sync(kFull, at, d);
+        if (mine == 0 && mi != kNone && at < top) best_x[at] = mx, best_id[at] = mi;
+    }
+}
+
+// The same of `parts` lists of `top` entries in order each: a place in a list is found by halving it.
+template <int kRowThreads>
+__device__ __forceinline__ void rank_lists(const float* x, const int* id, int parts, int top, float* best_x, int* best_id) {
+    const int n = parts * top;
+    int log_lanes = 4;  // lanes an entry, each with its share of the lists
+    while (log_lanes > 0 && n << log_lanes > kRowThreads) --log_lanes;
+    const int lanes = 1 << log_lanes, mine = threadIdx.x & (lanes - 1), step = kRowThreads >> log_lanes;
+    for (int i0 = 0; i0 < n; i0 += step) {
+        const int i = i0 + (static_cast<int>(threadIdx.x) >> log_lanes);
+        const float mx = i < n ? x[i] : 0.0f;
+        const int mi = i < n ? id[i] : kNone;
+        int at = 0;
+        for (int c = mine; c < parts; c += lanes) {
+            int lo = 0, hi = top;  // entries of list c before this one
+            while (lo < hi) {
+                const int j = (lo + hi) >> 1;
+                if (before(x[c * top + j], id[c * top + j], mx, mi)) lo = j + 1;
+                else hi = j;
+            }
+            at += lo;
+        }
+        for (int d = 1; d < lanes; d <<= 1) at += __shfl_xor_sync(kFull, at, d);
+        if (mine == 0 && mi != kNone && at < top) best_x[at] = mx, best_id[at] = mi;
     }
 }
 
@@ -191,7 +223,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
     const int64_t t = blockIdx.x / parts;
     const T* const row = static_cast<const T*>(p.logits) + t * p.row;
     const float c = p.scale * kLog2e;
-    if (TOP && tid == 0) sh.count = 0;
+    if (TOP && tid == 0) sh.count = 0, sh.hots = 0;
 
     // the row's first value at 16 bytes, and whole vectors from there; the ends are the first CTA's, one a thread
     const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
@@ -201,7 +233,16 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
     const int end_id = rank ? kNone : tid < head ? tid : tid >= 16 && tid < 16 + tail ? p.V - tail + tid - 16 : kNone;
     const float end_x = end_id != kNone ? ld1(row + end_id) : -INFINITY;
 
+    // the first given tokens' logits
+    int given_id = -1;
+    float given_x = 0.0f;
+    if (rank == 0 && tid < min(32, p.given)) {
+        given_id = p.tokens[t * p.given + tid];
+        if (given_id >= 0 && given_id < p.V) given_x = ld1(row + given_id);
+    }
+
     Sums v = no_sums();
+    uint4 u[kLoads];
     const auto load = [&](int at, uint4 (&u)[kLoads]) {
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) u[k] = at + kRowThreads * k < v1 ? body[at + kRowThreads * k] : V::none();
@@ -211,7 +252,6 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
         uint4 next[kLoads];
         load(v0 + tid, next);
         for (int at = v0 + tid; at < v1; at += kRowThreads * kLoads) {
-            uint4 u[kLoads];
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) u[k] = V::raised(next[k]);
             load(at + kRowThreads * kLoads, next);
@@ -265,12 +305,15 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
     if (lane == 0) sh.sums[warp] = v;
     __syncthreads();
     if constexpr (TOP) {
-        if (tid < kGroups) {
-            const float g = sh.group[tid];
+        {
+            // eight lanes a group count those before it
+            const float g = sh.group[tid >> 3];
             int at = 0;
-#pragma unroll 8
-            for (int j = 0; j < kGroups; ++j) at += before(sh.group[j], j, g, tid) ? 1 : 0;
-            if (at == p.top - 1) sh.bound = g;
+#pragma unroll
+            for (int j = tid & 7; j < kGroups; j += 8) at += before(sh.group[j], j, g, tid >> 3) ? 1 : 0;
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) at += __shfl_xor_sync(kFull, at, d);
+            if ((tid & 7) == 0 && at == p.top - 1) sh.bound = g;
         }
         __syncthreads();
         const float bound = sh.bound;
@@ -281,11 +324,25 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
             if (at < kPool) sh.pool_x[at] = x, sh.pool_id[at] = id;
         };
         if (end_id != kNone) offer(end_x, end_id);
-        // lanes whose values reach the bound: the warp reads each one's vectors again
-        for (uint32_t hot = __ballot_sync(kFull, v0 + tid < v1 && mine >= bound); hot; hot &= hot - 1) {
-            const int first = v0 + warp * 32 + __ffs(hot) - 1;
-            for (int at = first + kRowThreads * lane; at < v1; at += kRowThreads * 32) {
-                if (*static_cast<volatile int*>(&sh.count) > kPool) break;
+        const bool once = v1 - v0 <= kRowThreads * kLoads;
+        if (once && bound > V::low()) {
+            // the values are still here
+            if (v0 + tid < v1 && mine >= bound)
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
+                    float x[kN];
+                    V::unpack(u[k], x);
+#pragma unroll
+                    for (int i = 0; i < kN; ++i) offer(x[i], head + (v0 + tid + kRowThreads * k) * kN + i);
+                }
+        } else {
+            // the parts of the threads whose values reach the bound are read again, by all
+            if (v0 + tid < v1 && mine >= bound) sh.hot[atomicAdd(&sh.hots, 1)] = static_cast<int16_t>(tid);
+            __syncthreads();
+            const int each = (v1 - v0 + kRowThreads - 1) / kRowThreads, items = sh.hots * each;
+            for (int i = tid; i < items; i += kRowThreads) {
+                const int h = i / each, at = v0 + sh.hot[h] + kRowThreads * (i - h * each);
+                if (at >= v1 || *static_cast<volatile int*>(&sh.count) > kPool) continue;
                 float x[kN];
                 V::unpack(body[at], x);
 #pragma unroll
@@ -356,7 +413,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
         if (rank != 0) return;
         if (warp == 0) v = warp_join(lane < parts ? sh.part[lane] : no_sums(), c);
         if constexpr (TOP) {
-            rank_entries<kRowThreads>(sh.part_x, sh.part_id, parts * p.top, p.top, sh.best_x, sh.best_id);
+            rank_lists<kRowThreads>(sh.part_x, sh.part_id, parts, p.top, sh.best_x, sh.best_id);
             __syncthreads();
         }
     }
@@ -370,9 +427,12 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
     };
     if (p.entropy && lane == 0) p.entropy[t] = nothing ? 0.0f : v.m == INFINITY ? NAN : fmaxf(0.0f, log_sum - kLn2 * (v.w / v.s));
     for (int j = lane; j < p.given; j += 32) {
-        const int id = p.tokens[t * p.given + j];
-        if (id >= p.V) set_error(p.err, DEV_ERR_BAD_TOKEN);
-        p.logprobs[t * p.given + j] = id < 0 || id >= p.V ? 0.0f : logprob(ld1(row + id));
+        if (j >= 32) {
+            given_id = p.tokens[t * p.given + j];
+            if (given_id >= 0 && given_id < p.V) given_x = ld1(row + given_id);
+        }
+        if (given_id >= p.V) set_error(p.err, DEV_ERR_BAD_TOKEN);
+        p.logprobs[t * p.given + j] = given_id < 0 || given_id >= p.V ? 0.0f : logprob(given_x);
     }
     if (TOP && lane < p.top) {
         p.ids[t * p.top + lane] = sh.best_id[lane];

@@ -6,7 +6,7 @@
 // to the rows' type when it is stored, the second norm takes it unrounded.
 //
 // Each value is read once and stays in registers between the two sums, so the bound is memory
-// at many rows and the chain launch - load - sum - sum - store at few.  A row of up to 256
+// at many rows and the chain launch - load - sum - sum - store at few (one row of 4096: 2.8 us).  A row of up to 256
 // channels is one warp's, wider ones a CTA's with eight channels a thread: the widest loads
 // there are for 16-bit rows, and the eight that a packed block of 32 or 256 channels gives a
 // lane, so that the packed forms are quantized from registers.
@@ -69,6 +69,10 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
     }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) u[i] = make_uint4(0, 0, 0, 0);
+    }
     __device__ __forceinline__ void to(float (&x)[8]) const { ld8(reinterpret_cast<const T*>(u), x); }
 };
 
@@ -115,22 +119,24 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
     return v;
 }
 
+// Words of a weight in shared memory: a group of eight as two quads, so that neighbouring lanes' quads are neighbours.
+__device__ __forceinline__ int weight_at(int group, int half, int threads) { return 4 * (half * threads + group); }
+
 // NU: groups of eight channels a thread holds.  THREADS: at most so many a CTA; a row is a CTA's, with 128 a
 // warp's.  VEC: rows of whole aligned groups; otherwise a thread's channels lie a row's threads apart and are
-// loaded one by one.  Rows of up to 4096 channels (EARLY): a CTA keeps the weights in registers, goes through
-// rows and asks for the next one before it sums; wider ones have no registers for it, and enough threads to
-// hide the waits.
-template <typename T, int NU, int THREADS, bool VEC, bool EARLY = (THREADS <= 512)>
+// loaded one by one.  With one group a thread (AHEAD: rows of up to 8192 channels) a CTA keeps the weights in
+// shared memory, goes through rows and asks for everything that the next one needs before it sums (4096 rows of 4096
+// bf16 channels, two norms, gate and residual: 28.5 us; 42.4 with a CTA a row, 34.4 with the weights in registers).
+template <typename T, int NU, int THREADS, bool VEC>
 __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1024 / THREADS) k_norm(const __grid_constant__ NormParams p) {
-    static_assert(!EARLY || NU == 1, "rows a thread keeps whole");
-    constexpr bool WARP = THREADS == 128;
+    constexpr bool WARP = THREADS == 128, AHEAD = VEC && NU == 1;
     pdl_launch_dependents();
     pdl_wait();
+    extern __shared__ __align__(16) float weights[];  // AHEAD: of the two norms, two quads a thread
     __shared__ float part[4][32];
     const int threads = WARP ? 32 : static_cast<int>(blockDim.x), at = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int64_t step = WARP ? static_cast<int64_t>(gridDim.x) * 4 : gridDim.x;
     int64_t t = WARP ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
-    if (WARP && t >= p.T) return;
     const auto first = [&](int u) { return VEC ? (u * threads + at) * 8 : u * 8 * threads + at; };
     const auto channel = [&](int u, int i) { return first(u) + (VEC ? i : i * threads); };
     // channels behind the row's end are zeros
@@ -145,11 +151,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1024 / THREADS)
                 if (channel(u, i) < p.H) x[i] = ld1(row + channel(u, i));
         }
     };
-    const auto weight = [&](const float* w, int u, float (&x)[8]) {  // w + offset
-        load(w, u, x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], p.offset);
-    };
     const auto store = [&](T* row, int u, const float (&x)[8]) {
         if constexpr (VEC) {
             if (first(u) < p.H) st8(row + first(u), x);
@@ -163,8 +164,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1024 / THREADS)
     const T* const rs = static_cast<const T*>(p.residual);
     const T* const gs = static_cast<const T*>(p.gate);
     const bool gates = p.gate && p.gate_channel;
-    constexpr bool AHEAD = EARLY && VEC;
-    Raw<T> next_x{}, next_r{}, next_g{};
+    // a row's groups as they come from memory
+    Raw<T> next_x, next_r, next_g;
+    if constexpr (AHEAD) next_x.zero(), next_r.zero(), next_g.zero();
     const auto ask = [&](int64_t row) {
         if (first(0) >= p.H) return;
         next_x.load(xs + row * p.x_token + first(0));
@@ -172,18 +174,41 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1024 / THREADS)
         if (gates) next_g.load(gs + row * p.gate_token + first(0));
     };
     const auto act = [&](float x) { return p.sigmoid ? __frcp_rn(1.0f + expf(-x)) : x; };
-    float wa[8], wb[8];
-    if constexpr (AHEAD) ask(t);
-    if constexpr (EARLY) {
-        if (p.after_w) weight(p.after_w, 0, wa);
-        if (p.before_w) weight(p.before_w, 0, wb);
+    if constexpr (AHEAD)
+        if (t < p.T) ask(t);
+    float* const mine = weights + 8 * threads * (WARP ? 2 * (threadIdx.x >> 5) : 0);
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float* const w = k ? p.before_w : p.after_w;
+            if (!w) continue;
+            float x[8];
+            load(w, 0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], p.offset);
+            // (read by this thread alone)
+            float* const to = mine + k * 8 * threads;
+            st4(to + weight_at(at, 0, threads), make_float4(x[0], x[1], x[2], x[3]));
+            st4(to + weight_at(at, 1, threads), make_float4(x[4], x[5], x[6], x[7]));
+        }
     }
+    // w + offset of group u; k: 0 of the norm of x, 1 of the total's
+    const auto weight = [&](const float* w, int k, int u, float (&x)[8]) {
+        if constexpr (AHEAD) {
+            const float* const from = mine + k * 8 * threads;
+            const float4 a = ld4(from + weight_at(at, 0, threads)), b = ld4(from + weight_at(at, 1, threads));
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        } else {
+            load(w, u, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], p.offset);
+        }
+    };
     for (int turn = 0; t < p.T; t += step, turn ^= 2) {
-        float v[NU][8], r[8], g[8];
+        float v[NU][8];
+        const Raw<T> r = next_r, g = next_g;
         if constexpr (AHEAD) {
             next_x.to(v[0]);
-            next_r.to(r);
-            next_g.to(g);
         } else {
 #pragma unroll
             for (int u = 0; u < NU; ++u) load(xs + t * p.x_token, u, v[u]);
@@ -203,35 +228,48 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1024 / THREADS)
         if (p.gate && !p.gate_channel) g1 = act(g1);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            if constexpr (!AHEAD) {
-                if (p.residual) load(rs + t * p.residual_token, u, r);
+            float x[8];
+            if (p.after_w) {
+                weight(p.after_w, 0, u, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * inv_after * x[i];
+            } else if (p.after) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] *= inv_after;
+            }
+            if (gates) {
+                if constexpr (AHEAD) g.to(x);
+                else load(gs + t * p.gate_token, u, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] *= act(x[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] *= g1;
+            }
+            if constexpr (AHEAD) {
+                r.to(x);
+            } else {
+                if (p.residual) load(rs + t * p.residual_token, u, x);
                 else
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
-                if (gates) load(gs + t * p.gate_token, u, g);
+                    for (int i = 0; i < 8; ++i) x[i] = 0.0f;
             }
-            if constexpr (!EARLY)
-                if (p.after_w) weight(p.after_w, u, wa);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float y = v[u][i];
-                if (p.after) y *= inv_after;
-                if (p.after_w) y *= wa[i];
-                y *= gates ? act(g[i]) : g1;
-                v[u][i] = fmaf(y, p.scale, r[i]);
-            }
+            for (int i = 0; i < 8; ++i) v[u][i] = fmaf(v[u][i], p.scale, x[i]);
             if (p.total) store(static_cast<T*>(p.total) + t * p.total_token, u, v[u]);
         }
         if (!p.before) continue;
         const float inv = inverse(part[turn + 1]);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            if constexpr (!EARLY)
-                if (p.before_w) weight(p.before_w, u, wb);
+            float x[8];
+            if (p.before_w) {
+                weight(p.before_w, 1, u, x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[u][i] *= inv;
-                if (p.before_w) v[u][i] *= wb[i];
+                for (int i = 0; i < 8; ++i) v[u][i] = v[u][i] * inv * x[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] *= inv;
             }
             if (p.out) store(static_cast<T*>(p.out) + t * p.out_token, u, v[u]);
             if constexpr (VEC) {
@@ -251,17 +289,34 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 1024 / THREADS)
     }
 }
 
+template <typename T, int NU, int THREADS, bool VEC>
+cudaError_t launch_rows(const NormParams& p, cudaStream_t s) {
+    constexpr bool WARP = THREADS == 128;
+    const int threads = WARP ? 128 : (p.H + 256 * NU - 1) / (256 * NU) * 32;
+    const int64_t ctas = WARP ? (p.T + 3) / 4 : p.T;
+    // as many CTAs as the SMs hold at once go through the rows
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(ctas, 152 * (1024 / threads))));
+    const size_t smem = VEC && NU == 1 ? static_cast<size_t>(threads) * 64 : 0;
+    if (smem > 48 * 1024) {
+        static thread_local bool done[kMaxDevices] = {};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && (dev >= kMaxDevices || !done[dev])) {
+            e = cudaFuncSetAttribute(k_norm<T, NU, THREADS, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 * 64);
+            if (e == cudaSuccess && dev < kMaxDevices) done[dev] = true;
+        }
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(k_norm<T, NU, THREADS, VEC>, grid, dim3(static_cast<unsigned>(threads)), smem, s, p);
+}
+
 template <typename T, bool VEC>
 cudaError_t launch(const NormParams& p, cudaStream_t s) {
-    // as many CTAs as the SMs hold at once go through the rows
-    const auto grid = [&](int64_t ctas, int threads) { return dim3(static_cast<unsigned>(std::min<int64_t>(ctas, 152 * (1024 / threads)))); };
-    if (p.H <= 256) return launch_pdl(k_norm<T, 1, 128, VEC>, grid((p.T + 3) / 4, 128), dim3(128), 0, s, p);
-    const auto threads = [&](int units) { return (p.H + 256 * units - 1) / (256 * units) * 32; };
-    if (p.H <= 4096) return launch_pdl(k_norm<T, 1, 512, VEC>, grid(p.T, threads(1)), dim3(threads(1)), 0, s, p);
-    const dim3 rows(static_cast<unsigned>(p.T));
-    if (p.H <= 8192) return launch_pdl(k_norm<T, 1, 1024, VEC>, rows, dim3(threads(1)), 0, s, p);
-    if (p.H <= 16384) return launch_pdl(k_norm<T, 2, 1024, VEC>, rows, dim3(threads(2)), 0, s, p);
-    return launch_pdl(k_norm<T, 4, 1024, VEC>, rows, dim3(threads(4)), 0, s, p);
+    if (p.H <= 256) return launch_rows<T, 1, 128, VEC>(p, s);
+    if (p.H <= 4096) return launch_rows<T, 1, 512, VEC>(p, s);
+    if (p.H <= 8192) return launch_rows<T, 1, 1024, VEC>(p, s);
+    if (p.H <= 16384) return launch_rows<T, 2, 1024, VEC>(p, s);
+    return launch_rows<T, 4, 1024, VEC>(p, s);
 }
 
 template <typename T>

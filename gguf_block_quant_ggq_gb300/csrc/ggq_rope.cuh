@@ -7,6 +7,8 @@
 #pragma once
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ggq_device.cuh"
 #include "ggq_kv.cuh"
 
@@ -21,7 +23,7 @@ struct Rotary {
     int half;   // pairs of a head
     int first;  // first turned channel
     int pairs;  // 1: neighbours (2 j, 2 j + 1), 0: halves (j, j + half)
-    int whole;  // half and first are multiples of 8 and the table starts at 16 bytes (cache writer)
+    int whole;  // 4, 8: half and first are multiples of it and the table starts at 16 bytes (cache writer)
 };
 
 // Queries and keys outside the cache that are turned: rows, heads, strides in elements.
@@ -48,38 +50,33 @@ __device__ __forceinline__ const float2* rotary_row(const Rotary& r, int64_t tok
 __device__ __forceinline__ float turned_a(float a, float b, float2 cs) { return __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y)); }
 __device__ __forceinline__ float turned_b(float a, float b, float2 cs) { return __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x)); }
 
-// V consecutive elements of a row
-template <int V>
-__device__ __forceinline__ void ldv(const float* p, float (&x)[V]) {
-    if constexpr (V == 1) x[0] = *p;
-    else
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 f = ld4(p + i);
-            x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
-        }
-}
+// V consecutive elements of a row, as they come from memory
 template <int V, typename T>
-__device__ __forceinline__ void ldv(const T* p, float (&x)[V]) {
-    if constexpr (V == 1) {
-        x[0] = ld1(p);
-    } else if constexpr (V == 4) {
-        const float4 f = ld4(p);
-        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-    } else {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct RawV {
+    static constexpr int kBytes = V * static_cast<int>(sizeof(T));
+    using Word = typename std::conditional<kBytes == 16, uint4, typename std::conditional<kBytes == 8, uint2, T>::type>::type;
+    Word w;
+    __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const Word*>(p); }
+    __device__ __forceinline__ void to(float (&x)[V]) const {
+        if constexpr (V == 1) {
+            x[0] = ld1(&w);
+        } else if constexpr (V == 4) {
+            const float4 f = ld4(reinterpret_cast<const T*>(&w));
+            x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+        } else {
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 2 && __is_same(T, __half)) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                x[2 * i] = f.x, x[2 * i + 1] = f.y;
-            } else {
-                x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (__is_same(T, __half)) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+                    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+                } else {
+                    x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                }
             }
         }
     }
-}
+};
 template <int V>
 __device__ __forceinline__ void stv(float* p, const float (&x)[V]) {
     if constexpr (V == 1) *p = x[0];
@@ -150,7 +147,10 @@ __device__ __forceinline__ void rotate_tile(const RotateParams& p, int64_t r0, i
         }
         const T* const src = static_cast<const T*>(p.x) + t * p.x_token;
         T* const dst = static_cast<T*>(p.out) + t * p.out_token;
-        const auto one = [&](T* to, const float (&a)[V], const float (&b)[V]) {
+        const auto one = [&](T* to, const RawV<V, T>& ra, const RawV<V, T>& rb) {
+            float a[V], b[V];
+            ra.to(a);
+            rb.to(b);
             if (!turn) {
                 stv<V>(to + ca, a);
                 if (two) stv<V>(to + cb, b);
@@ -173,42 +173,28 @@ __device__ __forceinline__ void rotate_tile(const RotateParams& p, int64_t r0, i
         };
         int h = h0;
         for (; h + 4 <= h1; h += 4) {
-            float a[4][V], b[4][V];
+            RawV<V, T> a[4], b[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                ldv<V>(src + (h + k) * p.x_head + ca, a[k]);
-                if (two) ldv<V>(src + (h + k) * p.x_head + cb, b[k]);
+                a[k].load(src + (h + k) * p.x_head + ca);
+                b[k].load(src + (h + k) * p.x_head + (two ? cb : ca));
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) one(dst + (h + k) * p.out_head, a[k], b[k]);
         }
         for (; h < h1; ++h) {
-            float a[V], b[V];
-            ldv<V>(src + h * p.x_head + ca, a);
-            if (two) ldv<V>(src + h * p.x_head + cb, b);
+            RawV<V, T> a, b;
+            a.load(src + h * p.x_head + ca);
+            b.load(src + h * p.x_head + (two ? cb : ca));
             one(dst + h * p.out_head, a, b);
         }
     }
 }
 
-// Table entries of channels c .. c + 7 (of a rotation of whole eights): four pairs (PAIRS), or eight.
-struct Turn8 {
-    float4 cs[4];
-};
-__device__ __forceinline__ Turn8 turn8_of(const Rotary& r, int c, const float2* entry) {
-    Turn8 t;
-    const int at = c - r.first, j = r.pairs ? at / 2 : at < r.half ? at : at - r.half;
-    const bool turned = entry && at >= 0 && at < 2 * r.half;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        t.cs[i] = turned && (i < 2 || !r.pairs) ? reinterpret_cast<const float4*>(entry + j)[i] : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-    return t;
-}
-
-// Channels c .. c + 7 of the head that starts at `head`, turned.  entry: the row's table entries, null: as they are; known:
-// those of these channels, of a rotation of whole eights, or null.
+// Channels c .. c + 7 (c a multiple of 8) of the head that starts at `head`, turned.  entry: the row's table entries, null:
+// as they are.
 template <typename T>
-__device__ __forceinline__ void turned8(const Rotary& r, const T* head, int c, const float2* entry, const Turn8* known, float (&x)[8]) {
+__device__ __forceinline__ void turned8(const Rotary& r, const T* head, int c, const float2* entry, float (&x)[8]) {
     const auto load = [&](int at, float (&v)[8]) {
         const float4 a = ld4(head + at), b = ld4(head + at + 4);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
@@ -216,36 +202,71 @@ __device__ __forceinline__ void turned8(const Rotary& r, const T* head, int c, c
     load(c, x);
     const int at = c - r.first;
     if (!entry || at + 8 <= 0 || at >= 2 * r.half) return;
-    if (r.whole && r.pairs) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            const float4 f = known ? known->cs[i / 4] : *reinterpret_cast<const float4*>(entry + (at + i) / 2);
-            const float e0 = x[i], o0 = x[i + 1], e1 = x[i + 2], o1 = x[i + 3];
-            x[i] = turned_a(e0, o0, make_float2(f.x, f.y)), x[i + 1] = turned_b(e0, o0, make_float2(f.x, f.y));
-            x[i + 2] = turned_a(e1, o1, make_float2(f.z, f.w)), x[i + 3] = turned_b(e1, o1, make_float2(f.z, f.w));
-        }
-    } else if (r.whole) {
-        const bool low = at < r.half;
-        const int j = low ? at : at - r.half;
+    if (r.whole == 8) {
+        // eight of the first halves, of the second ones, or four pairs
+        const bool low = r.pairs || at < r.half;
+        const int j = r.pairs ? at / 2 : low ? at : at - r.half;
         float other[8];
-        load(low ? c + r.half : c - r.half, other);
+        if (!r.pairs) load(low ? c + r.half : c - r.half, other);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float4 f = known ? known->cs[i / 2] : *reinterpret_cast<const float4*>(entry + j + i);
-            const float2 c0 = make_float2(f.x, f.y), c1 = make_float2(f.z, f.w);
-            x[i] = low ? turned_a(x[i], other[i], c0) : turned_b(other[i], x[i], c0);
-            x[i + 1] = low ? turned_a(x[i + 1], other[i + 1], c1) : turned_b(other[i + 1], x[i + 1], c1);
+            if (r.pairs) {
+                const float2 cs = entry[j + i / 2];
+                const float e = x[i], o = x[i + 1];
+                x[i] = turned_a(e, o, cs), x[i + 1] = turned_b(e, o, cs);
+            } else {
+                const float4 f = *reinterpret_cast<const float4*>(entry + j + i);
+                const float2 c0 = make_float2(f.x, f.y), c1 = make_float2(f.z, f.w);
+                x[i] = low ? turned_a(x[i], other[i], c0) : turned_b(other[i], x[i], c0);
+                x[i + 1] = low ? turned_a(x[i + 1], other[i + 1], c1) : turned_b(other[i + 1], x[i + 1], c1);
+            }
         }
-    } else {  // odd places: channel by channel
+        return;
+    }
+    // channel by channel
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int k = at + i;
-            if (k < 0 || k >= 2 * r.half) continue;
-            const bool low = r.pairs ? !(k & 1) : k < r.half;
-            const int j = r.pairs ? k >> 1 : low ? k : k - r.half, step = r.pairs ? 1 : r.half;
-            const float other = ld1(head + c + i + (low ? step : -step));
-            x[i] = low ? turned_a(x[i], other, entry[j]) : turned_b(other, x[i], entry[j]);
-        }
+    for (int i = 0; i < 8; ++i) {
+        const int k = at + i;
+        if (k < 0 || k >= 2 * r.half) continue;
+        const bool low = r.pairs ? !(k & 1) : k < r.half;
+        const int j = r.pairs ? k >> 1 : low ? k : k - r.half, step = r.pairs ? 1 : r.half;
+        const float other = ld1(head + c + i + (low ? step : -step));
+        x[i] = low ? turned_a(x[i], other, entry[j]) : turned_b(other, x[i], entry[j]);
+    }
+}
+
+// Two quads of a head of D channels that one thread turns: unit u of D / 8 (of a rotation of whole quads).
+struct Turn4 {
+    int ca, cb;    // first channels
+    bool turn;
+    float2 cs[4];
+};
+__device__ __forceinline__ Turn4 turn4_of(const Rotary& r, int u, const float2* entry) {
+    Turn4 t;
+    t.turn = 4 * u < r.half;
+    if (t.turn) {
+        t.ca = r.first + (r.pairs ? 8 * u : 4 * u), t.cb = t.ca + (r.pairs ? 4 : r.half);
+    } else {
+        const int k = 8 * u - 2 * r.half;  // of the channels that stay
+        t.ca = k < r.first ? k : k + 2 * r.half, t.cb = k + 4 < r.first ? k + 4 : k + 4 + 2 * r.half;
+    }
+    t.turn = t.turn && entry;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float4 f = t.turn ? *reinterpret_cast<const float4*>(entry + 4 * u + i) : make_float4(1.f, 0.f, 1.f, 0.f);
+        t.cs[i] = make_float2(f.x, f.y), t.cs[i + 1] = make_float2(f.z, f.w);
+    }
+    return t;
+}
+__device__ __forceinline__ void turn4(const Turn4& t, bool pairs, float4& a, float4& b) {
+    if (!t.turn) return;
+    const float4 p = a, q = b;
+    if (pairs) {
+        a = make_float4(turned_a(p.x, p.y, t.cs[0]), turned_b(p.x, p.y, t.cs[0]), turned_a(p.z, p.w, t.cs[1]), turned_b(p.z, p.w, t.cs[1]));
+        b = make_float4(turned_a(q.x, q.y, t.cs[2]), turned_b(q.x, q.y, t.cs[2]), turned_a(q.z, q.w, t.cs[3]), turned_b(q.z, q.w, t.cs[3]));
+    } else {
+        a = make_float4(turned_a(p.x, q.x, t.cs[0]), turned_a(p.y, q.y, t.cs[1]), turned_a(p.z, q.z, t.cs[2]), turned_a(p.w, q.w, t.cs[3]));
+        b = make_float4(turned_b(p.x, q.x, t.cs[0]), turned_b(p.y, q.y, t.cs[1]), turned_b(p.z, q.z, t.cs[2]), turned_b(p.w, q.w, t.cs[3]));
     }
 }
 
