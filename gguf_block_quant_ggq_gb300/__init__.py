@@ -61,9 +61,8 @@ SIGNATURES = {
     "ggq_moe_route": (_I32, [_P, _P, _I32, _P, _I64, _I64, _P, _P, _P]),
     "ggq_norm": (_I32, [_P, _P, _P]),
     "ggq_rotary_table": (_I32, [_P, _P, _I64, _I64, _P, _P]),
-    "ggq_rotate": (_I32, [_P, _P, _I32, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P]),
-    "ggq_kv_append": (_I32, [_P, _P, _P, _I32, _I32, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P,
-                             _I64, _P]),
+    "ggq_rotate": (_I32, [_P, _P, _P, _P]),
+    "ggq_kv_append": (_I32, [_P, _P, _P, _P, _P]),
     "ggq_adapt": (_I32, [_P, _P, _P, _P]),
     "ggq_logprobs": (_I32, [_P, _P, _P]),
     "ggq_block_dots_qa": (_I32, [_P, _I32, _I32, _P, _I64, _I64, _P, _I64, _P, _P]),
@@ -120,6 +119,19 @@ class ggq_rotary(ctypes.Structure):
                 ("first", ctypes.c_int32), ("layout", ctypes.c_int32)]
 
 
+class ggq_rotate_args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("D", ctypes.c_int32), ("T", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64), ("positions", ctypes.c_void_p)]
+
+
+class ggq_append_args(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("T", ctypes.c_int64)] + [
+        f for n in ("q", "q_out", "k", "v")
+        for f in ((n, ctypes.c_void_p), (n + "_token", ctypes.c_int64), (n + "_head", ctypes.c_int64))] + [
+        ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
 class ggq_rotary_spec(ctypes.Structure):
     _fields_ = [("turn", ctypes.c_int32), ("base", ctypes.c_double), ("factors", ctypes.c_void_p), ("factor", ctypes.c_double),
                 ("original_len", ctypes.c_int64), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
@@ -149,11 +161,14 @@ class ggq_logprobs_args(ctypes.Structure):
 _ATTN = struct.Struct("@iiqqPqqPqqPqPPqqffqP")
 _ROUTER = struct.Struct("@iiiiiifP")
 _NORM = struct.Struct("@iiqqPqPqPqqPqPqPiiPPfff4x")
-_ROTARY = struct.Struct("@Pqiii4x")
+_ROTATE = struct.Struct("@Pqiii4xiiiqPqqPqqP")  # ggq_rotary, then ggq_rotate_args
+_APPEND = struct.Struct("@Pqiii4xiiqPqqPqqPqqPqqPP")  # ggq_rotary, then ggq_append_args
 _ADAPT = struct.Struct("@iqqPqPqPqPP")
 _LOGPROBS = struct.Struct("@iiqqPqPqPPPPf4x")
 assert _ATTN.size == ctypes.sizeof(ggq_attn) and _ROUTER.size == ctypes.sizeof(ggq_router)
-assert _NORM.size == ctypes.sizeof(ggq_norm_args) and _ROTARY.size == ctypes.sizeof(ggq_rotary)
+_ARGS_AT = ctypes.sizeof(ggq_rotary)
+assert _NORM.size == ctypes.sizeof(ggq_norm_args) and _ROTATE.size == _ARGS_AT + ctypes.sizeof(ggq_rotate_args)
+assert _APPEND.size == _ARGS_AT + ctypes.sizeof(ggq_append_args)
 assert _ADAPT.size == ctypes.sizeof(ggq_adapt_args) and _LOGPROBS.size == ctypes.sizeof(ggq_logprobs_args)
 
 
@@ -294,8 +309,9 @@ class Context:
         self._router_args = ctypes.create_string_buffer(_ROUTER.size)
         self._attn_at, self._router_at = ctypes.addressof(self._attn_args), ctypes.addressof(self._router_args)
         self._attn_ready = False
-        self._step_args = ctypes.create_string_buffer(max(_NORM.size, _ROTARY.size, _ADAPT.size, _LOGPROBS.size))
+        self._step_args = ctypes.create_string_buffer(max(_NORM.size, _ROTATE.size, _APPEND.size, _ADAPT.size, _LOGPROBS.size))
         self._step_at = ctypes.addressof(self._step_args)
+        self._step_more = self._step_at + _ARGS_AT
         h = ctypes.c_void_p()
         st = load().ggq_create(ctypes.byref(h), device)
         if st != 0:
@@ -353,14 +369,15 @@ class Context:
             raise ValueError("the channels of a head have to be dense")
         return t.data_ptr(), code, token, head
 
-    def _mat(self, t, rows, cols, dtype):
-        """(address, row stride) of a [rows][cols] tensor of `dtype` on the context's device whose rows are dense."""
+    def _mat(self, t, shape, dtype):
+        """(address, row stride) of a tensor of a two-dimensional `shape` and `dtype` on the context's device whose rows are
+        dense."""
         if t.dtype is not dtype or t.get_device() != self.device:
             raise ValueError(f"expected a {dtype} tensor on cuda:{self.device}, got {t.dtype} on {t.device}")
-        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-            raise ValueError(f"expected a [{rows}, {cols}] tensor, got {tuple(t.shape)}")
+        if t.shape != shape:
+            raise ValueError(f"expected a {list(shape)} tensor, got {tuple(t.shape)}")
         row, one = t.stride()
-        if one != 1 and cols > 1:
+        if one != 1 and shape[1] > 1:
             raise ValueError("the channels of a row have to be dense")
         return t.data_ptr(), row
 
@@ -562,7 +579,8 @@ class Context:
         (uint8, into `packed` where given) that the products take; a given `out` then gets the float rows too."""
         if x.dim() != 2:
             raise ValueError(f"expected a [tokens, channels] tensor, got {tuple(x.shape)}")
-        n, H = x.shape
+        shape = x.shape
+        n, H = shape
         dtype = x.dtype
         code = self._code(dtype)
         norms = (after is not None) + 2 * (before is not None)
@@ -580,18 +598,18 @@ class Context:
             elif tuple(packed.shape) != (n, width):
                 raise ValueError(f"expected a [{n}, {width}] output, got {tuple(packed.shape)}")
             pp = self._vec(packed, self._torch.uint8)
-        xp, xt = self._mat(x, n, H, dtype)
-        rp, rt = self._mat(residual, n, H, dtype) if residual is not None else (0, 0)
-        tp, tt = self._mat(total, n, H, dtype) if total is not None else (0, 0)
-        op, ot = self._mat(out, n, H, dtype) if out is not None else (0, 0)
+        xp, xt = self._mat(x, shape, dtype)
+        rp, rt = self._mat(residual, shape, dtype) if residual is not None else (0, 0)
+        tp, tt = self._mat(total, shape, dtype) if total is not None else (0, 0)
+        op, ot = self._mat(out, shape, dtype) if out is not None else (0, 0)
         gp = gt = gc = 0
         if gate is not None:
             if gate.dim() == 1 and gate.shape[0] == H:
                 gp, gc = self._vec(gate, dtype), 1
             elif gate.dim() == 2 and gate.shape[1] == 1 and H != 1:
-                gp, gt = self._mat(gate, n, 1, dtype)
+                gp, gt = self._mat(gate, (n, 1), dtype)
             else:
-                gp, gt = self._mat(gate, n, H, dtype)
+                gp, gt = self._mat(gate, shape, dtype)
                 gc = 1
         ap = bp = 0
         if after is not None and after is not True:
@@ -631,15 +649,14 @@ class Context:
                                             self._stream(stream)))
         return out
 
-    def _rotary(self, table, positions, n, layout, first):
-        """Fills the rotation's arguments; the address of the positions."""
-        if table.dim() != 3 or table.shape[2] != 2:
-            raise ValueError(f"expected a [positions, turn / 2, 2] table, got {tuple(table.shape)}")
+    def _rotary(self, table, positions, n):
+        """(address of the table, its positions, turned channels, address of the positions) of a rotation of n tokens."""
+        shape = table.shape
+        if len(shape) != 3 or shape[2] != 2:
+            raise ValueError(f"expected a [positions, turn / 2, 2] table, got {tuple(shape)}")
         if positions.numel() != n:
             raise ValueError(f"expected {n} positions, got {positions.numel()}")
-        _ROTARY.pack_into(self._step_args, 0, self._vec(table, self._f32), table.shape[0], 2 * table.shape[1], first,
-                          ROTARY_LAYOUT[layout])
-        return self._vec(positions, self._i32)
+        return self._vec(table, self._f32), shape[0], 2 * shape[1], self._vec(positions, self._i32)
 
     def rotate(self, x, table, positions, layout: str = "half", first: int = 0, out=None, stream=None):
         """x [tokens][heads][D] with the channels from `first` on turned by the table's rows at positions (int32
@@ -653,8 +670,10 @@ class Context:
         op, ocode, ot, oh = self._rows(out, heads, dim)
         if ocode != code or out.shape[0] != n:
             raise ValueError("out has to have x's type and tokens")
-        pos = self._rotary(table, positions, n, layout, first)
-        st = _lib.ggq_rotate(self.handle, self._step_at, code, heads, dim, xp, xt, xh, op, ot, oh, pos, n, self._stream(stream))
+        tp, rows, turn, pos = self._rotary(table, positions, n)
+        _ROTATE.pack_into(self._step_args, 0, tp, rows, turn, first, ROTARY_LAYOUT[layout], code, heads, dim, n, xp, xt, xh, op, ot,
+                          oh, pos)
+        st = _lib.ggq_rotate(self.handle, self._step_at, self._step_more, self._stream(stream))
         if st:
             self._check(st)
         return out
@@ -682,9 +701,10 @@ class Context:
                 raise ValueError("q and q_out have to agree with k in type and tokens")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        pos = self._rotary(table, positions, n, layout, first)
-        st = _lib.ggq_kv_append(self.handle, cache.ref, self._step_at, code, heads, qp, qt, qh, op, ot, oh, kp, kt, kh, vp, vt,
-                                vh, self._vec(slots, self._i64), pos, n, self._stream(stream))
+        tp, rows, turn, pos = self._rotary(table, positions, n)
+        _APPEND.pack_into(self._step_args, 0, tp, rows, turn, first, ROTARY_LAYOUT[layout], code, heads, n, qp, qt, qh, op, ot, oh,
+                          kp, kt, kh, vp, vt, vh, self._vec(slots, self._i64), pos)
+        st = _lib.ggq_kv_append(self.handle, cache.ref, self._step_at, self._step_more, self._stream(stream))
         if st:
             self._check(st)
         return q_out
@@ -707,9 +727,10 @@ class Context:
             raise ValueError(f"{n} rows for {seqs} sequences: q_start is needed")
         if q_start is not None and q_start.numel() != seqs + 1:
             raise ValueError(f"{seqs} sequences need {seqs + 1} row starts")
-        xp, xt = self._mat(x, n, adapters.K, dtype)
-        yp, yt = self._mat(y, n, adapters.N, dtype)
-        op, ot = self._mat(out, n, adapters.N, dtype)
+        rows = (n, adapters.N)
+        xp, xt = self._mat(x, (n, adapters.K), dtype)
+        yp, yt = self._mat(y, rows, dtype)
+        op, ot = self._mat(out, rows, dtype)
         _ADAPT.pack_into(self._step_args, 0, code, n, seqs, xp, xt, yp, yt, op, ot, self._vec(ids, self._i32),
                          self._vec(q_start, self._i32))
         st = _lib.ggq_adapt(self.handle, adapters.ref, self._step_at, self._stream(stream))
@@ -724,7 +745,8 @@ class Context:
         is None."""
         if logits.dim() != 2:
             raise ValueError(f"expected [tokens, vocabulary] logits, got {tuple(logits.shape)}")
-        n, V = logits.shape
+        shape = logits.shape
+        n, V = shape
         code = self._code(logits.dtype)
         given = 0
         if tokens is not None:
@@ -750,7 +772,7 @@ class Context:
                 raise ValueError(f"expected [{n}, {top_k}] alternatives, got {tuple(ids.shape)} and {tuple(top.shape)}")
         elif ids is not None or top is not None:
             raise ValueError("alternatives without top_k")
-        lp, row = self._mat(logits, n, V, logits.dtype)
+        lp, row = self._mat(logits, shape, logits.dtype)
         _LOGPROBS.pack_into(self._step_args, 0, code, top_k, n, V, lp, row, self._vec(tokens, self._i32), given,
                             self._vec(logprobs, self._f32), self._vec(entropy, self._f32), self._vec(ids, self._i32),
                             self._vec(top, self._f32), scale)

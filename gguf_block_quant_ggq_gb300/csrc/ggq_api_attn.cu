@@ -82,11 +82,11 @@ ggq_status rotary_params(ggq_ctx* c, const ggq_rotary* r, int D, const int32_t* 
     return GGQ_OK;
 }
 
-ggq_status rotate_params(ggq_ctx* c, int dtype, int n_heads, int D, const void* x, int64_t x_token, int64_t x_head, void* out,
+ggq_status rotate_params(ggq_ctx* c, int dt, int n_heads, int D, const void* x, int64_t x_token, int64_t x_head, void* out,
                          int64_t out_token, int64_t out_head, int64_t T, const char* op, RotateParams* p) {
     if (n_heads < 0 || n_heads > 16384) return fail(c, GGQ_ERR_SHAPE, "%s: %d heads", op, n_heads);
     if (n_heads > 0 && (!x || !out)) return fail(c, GGQ_ERR_INVALID_ARG, "%s: null pointer", op);
-    if (!multiple_of(x, dtype_bytes(dtype)) || !multiple_of(out, dtype_bytes(dtype)))
+    if (!multiple_of(x, dtype_bytes(dt)) || !multiple_of(out, dtype_bytes(dt)))
         return fail(c, GGQ_ERR_INVALID_ARG, "%s: misaligned heads", op);
     p->x = x;
     p->out = out;
@@ -128,41 +128,40 @@ ggq_status ggq_kv_store(ggq_ctx* c, const ggq_kv_cache* kv, int dtype, const voi
     return e == cudaSuccess ? GGQ_OK : cuda_fail(c, e, "kv_store launch");
 }
 
-ggq_status ggq_rotate(ggq_ctx* c, const ggq_rotary* r, int dtype, int n_heads, int D, const void* x, int64_t x_token,
-                      int64_t x_head, void* out, int64_t out_token, int64_t out_head, const int32_t* positions, int64_t T,
-                      void* stream) {
+ggq_status ggq_rotate(ggq_ctx* c, const ggq_rotary* r, const ggq_rotate_args* a, void* stream) {
     DeviceScope scope;
     ggq_status s = check_ctx(c, scope);
     if (s != GGQ_OK) return s;
-    const int dt = dtype_of(dtype);
-    if (dt < 0) return fail(c, GGQ_ERR_UNSUPPORTED, "rotate: element type %d; supported: F32, F16, BF16", dtype);
-    if (T < 0 || T > INT32_MAX) return fail(c, GGQ_ERR_SHAPE, "rotate: T=%lld", static_cast<long long>(T));
-    if (T == 0 || n_heads == 0) return GGQ_OK;
+    if (!a) return fail(c, GGQ_ERR_INVALID_ARG, "rotate: null arguments");
+    const int dt = dtype_of(a->dtype);
+    if (dt < 0) return fail(c, GGQ_ERR_UNSUPPORTED, "rotate: element type %d; supported: F32, F16, BF16", a->dtype);
+    if (a->T < 0 || a->T > INT32_MAX) return fail(c, GGQ_ERR_SHAPE, "rotate: T=%lld", static_cast<long long>(a->T));
+    if (a->T == 0 || a->n_heads == 0) return GGQ_OK;
     RotateParams p{};
-    s = rotary_params(c, r, D, positions, "rotate", &p.r);
-    if (s == GGQ_OK) s = rotate_params(c, dt, n_heads, D, x, x_token, x_head, out, out_token, out_head, T, "rotate", &p);
+    s = rotary_params(c, r, a->D, a->positions, "rotate", &p.r);
+    if (s == GGQ_OK)
+        s = rotate_params(c, dt, a->n_heads, a->D, a->x, a->x_token, a->x_head, a->out, a->out_token, a->out_head, a->T, "rotate", &p);
     if (s != GGQ_OK) return s;
     const cudaError_t e = launch_rotate(p, dt, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GGQ_OK : cuda_fail(c, e, "rotate launch");
 }
 
-ggq_status ggq_kv_append(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_rotary* r, int dtype, int n_heads, const void* q,
-                         int64_t q_token, int64_t q_head, void* q_out, int64_t q_out_token, int64_t q_out_head, const void* k,
-                         int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head, const int64_t* slots,
-                         const int32_t* positions, int64_t T, void* stream) {
+ggq_status ggq_kv_append(ggq_ctx* c, const ggq_kv_cache* kv, const ggq_rotary* r, const ggq_append_args* a, void* stream) {
     DeviceScope scope;
     ggq_status s = check_ctx(c, scope);
     if (s != GGQ_OK) return s;
+    if (!a) return fail(c, GGQ_ERR_INVALID_ARG, "kv_append: null arguments");
     KvParams p{};
     int dt = -1;
-    s = kv_params(c, kv, dtype, k, k_token, k_head, v, v_token, v_head, slots, T, "kv_append", &p, &dt);
-    if (s != GGQ_OK || T == 0) return s;
+    s = kv_params(c, kv, a->dtype, a->k, a->k_token, a->k_head, a->v, a->v_token, a->v_head, a->slots, a->T, "kv_append", &p, &dt);
+    if (s != GGQ_OK || a->T == 0) return s;
     RotateParams rot{};
-    s = rotary_params(c, r, kv->head_dim, positions, "kv_append", &rot.r);
+    s = rotary_params(c, r, kv->head_dim, a->positions, "kv_append", &rot.r);
     if (s == GGQ_OK)
-        s = rotate_params(c, dt, n_heads, kv->head_dim, q, q_token, q_head, q_out, q_out_token, q_out_head, T, "kv_append", &rot);
+        s = rotate_params(c, dt, a->n_heads, kv->head_dim, a->q, a->q_token, a->q_head, a->q_out, a->q_out_token, a->q_out_head, a->T,
+                          "kv_append", &rot);
     if (s != GGQ_OK) return s;
-    rot.slots = slots;
+    rot.slots = a->slots;
     const cudaError_t e = launch_kv_append(p, rot, dt, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GGQ_OK : cuda_fail(c, e, "kv_append launch");
 }

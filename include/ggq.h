@@ -236,6 +236,35 @@ typedef struct ggq_rotary {
     int32_t layout;         /* ggq_rotary_layout                                         */
 } ggq_rotary;
 
+/* Arguments of ggq_rotate (device pointers; strides in elements, a head's channels dense). */
+typedef struct ggq_rotate_args {
+    int32_t dtype;          /* ggq_dtype of x and out                                    */
+    int32_t n_heads, D;     /* D <= 1024                                                 */
+    int64_t T;
+    const void* x;          /* [T][n_heads][D]                                           */
+    int64_t x_token, x_head;
+    void* out;              /* [T][n_heads][D]; may be x, with its strides               */
+    int64_t out_token, out_head;
+    const int32_t* positions; /* [T] */
+} ggq_rotate_args;
+
+/* Arguments of ggq_kv_append: of ggq_kv_store and of ggq_rotate (of the queries; D is the cache's head_dim). */
+typedef struct ggq_append_args {
+    int32_t dtype;          /* ggq_dtype of q, q_out, k and v                            */
+    int32_t n_heads;        /* query heads, 0: none                                      */
+    int64_t T;
+    const void* q;
+    int64_t q_token, q_head;
+    void* q_out;            /* may be q, with its strides                                */
+    int64_t q_out_token, q_out_head;
+    const void* k;          /* [T][n_kv_heads][D]                                        */
+    int64_t k_token, k_head;
+    const void* v;
+    int64_t v_token, v_head;
+    const int64_t* slots;   /* [T] */
+    const int32_t* positions; /* [T] */
+} ggq_append_args;
+
 /* The angles of ggq_rotary_table (host memory). */
 typedef struct ggq_rotary_spec {
     int32_t turn;           /* as in ggq_rotary                                          */
@@ -586,15 +615,12 @@ ggq_status ggq_norm(ggq_ctx* ctx, const ggq_norm_args* args, void* stream);
  * spec and its factors are host memory, read before the call returns.  Needs no scratch. */
 ggq_status ggq_rotary_table(ggq_ctx* ctx, const ggq_rotary_spec* spec, int64_t first, int64_t n, float* table, void* stream);
 
-/* Rotate heads by their tokens' positions [T]: x [T][n_heads][D] of dtype (strides in elements, D
- * dense, D <= 1024) to out.  Of a head's channels the `turn` from `first` on are turned in pairs,
+/* Rotate heads by their tokens' positions: x [T][n_heads][D] to out.  Of a head's channels the `turn` from `first` on are turned in pairs,
  * j and j + turn / 2 of them (HALF) or 2 j and 2 j + 1 (PAIRS): (a, b) -> (a c - b s, a s + b c)
  * with (c, s) = table[position][j], in fp32, each product and the sum rounded; the others are
  * copied.  out may be x with its strides, and must not overlap it otherwise.  A position outside
  * the table turns nothing and is reported by ggq_sync_status.  Needs no scratch. */
-ggq_status ggq_rotate(ggq_ctx* ctx, const ggq_rotary* rotary, int dtype, int n_heads, int D, const void* x,
-                      int64_t x_token, int64_t x_head, void* out, int64_t out_token, int64_t out_head,
-                      const int32_t* positions, int64_t T, void* stream);
+ggq_status ggq_rotate(ggq_ctx* ctx, const ggq_rotary* rotary, const ggq_rotate_args* args, void* stream);
 
 /* ggq_kv_store with the rotation on the way: keys are turned as ggq_rotate turns them and
  * quantized unrounded (fp32), values are stored as they are, and the n_heads query heads q are
@@ -602,10 +628,7 @@ ggq_status ggq_rotate(ggq_ctx* ctx, const ggq_rotary* rotary, int dtype, int n_h
  * Rows of every token whose slot is negative (padding) are not stored; their queries are turned,
  * and their positions are not reported.  Other arguments, checks and reports as in ggq_kv_store
  * and ggq_rotate. */
-ggq_status ggq_kv_append(ggq_ctx* ctx, const ggq_kv_cache* cache, const ggq_rotary* rotary, int dtype, int n_heads,
-                         const void* q, int64_t q_token, int64_t q_head, void* q_out, int64_t q_out_token,
-                         int64_t q_out_head, const void* k, int64_t k_token, int64_t k_head, const void* v,
-                         int64_t v_token, int64_t v_head, const int64_t* slots, const int32_t* positions, int64_t T,
+ggq_status ggq_kv_append(ggq_ctx* ctx, const ggq_kv_cache* cache, const ggq_rotary* rotary, const ggq_append_args* args,
                          void* stream);
 
 /* Low-rank adapters beside a projection: out[t] = y[t] + scales[a] * B_a (A_a x[t]) for the rows t

@@ -265,5 +265,5 @@ def table_status(ctx, turn=8, n=4, first=0, base=10000.0, factor=1.0, factors=No
 def test_null_context():
     L = ggq.load()
     assert L.ggq_rotary_table(None, None, 0, 0, None, None) == 1
-    assert L.ggq_rotate(None, None, 0, 1, 64, None, 0, 0, None, 0, 0, None, 1, None) == 1
-    assert L.ggq_kv_append(None, None, None, 0, 0, None, 0, 0, None, 0, 0, None, 0, 0, None, 0, 0, None, None, 1, None) == 1
+    assert L.ggq_rotate(None, None, ctypes.byref(ggq.ggq_rotate_args()), None) == 1
+    assert L.ggq_kv_append(None, None, None, ctypes.byref(ggq.ggq_append_args()), None) == 1
