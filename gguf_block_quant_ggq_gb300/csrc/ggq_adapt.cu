@@ -258,7 +258,7 @@ struct Plan {
 
 // BF: banks of bf16, else f16.  NT: 8-column tiles of the rank.  MT: tiles of 16 rows.
 template <typename T, bool BF, int NT, int WARPS, int MT>
-__global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : 2) k_adapt(const __grid_constant__ AdaptParams p) {
+__global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : WARPS == 4 ? 4 : 2) k_adapt(const __grid_constant__ AdaptParams p) {
     using P = Plan<T, WARPS, MT>;
     // terms: of x and A's bank, of A x and B's bank
     constexpr bool F16 = __is_same(T, __half) && !BF;
@@ -394,16 +394,26 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : 2) k_adapt(const __gr
                 uint32_t u[4][kA][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) terms_of<!BF && !F16>(*reinterpret_cast<const uint4*>(bank + 8 * (j0 + j) * kBankPitch), u[j]);
+                // (of fp32 rows a block at a time: the instruction's own additions cut off what they do not hold, which
+                // over 4096 inputs showed, 1.1e-6 of the result)
+                constexpr bool ALONE = sizeof(T) == 4;
+                float block[4][4] = {};
 #pragma unroll
-                for (int i = 0; i < kX; ++i)
+                for (int i = kX - 1; i >= 0; --i)
 #pragma unroll
-                    for (int k = 0; k < kA; ++k) {
+                    for (int k = kA - 1; k >= 0; --k) {
                         if (i + k >= (kX > kA ? kX : kA)) continue;  // below the last bit
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) mma_k16<!F16>(acc[j0 + j], f[i][q], u[j][k][2 * q], u[j][k][2 * q + 1]);
+                            for (int j = 0; j < 4; ++j)
+                                mma_k16<!F16>(ALONE ? block[j] : acc[j0 + j], f[i][q], u[j][k][2 * q], u[j][k][2 * q + 1]);
                     }
+                if constexpr (ALONE)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j0 + j][e] += block[j][e];
             }
         }
     }
@@ -606,10 +616,14 @@ cudaError_t launch_type(const AdaptParams& p, cudaStream_t s) {
         if (p.R <= 64) return launch<T, BF, 8, 8, 4>(p, groups, parts, s);
         return launch<T, BF, 16, 8, 4>(p, groups, parts, s);
     }
-    // 16 CTAs a group while they are few (one row, 4096 to 14336, rank 16: 9.7 us with 16, 14.9 with 8), 4 of many (32 rows of
-    // 32 adapters of rank 64: 16.1 us with 4, 20.3 with 8; 256 of 32: 32.7 and 41.3)
-    const int parts = groups <= 16 ? 16 : groups <= 24 ? 8 : 4;
-    if (p.R <= 64) return launch<T, BF, 8, 8, 1>(p, groups, parts, s);
+    // Eight warps and 16 CTAs a group while they are few (one row, 4096 to 14336, rank 16: 9.5 us; 12.9 with 8 CTAs); 8 CTAs if two
+    // fit an SM, else 4 (64 rows of 24 adapters to 6144, rank 16: 10.8 us, 14.4 with 4; rank 64: 15.1 with 4, 23.0 with 16); of
+    // many groups small CTAs, four an SM (256 rows of 32 adapters, rank 64: 25.7 us, 32.6 with 4 of eight warps).
+    if (p.R <= 64) {
+        if (groups > 96) return launch<T, BF, 8, 4, 1>(p, groups, 8, s);
+        return launch<T, BF, 8, 8, 1>(p, groups, groups <= 16 ? 16 : p.R <= 32 ? 8 : 4, s);
+    }
+    const int parts = groups <= 16 ? 16 : 8;
     // (wide blocks of high ranks do not fit a CTA)
     if (p.R <= 128) return launch<T, BF, 16, 4, 1>(p, groups, parts, s);
     return launch<T, BF, 32, 4, 1>(p, groups, parts, s);
