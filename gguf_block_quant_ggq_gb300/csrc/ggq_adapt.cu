@@ -230,20 +230,21 @@ __host__ __device__ constexpr int up32(int r) { return (r + 31) / 32 * 32; }
 //   t    the whole A x as the matrix instruction's operand: [rows / 16][steps of 16][term][32 lanes][4 words],
 //        and before it the sums of half of the parts of a block;
 //   ring: the blocks' copies; those of the first product over t too.
-template <typename T, int WARPS, int MT>
+template <typename T, int NT, int WARPS, int MT>
 struct Plan {
-    int sums, t, stage1, stage2, stages1, stages2;
+    int sums, t, stage1, stage2, stages1, stages2, ctas;
     static constexpr int kTerms = sizeof(T) == 4 ? 3 : 2;  // of A x
     static constexpr int kParts = WARPS / MT, kBlock = 32 * kParts, kRows = 16 * MT;
-    __host__ __device__ constexpr explicit Plan(int R, bool alone = false) : sums(0), t(0), stage1(0), stage2(0), stages1(0), stages2(0) {
+    __host__ __device__ constexpr explicit Plan(int R, bool alone = false) : sums(0), t(0), stage1(0), stage2(0), stages1(0), stages2(0), ctas(1) {
         sums = kRows * (up32(R) + 4) * 4;
         t = kRows * up32(R) * 2 * kTerms;
         if (t < kParts / 2 * sums) t = kParts / 2 * sums;
         stage1 = kRows * row_pitch<T>(kBlock) + up32(R) * bank_pitch(2 * kBlock);
         stage2 = kRows * row_pitch<T>(kBlock) + kBlock * bank_pitch(2 * R);
-        // two to four blocks at once, of two CTAs an SM if they fit (and there are so many: not `alone`)
-        const int half = kSmemLimit / 2 - 2048;
-        const int room = bytes(2, 2) <= half && !alone ? half : kSmemLimit - 2048;
+        // two to four blocks at once, of as many CTAs an SM as have registers if they fit (and there are so many: not `alone`)
+        ctas = alone ? 1 : WARPS == 8 ? 2 : NT > 8 ? 3 : 4;
+        while (ctas > 1 && bytes(2, 2) > kSmemLimit / ctas - 2048) --ctas;
+        const int room = kSmemLimit / ctas - 2048;
         for (stages1 = 2; stages1 < 4 && bytes(stages1 + 1, 2) <= room;) ++stages1;
         for (stages2 = 2; stages2 < 4 && bytes(2, stages2 + 1) <= room;) ++stages2;
     }
@@ -258,8 +259,8 @@ struct Plan {
 
 // BF: banks of bf16, else f16.  NT: 8-column tiles of the rank.  MT: tiles of 16 rows.
 template <typename T, bool BF, int NT, int WARPS, int MT>
-__global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : WARPS == 4 ? 4 : 2) k_adapt(const __grid_constant__ AdaptParams p) {
-    using P = Plan<T, WARPS, MT>;
+__global__ void __launch_bounds__(32 * WARPS, NT > 16 ? 1 : WARPS == 8 ? 2 : NT > 8 ? 3 : 4) k_adapt(const __grid_constant__ AdaptParams p) {
+    using P = Plan<T, NT, WARPS, MT>;
     // terms: of x and A's bank, of A x and B's bank
     constexpr bool F16 = __is_same(T, __half) && !BF;
     constexpr int kX = sizeof(T) == 4 ? 3 : __is_same(T, __half) && BF ? 2 : 1, kA = BF || F16 ? 1 : 2, kT = P::kTerms, kB = BF ? 1 : 2;
@@ -463,25 +464,33 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : WARPS == 4 ? 4 : 2) k
         __syncthreads();
         if (sub < kHalf) put(mine, true);
         __syncthreads();
-        for (int i = tid; i < kRows * nt * 8; i += kThreads) {
-            const int at = i / (nt * 8) * pitch + i % (nt * 8);
-            float v = parts_sums[at];
+        constexpr int kLanes = kThreads / kRows;  // of a row
+        for (int i = tid % kLanes * 4; i < nt * 8; i += 4 * kLanes) {
+            const int at = tid / kLanes * pitch + i;
+            float4 v = ld4(parts_sums + at);
 #pragma unroll
-            for (int h = 1; h < kHalf; ++h) v += parts_sums[at + h * kRows * pitch];
-            sums[at] = v;
+            for (int h = 1; h < kHalf; ++h) {
+                const float4 w = ld4(parts_sums + at + h * kRows * pitch);
+                v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+            }
+            st4(sums + at, v);
         }
     }
     cluster_arrive();
     cluster_wait();
     // the sums of all CTAs, scaled, as the second product's operand
-    const int eights = wide / 8;
-    for (int i = tid; i < kRows * eights * 4; i += kThreads) {
-        // eight ranks of a row; four lanes add up a quarter of the CTAs each
-        const int r = (i >> 2) / eights, o = (i >> 2) - r * eights, quarter = i & 3;
-        float t[8] = {};
-        if (8 * o < rank && r < rows) {
-#pragma unroll 4
-            for (int c = quarter * parts / 4; c < (quarter + 1) * parts / 4; ++c) {
+    // Eight ranks of a row at a time, by four lanes that add up a quarter of the CTAs each; a thread has kAtOnce of them
+    // under way.
+    const int eights = (rank + 31) / 32 * 4, items = kRows * eights;
+    constexpr int kAtOnce = MT == 1 ? 1 : 2;
+    for (int i0 = tid >> 2; i0 < items; i0 += kAtOnce * (kThreads / 4)) {
+        const int quarter = tid & 3;
+        float t[kAtOnce][8] = {};
+        for (int c = quarter * parts / 4; c < (quarter + 1) * parts / 4; ++c)
+#pragma unroll
+            for (int n = 0; n < kAtOnce; ++n) {
+                const int i = i0 + n * (kThreads / 4), r = i / eights, o = i - r * eights;
+                if (i >= items || r >= rows || 8 * o >= rank) continue;
                 const uint32_t at = cluster_addr(sums + r * pitch + 8 * o, c);
                 float v[8];
 #pragma unroll
@@ -490,26 +499,27 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : WARPS == 4 ? 4 : 2) k
                                  : "=f"(v[4 * q]), "=f"(v[4 * q + 1]), "=f"(v[4 * q + 2]), "=f"(v[4 * q + 3])
                                  : "r"(at + 16 * q));
 #pragma unroll
-                for (int e = 0; e < 8; ++e) t[e] += v[e];
+                for (int e = 0; e < 8; ++e) t[n][e] += v[e];
             }
-        }
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1)
+        for (int n = 0; n < kAtOnce; ++n) {
+            const int i = i0 + n * (kThreads / 4), r = i / eights, o = i - r * eights;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] += __shfl_xor_sync(kFull, t[e], d);
+            for (int d = 1; d < 4; d <<= 1)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = 8 * o + e < rank ? t[e] * scale : 0.0f;
-        // lane 4 (r % 8) + o % 4 of the steps of these 32 ranks; register (r / 8) % 2 and that + 2
-        const int lane4 = ((r & 7) * 4 + (o & 3)) * 4 + ((r >> 3) & 1);
-        // (a step: four neighbours as two pairs)
-        uint32_t* const to = t_words + ((r >> 4) * (wide / 16) + (o >> 2) * 2) * kT * 128 + lane4;
+                for (int e = 0; e < 8; ++e) t[n][e] += __shfl_xor_sync(kFull, t[n][e], d);
+            if (i >= items) continue;
+            // this lane's pair of the eight is lane 4 (r % 8) + o % 4's, registers (r / 8) % 2 and that + 2 of a step of 16
+            uint32_t* const to = t_words + ((r >> 4) * (wide / 16) + (o >> 2) * 2) * kT * 128 + ((r & 7) * 4 + (o & 3)) * 4 + ((r >> 3) & 1);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (q != quarter) continue;
-            uint32_t v[kT];
-            split(t[2 * q], t[2 * q + 1], v);
+            for (int q = 0; q < 4; ++q) {
+                if (q != quarter) continue;
+                const int e = 8 * o + 2 * q;
+                uint32_t v[kT];
+                split(e < rank ? t[n][2 * q] * scale : 0.0f, e + 1 < rank ? t[n][2 * q + 1] * scale : 0.0f, v);
 #pragma unroll
-            for (int k = 0; k < kT; ++k) to[((q >> 1) * kT + k) * 128 + 2 * (q & 1)] = v[k];
+                for (int k = 0; k < kT; ++k) to[((q >> 1) * kT + k) * 128 + 2 * (q & 1)] = v[k];
+            }
         }
     }
     cluster_arrive();  // nobody leaves before its sums are read
@@ -561,9 +571,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : WARPS == 4 ? 4 : 2) k
             T* const to = (r ? out_hi : out_lo) + b * kBlock;
             float v[8];
             if (p.y_whole) {
-                const T* const from = reinterpret_cast<const T*>(stage + at * kPitch) + 32 * sub + 8 * tq;
-                const float4 a = ld4(from), c = ld4(from + 4);
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = c.x, v[5] = c.y, v[6] = c.z, v[7] = c.w;
+                ld8(reinterpret_cast<const T*>(stage + at * kPitch) + 32 * sub + 8 * tq, v);
             } else {
                 const T* const from = y + sh.row[at] * p.y_token + n0 + n;
 #pragma unroll
@@ -573,7 +581,9 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : WARPS == 4 ? 4 : 2) k
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) v[2 * j + e] += o[j][2 * r + e];
-            if (p.out_whole && n + 8 <= outputs) {
+            if (p.out_whole == 2 && n + 8 <= outputs) {
+                st8(to, v);
+            } else if (p.out_whole && n + 8 <= outputs) {
                 st4(to, make_float4(v[0], v[1], v[2], v[3]));
                 st4(to + 4, make_float4(v[4], v[5], v[6], v[7]));
             } else {
@@ -588,7 +598,7 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 8 ? 1 : WARPS == 4 ? 4 : 2) k
 
 template <typename T, bool BF, int NT, int WARPS, int MT>
 cudaError_t launch(AdaptParams p, int64_t groups, int parts, cudaStream_t s) {
-    using P = Plan<T, WARPS, MT>;
+    using P = Plan<T, NT, WARPS, MT>;
     static_assert(P(8 * NT).bytes() + 1024 <= kSmemLimit, "ring, operand and sums of the largest rank in a CTA's shared memory");
     const P plan(p.R, groups * parts <= 152);
     p.stages1 = plan.stages1, p.stages2 = plan.stages2;
@@ -607,15 +617,15 @@ cudaError_t launch(AdaptParams p, int64_t groups, int parts, cudaStream_t s) {
 
 template <typename T, bool BF>
 cudaError_t launch_type(const AdaptParams& p, cudaStream_t s) {
-    const int64_t rows = p.q_start && p.T > 8 * p.seqs && p.R <= 128 ? 64 : 16;
-    const int64_t groups = p.q_start ? p.T / rows + std::min(p.seqs, p.T) : p.seqs;
-    if (rows == 64) {  // more than eight rows a sequence
-        // CTAs a tile: so many that two an SM are in flight at once (five prompts of 150 to 1000 rows, 47 tiles: 52.8 us
-        // with 4, 46.1 with 5, 63.8 with 6, whose clusters no longer fit all at once)
-        const int parts = std::max<int>(4, std::min<int>(8, 250 / groups));
-        if (p.R <= 64) return launch<T, BF, 8, 8, 4>(p, groups, parts, s);
-        return launch<T, BF, 16, 8, 4>(p, groups, parts, s);
+    if (p.q_start && p.T > 8 * p.seqs && p.R <= 128) {
+        // More than eight rows a sequence: tiles of 32 rows, and so many CTAs of a tile that those which fit the SMs at once
+        // are in flight (five prompts of 150 to 1000 rows, 92 tiles, rank 32: 49.5 us with 4, 40.1 with 6, 61.7 with 8).
+        const int64_t tiles = p.T / 32 + std::min(p.seqs, p.T);
+        const auto parts = [&](int ctas) { return std::max<int>(4, std::min<int>(8, 145 * ctas / tiles)); };
+        if (p.R <= 64) return launch<T, BF, 8, 4, 2>(p, tiles, parts(Plan<T, 8, 4, 2>(p.R).ctas), s);
+        return launch<T, BF, 16, 4, 2>(p, tiles, parts(Plan<T, 16, 4, 2>(p.R).ctas), s);
     }
+    const int64_t groups = p.q_start ? p.T / 16 + std::min(p.seqs, p.T) : p.seqs;
     // Eight warps and 16 CTAs a group while they are few (one row, 4096 to 14336, rank 16: 9.5 us; 12.9 with 8 CTAs); 8 CTAs if two
     // fit an SM, else 4 (64 rows of 24 adapters to 6144, rank 16: 10.8 us, 14.4 with 4; rank 64: 15.1 with 4, 23.0 with 16); of
     // many groups small CTAs, four an SM (256 rows of 32 adapters, rank 64: 25.7 us, 32.6 with 4 of eight warps).
@@ -641,7 +651,7 @@ cudaError_t launch_adapt(const AdaptParams& given, int dtype, cudaStream_t s) {
     };
     p.x_whole = whole(p.x, p.x_token, 16);
     p.y_whole = whole(p.y, p.y_token, 16) ? 2 : whole(p.y, p.y_token, 4 * size) ? 1 : 0;
-    p.out_whole = whole(p.out, p.out_token, 4 * size);
+    p.out_whole = whole(p.out, p.out_token, 16) ? 2 : whole(p.out, p.out_token, 4 * size) ? 1 : 0;
     const bool bf = p.bank == 2;
     if (dtype == 0) return bf ? launch_type<float, true>(p, s) : launch_type<float, false>(p, s);
     if (dtype == 1) return bf ? launch_type<__half, true>(p, s) : launch_type<__half, false>(p, s);

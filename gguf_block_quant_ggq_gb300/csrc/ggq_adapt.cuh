@@ -23,7 +23,7 @@ struct AdaptParams {
     const int32_t* q_start;  // [seqs + 1] or null: a row a sequence
     int64_t T, seqs;
     int bank;   // 1 f16, 2 bf16
-    int x_whole, y_whole, out_whole;  // rows start at 16 bytes (y: 2; 1: at four elements), out: at four elements (set by the launch)
+    int x_whole, y_whole, out_whole;  // rows start at 16 bytes (y, out: 2; 1: at four elements) (set by the launch)
     int stages1, stages2;            // blocks of the two products' rings (set by the launch)
     int* err;
 };

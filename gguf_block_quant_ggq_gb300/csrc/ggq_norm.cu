@@ -21,46 +21,6 @@ namespace ggq {
 
 namespace {
 
-__device__ __forceinline__ void ld8(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void ld8(const __half* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void ld8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-}
-__device__ __forceinline__ void st8(float* p, const float (&x)[8]) {
-    st4(p, make_float4(x[0], x[1], x[2], x[3]));
-    st4(p + 4, make_float4(x[4], x[5], x[6], x[7]));
-}
-template <typename T2, typename F>
-__device__ __forceinline__ void st8_pairs(void* p, const float (&x)[8], F pack) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const T2 h = pack(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void st8(__half* p, const float (&x)[8]) {
-    st8_pairs<__half2>(p, x, [](float a, float b) { return __floats2half2_rn(a, b); });
-}
-__device__ __forceinline__ void st8(__nv_bfloat16* p, const float (&x)[8]) {
-    st8_pairs<__nv_bfloat162>(p, x, [](float a, float b) { return __floats2bfloat162_rn(a, b); });
-}
-
 // Eight channels as they come from memory: asked for a row ahead
 template <typename T>
 struct Raw {
