@@ -6,13 +6,13 @@
 // One launch: a cluster of CTAs takes a group of rows of one adapter.  Its CTAs share the inputs: each multiplies
 // its part of K, the partial A x (rows x rank, fp32) meet through distributed shared memory, summed in the order
 // of the CTAs, and each CTA then takes its part of the N outputs.  So one row's banks are read by up to 16 SMs,
-// with no scratch and no second launch.  Groups are 64 rows of a sequence (prompts) or 16: of a sequence, or of
+// with no scratch and no second launch.  Groups are 32 rows of a sequence (long prompts) or 16: of a sequence, or of
 // single tokens, where a cluster stands for a row and works if its row is the first, 17th, ... of its adapter, so
 // that a bank is read once for 16 rows whatever the order of the ids is.
 //
 // Inside a CTA, blocks of x and bank (then of y and bank) come through a ring of shared memory by asynchronous
-// copies; memory is the bound, so what counts is bytes in flight: 50 to 100 KB an SM.  Eight warps are 4 tiles of
-// 16 rows times 2 parts of a block of 64 channels (outputs), or 1 times 8 parts of 256 (four: 128).  The order of the summed
+// copies; memory is the bound, so what counts is bytes in flight: 50 to 100 KB an SM.  Four warps are 2 tiles of
+// 16 rows times 2 parts of a block of 64 channels (outputs), or 1 times 4 parts of 128 (eight: 256).  The order of the summed
 // index is free as long as both operands of the matrix instruction share it, so a lane takes eight neighbouring
 // values as its elements of four k = 8 steps; the order of the outputs is free too: a lane's columns of four
 // 8-column tiles are eight neighbouring outputs, so y moves in whole vectors.
@@ -241,7 +241,7 @@ struct Plan {
         if (t < kParts / 2 * sums) t = kParts / 2 * sums;
         stage1 = kRows * row_pitch<T>(kBlock) + up32(R) * bank_pitch(2 * kBlock);
         stage2 = kRows * row_pitch<T>(kBlock) + kBlock * bank_pitch(2 * R);
-        // two to four blocks at once, of as many CTAs an SM as have registers if they fit (and there are so many: not `alone`)
+        // two to four blocks at once, of as many CTAs an SM as have registers if they fit (unless they all run `alone`)
         ctas = alone ? 1 : WARPS == 8 ? 2 : NT > 8 ? 3 : 4;
         while (ctas > 1 && bytes(2, 2) > kSmemLimit / ctas - 2048) --ctas;
         const int room = kSmemLimit / ctas - 2048;
@@ -596,11 +596,15 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 16 ? 1 : WARPS == 8 ? 2 : NT 
     cluster_wait();
 }
 
+// Clusters of so many CTAs, one an SM, that this part holds at once (its clusters of SMs differ in size).
+constexpr int at_once(int parts) { return parts > 8 ? 7 : parts > 4 ? 15 : 36; }
+
+// groups: of the grid; working: at most so many of them have rows of an adapter.
 template <typename T, bool BF, int NT, int WARPS, int MT>
-cudaError_t launch(AdaptParams p, int64_t groups, int parts, cudaStream_t s) {
+cudaError_t launch(AdaptParams p, int64_t groups, int64_t working, int parts, cudaStream_t s) {
     using P = Plan<T, NT, WARPS, MT>;
     static_assert(P(8 * NT).bytes() + 1024 <= kSmemLimit, "ring, operand and sums of the largest rank in a CTA's shared memory");
-    const P plan(p.R, groups * parts <= 152);
+    const P plan(p.R, working <= at_once(parts));
     p.stages1 = plan.stages1, p.stages2 = plan.stages2;
     static thread_local bool done[kMaxDevices] = {};
     const auto kernel = k_adapt<T, BF, NT, WARPS, MT>;
@@ -615,28 +619,33 @@ cudaError_t launch(AdaptParams p, int64_t groups, int parts, cudaStream_t s) {
     return launch_cluster(kernel, dim3(static_cast<unsigned>(groups * parts)), dim3(32 * WARPS), plan.bytes(), parts, s, p);
 }
 
+// What counts is that all working clusters are in flight at once, each of as many CTAs as that leaves (4096 to 4096, bf16
+// banks).  Of single tokens at most one group an adapter, and one more for each 16 rows, works.
 template <typename T, bool BF>
 cudaError_t launch_type(const AdaptParams& p, cudaStream_t s) {
-    if (p.q_start && p.T > 8 * p.seqs && p.R <= 128) {
-        // More than eight rows a sequence: tiles of 32 rows, and so many CTAs of a tile that those which fit the SMs at once
-        // are in flight (five prompts of 150 to 1000 rows, 92 tiles, rank 32: 49.5 us with 4, 40.1 with 6, 61.7 with 8).
-        const int64_t tiles = p.T / 32 + std::min(p.seqs, p.T);
+    const int64_t seqs = std::min(p.seqs, p.T), groups = p.q_start ? p.T / 16 + seqs : p.seqs;
+    const int64_t working = p.q_start ? groups : std::min(p.seqs, p.n + p.seqs / 16);
+    if (p.q_start && p.T > 8 * p.seqs && p.R <= 128 && working > (p.R <= 64 ? 74 : at_once(4))) {
+        // Prompts whose groups of 16 rows do not fit: tiles of 32 rows, and so many CTAs of a tile that those which fit the
+        // SMs at once are in flight (five prompts of 150 to 1000 rows, 92 tiles, fp32, rank 32: 49.5 us with 4, 40.1 with 6,
+        // 61.7 with 8; one of 2048, fp32, rank 64: 43.3 us, 63.6 in groups; one of 1024: 37.7, 33.1 in groups).
+        const int64_t tiles = p.T / 32 + seqs;
         const auto parts = [&](int ctas) { return std::max<int>(4, std::min<int>(8, 145 * ctas / tiles)); };
-        if (p.R <= 64) return launch<T, BF, 8, 4, 2>(p, tiles, parts(Plan<T, 8, 4, 2>(p.R).ctas), s);
-        return launch<T, BF, 16, 4, 2>(p, tiles, parts(Plan<T, 16, 4, 2>(p.R).ctas), s);
+        if (p.R <= 64) return launch<T, BF, 8, 4, 2>(p, tiles, tiles, parts(Plan<T, 8, 4, 2>(p.R).ctas), s);
+        return launch<T, BF, 16, 4, 2>(p, tiles, tiles, parts(Plan<T, 16, 4, 2>(p.R).ctas), s);
     }
-    const int64_t groups = p.q_start ? p.T / 16 + std::min(p.seqs, p.T) : p.seqs;
-    // Eight warps and 16 CTAs a group while they are few (one row, 4096 to 14336, rank 16: 9.5 us; 12.9 with 8 CTAs); 8 CTAs if two
-    // fit an SM, else 4 (64 rows of 24 adapters to 6144, rank 16: 10.8 us, 14.4 with 4; rank 64: 15.1 with 4, 23.0 with 16); of
-    // many groups small CTAs, four an SM (256 rows of 32 adapters, rank 64: 25.7 us, 32.6 with 4 of eight warps).
-    if (p.R <= 64) {
-        if (groups > 96) return launch<T, BF, 8, 4, 1>(p, groups, 8, s);
-        return launch<T, BF, 8, 8, 1>(p, groups, groups <= 16 ? 16 : p.R <= 32 ? 8 : 4, s);
-    }
-    const int parts = groups <= 16 ? 16 : 8;
+    // Many groups of low ranks: small CTAs, four an SM (192 rows of 64 adapters, fp32, rank 64: 30.2 us, 37.8 with 4 of
+    // eight warps; 96 of 32: 15.8 and 14.6).
+    if (p.R <= 64 && working > 74) return launch<T, BF, 8, 4, 1>(p, groups, working, 8, s);
+    // 16 CTAs of a group, 8 or 4, as many as fit (a prompt of 64 rows, fp32, rank 16: 9.2 us, 9.9 with 8; one of 128: 11.7 and
+    // 10.2; one of 256, rank 64: 23.6 with 8, 16.1 with 4).  Two CTAs of low ranks fit an SM; of single tokens, half of the
+    // adapters are taken to be in use (64 rows, 8 of 24 adapters, rank 64: 12.6 us with 8, 15.0 with 4).
+    const int most = at_once(8) * (p.R <= 32 ? 2 : 1) * (p.q_start ? 1 : 2);
+    const int parts = working <= at_once(16) ? 16 : working <= most ? 8 : 4;
+    if (p.R <= 64) return launch<T, BF, 8, 8, 1>(p, groups, working, parts, s);
     // (wide blocks of high ranks do not fit a CTA)
-    if (p.R <= 128) return launch<T, BF, 16, 4, 1>(p, groups, parts, s);
-    return launch<T, BF, 32, 4, 1>(p, groups, parts, s);
+    if (p.R <= 128) return launch<T, BF, 16, 4, 1>(p, groups, working, parts, s);
+    return launch<T, BF, 32, 4, 1>(p, groups, working, parts, s);
 }
 
 }  // namespace

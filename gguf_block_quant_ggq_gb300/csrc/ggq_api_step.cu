@@ -64,6 +64,14 @@ ggq_status ggq_norm(ggq_ctx* c, const ggq_norm_args* a, void* stream) {
     if (!multiple_of(a->x, size) || !multiple_of(a->residual, size) || !multiple_of(a->gate, size) || !multiple_of(a->total, size) ||
         !multiple_of(a->out, size) || !multiple_of(a->after, 4) || !multiple_of(a->before, 4))
         return fail(c, GGQ_ERR_INVALID_ARG, "norm: misaligned pointer");
+    const auto apart = [&](const void* to, int64_t to_token, const void* from, int64_t from_token) {
+        return to && to == from && a->T > 1 && to_token != from_token;
+    };
+    if (apart(a->total, a->total_token, a->x, a->x_token) || apart(a->total, a->total_token, a->residual, a->residual_token) ||
+        apart(a->out, a->out_token, a->x, a->x_token) || apart(a->out, a->out_token, a->residual, a->residual_token))
+        return fail(c, GGQ_ERR_INVALID_ARG, "norm: rows that are updated in place have one stride");
+    if (a->total && (a->total == a->out || a->total == a->packed))
+        return fail(c, GGQ_ERR_INVALID_ARG, "norm: total and its norm need a place each");
     NormParams p{};
     p.x = a->x;
     p.residual = a->residual;
@@ -167,6 +175,7 @@ ggq_status ggq_adapt(ggq_ctx* c, const ggq_adapters* b, const ggq_adapt_args* a,
         return fail(c, GGQ_ERR_INVALID_ARG, "adapt: rows of x must start at multiples of 4 elements (pointer and stride)");
     if (a->out == a->y && a->T > 1 && a->out_token != a->y_token)
         return fail(c, GGQ_ERR_INVALID_ARG, "adapt: rows that are updated in place have one stride");
+    if (a->out == a->x) return fail(c, GGQ_ERR_INVALID_ARG, "adapt: out must not be x, which every part of a row's outputs reads");
     AdaptParams p{};
     p.a = b->a;
     p.b = b->b;

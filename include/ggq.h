@@ -214,7 +214,7 @@ typedef struct ggq_norm_args {
     int64_t residual_token;
     const void* gate;       /* [T][H], one row for all tokens (gate_token = 0) or one value a token (gate_channel = 0); or NULL */
     int64_t gate_token, gate_channel;
-    void* total;            /* [T][H] or NULL; may be x or residual, with its stride     */
+    void* total;            /* [T][H] or NULL; may be x or residual, with its stride (not both it and out) */
     int64_t total_token;
     void* out;              /* [T][H] or NULL; may be x or residual, with its stride     */
     int64_t out_token;
@@ -633,11 +633,11 @@ ggq_status ggq_kv_append(ggq_ctx* ctx, const ggq_kv_cache* cache, const ggq_rota
 
 /* Low-rank adapters beside a projection: out[t] = y[t] + scales[a] * B_a (A_a x[t]) for the rows t
  * of every sequence whose adapter is a; rows of sequences without one are copied (not touched where
- * out is y), rows of no sequence are not written.  Products and sums are fp32 whatever the types:
- * 16-bit rows and banks enter exactly, fp32 rows of sequences of more than eight rows with 22 bits
- * or more.  x rows start at multiples of 4 elements (pointer and stride).  An adapter id outside 0 ..
- * n - 1 counts as none, row ranges outside 0 .. T are cut; both are reported by ggq_sync_status.  No
- * row may be of two sequences.  Needs no scratch. */
+ * out is y), rows of no sequence are not written.  Sums are fp32 whatever the types; rows and banks
+ * enter exactly (fp32 rows with 24 bits), scales[a] A_a x[t] with 24 bits beside fp32 rows and with 16
+ * beside 16-bit ones.  x rows start at multiples of 4 elements (pointer and stride), and out must not
+ * overlap x.  An adapter id from n on counts as none and row ranges outside 0 .. T are cut; both are
+ * reported by ggq_sync_status.  No row may be of two sequences.  Needs no scratch. */
 ggq_status ggq_adapt(ggq_ctx* ctx, const ggq_adapters* adapters, const ggq_adapt_args* args, void* stream);
 
 /* Log probabilities of rows of logits, p = softmax(scale * logits):

@@ -2,7 +2,8 @@
 
 Tolerance (fp32 sums of exact products; units of 2^-24 of the sum of magnitudes): a lane adds at most 16 products of
 every 512 inputs, 5 joins of lanes, K / 512 steps and 32 parts of the inputs, the scale, then 8 products and 5 joins of
-the outputs and the addition of y.  fp32 rows in tiles keep 22 bits of x and of A x: three more roundings of 2^-22."""
+the outputs and the addition of y.  fp32 rows are three terms of 8 bits, whose products below the last bit are left out,
+and so is A x: twelve units cover both."""
 import ctypes
 
 import pytest
@@ -111,6 +112,43 @@ def test_ragged_sequences(ctx, dtype, bank, R, K, N):
 
 
 @gpu
+@pytest.mark.parametrize("bank", BANKS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,K,N", [(8, 72, 40), (16, 1024, 260), (32, 520, 77), (64, 4096, 128), (128, 1032, 200), (77, 264, 65), (256, 512, 64)])
+def test_long_prompts(ctx, dtype, bank, R, K, N):
+    """From some hundred rows on: groups of 16 rows on four CTAs, then tiles of 32."""
+    c = Case(3, R, K, N, dtype, bank, ranks=[R, (R + 1) // 2, max(1, R - 3)])
+    ad = ctx.adapters(c.a, c.b, ranks=c.ranks, scales=c.scales)
+    for lens, ids in (([480], [0]), ([150, 0, 33, 417], [2, 0, 1, 0]), ([1300], [2]), ([31, 700, 64, 1, 900], [0, 1, -1, 2, 0]), ([2400], [1])):
+        start = [sum(lens[:i]) for i in range(len(lens) + 1)]
+        x, y = c.rows(start[-1] + 2, pad=1)
+        out = torch.full((start[-1] + 2, c.N), 9.0, device="cuda", dtype=dtype)
+        ctx.adapt(ad, x, y, ints(ids), q_start=ints(start), out=out)
+        assert bool((out[start[-1]:] == 9).all())
+        c.check(out[:start[-1]], x[:start[-1]], y[:start[-1]], ids, start)
+        same = y.clone()
+        ctx.adapt(ad, x, same, ints(ids), q_start=ints(start), out=same)
+        assert torch.equal(same[:start[-1]], out[:start[-1]]) and torch.equal(same[start[-1]:], y[start[-1]:])
+    ctx.sync_status()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R", [16, 64, 96, 160])
+@pytest.mark.parametrize("n", [20, 45, 90])
+def test_many_adapters(ctx, dtype, R, n):
+    """Single tokens and short sequences of more adapters than SMs take at once."""
+    c = Case(n, R, 520, 100, dtype, torch.bfloat16, ranks=[R if i % 3 else R // 2 for i in range(n)])
+    ad = ctx.adapters(c.a, c.b, ranks=c.ranks, scales=c.scales)
+    ids = [(7 * i) % (n + 1) - 1 for i in range(200)]
+    x, y = c.rows(200)
+    c.check(ctx.adapt(ad, x, y, ints(ids)), x, y, ids)
+    start = [4 * i for i in range(51)]
+    c.check(ctx.adapt(ad, x, y, ints(ids[:50]), q_start=ints(start)), x, y, ids[:50], start)
+    ctx.sync_status()
+
+
+@gpu
 @pytest.mark.parametrize("T", [3, 200])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_what_stands_behind_a_rank_is_not_used(ctx, dtype, T):
@@ -140,7 +178,7 @@ def test_values_that_are_not_finite_stay_in_their_row(ctx, T):
 @gpu
 @pytest.mark.parametrize("T", [1, 100])
 def test_large_and_small_fp32_values(ctx, T):
-    """Rows of very different size: products keep their 22 bits whatever the exponents are."""
+    """Rows of very different size: products keep their bits whatever the exponents are."""
     c = Case(1, 16, 1024, 64, torch.float32, torch.float16)
     ad = ctx.adapters(c.a, c.b, scales=c.scales)
     x, y = c.rows(T)
@@ -168,7 +206,7 @@ def test_outside_ids_and_ranges(ctx):
 
 @gpu
 def test_results_do_not_depend_on_the_company(ctx):
-    """A row's value is the same alone and in a batch of any order (single tokens)."""
+    """A row's value is the same in any order of the batch (single tokens)."""
     c = Case(3, 32, 1024, 300, torch.bfloat16, torch.bfloat16)
     ad = ctx.adapters(c.a, c.b)
     ids = [0, 1, 0, 2, 0, 0, 1, 0, 0, 0, 0, 0]
@@ -197,6 +235,9 @@ def test_refusals(ctx):
     wide = torch.zeros((4, 68), device="cuda")
     with pytest.raises(ggq.GGQError, match="multiples of 4"):
         ctx.adapt(ad, wide[:, 1:65], y, ids)
+    with pytest.raises(ggq.GGQError, match="must not be x"):
+        square = ctx.adapters(c.a, torch.zeros((2, 64, 8), device="cuda").bfloat16())
+        ctx.adapt(square, x, x, ids, out=x)
     with pytest.raises(ggq.GGQError, match="one stride"):
         big = torch.zeros((8, 40), device="cuda")
         ctx.adapt(ad, x, big[:4], ids, out=big[::2][:4])

@@ -178,6 +178,12 @@ def test_refusals(ctx):
             with pytest.raises(ggq.GGQError) as e:
                 ctx.norm(x, **bad)
             assert e.value.status == status
+    with pytest.raises(ggq.GGQError, match="a place each"):
+        ctx.norm(x, before=w, out=x, total=x)
+    wide = torch.zeros((4, 256), device="cuda")
+    for bad in (dict(total=wide[:2]), dict(before=w, out=wide[:2]), dict(residual=wide[:2], total=wide[::2])):
+        with pytest.raises(ggq.GGQError, match="one stride"):
+            ctx.norm(wide[::2], **bad)
     odd = torch.zeros((2, 264), device="cuda")[:, 1:257]
     with pytest.raises(ggq.GGQError, match="16 bytes"):
         ctx.norm(odd, before=True, act="Q8_K")
