@@ -7,8 +7,9 @@
 // its part of K, the partial A x (rows x rank, fp32) meet through distributed shared memory, summed in the order
 // of the CTAs, and each CTA then takes its part of the N outputs.  So one row's banks are read by up to 16 SMs,
 // with no scratch and no second launch.  Groups are 32 rows of a sequence (long prompts) or 16: of a sequence, or of
-// single tokens, where a cluster stands for a row and works if its row is the first, 17th, ... of its adapter, so
-// that a bank is read once for 16 rows whatever the order of the ids is.
+// single tokens of one adapter, so that a bank is read once for 16 rows whatever the order of the ids is: each cluster
+// counts through the ids and takes its group (64 rows of 24 adapters to 6144 outputs, bf16, rank 64: 11.9 us, where a
+// cluster a row, of which those work whose row is the first, 17th, ... of its adapter, took 14.7; so go more than 256 rows).
 //
 // Inside a CTA, blocks of x and bank (then of y and bank) come through a ring of shared memory by asynchronous
 // copies; memory is the bound, so what counts is bytes in flight: 50 to 100 KB an SM.  Four warps are 2 tiles of
@@ -36,6 +37,7 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxWarps = 8;
+constexpr int kAdaptSorted = 256;  // single tokens of a call whose ids every cluster looks at
 
 // ---------------------------------------------------------------- groups
 
@@ -71,19 +73,70 @@ __device__ __forceinline__ int block_scan(int v, int* count, int& total) {
     return before + sum - v;
 }
 
-// An adapter id that counts: -1 for none, one outside the adapters or of rank 0.
+// An adapter id that counts: -1 for none or one outside the adapters.
 __device__ __forceinline__ int adapter_of(const AdaptParams& p, int64_t seq) {
     const int a = p.ids[seq];
     if (a >= p.n) set_error(p.err, DEV_ERR_BAD_ADAPTER);
-    return a < 0 || a >= p.n || (p.ranks && p.ranks[a] <= 0) ? -1 : a;
+    return a < 0 || a >= p.n ? -1 : a;
 }
 
 // Finds the rows of cluster `c`: sh.rows of them (0: none) of adapter sh.adapter (-1: rows that stay as they are).
+// scratch: kAdaptSorted words of shared memory.
 template <int WARPS, int ROWS>
-__device__ __forceinline__ void find_group(const AdaptParams& p, Group<ROWS>& sh, int64_t c) {
+__device__ __forceinline__ void find_group(const AdaptParams& p, Group<ROWS>& sh, int* scratch, int64_t c) {
     constexpr int kThreads = 32 * WARPS;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) sh.rows = 0;
+    if (!p.q_start && p.seqs <= kAdaptSorted) {
+        // every row's place among its adapter's (-1: rows without one); every ROWS-th begins a group
+        constexpr int kEach = kAdaptSorted / kThreads;  // rows a thread
+        const int seqs = static_cast<int>(p.seqs);
+        int id[kEach], place[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int j = k * kThreads + tid;
+            id[k] = -1, place[k] = 0;
+            if (j < seqs) id[k] = adapter_of(p, j);
+            scratch[j] = id[k];
+        }
+        if (tid == 0) sh.adapter = -2;
+        __syncthreads();
+        bool begins[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int j = k * kThreads + tid;
+            if (j < seqs)
+                for (int i = 0; i < j; i += 4) {
+                    const int4 a = *reinterpret_cast<const int4*>(scratch + i);
+                    place[k] += (a.x == id[k]) + (i + 1 < j && a.y == id[k]) + (i + 2 < j && a.z == id[k]) + (i + 3 < j && a.w == id[k]);
+                }
+            begins[k] = j < seqs && place[k] % ROWS == 0;
+            const unsigned there = __ballot_sync(kFull, begins[k]);
+            if (lane == 0) sh.count[k * WARPS + warp] = __popc(there);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            int at = __popc(__ballot_sync(kFull, begins[k]) & ((1u << lane) - 1));
+#pragma unroll
+            for (int w = 0; w < kEach * WARPS; ++w) at += w < k * WARPS + warp ? sh.count[w] : 0;
+            if (begins[k] && at == c) sh.adapter = id[k], sh.first = place[k];
+        }
+        __syncthreads();
+        int rows = 0;
+        if (sh.adapter > -2) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int64_t at = place[k] - sh.first;
+                const bool mine = k * kThreads + tid < seqs && id[k] == sh.adapter && at >= 0 && at < ROWS;
+                if (mine) sh.row[at] = k * kThreads + tid;
+                rows += __syncthreads_count(mine);
+            }
+        }
+        if (tid == 0) sh.rows = rows;
+        __syncthreads();
+        return;
+    }
     if (!p.q_start) {
         const int id = p.ids[c];
         int next = tid < p.seqs ? p.ids[tid] : -1;
@@ -271,19 +324,30 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 16 ? 1 : WARPS == 8 ? 2 : NT 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Group<kRows> sh;
     const int parts = static_cast<int>(cluster_size()), part = static_cast<int>(cluster_rank());
-    find_group<WARPS>(p, sh, blockIdx.x / parts);
+    find_group<WARPS>(p, sh, reinterpret_cast<int*>(smem), blockIdx.x / parts);
     const int rows = sh.rows, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tq = lane & 3;
     if (rows == 0) return;  // of all the cluster's CTAs
     const T* const y = static_cast<const T*>(p.y);
     T* const out = static_cast<T*>(p.out);
     const int64_t n_step = ((p.N + 31) / 32 + parts - 1) / parts * 32, n0 = min(p.N, part * n_step), n1 = min(p.N, n0 + n_step);
-    if (sh.adapter < 0) {
+    const int rank = sh.adapter < 0 ? 0 : p.ranks ? min(p.R, p.ranks[sh.adapter]) : p.R;
+    if (rank <= 0) {
         if (p.out == p.y) return;
-        for (int r = warp; r < rows; r += WARPS)
-            for (int64_t n = n0 + lane; n < n1; n += 32) out[sh.row[r] * p.out_token + n] = y[sh.row[r] * p.y_token + n];
+        constexpr int kEach = 16 / sizeof(T);
+        const bool wide = p.y_whole == 2 && p.out_whole == 2;
+        const int count = static_cast<int>(n1 - n0), each = wide ? kEach : 1, chunks = (count + each - 1) / each;
+        for (int64_t i = tid; i < static_cast<int64_t>(rows) * chunks; i += kThreads) {
+            const int r = static_cast<int>(i / chunks), n = static_cast<int>(i - static_cast<int64_t>(r) * chunks) * each;
+            const T* const from = y + sh.row[r] * p.y_token + n0 + n;
+            T* const to = out + sh.row[r] * p.out_token + n0 + n;
+            if (wide && n + each <= count) {
+                *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+            } else {
+                for (int e = 0; e < each && n + e < count; ++e) to[e] = from[e];
+            }
+        }
         return;
     }
-    const int rank = p.ranks ? min(p.R, p.ranks[sh.adapter]) : p.R;
     const float scale = p.scales ? p.scales[sh.adapter] : 1.0f;
     const int k_step = ((p.K + 31) / 32 + parts - 1) / parts * 32, k0 = min(p.K, part * k_step), k1 = min(p.K, k0 + k_step);
     const uint16_t* const bank_a = static_cast<const uint16_t*>(p.a) + static_cast<int64_t>(sh.adapter) * p.R * p.K;
@@ -623,7 +687,8 @@ cudaError_t launch(AdaptParams p, int64_t groups, int64_t working, int parts, cu
 // banks).  Of single tokens at most one group an adapter, and one more for each 16 rows, works.
 template <typename T, bool BF>
 cudaError_t launch_type(const AdaptParams& p, cudaStream_t s) {
-    const int64_t seqs = std::min(p.seqs, p.T), groups = p.q_start ? p.T / 16 + seqs : p.seqs;
+    const int64_t seqs = std::min(p.seqs, p.T);
+    const int64_t groups = p.q_start ? p.T / 16 + seqs : p.seqs <= kAdaptSorted ? std::min(p.seqs, p.n + 1 + p.seqs / 16) : p.seqs;
     const int64_t working = p.q_start ? groups : std::min(p.seqs, p.n + p.seqs / 16);
     if (p.q_start && p.T > 8 * p.seqs && p.R <= 128 && working > (p.R <= 64 ? 74 : at_once(4))) {
         // Prompts whose groups of 16 rows do not fit: tiles of 32 rows, and so many CTAs of a tile that those which fit the
@@ -634,8 +699,8 @@ cudaError_t launch_type(const AdaptParams& p, cudaStream_t s) {
         if (p.R <= 64) return launch<T, BF, 8, 4, 2>(p, tiles, tiles, parts(Plan<T, 8, 4, 2>(p.R).ctas), s);
         return launch<T, BF, 16, 4, 2>(p, tiles, tiles, parts(Plan<T, 16, 4, 2>(p.R).ctas), s);
     }
-    // Many groups of low ranks: small CTAs, four an SM (192 rows of 64 adapters, fp32, rank 64: 30.2 us, 37.8 with 4 of
-    // eight warps; 96 of 32: 15.8 and 14.6).
+    // Many groups of low ranks: small CTAs, four an SM (192 rows of 64 adapters, fp32, rank 64, a cluster a row: 30.2 us, 37.8
+    // with 4 of eight warps; 96 of 32: 15.8 and 14.6; a cluster a group takes 23.9 and 14.8).
     if (p.R <= 64 && working > 74) return launch<T, BF, 8, 4, 1>(p, groups, working, 8, s);
     // 16 CTAs of a group, 8 or 4, as many as fit (a prompt of 64 rows, fp32, rank 16: 9.2 us, 9.9 with 8; one of 128: 11.7 and
     // 10.2; one of 256, rank 64: 23.6 with 8, 16.1 with 4).  Two CTAs of low ranks fit an SM; of single tokens, half of the

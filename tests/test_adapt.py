@@ -80,7 +80,7 @@ def ints(a):
 def test_single_tokens(ctx, dtype, bank, R, K, N):
     c = Case(5, R, K, N, dtype, bank, ranks=[R, 1, (R + 1) // 2, R, 0])
     ad = ctx.adapters(c.a, c.b, ranks=c.ranks, scales=c.scales)
-    for ids in ([0], [2, 2, -1, 1], [3] * 9 + [4, 0], [i * i % 5 for i in range(40)] + [-7], [1] * 300 + [2]):
+    for ids in ([0], [2, 2, -1, 1], [3] * 9 + [4, 0], [i * i % 5 for i in range(40)] + [-7], [1] * 300 + [2], [i * i % 6 - 1 for i in range(261)]):
         x, y = c.rows(len(ids), pad=1)
         got = ctx.adapt(ad, x, y, ints(ids))
         c.check(got, x, y, ids)
