@@ -130,7 +130,9 @@ if __name__ == "__main__":
                     "k_gmm<kind, format, dump>, k_gmmtc<format, dump>, k_direct<kind, format, "
                     "tokens, dump>, k_attn_stream<K is 4-bit, V is 4-bit, channels, rows (0 8 of fp32, 1 8 and 2 16 of 16 "
                     "bits)>, k_attn_prompt<K, V, channels, bf16>, k_attn_promptf<K, V, channels>, k_attn_rows<K, V, "
-                    "channels>, k_kv<store, channels, element> and k_route<keys a lane, element>; "
+                    "channels>, k_kv<store, channels, element>, k_kv_append<channels, query channels at once, element>, k_route<keys a "
+                    "lane, element>, k_norm<element, groups of 8 a thread, threads, whole groups>, k_rotate<channels at once, element>, "
+                    "k_adapt<element, bf16 banks, tiles of 8 ranks, warps, tiles of 16 rows> and k_logprobs<element, alternatives, threads>; "
                     "k_attn_prompt and k_attn_promptf launch with 96 and 72 registers and split them by warp role; formats 0 Q4_0, 1 Q8_0, 2 Q4_K, 3 Q5_K, 4 Q6_K, 5 MXFP4, 6 Q2_K, 7 Q3_K.\n\n")
             f.write(ptxas_summary())
     else:
