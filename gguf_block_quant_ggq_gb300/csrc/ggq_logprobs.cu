@@ -31,6 +31,7 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kMaxWarps = 16;
+constexpr int kMaxParts = 8;  // CTAs a row
 constexpr int kPool = 512;
 constexpr int kNone = INT32_MAX;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -100,9 +101,9 @@ struct Shared {
     float pick_x[kMaxWarps];
     int pick_id[kMaxWarps];
     // of the cluster's CTAs, in the first one
-    Sums part[16];
-    float part_x[16 * kLogprobsMaxTop];
-    int part_id[16 * kLogprobsMaxTop];
+    Sums part[kMaxParts];
+    float part_x[kMaxParts * kLogprobsMaxTop];
+    int part_id[kMaxParts * kLogprobsMaxTop];
 };
 
 // The entries of (x, id)[n] that come first, in order, to best_x, best_id (entries without an id come nowhere).  As many
@@ -127,7 +128,7 @@ __device__ __forceinline__ void rank_entries(const float* x, const int* id, int 
 template <int kRowThreads>
 __device__ __forceinline__ void rank_lists(const float* x, const int* id, int parts, int top, float* best_x, int* best_id) {
     const int n = parts * top;
-    int log_lanes = 4;  // lanes an entry, each with its share of the lists
+    int log_lanes = 3;  // lanes an entry, each with its share of the lists
     while (log_lanes > 0 && n << log_lanes > kRowThreads) --log_lanes;
     const int lanes = 1 << log_lanes, mine = threadIdx.x & (lanes - 1), step = kRowThreads >> log_lanes;
     for (int i0 = 0; i0 < n; i0 += step) {
@@ -443,22 +444,18 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
 template <typename T, bool TOP>
 cudaError_t launch(const LogprobsParams& p, cudaStream_t s) {
     constexpr int kRowThreads = 512;
-    // CTAs a row: as many as the SMs take at once, with at least two loads a thread
+    // CTAs a row: a cluster costs 1 us and pays from some 16 thousand logits a CTA on, as long as each has an SM, or two half
+    // of one (top 8, us with 1 / 2 / 4 / 8 / 16 CTAs: one row of 131072 fp32 8.9 / 7.4 / 6.0 / 5.5 / 6.0, of 32000 bf16 5.0 / 5.7 /
+    // 5.7 / 5.8 / 6.3; 19 rows of 262144 bf16 13.8 / 10.0 / 9.4 / 8.5 / 12.1; 76 17.6 / 13.2 / 18.2 / 22.4 / 34.9)
     int parts = 1;
-    while (parts < 16 && p.T * parts * 2 <= 304 && p.V / (2 * parts) >= kRowThreads * 2 * Vec<T>::kN) parts *= 2;
-    // many rows: smaller CTAs, so that an SM sums some while it ranks others
-    if (parts == 1 && p.T >= 608) return launch_cluster(k_logprobs<T, TOP, 256>, dim3(static_cast<unsigned>(p.T)), dim3(256), 0, 1, s, p);
-    if (parts > 8) {
-        static thread_local bool wide[kMaxDevices] = {};
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess && (dev >= kMaxDevices || !wide[dev])) {
-            e = cudaFuncSetAttribute(k_logprobs<T, TOP, kRowThreads>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e == cudaSuccess && dev < kMaxDevices) wide[dev] = true;
-        }
-        if (e != cudaSuccess) return e;
-    }
-    return launch_cluster(k_logprobs<T, TOP, kRowThreads>, dim3(static_cast<unsigned>(p.T * parts)), dim3(kRowThreads), 0, parts, s, p);
+    while (parts < kMaxParts && p.T * parts * 2 <= (parts == 1 ? 304 : 152) && p.V / (2 * parts) >= 16384) parts *= 2;
+    // Smaller CTAs for short rows, and for more rows than SMs hold of the large ones, so that an SM sums some while it ranks
+    // others (bf16, us with 256 / 512 threads: 500 rows of 32000 10.1 / 13.7, 2048 of 100003 79 / 88); but not of long rows
+    // that come in few waves (620 rows of 200064 fp32: 108 / 91).
+    const bool lengthy = static_cast<int64_t>(p.V) * sizeof(T) > 256 * 1024 && p.T > 608;
+    if (parts == 1 && (p.V <= 16384 || (p.T > 304 && !lengthy)))
+        return launch_cluster(k_logprobs<T, TOP, 256>, dim3(static_cast<unsigned>(p.T)), dim3(256), 0, 1, s, p);
+    return launch_cluster(k_logprobs<T, TOP, 512>, dim3(static_cast<unsigned>(p.T * parts)), dim3(512), 0, parts, s, p);
 }
 
 template <typename T>

@@ -1,5 +1,9 @@
 """How the calls of a decoding step behave as calls: captured into graphs and replayed on new inputs, on given streams
 and on two streams at once, with offsets beyond 32 bits, and with requests for nothing."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -197,3 +201,33 @@ def test_many_tokens(ctx):
     size = y[:4000].double().abs() + torch.stack([(x[:4000].double().abs() @ ad.a[i].double().abs().T) @ ad.b[i].double().abs().T for i in range(2)])[which.long(), torch.arange(4000, device="cuda")]
     assert bool(((one - exact).abs() <= 64 * 2.0 ** -24 * size).all())
     ctx.sync_status()
+
+
+FIRST = """
+import torch
+import gguf_block_quant_ggq_gb300 as ggq
+ctx = ggq.Context(0)
+x, ids = torch.randn(300, 1024, device="cuda"), torch.zeros(300, dtype=torch.int32, device="cuda")
+wide, logits = torch.randn(4, 8192, device="cuda"), torch.randn(3, 131072, device="cuda")
+ad = ctx.adapters(torch.randn(2, 16, 1024, device="cuda").half(), torch.randn(2, 1024, 16, device="cuda").half())
+cache = ctx.kv_cache("Q8_0", "Q4_0", 10, 32, 2, 64)
+k = x.view(300, 16, 64)
+def run():
+    table = ctx.rotary_table(100, 64)
+    return [table, ctx.norm(x, before=True)[0], ctx.norm(wide, before=True)[0], ctx.adapt(ad, x, x, ids), ctx.rotate(k, table, ids),
+            ctx.kv_append(cache, k[:, :2], k[:, 2:4], torch.arange(300, device="cuda"), table, ids, q=k), ctx.logprobs(logits, ids[:3], top_k=3)[0]]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+ctx.sync_status()
+"""
+
+
+def test_first_calls_of_a_process_are_captured(ctx):
+    done = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert done.returncode == 0, done.stderr[-2000:]
