@@ -21,6 +21,7 @@ import gguf_block_quant_ggq_gb300 as ggq  # noqa: E402
 
 LAYERS, HIDDEN, HEADS, KV_HEADS, DIM, VOCAB = 2, 1024, 16, 4, 64, 2048
 EXPERTS, INTER, TOP_K, PAGE, ADAPTERS, RANK, BEST = 32, 256, 4, 64, 3, 8, 5
+SPREAD = 2.0  # of the scaled logits
 QKV = (HEADS + 2 * KV_HEADS) * DIM
 
 
@@ -33,6 +34,7 @@ class Model:
         rand = lambda *s: torch.randn(s, device="cuda", generator=gen)  # noqa: E731
         self.embed = rand(VOCAB, HIDDEN)
         self.head = pack(syn.weights("Q4_K", VOCAB, HIDDEN, g))
+        self.scale = 1.0  # of the logits (1 / temperature)
         self.layers = []
         for _ in range(LAYERS):
             banks = [pack(syn.expert_bank(f, EXPERTS, *s, g)) for f, s in (("Q4_K", (INTER, HIDDEN)), ("Q4_K", (INTER, HIDDEN)),
@@ -104,9 +106,9 @@ class Model:
         self.lens += 1
         x, logits = self.forward(self.tokens, pos, slots, self.lens)
         best = self.ctx.logprobs(logits, top_k=1)[2]
-        lp, entropy, ids, top = self.ctx.logprobs(logits, best, top_k=BEST)
+        lp, entropy, ids, top = self.ctx.logprobs(logits, best, top_k=BEST, scale=self.scale)
         self.tokens.copy_(best[:, 0])
-        return x, lp, entropy, ids, top
+        return x, lp, entropy, ids, top, logits * self.scale
 
     def capture(self):
         lens, tokens = self.lens.clone(), self.tokens.clone()
@@ -136,6 +138,7 @@ def main(steps=32, prompts=(37, 200, 5, 90)):
         model = Model(ctx, users, max_len)
         x, logits = model.prompts(tokens)
         ends = torch.tensor(prompts, device="cuda").cumsum(0) - 1
+        model.scale = SPREAD / float(logits.std())  # synthetic weights know no temperature
         model.tokens = ctx.logprobs(logits[ends], top_k=1)[2][:, 0].long()
         results = []
         if graph:
