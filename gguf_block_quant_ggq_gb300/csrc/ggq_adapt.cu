@@ -380,14 +380,15 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 16 ? 1 : WARPS == 8 ? 2 : NT 
         }
         return h;
     };
-    // its copies of the block of columns b kBlock .. of `count` columns
+    // Its copies of the block of columns b kBlock .. of `count` columns.  A copy of no bytes names an address all the same, which
+    // has to be a multiple of 16 bytes as every other one: the bank's, since rows of x may start at 8.
     const auto copy_rows = [&](const Share& h, int b, int count, uint32_t to) {
         const int have = max(0, min(h.per, count - b * kBlock - h.column));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i * h.step >= kRows) break;
             if (!h.at[i]) continue;  // (what stands in the place of a row that is not there stays in that row)
-            const void* const src = have ? static_cast<const void*>(h.at[i] + b * kBlock) : p.x;
+            const void* const src = have ? static_cast<const void*>(h.at[i] + b * kBlock) : p.a;
             const uint32_t dst = to + h.to + i * h.step * kPitch;
             if (sizeof(T) == 4 || h.per == 8) copy16(dst, src, have * static_cast<int>(sizeof(T)));
             else copy8(dst, src, have * static_cast<int>(sizeof(T)));

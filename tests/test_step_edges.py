@@ -1,0 +1,54 @@
+"""Calls of a decoding step at the edges of what they take: alignments, streams, places, scales, sizes, precision."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import test_adapt  # noqa: E402
+import gguf_block_quant_ggq_gb300 as ggq  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from gguf_block_quant_ggq_gb300 import _build
+    _build.build()
+    c = ggq.Context(0)
+    yield c
+    c.close()
+
+
+def ints(a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+def at(t, shift, pad=16):
+    """The rows of t, `shift` elements behind 16 bytes, inside wider ones whose stride is a multiple of 16 elements."""
+    rows, width = t.shape
+    wide = torch.full((rows, (width + shift + pad) // 16 * 16 + 16), 5.0, device="cuda", dtype=t.dtype)
+    part = wide[:, shift:shift + width]
+    part.copy_(t)
+    return part
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("R,K,N", [(16, 520, 1000), (64, 1032, 40), (72, 264, 520), (160, 264, 328)])
+@pytest.mark.parametrize("shifts", [(4, 0, 0), (4, 4, 0), (0, 4, 0), (4, 0, 4), (4, 0, 1), (0, 1, 0), (12, 8, 8)])  # of x, y, out
+def test_adapt_rows_of_each_alignment(ctx, dtype, R, K, N, shifts):
+    """Rows of x at 8 bytes beside rows of y and out at 16, and the other way round: outputs of no whole block, and parts of
+    the outputs shorter than a block."""
+    c = test_adapt.Case(5, R, K, N, dtype, torch.bfloat16, ranks=[R, R // 2, R - 3, R, 8])
+    ad = ctx.adapters(c.a, c.b, ranks=c.ranks, scales=c.scales)
+    for lens, ids in (([1] * 3, [2, 0, -1]), ([1] * 70, [i * i % 6 - 1 for i in range(70)]), ([1] * 270, [i % 5 for i in range(270)]), ([37], [1]),
+                      ([700, 0, 801], [3, 0, 2])):
+        start = [sum(lens[:i]) for i in range(len(lens) + 1)]
+        x, y = (at(t, s) for t, s in zip(c.rows(start[-1]), shifts))
+        out = at(torch.zeros_like(y), shifts[2])
+        q_start = None if max(lens) == 1 else ints(start)
+        assert ctx.adapt(ad, x, y, ints(ids), q_start=q_start, out=out) is out
+        c.check(out, x, y, ids, start)
+        for t in (x, y, out):  # nothing beside the rows
+            assert bool((t._base[:, t.shape[1] + t.storage_offset():] == 5).all())
+    ctx.sync_status()
