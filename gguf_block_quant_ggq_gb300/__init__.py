@@ -263,9 +263,11 @@ class KVCache:
 class Adapters:
     """Low-rank adapters of one projection: a [n][rank][K] and b [n][N][rank] of one 16-bit type on the context's
     device, ranks int32 [n] (default: all), scales float32 [n] (default: 1).  Ranks that are no multiple of 8 are
-    laid out anew with the next one, once; else the tensors are used as they are."""
+    laid out anew with the next one, once, on `stream` (default: torch's current one) and in its memory; the object is
+    made when that is done, so that any stream may use it (inside a capture, the captured stream alone).  Other
+    tensors are used as they are."""
 
-    def __init__(self, ctx, a, b, ranks=None, scales=None):
+    def __init__(self, ctx, a, b, ranks=None, scales=None, stream=None):
         torch = ctx._torch
         if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] or a.dtype is not b.dtype:
             raise ValueError(f"expected banks [n, rank, K] and [n, N, rank] of one type, got {tuple(a.shape)} {a.dtype} and "
@@ -277,11 +279,16 @@ class Adapters:
             ctx._vec(t, t.dtype)
         if rank % 8:
             wide = (rank + 7) // 8 * 8
-            na, nb = a.new_zeros((n, wide, K)), b.new_zeros((n, b.shape[1], wide))
-            na[:, :rank], nb[:, :, :rank] = a, b
-            a, b = na, nb
-            if ranks is None:
-                ranks = torch.full((n,), rank, dtype=torch.int32, device=a.device)
+            if stream is None:
+                stream = torch.cuda.current_stream(ctx._dev)
+            with torch.cuda.stream(stream):
+                na, nb = a.new_zeros((n, wide, K)), b.new_zeros((n, b.shape[1], wide))
+                na[:, :rank], nb[:, :, :rank] = a, b
+                a, b = na, nb
+                if ranks is None:
+                    ranks = torch.full((n,), rank, dtype=torch.int32, device=a.device)
+                if not torch.cuda.is_current_stream_capturing():
+                    stream.synchronize()
         for t, name in ((ranks, "ranks"), (scales, "scales")):
             if t is not None and t.numel() != n:
                 raise ValueError(f"expected {n} {name}, got {t.numel()}")
@@ -709,9 +716,9 @@ class Context:
             self._check(st)
         return q_out
 
-    def adapters(self, a, b, ranks=None, scales=None) -> Adapters:
+    def adapters(self, a, b, ranks=None, scales=None, stream=None) -> Adapters:
         """Low-rank adapters of one projection (see Adapters)."""
-        return Adapters(self, a, b, ranks, scales)
+        return Adapters(self, a, b, ranks, scales, stream)
 
     def adapt(self, adapters: Adapters, x, y, ids, q_start=None, out=None, stream=None):
         """y + scale * B (A x) with each sequence's adapter: x [tokens][K], y [tokens][N] (the projection's output), ids

@@ -52,3 +52,49 @@ def test_adapt_rows_of_each_alignment(ctx, dtype, R, K, N, shifts):
         for t in (x, y, out):  # nothing beside the rows
             assert bool((t._base[:, t.shape[1] + t.storage_offset():] == 5).all())
     ctx.sync_status()
+
+
+@pytest.mark.parametrize("rank", [4, 13, 16])
+def test_adapters_are_ready_for_every_stream(ctx, rank):
+    """Banks that are laid out anew while the current stream is busy, and a call on another stream right behind them."""
+    c = test_adapt.Case(3, rank, 520, 96, torch.bfloat16, torch.float16)
+    x, y = c.rows(9)
+    ids = [0, 2, 1, 0, -1, 2, 2, 1, 0]
+    which, s = ints(ids), torch.cuda.Stream()
+    for given in (None, s):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)  # some 25 ms
+        ad = ctx.adapters(c.a, c.b, scales=c.scales, stream=given)
+        got = ctx.adapt(ad, x, y, which, stream=s)
+        torch.cuda.synchronize()
+        c.check(got, x, y, ids)
+    ctx.sync_status()
+
+
+def test_adapters_new_layout_is_of_the_given_streams_memory(ctx):
+    a, b = torch.ones((1, 9, 4096), device="cuda").half(), torch.ones((1, 65536, 9), device="cuda").half()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    ad = ctx.adapters(a, b, stream=s)
+    where, size = ad.b.data_ptr(), ad.b.untyped_storage().nbytes()
+    torch.cuda.synchronize()
+    del ad
+    with torch.cuda.stream(s):  # the block is the given stream's again
+        assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() == where
+
+
+def test_adapters_made_inside_a_capture(ctx):
+    c = test_adapt.Case(2, 5, 264, 40, torch.float32, torch.bfloat16)
+    x, y = c.rows(3)
+    which = ints([1, 0, 1])
+    ctx.adapt(ctx.adapters(c.a, c.b, scales=c.scales), x, y, which)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ctx.adapt(ctx.adapters(c.a, c.b, scales=c.scales), x, y, which)
+    for _ in range(2):
+        c.a.copy_(c.a.flip(1))
+        c.b.copy_(c.b * 0.5)
+        graph.replay()
+        c.check(got, x, y, [1, 0, 1])
+    ctx.sync_status()
