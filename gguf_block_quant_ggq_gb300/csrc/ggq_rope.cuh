@@ -114,7 +114,7 @@ __device__ __forceinline__ void rotate_tile(const RotateParams& p, int64_t r0, i
     for (int item = threadIdx.x; item < items; item += blockDim.x) {
         const int row = item / p.units, u = item - row * p.units;
         const int64_t t = r0 + row;
-        const bool turn = u < turned;
+        bool turn = u < turned;
         int ca, cb;  // first channels of the unit's two vectors
         bool two = true;
         float2 cs[V];
@@ -133,9 +133,10 @@ __device__ __forceinline__ void rotate_tile(const RotateParams& p, int64_t r0, i
                     }
                 }
             } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) cs[i] = make_float2(1.0f, 0.0f);
+                // as they are (0 times what is not finite is NaN)
                 if (!p.slots || p.slots[t] >= 0) set_error(p.err, DEV_ERR_BAD_POSITION);
+                if (p.in_place) continue;
+                turn = false;
             }
         } else {
             if (p.in_place) continue;

@@ -1,9 +1,12 @@
 """Calls of a decoding step at the edges of what they take: alignments, streams, places, scales, sizes, precision."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import test_adapt  # noqa: E402
+import test_rotary  # noqa: E402
 import gguf_block_quant_ggq_gb300 as ggq  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -97,4 +100,38 @@ def test_adapters_made_inside_a_capture(ctx):
         c.b.copy_(c.b * 0.5)
         graph.replay()
         c.check(got, x, y, [1, 0, 1])
+    ctx.sync_status()
+
+
+def same_bits(a, b):
+    """Equal bit for bit, but for the bits inside a NaN."""
+    whole = {4: torch.int32, 2: torch.int16}[a.element_size()]
+    return torch.equal(a.isnan(), b.isnan()) and bool(((a.contiguous().view(whole) == b.contiguous().view(whole)) | a.isnan()).all())
+
+
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D,turn,first", [(64, 64, 0), (128, 64, 64), (64, 24, 20), (64, 10, 3)])  # eight, four and one at once
+def test_positions_outside_turn_nothing(ctx, dtype, layout, D, turn, first):
+    """Rows of such positions come as they are: infinities, NaN and signs of zeros too."""
+    table = ctx.rotary_table(10, turn)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(turn)
+    x = torch.randn((6, 5, D), device="cuda", generator=g).to(dtype)
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -0.0, 0.0, -1.0], device="cuda").to(dtype)
+    x[1:5] = torch.where(torch.rand((4, 5, D), device="cuda", generator=g) < 0.4, odd[torch.randint(0, 6, (4, 5, D), device="cuda", generator=g)], x[1:5])
+    pos = ints([3, 10, -1, 2 ** 31 - 1, -2 ** 31, 9])
+    want = test_rotary.turned(x, table, pos, layout, first).to(dtype)
+    want[1:5] = x[1:5]
+    assert same_bits(ctx.rotate(x, table, pos, layout=layout, first=first), want)
+    y = x.clone()
+    ctx.rotate(y, table, pos, layout=layout, first=first, out=y)
+    assert same_bits(y, want)
+    # queries on the way into the cache; padded rows are not reported
+    cache = ctx.kv_cache("Q8_0", "Q8_0", 1, 16, 5, D)
+    slots = torch.tensor([0, -1, -1, -1, -1, 5], device="cuda")
+    keys = torch.zeros_like(x)
+    with pytest.raises(ggq.GGQError, match="position"):
+        ctx.sync_status()
+    assert same_bits(ctx.kv_append(cache, keys, keys, slots, table, pos, layout=layout, first=first, q=x), want)
     ctx.sync_status()
