@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
     if (parts > 1) cluster_arrive();  // every CTA runs before one writes to another
     const int64_t t = blockIdx.x / parts;
     const T* const row = static_cast<const T*>(p.logits) + t * p.row;
-    const float c = p.scale * kLog2e;
+    const float c = fminf(p.scale * kLog2e, 0x1.fffffep127f);  // (0 times infinity is no weight)
     if (TOP && tid == 0) sh.count = 0, sh.hots = 0;
 
     // the row's first value at 16 bytes, and whole vectors from there; the ends are the first CTA's, one a thread

@@ -135,3 +135,26 @@ def test_positions_outside_turn_nothing(ctx, dtype, layout, D, turn, first):
         ctx.sync_status()
     assert same_bits(ctx.kv_append(cache, keys, keys, slots, table, pos, layout=layout, first=first, q=x), want)
     ctx.sync_status()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [5, 5000, 131072])
+def test_logprobs_at_the_ends_of_the_scale(ctx, dtype, V):
+    """Scales whose product with log2(e) leaves fp32: the largest logits alone remain; and scales that leave them all alike."""
+    x = ((torch.arange(V, device="cuda") * 7919) % V).to(torch.float32).div(V).to(dtype)[None].repeat(2, 1)
+    x[0, V // 2], x[1, 1], x[1, V - 2] = 3.0, 3.0, 3.0
+    tokens = ints([[V // 2, 0], [V - 2, 2]])
+    for scale in (1e30, 2.35e38, 2.5e38, 3.4e38):
+        lp, ent, ids, top = ctx.logprobs(x, tokens, top_k=2, scale=scale)
+        # log p of the others is below -2 scale (rounded), the sums are 1 and 2 exactly
+        assert lp[0, 0] == 0.0 and abs(float(lp[1, 0]) + math.log(2.0)) <= 2.0 ** -23 and bool((lp[:, 1].double() < -1.9 * scale).all())
+        assert ent[0] == 0.0 and abs(float(ent[1]) - math.log(2.0)) <= 2.0 ** -23
+        assert ids[0, 0] == V // 2 and ids[1].tolist() == [1, V - 2]
+        assert top[0, 0] == 0.0 and float(top[0, 1]) < -1.9 * scale and float((top[1] + math.log(2.0)).abs().max()) <= 2.0 ** -23
+    room = (V / 512 + 64) * 2.0 ** -24 + 2.0 ** -22 + 2.0 ** -23 * math.log(V)  # of a sum of ones, and its logarithm
+    for scale in (1e-30, 1.2e-38, 1e-44):
+        lp, ent, ids, top = ctx.logprobs(x, tokens, top_k=2, scale=scale)
+        for t in (lp, top, -ent):
+            assert float((t.double() + math.log(V)).abs().max()) <= room
+        assert ids[0, 0] == V // 2 and ids[1].tolist() == [1, V - 2]
+    ctx.sync_status()
