@@ -593,6 +593,8 @@ class Context:
         norms = (after is not None) + 2 * (before is not None)
         if before is None and (out is not None or act is not None):
             raise ValueError("out and packed rows are the norm of the total: `before` is needed")
+        if packed is not None and act is None:
+            raise ValueError("packed rows of which format? `act` is needed")
         if before is not None and out is None and act is None:
             out = self._empty((n, H), dtype, stream)
         if total is None and (residual is not None or before is None):

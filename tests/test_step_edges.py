@@ -158,3 +158,14 @@ def test_logprobs_at_the_ends_of_the_scale(ctx, dtype, V):
             assert float((t.double() + math.log(V)).abs().max()) <= room
         assert ids[0, 0] == V // 2 and ids[1].tolist() == [1, V - 2]
     ctx.sync_status()
+
+
+def test_a_buffer_for_packed_rows_needs_their_format(ctx):
+    """Given buffers are written or the call is refused: nothing is left as it was without a word."""
+    x, w = torch.randn((3, 256), device="cuda"), torch.ones(256, device="cuda")
+    packed = torch.zeros((3, ggq.row_bytes("Q8_K", 256)), dtype=torch.uint8, device="cuda")
+    for more in (dict(before=w), dict(before=w, out=torch.empty_like(x)), dict(after=w), dict(residual=x)):
+        with pytest.raises(ValueError, match="act"):
+            ctx.norm(x, packed=packed, **more)
+    assert not bool(packed.any())
+    assert ctx.norm(x, before=w, act="Q8_K", packed=packed)[0] is packed and bool(packed.any())
