@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "../../include/ggq.h"
 #include "ggq_adapt.cuh"
@@ -112,8 +113,8 @@ ggq_status ggq_rotary_table(ggq_ctx* c, const ggq_rotary_spec* r, int64_t first,
         return fail(c, GGQ_ERR_SHAPE, "rotary_table: %d channels (even, 2..%d), positions %lld + %lld (at most 2^31)", r->turn,
                     kRotaryMaxDim, static_cast<long long>(first), static_cast<long long>(n));
     if (!std::isfinite(r->base) || r->base <= 1.0 || !std::isfinite(r->factor) || r->factor < 1.0 || r->original_len < 0 ||
-        !std::isfinite(r->magnitude))
-        return fail(c, GGQ_ERR_INVALID_ARG, "rotary_table: base above 1, factor of at least 1, original_len not negative, finite magnitude");
+        !(std::abs(r->magnitude) <= std::numeric_limits<float>::max()))
+        return fail(c, GGQ_ERR_INVALID_ARG, "rotary_table: base above 1, factor of at least 1, original_len not negative, a magnitude that is finite in fp32");
     const bool mixed = r->factor > 1.0 && r->original_len > 0;
     if (mixed && !(std::isfinite(r->beta_fast) && r->beta_slow > 0.0 && r->beta_fast >= r->beta_slow))
         return fail(c, GGQ_ERR_INVALID_ARG, "rotary_table: beta_fast at least beta_slow, both above 0");

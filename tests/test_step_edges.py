@@ -169,3 +169,12 @@ def test_a_buffer_for_packed_rows_needs_their_format(ctx):
             ctx.norm(x, packed=packed, **more)
     assert not bool(packed.any())
     assert ctx.norm(x, before=w, act="Q8_K", packed=packed)[0] is packed and bool(packed.any())
+
+
+def test_magnitudes_beyond_fp32_are_refused(ctx):
+    """A table of infinities and of 0 times infinity is no table."""
+    for magnitude in (1e39, -1e39, 3.4028236e38):
+        with pytest.raises(ggq.GGQError, match="magnitude"):
+            ctx.rotary_table(4, 8, magnitude=magnitude)
+    assert bool(ctx.rotary_table(4, 8, magnitude=3e38).isfinite().all())
+    ctx.sync_status()
