@@ -602,8 +602,11 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 16 ? 1 : WARPS == 8 ? 2 : NT 
         if (!busy) continue;
         const uint8_t* const bank = stage + kRows * kPitch + (32 * sub + 8 * (g >> 1) + (g & 1)) * b_pitch + 16 * tq;
         const int n = b * kBlock + 32 * sub + 8 * tq;  // this lane's eight outputs, from n0
+        // (of fp32 rows 32 ranks at a time, as above: 256 ranks of f16 banks 1.5e-6 of the result otherwise, 3.1e-7 so)
+        constexpr bool ALONE = sizeof(T) == 4;
         float o[4][4] = {};
         for (int s0 = 0; 32 * s0 < rank; ++s0) {
+            float block[4][4] = {};
             uint4 u[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const uint4*>(bank + 2 * j * b_pitch + 64 * s0);
@@ -625,9 +628,14 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 16 ? 1 : WARPS == 8 ? 2 : NT 
                     for (int k = 0; k < kB; ++k) {
                         if (i + k >= kT) continue;  // below the last bit
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mma_k16<true>(o[j], f, w[j][k][2 * q], w[j][k][2 * q + 1]);
+                        for (int j = 0; j < 4; ++j) mma_k16<true>(ALONE ? block[j] : o[j], f, w[j][k][2 * q], w[j][k][2 * q + 1]);
                     }
                 }
+            if constexpr (ALONE)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[j][e] += block[j][e];
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {

@@ -178,3 +178,55 @@ def test_magnitudes_beyond_fp32_are_refused(ctx):
             ctx.rotary_table(4, 8, magnitude=magnitude)
     assert bool(ctx.rotary_table(4, 8, magnitude=3e38).isfinite().all())
     ctx.sync_status()
+
+
+def plans(n):
+    """(lengths, adapters) whose rows go as one group, many groups, more groups than SMs take at once, prompts in tiles."""
+    return [([1], [0]), ([1] * 40, [i % n for i in range(40)]), ([1] * 200, [i % n for i in range(200)]), ([1] * 300, [i % n for i in range(300)]),
+            ([33, 100], [0, n - 1]), ([700, 800], [0, n - 1]), ([2500], [n - 1])]
+
+
+@pytest.mark.parametrize("bank", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("R", [8, 64, 72, 128, 256])
+@pytest.mark.parametrize("n", [2, 90])
+def test_adapt_keeps_the_bits_of_fp32_rows(ctx, bank, R, n):
+    """A one a rank and a one an output: the outputs are inputs.  Each of the two products may cut what its additions do not
+    hold, 2^-23 of a value; a term of 8 bits less in either would show as up to 2^-18."""
+    K, N = 264, 300
+    g = torch.Generator(device="cuda")
+    g.manual_seed(R)
+    pick = torch.stack([torch.randperm(K, device="cuda", generator=g)[:R] for _ in range(n)])  # input of each rank
+    a = torch.zeros((n, R, K), device="cuda", dtype=bank)
+    a.scatter_(2, pick[:, :, None], 1.0)
+    b = torch.zeros((n, N, R), device="cuda", dtype=bank)
+    to = torch.randint(0, R, (n, N), device="cuda", generator=g)  # rank of each output
+    b.scatter_(2, to[:, :, None], 1.0)
+    ad = ctx.adapters(a, b)
+    for lens, ids in plans(n):
+        T = sum(lens)
+        x, y = torch.randn((T, K), device="cuda", generator=g), torch.zeros((T, N), device="cuda")
+        start = [sum(lens[:i]) for i in range(len(lens) + 1)]
+        got = ctx.adapt(ad, x, y, ints(ids), q_start=None if max(lens) == 1 else ints(start))
+        of = torch.repeat_interleave(torch.tensor(ids, device="cuda"), torch.tensor(lens, device="cuda"))
+        want = x.gather(1, pick.gather(1, to)[of])
+        off = ((got.double() - want.double()).abs() / want.double().abs()).max()
+        assert float(off) <= 2.0 ** -22, (lens[:3], float(off) * 2 ** 24)
+    ctx.sync_status()
+
+
+@pytest.mark.parametrize("bank", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("R", [16, 64, 96, 256])
+def test_adapt_sums_fp32_rows_in_fp32(ctx, bank, R):
+    """A value passes at most 88 additions of 4096 inputs and their rank (the bound in test_adapt.py), each off by one unit of
+    2^-24 of what is summed so far, whose mean square is at most the whole's: sqrt(88) units together, 5.6e-7."""
+    c = test_adapt.Case(2, R, 4096, 256, torch.float32, bank)
+    ad = ctx.adapters(c.a, c.b, scales=c.scales)
+    for lens, ids in plans(2):
+        start = [sum(lens[:i]) for i in range(len(lens) + 1)]
+        x, y = c.rows(start[-1])
+        y = torch.zeros_like(y)
+        got = ctx.adapt(ad, x, y, ints(ids), q_start=None if max(lens) == 1 else ints(start))
+        want, _ = c.exact(x, y, ids, start)
+        off = float((got.double() - want).norm() / want.norm())
+        assert off <= 5.6e-7, (lens[:3], off)
+    ctx.sync_status()
