@@ -6,6 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import test_adapt  # noqa: E402
+import test_norm  # noqa: E402
 import test_rotary  # noqa: E402
 import gguf_block_quant_ggq_gb300 as ggq  # noqa: E402
 
@@ -229,4 +230,47 @@ def test_adapt_sums_fp32_rows_in_fp32(ctx, bank, R):
         want, _ = c.exact(x, y, ids, start)
         off = float((got.double() - want).norm() / want.norm())
         assert off <= 5.6e-7, (lens[:3], off)
+    ctx.sync_status()
+
+
+@pytest.mark.parametrize("form", ["both", "after", "before", "in place"])
+@pytest.mark.parametrize("rows,width,dtype", [
+    (1000, 4096, torch.bfloat16), (1000, 4096, torch.float32), (500, 8192, torch.float32), (7400, 264, torch.float16),  # 304, 304, 152, 2432 CTAs
+    (15000, 64, torch.bfloat16), (15000, 37, torch.float32),  # 1216 CTAs of four rows
+    (1400, 2051, torch.bfloat16), (470, 8200, torch.float16), (470, 16384, torch.bfloat16), (470, 20001, torch.float32)])  # 456, 152, 152, 152
+def test_norm_of_several_rows_a_cta(ctx, rows, width, dtype, form):
+    """As many rows as three turns of every CTA take, all of them against 64 bits."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows + width)
+    rn = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    size = torch.exp(2 * rn(rows, 1))  # rows differ, so that a neighbour's sum shows
+    x, res, gate = (rn(rows, width) * size).to(dtype), (rn(rows, width) * size.flip(0)).to(dtype), rn(rows, width).to(dtype)
+    wa, wb = 0.3 * rn(width), 0.3 * rn(width)
+    if form == "after":
+        gate = rn(rows, 1).to(dtype)
+    after, before = None if form == "before" else wa, None if form == "after" else wb
+    residual = None if form == "before" else res
+    want, t, off_out, off_t = test_norm.formula(x, after, gate, True, 0.3, residual, before, 1e-5, 1.0)
+    x_in, r_in = x.clone(), res.clone()
+    out, total = ctx.norm(x_in, before=before, after=after, gate=gate, gate_act="sigmoid", scale=0.3,
+                          residual=None if residual is None else r_in, eps=1e-5, offset=1.0,
+                          **(dict(out=x_in, total=r_in) if form == "in place" else {}))
+    if total is not None:
+        test_norm.check(total, t, off_t, dtype)
+    if out is not None:
+        test_norm.check(out, want, off_out, dtype)
+    if form != "in place":
+        assert torch.equal(x_in, x) and torch.equal(r_in, res)
+    ctx.sync_status()
+
+
+@pytest.mark.parametrize("act,rows,width", [("Q8_K", 1000, 4096), ("Q8_0", 500, 8192), ("Q8_1", 15000, 96), ("Q8_K", 15000, 256), ("Q8_K", 470, 16384)])
+def test_packed_norm_of_several_rows_a_cta(ctx, act, rows, width):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(width)
+    x, res = torch.randn((2, rows, width), device="cuda", generator=g).unbind(0)
+    w = torch.randn(width, device="cuda", generator=g)
+    rows32, total = ctx.norm(x, before=w, after=True, residual=res)
+    packed, same = ctx.norm(x, before=w, after=True, residual=res, act=act)
+    assert torch.equal(packed, ctx.quantize_act(act, rows32)) and torch.equal(total, same)
     ctx.sync_status()
