@@ -394,9 +394,9 @@ class Context:
             raise ValueError(f"expected a float32, float16 or bfloat16 tensor, got {dtype}")
         return code
 
-    def _own(self, cache):
+    def _own(self, cache, what="cache is"):
         if cache.device != self.device:
-            raise ValueError(f"the cache lies on cuda:{cache.device}, this context works on cuda:{self.device}")
+            raise ValueError(f"the {what} of cuda:{cache.device}, this context works on cuda:{self.device}")
 
     def _check(self, st):
         if st != 0:
@@ -580,8 +580,8 @@ class Context:
              eps: float = 1e-6, offset: float = 0.0, act: str | None = None, out=None, total=None, packed=None, stream=None):
         """(out, total): total = residual + scale * act(gate) * norm(x; after), out = norm(total; before), of x [tokens][H].
 
-        before, after: float32 weights [H] (offset is added to them), True for a norm without weights, None for
-        no norm.  gate: of x's type, [tokens][H], [H], or [tokens][1].  total is made where there is a residual, or
+        before, after: float32 weights [H] (offset is added to them), True for a norm without weights (nor offset), None
+        for no norm.  gate: of x's type, [tokens][H], [H], or [tokens][1].  total is made where there is a residual, or
         nothing else to return; given buffers are always written.  act: out is packed Q8_K, Q8_1 or Q8_0 rows
         (uint8, into `packed` where given) that the products take; a given `out` then gets the float rows too."""
         if x.dim() != 2:
@@ -725,8 +725,9 @@ class Context:
     def adapt(self, adapters: Adapters, x, y, ids, q_start=None, out=None, stream=None):
         """y + scale * B (A x) with each sequence's adapter: x [tokens][K], y [tokens][N] (the projection's output), ids
         int32 [sequences] (negative: none), q_start int32 [sequences + 1] unless every sequence has one token; out may
-        be y."""
-        self._own(adapters)
+        be y.  Rows of no sequence (behind the last one, say) are not written: of an out that is not given they hold
+        anything."""
+        self._own(adapters, "adapters are")
         n, seqs = x.shape[0], ids.numel()
         dtype = x.dtype
         code = self._code(dtype)

@@ -9,7 +9,9 @@
 // with no scratch and no second launch.  Groups are 32 rows of a sequence (long prompts) or 16: of a sequence, or of
 // single tokens of one adapter, so that a bank is read once for 16 rows whatever the order of the ids is: each cluster
 // counts through the ids and takes its group (64 rows of 24 adapters to 6144 outputs, bf16, rank 64: 11.9 us, where a
-// cluster a row, of which those work whose row is the first, 17th, ... of its adapter, took 14.7; so go more than 256 rows).
+// cluster a row, of which those work whose row is the first, 17th, ... of its adapter, took 14.7).  So go more than 256 rows,
+// each of whose clusters counts up to its own: the time grows with their square (24 adapters of rank 64, bf16: 18 us for
+// 256 rows, 41 for 512, 73 for 1024, 0.47 ms for 4096).
 //
 // Inside a CTA, blocks of x and bank (then of y and bank) come through a ring of shared memory by asynchronous
 // copies; memory is the bound, so what counts is bytes in flight: 50 to 100 KB an SM.  Four warps are 2 tiles of
@@ -20,8 +22,8 @@
 //
 // Operands of the matrix instruction (m16n8k16) are bf16 terms: an fp32 value is three of 8 bits each, an f16 value
 // two, exactly, and products of terms that lie below the last bit of the whole are left out.  f16 rows with f16 banks
-// enter as they are.  A x, fp32, is an operand of three terms for fp32 rows and of two for 16-bit ones (off by 2^-17,
-// a hundredth of the output's rounding).  (tf32 instructions, of which an fp32 value takes two, run at a third of the
+// enter as they are.  A x, fp32, is an operand of three terms for fp32 rows and of two for 16-bit ones (2.5e-6 of the
+// result, where the rounding of fp16 outputs is 2.1e-4 and of bf16 ones 1.7e-3).  A value that rounds to an infinity as bf16 gives NaN.  (tf32 instructions, of which an fp32 value takes two, run at a third of the
 // rate a product on this part.)
 #include <algorithm>
 
@@ -461,7 +463,8 @@ __global__ void __launch_bounds__(32 * WARPS, NT > 16 ? 1 : WARPS == 8 ? 2 : NT 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) terms_of<!BF && !F16>(*reinterpret_cast<const uint4*>(bank + 8 * (j0 + j) * kBankPitch), u[j]);
                 // (of fp32 rows a block at a time: the instruction's own additions cut off what they do not hold, which
-                // over 4096 inputs showed, 1.1e-6 of the result)
+                // over 4096 inputs showed, 1.1e-6 of the result; 16-bit rows leave that to the instruction, since their output's
+                // rounding is 200 times as much)
                 constexpr bool ALONE = sizeof(T) == 4;
                 float block[4][4] = {};
 #pragma unroll

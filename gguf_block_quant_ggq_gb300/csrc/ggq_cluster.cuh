@@ -28,11 +28,6 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* mine, uint32_t rank
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-    return v;
-}
 
 // A launch with programmatic dependent launch in clusters of `size` CTAs along x (1 .. 16).
 template <typename P>

@@ -7,12 +7,14 @@
 // A row is a cluster's: its CTAs take neighbouring parts and the first one joins them through
 // distributed shared memory, so few rows use many SMs without scratch or a second launch.
 //
-// The best: in the pass nothing but the largest logit of each thread is kept.  Of 64 groups of eight
-// lanes the `top`-th largest maximum is a bound that at least `top` logits reach; threads whose maximum
+// The best: in the pass nothing but the largest logit of each thread is kept.  Of the CTA's groups of
+// eight lanes (64, or 32 of a CTA of 256 threads) the `top`-th largest maximum is a bound that at least `top` logits reach; threads whose maximum
 // reaches it (a handful) have their part read again, by all, and what reaches the bound goes to a pool, whose
 // entries find their places by counting those before them (value, then id), so the order in which
-// they arrive does not show.  Where ties overflow the pool (a mask that leaves fewer than `top`), the
-// places are found one after another by passes over the part.
+// they arrive does not show.  Where ties overflow the pool the places are found one after another, by `top` passes over
+// the part: so in a CTA of whose groups fewer than `top` hold a value that its mask leaves (2048 rows of 100003 bf16
+// logits, 8 and 20 best: 80 and 96 us, 0.19 and 0.20 ms with 50 values left in a row, 1.4 and 3.3 ms with 5; one row of 131072
+// fp32 5.3 and 6.5 us, 25 and 53 with 50 or 5).
 //
 // Sums of 16-bit logits take five instructions a value, so that memory is the bound: masked
 // values are raised to one that weighs 0 while they are packed, pairs are multiplied and added at once.
@@ -443,15 +445,16 @@ __global__ void __launch_bounds__(kRowThreads, 1024 / kRowThreads) k_logprobs(co
 
 template <typename T, bool TOP>
 cudaError_t launch(const LogprobsParams& p, cudaStream_t s) {
-    constexpr int kRowThreads = 512;
     // CTAs a row: a cluster costs 1 us and pays from some 16 thousand logits a CTA on, as long as each has an SM, or two half
     // of one (top 8, us with 1 / 2 / 4 / 8 / 16 CTAs: one row of 131072 fp32 8.9 / 7.4 / 6.0 / 5.5 / 6.0, of 32000 bf16 5.0 / 5.7 /
     // 5.7 / 5.8 / 6.3; 19 rows of 262144 bf16 13.8 / 10.0 / 9.4 / 8.5 / 12.1; 76 17.6 / 13.2 / 18.2 / 22.4 / 34.9)
     int parts = 1;
     while (parts < kMaxParts && p.T * parts * 2 <= (parts == 1 ? 304 : 152) && p.V / (2 * parts) >= 16384) parts *= 2;
     // Smaller CTAs for short rows, and for more rows than SMs hold of the large ones, so that an SM sums some while it ranks
-    // others (bf16, us with 256 / 512 threads: 500 rows of 32000 10.1 / 13.7, 2048 of 100003 79 / 88); but not of long rows
-    // that come in few waves (620 rows of 200064 fp32: 108 / 91).
+    // others (bf16, us with 256 / 512 threads: 500 rows of 32000 10.1 / 13.7, 2048 of 100003 79 / 88); but not of rows above
+    // 256 KB, whose reading outweighs that (200064 logits, fp32: 620 rows 115 / 94, 2048 286 / 253, 4096 545 / 499; bf16: 62 / 55,
+    // 151 / 143, 281 / 273; at the border, 131072 bf16: 620 rows 41 / 38, 2048 98 / 98, 8192 348 / 354).  Up to 608 rows the
+    // larger CTAs do not fill the SMs twice and the two differ little (500 rows of 131072, fp32 47.5 / 46.1, bf16 29.0 / 29.5).
     const bool lengthy = static_cast<int64_t>(p.V) * sizeof(T) > 256 * 1024 && p.T > 608;
     if (parts == 1 && (p.V <= 16384 || (p.T > 304 && !lengthy)))
         return launch_cluster(k_logprobs<T, TOP, 256>, dim3(static_cast<unsigned>(p.T)), dim3(256), 0, 1, s, p);

@@ -9,7 +9,11 @@
 // at many rows and the chain launch - load - sum - sum - store at few (one row of 4096: 2.8 us).  A row of up to 256
 // channels is one warp's, wider ones a CTA's with eight channels a thread: the widest loads
 // there are for 16-bit rows, and the eight that a packed block of 32 or 256 channels gives a
-// lane, so that the packed forms are quantized from registers.
+// lane, so that the packed forms are quantized from registers.  4096 rows of 4096 with a residual take 23.6 us as bf16
+// rows (floor 19.8) and 28.7 to 29.7 as blocks (17.5), of fp32 52.0 (39.5) and 49.9 to 54.0 (32.4).
+//
+// Rows beyond 8192 channels, and odd or unaligned ones, are read without a row ahead, the latter value by value: 1024 of 16384
+// 32.9 us (bf16, floor 19.8) and 53.0 (fp32, 39.5), 4096 of 4095 67.3 and 62.2.
 #include <algorithm>
 
 #include "ggq_device.cuh"

@@ -15,8 +15,8 @@ struct NormParams {
     void* total;            // or null
     void* out;              // or null
     uint8_t* packed;        // or null
-    const float* after_w;   // or null: ones
-    const float* before_w;  // or null: ones
+    const float* after_w;   // or null: none
+    const float* before_w;  // or null: none
     int64_t x_token, residual_token, gate_token, total_token, out_token;  // strides in elements
     int64_t T;
     int H;
