@@ -588,8 +588,8 @@ ggq_status ggq_moe_route(ggq_ctx* ctx, const ggq_router* router, int dtype, cons
                          int32_t* ids, float* weights, void* stream);
 
 /* Synchronise `stream` and read the device error word: GGQ_OK, or
- * GGQ_ERR_DEVICE (a bounded wait inside a kernel ran out, or an expert id, slot,
- * page, length or row range was out of bounds; the word is cleared in the stream's
+ * GGQ_ERR_DEVICE (a bounded wait inside a kernel ran out, or an expert or adapter id, slot,
+ * page, length, row range, position or token id was out of bounds; the word is cleared in the stream's
  * order), or GGQ_ERR_CUDA.  No other stream is waited for. */
 ggq_status ggq_sync_status(ggq_ctx* ctx, void* stream);
 
@@ -600,7 +600,8 @@ ggq_status ggq_sync_status(ggq_ctx* ctx, void* stream);
  * with r(v) = 1 / sqrt(mean(v^2) + eps) over the token's channels and act the identity or the
  * sigmoid.  A norm without weights has no factor behind r: offset is added to given weights alone.
  * Everything in between is fp32 (a sum of squares that leaves fp32, at magnitudes about 2^63, gives
- * zeros; with eps = 0 squares below 2^-126, of magnitudes below 2^-63, lose bits); total is rounded where it is stored, its norm takes it unrounded.
+ * zeros; with eps = 0 squares below 2^-126, of magnitudes below 2^-63, lose bits); total is rounded
+ * where it is stored, its norm takes it unrounded.
  * `total` without norms & 2 and `out` or `packed` with it are what a call needs at least.
  * packed: the same rows as out, before their rounding to dtype, as blocks that
  * ggq_mul_mat_vec_q, _qa and ggq_moe_experts_q take, byte for byte what ggq_quantize_act makes
@@ -615,15 +616,15 @@ ggq_status ggq_norm(ggq_ctx* ctx, const ggq_norm_args* args, void* stream);
  * within L positions are, those that turn more than beta_fast times are not, and in between the
  * two are mixed by the channel's place (YaRN: Peng et al. 2023, section 3.2; its magnitude
  * 0.1 ln(factor) + 1 is the caller's to give).  Angles are off by 2^-27 of a turn up to position 2^26
- * (beyond it by the frequencies' own rounding to fp64).
+ * where the frequency is at most 1 (factors from 1 on), else by its own rounding to fp64, 2^-53 of the angle.
  * spec and its factors are host memory, read before the call returns.  Needs no scratch. */
 ggq_status ggq_rotary_table(ggq_ctx* ctx, const ggq_rotary_spec* spec, int64_t first, int64_t n, float* table, void* stream);
 
 /* Rotate heads by their tokens' positions: x [T][n_heads][D] to out.  Of a head's channels the `turn` from `first` on are turned in pairs,
  * j and j + turn / 2 of them (HALF) or 2 j and 2 j + 1 (PAIRS): (a, b) -> (a c - b s, a s + b c)
  * with (c, s) = table[position][j], in fp32, each product and the sum rounded; the others are
- * copied.  out may be x with its strides, and must not overlap it otherwise.  A position outside
- * the table turns nothing and is reported by ggq_sync_status.  Needs no scratch. */
+ * copied.  Positions count the table's rows, whatever position its first one was made for.  out may be x with its strides, and must not overlap it otherwise.  A position outside
+ * the table turns nothing (the row is copied) and is reported by ggq_sync_status.  Needs no scratch. */
 ggq_status ggq_rotate(ggq_ctx* ctx, const ggq_rotary* rotary, const ggq_rotate_args* args, void* stream);
 
 /* ggq_kv_store with the rotation on the way: keys are turned as ggq_rotate turns them and
